@@ -498,6 +498,198 @@ sls_status sls_selection_recall(const sls_attn_desc* desc, const void* q, const 
                                 int32_t k_fixed, const int32_t* ctx_len, float* recall, void* workspace,
                                 size_t workspace_bytes, void* stream);
 
+/* ---- per-head norm and position rotation ------------------------------- */
+
+/*
+ * Shapes of sls_qk_norm_rope.
+ *   num_q_heads, num_kv_heads  >= 0, at least one head in all
+ *   head_dim     D in {64, 128}
+ *   rotary_dim   R: the first R channels of a head are rotated, the others
+ *                pass through; a multiple of 16 in [0, D]
+ *   interleaved  0: channel i pairs with i + R/2;  1: 2i pairs with 2i + 1
+ *   dtype        SLS_DTYPE_F32 or SLS_DTYPE_BF16 (q, k, weights, outputs)
+ *   eps          added to the mean square, >= 0
+ *   theta        base of the frequencies f_i = theta^(-2i/R), i < R/2, > 0
+ *   inv_freq     HOST pointer to R/2 frequencies in radians per position
+ *                (each finite), or NULL for those of theta
+ */
+typedef struct sls_rope_desc {
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t dtype;
+  float eps;
+  double theta;
+  const double* inv_freq;
+} sls_rope_desc;
+
+/*
+ * Root-mean-square norm of every query and key head and the rotation by the
+ * token's position, in one pass.  For token t and head vector x:
+ *   y = x * w / sqrt(mean(x^2) + eps)        (w NULL: y = x, no norm)
+ *   (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ * for every channel pair (a, b) with the angle positions[t] * f_i.
+ * The arithmetic is fp32; angles are reduced modulo one turn in 64-bit fixed
+ * point, so far positions lose nothing; results are rounded once.
+ *   q [N, Hq, D], k [N, Hkv, D]   read, with strides in elements between
+ *        tokens and between heads (>= 0, multiples of 8 for bf16 and 4 for
+ *        fp32; channels are contiguous), so the head slices of one packed
+ *        projection can be passed as they are
+ *   q_weight, k_weight  [D] dtype, or NULL
+ *   positions [N] int32; a token with a negative position is skipped (its
+ *        outputs are left as they were)
+ *   q_out, k_out  written, strides as above and without overlap.  They may
+ *        be q and k themselves (same pointer and strides); any other overlap
+ *        of inputs and outputs gives unspecified results.
+ * q (k) and its output are ignored when num_q_heads (num_kv_heads) is 0;
+ * num_tokens 0 does nothing.
+ * Errors: SLS_EINVAL for null or misaligned pointers, bad strides or bad
+ * values; SLS_EUNSUPPORTED for another head_dim, rotary_dim or dtype.
+ */
+sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens,
+                            const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                            const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* q_weight, const void* k_weight,
+                            const int32_t* positions,
+                            void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride,
+                            void* k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                            void* stream);
+
+/* ---- the 8-bit KV cache ------------------------------------------------- */
+
+/* Code formats: the value of a code c is c * s with the block's scale s. */
+#define SLS_KV8_INT8 0  /* two's complement integers -127..127, s = max|x| / 127 */
+#define SLS_KV8_E4M3 1  /* 4-bit exponent, 3-bit mantissa floats, s = max|x| / 448 */
+
+/*
+ * A K/V cache held in 8 bits with one scale for each block of `block` tokens
+ * of each KV head (bf16 descriptors only).  The struct lives on the host, the
+ * pointers are device memory of the caller.  Blocks are quantised once, when
+ * their last token arrives; the tokens of a sequence's newest, partial block
+ * wait in bf16 in the tail buffers (token position t at slot t % block).
+ * Complete block: amax = max |x| over its block * D elements, and with
+ * top = 127 or 448
+ *   s = amax / top,  code = round(x * top / amax) to the nearest code, ties
+ *   to even (each step one IEEE float32 operation); amax = 0 gives s = 0 and
+ *   codes 0; an infinity or NaN in the block gives s = NaN and codes 0, so
+ *   that it shows in every output that attends to the block.
+ *   format    SLS_KV8_INT8 or SLS_KV8_E4M3
+ *   block     power of two in [16, 256], Cap % block == 0
+ *   k_codes, v_codes    [B, Hkv, Cap, D] one byte each
+ *   k_scales, v_scales  [B, Hkv, Cap/block] float
+ *   k_tail, v_tail      [B, Hkv, block, D] bf16
+ * All pointers 16-byte aligned but for the scales (4).
+ */
+typedef struct sls_kv8_cache {
+  int32_t format;
+  int32_t block;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scales;
+  float* v_scales;
+  void* k_tail;
+  void* v_tail;
+} sls_kv8_cache;
+
+/*
+ * Append new tokens of every sequence to its cache: one decoded token, a
+ * whole prompt or a piece of one.  Sequence b appends its first new_len[b]
+ * (clamped to [0, max_new]; NULL: max_new) tokens at positions ctx_len[b]
+ * and up: blocks that become complete are quantised, the tokens of the
+ * newest, partial block go to the tail buffers, and ctx_out[b] =
+ * ctx_len[b] + the count.  A sequence whose tokens do not all fit is left
+ * unchanged (ctx_out[b] = ctx_len[b]).
+ *   k_new, v_new  [B, max_new, Hkv, D] bf16 (read), strides in elements
+ *                 between sequences, tokens and heads (>= 0, multiples of 8;
+ *                 channels contiguous)
+ *   kmin, kmax    [B, Hkv, Cap/P, D] bf16 page min/max of the (unquantised)
+ *                 keys to keep current as sls_pagemeta_update does, or both
+ *                 NULL
+ *   mass          [B, Hkv, Cap/block] float: set to 0 for every block that
+ *                 becomes complete, or NULL
+ *   ctx_len       [B] int32 (read); ctx_out [B] int32 (written; may be
+ *                 ctx_len itself)
+ *   pos_out       [B] int32 receiving the first written position (-1 when
+ *                 nothing was written), or NULL
+ * max_new 0 appends nothing (ctx_out and pos_out are still written).
+ */
+sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
+                          const void* k_new, int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride,
+                          const void* v_new, int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride,
+                          int32_t max_new, const int32_t* new_len, void* kmin, void* kmax, float* mass,
+                          const int32_t* ctx_len, int32_t* ctx_out, int32_t* pos_out, void* stream);
+
+/* Bytes of workspace sls_kv8_decode_attend needs (with_mass: when it is
+ * given mass_out); 0 for an invalid or unsupported descriptor or cache. */
+size_t sls_kv8_decode_attend_workspace_size(const sls_attn_desc* desc, const sls_kv8_cache* cache,
+                                            int32_t with_mass);
+
+/*
+ * Decode attention over an 8-bit cache: softmax(scale q.k^) v^ with k^, v^
+ * the stored values (codes times scales; bf16 tail tokens as they are), over
+ * the positions < ctx_len[b] (page_idx NULL) or over the valid tokens of the
+ * listed pages, with the sink as in sls_combine_splits.  Rows of uneven
+ * length are cut into equal ranges over the GPU.
+ *   desc      bf16, G <= 8, D 64 or 128, B*Hkv <= 4096, B*Hkv*Cap < 2^31;
+ *             with page_idx pages of >= 16 tokens (the page size does not
+ *             matter otherwise); of the flags only SLS_FLAG_TEST_WAIT_TIMEOUT
+ *   page_idx, idx_stride, count, k_fixed   as in sls_sparse_decode_attend
+ *             (-1 entries are skipped, bad ones counted for
+ *             sls_pipeline_check and skipped)
+ *   sink      [Hq] float or NULL;  out [B, Hq, D] bf16;  lse [B, Hq] float
+ *             or NULL
+ *   mass_in, mass_out  [B, Hkv, Cap/block] float, or mass_out NULL: every
+ *             complete block of the context gets mass_out = mass_in (NULL: 0)
+ *             + the sum over the group's query heads and the block's tokens
+ *             of the softmax weight; the other blocks' entries are left as
+ *             they were.  mass_in may be mass_out.  Only without page_idx.
+ *             The sums do not depend on the order in which CTAs finish.
+ *   workspace >= sls_kv8_decode_attend_workspace_size() bytes, 16-byte
+ *             aligned, zero-filled before its first use (every call leaves
+ *             its arrival counters at zero); calls sharing it must not run
+ *             concurrently
+ * Rows with no token: out = 0, lse = -inf (or the sink alone).
+ */
+sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* q,
+                                 const int32_t* page_idx, int32_t idx_stride, const int32_t* count,
+                                 int32_t k_fixed, const int32_t* ctx_len, const float* sink, void* out,
+                                 float* lse, const float* mass_in, float* mass_out, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
+ * Bound a cache by the attention weight its blocks have drawn.  A sequence
+ * with more than keep complete blocks keeps, in every KV head's row, its
+ * first n_sink_blocks, its newest n_recent_blocks complete blocks and those
+ * with the largest mass of the others, ties to the lower block (NaN counts as
+ * the largest), keep in all, in their old order without gaps, so the row
+ * looks as if the evicted tokens had never been appended.  The tail stays;
+ * ctx_out[b] = min(ctx_len[b]/block, keep) * block + ctx_len[b] % block.
+ *   desc, src     the cache to cut; dst_capacity, dst  the cache to write:
+ *                 the source itself (dst NULL or equal to src, dst_capacity
+ *                 = Cap: in place) or another one with the same format and
+ *                 block and no memory in common (every kept block is copied,
+ *                 and the valid tail tokens).
+ *                 (keep + 1) * block <= dst_capacity, dst_capacity % block
+ *                 == 0
+ *   keep >= 1, 0 <= n_sink_blocks + n_recent_blocks <= keep
+ *   mass          [B, Hkv, Cap/block] float (read); mass_out [B, Hkv,
+ *                 dst_capacity/block] the kept blocks' sums, or NULL.  In
+ *                 place mass_out must be mass.
+ *   kmin, kmax    page min/max to take along, or both NULL, to kmin_out,
+ *                 kmax_out [B, Hkv, dst_capacity/P, D] (in place: the same
+ *                 buffers); needs P <= block and P dividing dst_capacity
+ *   kept_idx      [B*Hkv, keep] int32 (written): the kept blocks' old
+ *                 numbers, ascending, -1 padded when the row has fewer
+ *   ctx_len [B] (read), ctx_out [B] (written; may be ctx_len itself)
+ */
+sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, int32_t dst_capacity,
+                         const sls_kv8_cache* dst, int32_t keep, int32_t n_sink_blocks,
+                         int32_t n_recent_blocks, const float* mass, float* mass_out, const void* kmin,
+                         const void* kmax, void* kmin_out, void* kmax_out, int32_t* kept_idx,
+                         const int32_t* ctx_len, int32_t* ctx_out, void* stream);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Message of the last failing call on this thread ("" if none). */

@@ -12,6 +12,7 @@ LIB_PATH = _build.LIB
 SLS_OK, SLS_EINVAL, SLS_EUNSUPPORTED, SLS_EOVERFLOW, SLS_EWORKSPACE, SLS_ECUDA = 0, -1, -2, -3, -4, -5
 SLS_ETIMEOUT, SLS_EDEVICE = -6, -7
 SLS_DTYPE_F32, SLS_DTYPE_BF16 = 0, 1
+SLS_KV8_INT8, SLS_KV8_E4M3 = 0, 1
 SLS_FLAG_CUDA_CORES = 1
 SLS_FLAG_NO_TMA = 2
 SLS_FLAG_TEST_WAIT_TIMEOUT = 4  # test hook of the bounded waits (include/sls.h)
@@ -26,6 +27,21 @@ class AttnDesc(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class RopeDesc(ctypes.Structure):
+    """ctypes mirror of sls_rope_desc."""
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("theta", ctypes.c_double),
+                ("inv_freq", ctypes.POINTER(ctypes.c_double))]
+
+
+class Kv8CacheDesc(ctypes.Structure):
+    """ctypes mirror of sls_kv8_cache."""
+    _fields_ = [("format", ctypes.c_int32), ("block", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "k_tail", "v_tail")]
+
+
 class Stats(ctypes.Structure):
     """sls_stats: which paths the library took (include/sls.h)."""
     _fields_ = [(n, ctypes.c_uint64) for n in (
@@ -37,7 +53,9 @@ class Stats(ctypes.Structure):
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
+_L = ctypes.c_int64
 _D = ctypes.POINTER(AttnDesc)
+_C = ctypes.POINTER(Kv8CacheDesc)
 SIGNATURES = {
     "sls_pagemeta_build": (_I, [_D, _P, _P, _P, _P, _P]),
     "sls_pagemeta_update": (_I, [_D, _P, _P, _P, _P, _P]),
@@ -68,6 +86,12 @@ SIGNATURES = {
                                    _P, ctypes.c_size_t, _P]),
     "sls_selection_recall_workspace_size": (ctypes.c_size_t, [_D]),
     "sls_selection_recall": (_I, [_D, _P, _P, _P, _I, _P, _I, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sls_qk_norm_rope": (_I, [ctypes.POINTER(RopeDesc), _I, _P, _L, _L, _P, _L, _L, _P, _P, _P, _P, _L, _L, _P, _L, _L,
+                              _P]),
+    "sls_kv8_append": (_I, [_D, _C, _P, _L, _L, _L, _P, _L, _L, _L, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sls_kv8_decode_attend_workspace_size": (ctypes.c_size_t, [_D, _C, _I]),
+    "sls_kv8_decode_attend": (_I, [_D, _C, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "sls_kv8_evict": (_I, [_D, _C, _I, _C, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "sls_pipeline_check": (_I, []),
     "sls_last_error": (ctypes.c_char_p, []),
     "sls_version": (_I, []),

@@ -1,5 +1,6 @@
 // C ABI of libsls: host-side validation, then launch.  Nothing here touches
 // device memory or synchronises; a failed check returns before any launch.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -152,7 +153,8 @@ sls_status sls_pipeline_check(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(SLS_ECUDA, "device synchronisation failed");
   unsigned int timeouts = 0, bad = 0;
   for (auto take : {sls::take_status_attend_cc, sls::take_status_attend_mma, sls::take_status_attend_tma,
-                    sls::take_status_attend_refined, sls::take_status_quest_step, sls::take_status_recall}) {
+                    sls::take_status_attend_refined, sls::take_status_quest_step, sls::take_status_recall,
+                    sls::take_status_attend_kv8}) {
     const sls::DeviceStatus st = take();
     timeouts += st.wait_timeouts;
     bad += st.bad_page_ids;
@@ -554,6 +556,221 @@ sls_status sls_combine_splits(const sls_attn_desc* desc, const float* o_part, co
   if (num_splits < 1 || num_splits > 1024) return fail(SLS_EINVAL, "num_splits %d not in [1, 1024]", num_splits);
   return cuda_status(sls::launch_combine(s, o_part, m_part, l_part, num_splits, sink, out, lse, (cudaStream_t)stream),
                      "sls_combine_splits");
+}
+
+// ---- per-head norm and rotation, the 8-bit cache
+
+sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens, const void* q, int64_t q_token_stride,
+                            int64_t q_head_stride, const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* q_weight, const void* k_weight, const int32_t* positions, void* q_out,
+                            int64_t q_out_token_stride, int64_t q_out_head_stride, void* k_out,
+                            int64_t k_out_token_stride, int64_t k_out_head_stride, void* stream) {
+  if (!rope) return fail(SLS_EINVAL, "rope is NULL");
+  const int Hq = rope->num_q_heads, Hkv = rope->num_kv_heads, D = rope->head_dim, R = rope->rotary_dim;
+  if (Hq < 0 || Hkv < 0 || Hq > (1 << 20) || Hkv > (1 << 20) || Hq + Hkv < 1)
+    return fail(SLS_EINVAL, "head counts Hq=%d Hkv=%d", Hq, Hkv);
+  if (D != 64 && D != 128) return fail(SLS_EUNSUPPORTED, "head_dim %d not in {64, 128}", D);
+  if (rope->dtype != SLS_DTYPE_F32 && rope->dtype != SLS_DTYPE_BF16)
+    return fail(SLS_EUNSUPPORTED, "dtype %d", rope->dtype);
+  if (R < 0 || R > D || R % 16) return fail(SLS_EUNSUPPORTED, "rotary_dim %d not a multiple of 16 in [0, %d]", R, D);
+  if (rope->interleaved != 0 && rope->interleaved != 1) return fail(SLS_EINVAL, "interleaved must be 0 or 1");
+  if (!(rope->eps >= 0.f) || std::isinf(rope->eps)) return fail(SLS_EINVAL, "eps must be finite and >= 0");
+  if (!rope->inv_freq && (!(rope->theta > 0.0) || std::isinf(rope->theta)))
+    return fail(SLS_EINVAL, "theta must be finite and > 0");
+  if (num_tokens < 0) return fail(SLS_EINVAL, "num_tokens %d < 0", num_tokens);
+  const int vec = rope->dtype == SLS_DTYPE_F32 ? 4 : 8;
+  sls::RopeArgs a = {};
+  auto side = [&](const char* name, int heads, const void* in, int64_t it, int64_t ih, const void* w, void* out,
+                  int64_t ot, int64_t oh) -> sls_status {
+    if (!in || !out) return fail(SLS_EINVAL, "%s or its output is NULL", name);
+    if (((uintptr_t)in | (uintptr_t)out | (uintptr_t)w) & 15)
+      return fail(SLS_EINVAL, "%s, its weight and its output must be 16-byte aligned", name);
+    const int64_t lim = int64_t(1) << 40;
+    if (it < 0 || ih < 0 || ot < 0 || oh < 0 || it > lim || ih > lim || ot > lim || oh > lim || it % vec || ih % vec ||
+        ot % vec || oh % vec)
+      return fail(SLS_EINVAL, "strides of %s must be multiples of %d elements in [0, 2^40]", name, vec);
+    // no two output vectors overlap: one of the two axes steps past the whole extent of the other
+    const bool one_t = num_tokens == 1, one_h = heads == 1;
+    const bool t_out = (one_h || oh >= D) && (one_t || ot >= (heads - 1) * oh + D);
+    const bool h_out = (one_t || ot >= D) && (one_h || oh >= (num_tokens - 1) * ot + D);
+    if (!t_out && !h_out) return fail(SLS_EINVAL, "output vectors of %s overlap", name);
+    return SLS_OK;
+  };
+  if (num_tokens == 0) return ok();
+  sls_status r;
+  REQUIRE(positions);
+  if (Hq && (r = side("q", Hq, q, q_token_stride, q_head_stride, q_weight, q_out, q_out_token_stride, q_out_head_stride)))
+    return r;
+  if (Hkv && (r = side("k", Hkv, k, k_token_stride, k_head_stride, k_weight, k_out, k_out_token_stride,
+                       k_out_head_stride)))
+    return r;
+  for (int i = 0; i < R / 2; ++i) {
+    const double f = rope->inv_freq ? rope->inv_freq[i] : std::pow(rope->theta, -2.0 * i / R);
+    if (!std::isfinite(f)) return fail(SLS_EINVAL, "frequency %d is not finite", i);
+    const double turns = f / 6.283185307179586476925286766559;
+    double frac = turns - std::floor(turns);  // in [0, 1]
+    if (frac >= 1.0) frac = 0.0;
+    a.freq[i] = (uint64_t)std::ldexp(frac, 64);
+  }
+  a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight; a.qo = q_out; a.ko = k_out; a.pos = positions;
+  a.q_t = q_token_stride; a.q_h = q_head_stride; a.k_t = k_token_stride; a.k_h = k_head_stride;
+  a.qo_t = q_out_token_stride; a.qo_h = q_out_head_stride; a.ko_t = k_out_token_stride; a.ko_h = k_out_head_stride;
+  a.N = num_tokens; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.R = R;
+  a.interleaved = rope->interleaved; a.dtype = rope->dtype; a.eps = rope->eps;
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_qk_norm_rope(a, (cudaStream_t)stream), "sls_qk_norm_rope");
+}
+
+static sls_status check_kv8(const sls::Shape& s, const sls_kv8_cache* c, int capacity, const char* name, sls::Kv8* out) {
+  if (!c) return fail(SLS_EINVAL, "%s is NULL", name);
+  if (s.dtype != SLS_DTYPE_BF16) return fail(SLS_EUNSUPPORTED, "the 8-bit cache takes bf16 descriptors only");
+  if (c->format != SLS_KV8_INT8 && c->format != SLS_KV8_E4M3)
+    return fail(SLS_EUNSUPPORTED, "%s format %d", name, c->format);
+  if (!pow2(c->block) || c->block < 16 || c->block > 256)
+    return fail(SLS_EINVAL, "%s block %d must be a power of two in [16, 256]", name, c->block);
+  if (capacity < c->block || capacity % c->block)
+    return fail(SLS_EINVAL, "%s capacity %d not a multiple of its block %d", name, capacity, c->block);
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !c->k_tail || !c->v_tail)
+    return fail(SLS_EINVAL, "%s has a NULL pointer", name);
+  if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes | (uintptr_t)c->k_tail | (uintptr_t)c->v_tail) & 15)
+    return fail(SLS_EINVAL, "%s codes and tails must be 16-byte aligned", name);
+  if (((uintptr_t)c->k_scales | (uintptr_t)c->v_scales) & 3)
+    return fail(SLS_EINVAL, "%s scales must be 4-byte aligned", name);
+  *out = sls::Kv8{c->format, c->block, __builtin_ctz((unsigned)c->block), c->k_codes, c->v_codes,
+                  c->k_scales, c->v_scales, c->k_tail, c->v_tail};
+  return SLS_OK;
+}
+
+sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* k_new,
+                          int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                          int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t max_new,
+                          const int32_t* new_len, void* kmin, void* kmax, float* mass, const int32_t* ctx_len,
+                          int32_t* ctx_out, int32_t* pos_out, void* stream) {
+  sls::Shape s;
+  sls::Kv8 c;
+  sls_status r = check_desc(desc, &s);
+  if (r || (r = check_kv8(s, cache, s.Cap, "cache", &c))) return r;
+  REQUIRE(ctx_len); REQUIRE(ctx_out);
+  if (max_new < 0) return fail(SLS_EINVAL, "max_new %d < 0", max_new);
+  if (max_new > 0) {
+    REQUIRE16(k_new); REQUIRE16(v_new);
+  }
+  for (int64_t st : {k_seq_stride, k_token_stride, k_head_stride, v_seq_stride, v_token_stride, v_head_stride})
+    if (st < 0 || st > (int64_t(1) << 40) || st % 8)
+      return fail(SLS_EINVAL, "strides of the new tokens must be multiples of 8 elements in [0, 2^40]");
+  if ((kmin == nullptr) != (kmax == nullptr)) return fail(SLS_EINVAL, "kmin and kmax: both or neither");
+  if (kmin) {
+    REQUIRE16(kmin); REQUIRE16(kmax);
+    if (s.P == 1) return fail(SLS_EINVAL, "page_size 1: an 8-bit cache has no page summaries of single keys (pass NULL)");
+  }
+  const int64_t units = (int64_t)(max_new / std::min(c.block, s.P)) + 2;
+  int64_t ctas;
+  if (!checked_mul((int64_t)s.B * s.Hkv * 2, units, &ctas) || ctas > INT32_MAX)
+    return fail(SLS_EOVERFLOW, "grid too large");
+  sls::Kv8New n = {k_new, v_new, k_seq_stride, k_token_stride, k_head_stride,
+                   v_seq_stride, v_token_stride, v_head_stride, max_new, new_len};
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_kv8_append(s, c, n, kmin, kmax, mass, ctx_len, ctx_out, pos_out, (cudaStream_t)stream),
+                     "sls_kv8_append");
+}
+
+size_t sls_kv8_decode_attend_workspace_size(const sls_attn_desc* desc, const sls_kv8_cache* cache, int32_t with_mass) {
+  sls::Shape s;
+  sls::Kv8 c;
+  if (check_desc(desc, &s) || check_kv8(s, cache, s.Cap, "cache", &c) || !sls::kv8_attend_supported(s)) return 0;
+  return sls::kv8_attend_workspace(s, c, with_mass != 0);
+}
+
+sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* q,
+                                 const int32_t* page_idx, int32_t idx_stride, const int32_t* count, int32_t k_fixed,
+                                 const int32_t* ctx_len, const float* sink, void* out, float* lse,
+                                 const float* mass_in, float* mass_out, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  sls::Shape s;
+  sls::Kv8 c;
+  sls_status r = check_desc(desc, &s);
+  if (r || (r = check_kv8(s, cache, s.Cap, "cache", &c))) return r;
+  if (s.flags & ~SLS_FLAG_TEST_WAIT_TIMEOUT)
+    return fail(SLS_EUNSUPPORTED, "the 8-bit cache has one attend kernel: flags 0x%x", s.flags);
+  if (!sls::kv8_attend_supported(s))
+    return fail(SLS_EUNSUPPORTED, "at most 4096 rows (B*Hkv) and 2^31 - 1 cache slots in all");
+  REQUIRE16(q); REQUIRE(ctx_len); REQUIRE16(out);
+  if (page_idx) {
+    if (s.P < 16) return fail(SLS_EUNSUPPORTED, "page lists need pages of >= 16 tokens (P=%d)", s.P);
+    if (idx_stride < 1) return fail(SLS_EINVAL, "idx_stride %d < 1", idx_stride);
+    if ((int64_t)idx_stride * s.P > INT32_MAX) return fail(SLS_EOVERFLOW, "idx_stride %d pages of %d tokens", idx_stride, s.P);
+    if (!count && (k_fixed < 0 || k_fixed > idx_stride))
+      return fail(SLS_EINVAL, "k_fixed %d not in [0, idx_stride=%d]", k_fixed, idx_stride);
+    if (mass_out) return fail(SLS_EUNSUPPORTED, "weight sums need dense attention (page_idx NULL)");
+  }
+  if (mass_in && !mass_out) return fail(SLS_EINVAL, "mass_in without mass_out");
+  const size_t need = sls::kv8_attend_workspace(s, c, mass_out != nullptr);
+  if (!workspace || workspace_bytes < need)
+    return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  REQUIRE16(workspace);
+  return cuda_status(sls::launch_kv8_attend(s, c, q, page_idx, idx_stride, count, k_fixed, ctx_len, sink, out, lse,
+                                            mass_in, mass_out, workspace, (cudaStream_t)stream),
+                     "sls_kv8_decode_attend");
+}
+
+sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, int32_t dst_capacity,
+                         const sls_kv8_cache* dst, int32_t keep, int32_t n_sink_blocks, int32_t n_recent_blocks,
+                         const float* mass, float* mass_out, const void* kmin, const void* kmax, void* kmin_out,
+                         void* kmax_out, int32_t* kept_idx, const int32_t* ctx_len, int32_t* ctx_out, void* stream) {
+  sls::Shape s;
+  sls::Kv8Evict e = {};
+  sls_status r = check_desc(desc, &s);
+  if (r || (r = check_kv8(s, src, s.Cap, "src", &e.src))) return r;
+  if (!dst) dst = src;
+  if ((r = check_kv8(s, dst, dst_capacity, "dst", &e.dst))) return r;
+  REQUIRE(mass); REQUIRE(kept_idx); REQUIRE(ctx_len); REQUIRE(ctx_out);
+  if (e.dst.format != e.src.format || e.dst.block != e.src.block)
+    return fail(SLS_EINVAL, "src and dst must have the same format and block");
+  if (keep < 1 || n_sink_blocks < 0 || n_recent_blocks < 0 || (int64_t)n_sink_blocks + n_recent_blocks > keep)
+    return fail(SLS_EINVAL, "keep=%d must be >= 1 and hold n_sink_blocks=%d + n_recent_blocks=%d", keep, n_sink_blocks,
+                n_recent_blocks);
+  if (((int64_t)keep + 1) * e.src.block > dst_capacity)
+    return fail(SLS_EINVAL, "dst capacity %d cannot hold keep=%d blocks of %d and a partial one", dst_capacity, keep,
+                e.src.block);
+  const bool same = e.dst.kc == e.src.kc;
+  const int64_t rows = (int64_t)s.B * s.Hkv;
+  int64_t ctas;
+  if (!checked_mul(rows, 64, &ctas) || ctas > INT32_MAX || rows * dst_capacity > (int64_t(1) << 41))
+    return fail(SLS_EOVERFLOW, "too many rows");
+  if (same) {
+    if (e.dst.vc != e.src.vc || e.dst.ks != e.src.ks || e.dst.vs != e.src.vs || e.dst.kt != e.src.kt ||
+        e.dst.vt != e.src.vt || dst_capacity != s.Cap || mass_out != mass || kmin_out != kmin ||
+        kmax_out != kmax)
+      return fail(SLS_EINVAL, "in place every destination must be the source's own buffer and dst_capacity Cap");
+  }
+  if ((kmin == nullptr) != (kmax == nullptr) || (kmin == nullptr) != (kmin_out == nullptr) ||
+      (kmin == nullptr) != (kmax_out == nullptr))
+    return fail(SLS_EINVAL, "kmin, kmax and their outputs: all or none");
+  if (kmin) {
+    REQUIRE16(kmin); REQUIRE16(kmax); REQUIRE16(kmin_out); REQUIRE16(kmax_out);
+    if (s.P > e.src.block) return fail(SLS_EUNSUPPORTED, "page summaries move with blocks: page %d > block %d", s.P, e.src.block);
+  }
+  if (!same) {  // no destination may share memory with what is read
+    struct Range { uintptr_t a; int64_t n; };
+    auto at = [](const void* p, int64_t n) { return Range{(uintptr_t)p, p ? n : 0}; };
+    const int64_t st = rows * s.Cap, dt = rows * dst_capacity, bl = e.src.block;
+    const Range in[] = {at(e.src.kc, st * s.D), at(e.src.vc, st * s.D), at(e.src.ks, st / bl * 4), at(e.src.vs, st / bl * 4),
+                        at(e.src.kt, rows * bl * s.D * 2), at(e.src.vt, rows * bl * s.D * 2), at(mass, st / bl * 4),
+                        at(kmin, st / s.P * s.D * 2), at(kmax, st / s.P * s.D * 2)};
+    const Range to[] = {at(e.dst.kc, dt * s.D), at(e.dst.vc, dt * s.D), at(e.dst.ks, dt / bl * 4), at(e.dst.vs, dt / bl * 4),
+                        at(e.dst.kt, rows * bl * s.D * 2), at(e.dst.vt, rows * bl * s.D * 2), at(mass_out, dt / bl * 4),
+                        at(kmin_out, dt / s.P * s.D * 2), at(kmax_out, dt / s.P * s.D * 2)};
+    for (const Range& x : in)
+      for (const Range& y : to)
+        if (x.n && y.n && x.a < y.a + y.n && y.a < x.a + x.n)
+          return fail(SLS_EINVAL, "source and destination share memory without being the same cache");
+  }
+  e.cap = s.Cap; e.dcap = dst_capacity; e.keep = keep; e.n_sink = n_sink_blocks; e.n_recent = n_recent_blocks;
+  e.in_place = same; e.mass = mass; e.mass_out = mass_out;
+  e.kmin = kmin; e.kmax = kmax; e.kmin_out = kmin_out; e.kmax_out = kmax_out;
+  e.kept = kept_idx; e.ctx_len = ctx_len; e.ctx_out = ctx_out;
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_kv8_evict(s, e, (cudaStream_t)stream), "sls_kv8_evict");
 }
 
 }  // extern "C"

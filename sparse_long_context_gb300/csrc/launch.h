@@ -109,6 +109,7 @@ DeviceStatus take_status_attend_tma();
 DeviceStatus take_status_attend_refined();
 DeviceStatus take_status_quest_step();
 DeviceStatus take_status_recall();
+DeviceStatus take_status_attend_kv8();
 
 // Fused Quest step (bf16, pages of >= 16 tokens): select + attend + combine
 // in one launch.  *handled is false (and nothing is enqueued) when the shape
@@ -119,6 +120,54 @@ cudaError_t launch_quest_step(const Shape& s, const void* q, const void* k_cache
                               const void* kmin, const void* kmax, const int32_t* ctx_len, int k, int n_sink,
                               int n_local, const float* sink, int32_t* page_idx, void* out, float* lse,
                               int num_splits, float min_sparsity, cudaStream_t st, bool* handled);
+
+// Per-head norm and rotation.  freq: turns per position as 64-bit fixed point
+// fractions (one turn = 2^64), half the rotary channels of them.
+struct RopeArgs {
+  const void *q, *k, *wq, *wk;
+  void *qo, *ko;
+  const int32_t* pos;
+  int64_t q_t, q_h, k_t, k_h, qo_t, qo_h, ko_t, ko_h;  // strides in elements
+  int N, Hq, Hkv, D, R, interleaved, dtype;
+  float eps;
+  uint64_t freq[64];
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, cudaStream_t st);
+
+// The 8-bit cache as the kernels see it.
+struct Kv8 {
+  int format, block, bshift;
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  void *kt, *vt;
+};
+struct Kv8New {
+  const void *k, *v;
+  int64_t kb, kt, kh, vb, vt, vh;  // strides in elements
+  int max_new;
+  const int32_t* new_len;
+};
+cudaError_t launch_kv8_append(const Shape& s, const Kv8& c, const Kv8New& n, void* kmin, void* kmax, float* mass,
+                              const int32_t* ctx_len, int32_t* ctx_out, int32_t* pos_out, cudaStream_t st);
+bool kv8_attend_supported(const Shape& s);
+size_t kv8_attend_workspace(const Shape& s, const Kv8& c, bool with_mass);
+cudaError_t launch_kv8_attend(const Shape& s, const Kv8& c, const void* q, const int32_t* page_idx, int idx_stride,
+                              const int32_t* count, int k_fixed, const int32_t* ctx_len, const float* sink,
+                              void* out, float* lse, const float* mass_in, float* mass_out, void* ws,
+                              cudaStream_t st);
+struct Kv8Evict {
+  Kv8 src, dst;
+  int cap, dcap, keep, n_sink, n_recent;
+  bool in_place;
+  const float* mass;
+  float* mass_out;
+  const void *kmin, *kmax;
+  void *kmin_out, *kmax_out;
+  int32_t* kept;
+  const int32_t* ctx_len;
+  int32_t* ctx_out;
+};
+cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st);
 
 // Selection quality: attention-mass recall of page lists (a diagnostic).
 size_t recall_workspace(const Shape& s);

@@ -141,3 +141,33 @@ class DecodeLoop:
     def replay(self):
         self.graph.replay()
         return self.out, self.lse
+
+
+class Kv8DecodeLoop:
+    """The multi-step decode loop over an 8-bit cache: one step rotates and appends the token in the fixed buffer
+    `qkv` [B, Hq + 2 Hkv, D], attends, and advances the lengths (ops.Kv8Decode).  capture() records one step in a
+    CUDA graph; each replay decodes one more token with no host work."""
+
+    def __init__(self, step: ops.Kv8Decode, sink=None):
+        d = step.desc
+        self.step, self.sink = step, sink
+        self.qkv = torch.zeros((d.batch, d.num_q_heads + 2 * d.num_kv_heads, d.head_dim), dtype=torch.bfloat16,
+                               device=step.q.device)
+        self.graph = None
+
+    def run_once(self):
+        return self.step(self.qkv, self.sink)
+
+    def capture(self, stream=None):
+        """Records one step (nothing runs until replay())."""
+        stream = stream or torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        self.graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(self.graph, stream=stream):
+            self.out, self.lse = self.run_once()
+        torch.cuda.current_stream().wait_stream(stream)
+        return self.graph
+
+    def replay(self):
+        self.graph.replay()
+        return self.out, self.lse

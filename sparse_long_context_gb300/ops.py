@@ -355,6 +355,233 @@ def selection_recall(desc: L.AttnDesc, q, k_cache, page_idx, ctx_len, count=None
     return recall
 
 
+# ------------------------------------------------- per-head norm and rotation
+
+def _local(t: torch.Tensor, name: str, dtype=None, shape=None, strided: bool = False):
+    """A tensor of the current device (whose stream the call goes to); strided: only the last dimension must be
+    contiguous."""
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if strided:
+        if t.stride(-1) != 1 and t.numel():
+            raise ValueError(f"{name} must have contiguous channels")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def make_rope(num_q_heads: int, num_kv_heads: int, head_dim: int, dtype, rotary_dim: Optional[int] = None,
+              theta: float = 10000.0, interleaved: bool = False, eps: float = 1e-6, inv_freq=None) -> L.RopeDesc:
+    """Descriptor of qk_norm_rope (sls_rope_desc).  rotary_dim defaults to head_dim; inv_freq, if given, holds the
+    rotary_dim / 2 frequencies in radians per position (any host sequence of numbers)."""
+    rotary_dim = head_dim if rotary_dim is None else int(rotary_dim)
+    freq = None
+    if inv_freq is not None:
+        values = [float(f) for f in inv_freq]
+        if len(values) != rotary_dim // 2:
+            raise ValueError(f"inv_freq must hold rotary_dim / 2 = {rotary_dim // 2} values, got {len(values)}")
+        freq = (ctypes.c_double * max(len(values), 1))(*values)
+    rope = L.RopeDesc(int(num_q_heads), int(num_kv_heads), int(head_dim), rotary_dim, int(bool(interleaved)),
+                      _DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype), float(eps), float(theta), freq)
+    rope.keep_alive = freq
+    return rope
+
+
+def qk_norm_rope(rope: L.RopeDesc, q, k, positions, q_weight=None, k_weight=None, q_out=None, k_out=None):
+    """Per-head RMS norm (where a weight is given) and rotation by the token's position (sls_qk_norm_rope).
+    q [N, Hq, D] and k [N, Hkv, D] may be strided views of one projection's output; positions [N] int32, negative
+    ones skipped.  The outputs default to new contiguous tensors and may be q and k themselves.  A side with no
+    heads is passed as None.  Returns (q_out, k_out)."""
+    n, d = int(positions.shape[0]), rope.head_dim
+    dtype = torch.float32 if rope.dtype == L.SLS_DTYPE_F32 else torch.bfloat16
+    _local(positions, "positions", torch.int32, (n,))
+    args = []
+    outs = []
+    for name, heads, x, w, out in (("q", rope.num_q_heads, q, q_weight, q_out),
+                                   ("k", rope.num_kv_heads, k, k_weight, k_out)):
+        if heads == 0:
+            args.append((None, 0, 0, None, None, 0, 0))
+            outs.append(None)
+            continue
+        _local(x, name, dtype, (n, heads, d), strided=True)
+        if out is None:
+            out = torch.empty((n, heads, d), dtype=dtype, device=x.device)
+        else:
+            _local(out, name + "_out", dtype, (n, heads, d), strided=True)
+        if w is not None:
+            _local(w, name + "_weight", dtype, (d,))
+        args.append((_ptr(x), x.stride(0), x.stride(1), _ptr(w), _ptr(out), out.stride(0), out.stride(1)))
+        outs.append(out)
+    a, b = args
+    L.call("sls_qk_norm_rope", ctypes.byref(rope), n, a[0], a[1], a[2], b[0], b[1], b[2], a[3], b[3], _ptr(positions),
+           a[4], a[5], a[6], b[4], b[5], b[6], _stream())
+    return outs[0], outs[1]
+
+
+# -------------------------------------------------------------- 8-bit KV cache
+
+_KV8_FORMATS = {"int8": L.SLS_KV8_INT8, "e4m3": L.SLS_KV8_E4M3}
+
+
+class Kv8Cache:
+    """A K/V cache in 8 bits with one scale per block of tokens and KV head (sls_kv8_cache): codes
+    [B, Hkv, Cap, D] uint8, scales [B, Hkv, Cap/block] fp32, and the bf16 tail buffers [B, Hkv, block, D] in which
+    the tokens of the newest, partial block wait.  fmt is "int8" or "e4m3"."""
+
+    def __init__(self, desc: L.AttnDesc, fmt: str, block: int, k_codes, v_codes, k_scales, v_scales, k_tail, v_tail):
+        B, H, Cap, D = desc.batch, desc.num_kv_heads, desc.capacity, desc.head_dim
+        block = int(block)
+        if fmt not in _KV8_FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(_KV8_FORMATS)}, got {fmt!r}")
+        if block < 1 or Cap % block:
+            raise ValueError(f"block {block} must divide the capacity {Cap}")
+        for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
+            _local(t, name, torch.uint8, (B, H, Cap, D))
+        for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+            _local(t, name, torch.float32, (B, H, Cap // block))
+        for t, name in ((k_tail, "k_tail"), (v_tail, "v_tail")):
+            _local(t, name, torch.bfloat16, (B, H, block, D))
+        self.fmt, self.block = fmt, block
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_tail, self.v_tail = k_tail, v_tail
+        self.c = L.Kv8CacheDesc(_KV8_FORMATS[fmt], block, *(t.data_ptr() for t in (
+            k_codes, v_codes, k_scales, v_scales, k_tail, v_tail)))
+
+    @classmethod
+    def empty(cls, desc: L.AttnDesc, fmt: str = "int8", block: int = 64, device="cuda") -> "Kv8Cache":
+        """A new cache of the descriptor's shape (zero-filled)."""
+        B, H, Cap, D = desc.batch, desc.num_kv_heads, desc.capacity, desc.head_dim
+        new = lambda shape, dt: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
+        return cls(desc, fmt, block, new((B, H, Cap, D), torch.uint8), new((B, H, Cap, D), torch.uint8),
+                   new((B, H, Cap // block), torch.float32), new((B, H, Cap // block), torch.float32),
+                   new((B, H, block, D), torch.bfloat16), new((B, H, block, D), torch.bfloat16))
+
+    def values(self):
+        """The complete blocks' K and V as fp32 [B, H, Cap, D] (codes times scales; for inspection)."""
+        dt = torch.int8 if self.fmt == "int8" else torch.float8_e4m3fn
+        def one(codes, scales):
+            B, H, Cap, D = codes.shape
+            x = codes.view(dt).float().view(B, H, Cap // self.block, self.block, D)
+            return (x * scales[..., None, None]).view(B, H, Cap, D)
+        return one(self.k_codes, self.k_scales), one(self.v_codes, self.v_scales)
+
+
+def kv8_append(desc: L.AttnDesc, cache: Kv8Cache, k_new, v_new, ctx_len, new_len=None, kmin=None, kmax=None,
+               mass=None, ctx_out=None, pos_out=None):
+    """Appends the first new_len[b] (None: all) tokens of k_new, v_new [B, T, Hkv, D] to every sequence
+    (sls_kv8_append): complete blocks are quantised, the rest waits in the tail.  ctx_out defaults to ctx_len
+    (advanced in place).  The new tensors may be strided views with contiguous channels."""
+    B, H, D = desc.batch, desc.num_kv_heads, desc.head_dim
+    if k_new.dim() != 4:
+        raise ValueError(f"k_new must be [B, T, Hkv, D], got {tuple(k_new.shape)}")
+    T = int(k_new.shape[1])
+    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
+        _local(t, name, torch.bfloat16, (B, T, H, D), strided=True)
+    ctx_out = ctx_len if ctx_out is None else ctx_out
+    for t, name in ((ctx_len, "ctx_len"), (new_len, "new_len"), (ctx_out, "ctx_out"), (pos_out, "pos_out")):
+        if t is not None:
+            _local(t, name, torch.int32, (B,))
+    for t, name in ((kmin, "kmin"), (kmax, "kmax")):
+        if t is not None:
+            _local(t, name, torch.bfloat16, (B, H, desc.capacity // desc.page_size, D))
+    if mass is not None:
+        _local(mass, "mass", torch.float32, (B, H, desc.capacity // cache.block))
+    ks, vs = k_new.stride(), v_new.stride()
+    L.call("sls_kv8_append", ctypes.byref(desc), ctypes.byref(cache.c), _ptr(k_new), ks[0], ks[1], ks[2], _ptr(v_new),
+           vs[0], vs[1], vs[2], T, _ptr(new_len), _ptr(kmin), _ptr(kmax), _ptr(mass), _ptr(ctx_len), _ptr(ctx_out),
+           _ptr(pos_out), _stream())
+    return ctx_out
+
+
+def kv8_attend_workspace(desc: L.AttnDesc, cache: Kv8Cache, mass: bool = False, device="cuda"):
+    """Zero-filled workspace of kv8_decode_attend (reusable); mass: for calls that sum the blocks' weights."""
+    n = L.load().sls_kv8_decode_attend_workspace_size(ctypes.byref(desc), ctypes.byref(cache.c), int(bool(mass)))
+    return torch.zeros(max(int(n), 1), dtype=torch.uint8, device=device)
+
+
+def kv8_decode_attend(desc: L.AttnDesc, cache: Kv8Cache, q, ctx_len, page_idx=None, count=None,
+                      k_fixed: Optional[int] = None, sink=None, mass_in=None, mass_out=None, out=None, lse=None,
+                      workspace=None, want_lse: bool = True):
+    """Decode attention over an 8-bit cache (sls_kv8_decode_attend): dense, or over page lists [rows, stride].
+    mass_out, if given, receives every complete block's summed softmax weight added to mass_in.  Returns
+    (out, lse)."""
+    B, Hq, D = desc.batch, desc.num_q_heads, desc.head_dim
+    _local(q, "q", torch.bfloat16, (B, Hq, D))
+    _local(ctx_len, "ctx_len", torch.int32, (B,))
+    if out is None:
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _local(out, "out", torch.bfloat16, (B, Hq, D))
+    if lse is not None:
+        _local(lse, "lse", torch.float32, (B, Hq))
+    elif want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if sink is not None:
+        _local(sink, "sink", torch.float32, (Hq,))
+    stride = kf = 0
+    if page_idx is not None:
+        rows = B * desc.num_kv_heads
+        stride = int(page_idx.shape[-1])
+        kf = stride if k_fixed is None else int(k_fixed)
+        _local(page_idx, "page_idx", torch.int32, (rows, stride))
+        if count is not None:
+            _local(count, "count", torch.int32, (rows,))
+    for t, name in ((mass_in, "mass_in"), (mass_out, "mass_out")):
+        if t is not None:
+            _local(t, name, torch.float32, (B, desc.num_kv_heads, desc.capacity // cache.block))
+    if workspace is None:
+        workspace = kv8_attend_workspace(desc, cache, mass_out is not None, q.device)
+    else:
+        _local(workspace, "workspace", torch.uint8)
+    L.call("sls_kv8_decode_attend", ctypes.byref(desc), ctypes.byref(cache.c), _ptr(q), _ptr(page_idx), stride,
+           _ptr(count), kf, _ptr(ctx_len), _ptr(sink), _ptr(out), _ptr(lse), _ptr(mass_in), _ptr(mass_out),
+           _ptr(workspace), workspace.numel(), _stream())
+    return out, lse
+
+
+def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sink_blocks: int = 0,
+              n_recent_blocks: int = 0, dst_desc: Optional[L.AttnDesc] = None, dst: Optional[Kv8Cache] = None,
+              ctx_out=None, mass_out=None, kept_idx=None, kmin=None, kmax=None, kmin_out=None, kmax_out=None):
+    """Keeps at most `keep` complete blocks of every row by accumulated attention weight (sls_kv8_evict), in place
+    (dst None) or into another cache of dst_desc's capacity.  The outputs default to the inputs' buffers in place,
+    and ctx_out to ctx_len in place only.  Returns (ctx_out, kept_idx)."""
+    B, H, D, P = desc.batch, desc.num_kv_heads, desc.head_dim, desc.page_size
+    if (dst is None) != (dst_desc is None):
+        raise ValueError("dst and dst_desc: both or neither")
+    cap, dcap = desc.capacity, desc.capacity if dst is None else dst_desc.capacity
+    if dst is None:
+        mass_out = mass if mass_out is None else mass_out
+        kmin_out = kmin if kmin_out is None else kmin_out
+        kmax_out = kmax if kmax_out is None else kmax_out
+        ctx_out = ctx_len if ctx_out is None else ctx_out
+    else:
+        if (dst_desc.batch, dst_desc.num_kv_heads, dst_desc.head_dim, dst_desc.page_size, dst_desc.dtype) != (
+                B, H, D, P, desc.dtype):
+            raise ValueError("dst_desc must describe the same rows and pages as desc")
+        if ctx_out is None:
+            ctx_out = torch.empty_like(ctx_len)
+    if kept_idx is None:
+        kept_idx = torch.empty((B * H, keep), dtype=torch.int32, device=ctx_len.device)
+    _local(kept_idx, "kept_idx", torch.int32, (B * H, keep))
+    for t, name in ((ctx_len, "ctx_len"), (ctx_out, "ctx_out")):
+        _local(t, name, torch.int32, (B,))
+    _local(mass, "mass", torch.float32, (B, H, cap // cache.block))
+    if mass_out is not None:
+        _local(mass_out, "mass_out", torch.float32, (B, H, dcap // cache.block))
+    for t, name, c in ((kmin, "kmin", cap), (kmax, "kmax", cap), (kmin_out, "kmin_out", dcap),
+                       (kmax_out, "kmax_out", dcap)):
+        if t is not None:
+            _local(t, name, torch.bfloat16, (B, H, c // P, D))
+    L.call("sls_kv8_evict", ctypes.byref(desc), ctypes.byref(cache.c), dcap,
+           None if dst is None else ctypes.byref(dst.c), int(keep), int(n_sink_blocks), int(n_recent_blocks),
+           _ptr(mass), _ptr(mass_out), _ptr(kmin), _ptr(kmax), _ptr(kmin_out), _ptr(kmax_out), _ptr(kept_idx),
+           _ptr(ctx_len), _ptr(ctx_out), _stream())
+    return ctx_out, kept_idx
+
+
 # ------------------------------------------------------------ decode step
 
 class QuestDecode:
@@ -473,3 +700,75 @@ class DeltaDecode:
                 raise ValueError("the refined step needs the residuals")
             return self.attend_refined(q, k_cache, v_cache, codes, scales, res, ctx_len, sink)
         return self.attend(q, k_cache, v_cache, ctx_len, sink)
+
+
+class Kv8Decode:
+    """One decode step over an 8-bit cache from the projected heads on: norm and rotation of q and k
+    (qk_norm_rope), append of the token (kv8_append), and the attention, dense or, with k_budget > 0, over the
+    k_budget pages per KV head that Quest selection picks from page min/max kept of the unquantised keys.  The
+    buffers are preallocated, so a step can be captured in a CUDA graph.  With mass=True every block's attention
+    weight is summed (dense only), and evict() cuts the cache to a budget of blocks by it."""
+
+    def __init__(self, desc: L.AttnDesc, rope: L.RopeDesc, fmt: str = "int8", block: int = 64, k_budget: int = 0,
+                 n_sink_pages: int = 0, n_local_tokens: int = 0, mass: bool = False, device="cuda",
+                 q_weight=None, k_weight=None):
+        if (rope.num_q_heads, rope.num_kv_heads, rope.head_dim, rope.dtype) != (
+                desc.num_q_heads, desc.num_kv_heads, desc.head_dim, desc.dtype):
+            raise ValueError("rope and desc must describe the same heads")
+        if mass and k_budget:
+            raise ValueError("weight sums need dense attention (k_budget 0)")
+        B, Hq, H, D, P = desc.batch, desc.num_q_heads, desc.num_kv_heads, desc.head_dim, desc.page_size
+        self.desc, self.rope = desc, rope
+        self.k, self.n_sink, self.n_local = int(k_budget), int(n_sink_pages), int(n_local_tokens)
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.cache = Kv8Cache.empty(desc, fmt, block, device)
+        new = lambda shape, dt=torch.bfloat16: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
+        self.ctx_len = new(B, torch.int32)      # tokens held (less than the positions seen, after an eviction)
+        self.positions = new(B, torch.int32)    # position of the next token
+        self.q, self.k_new = new((B, Hq, D)), new((B, H, D))
+        self.out, self.lse = new((B, Hq, D)), new((B, Hq), torch.float32)
+        self.kmin = self.kmax = self.page_idx = self.select_workspace = self.mass = None
+        if self.k:
+            self.kmin, self.kmax = new((B, H, desc.capacity // P, D)), new((B, H, desc.capacity // P, D))
+            self.page_idx = new((B * H, self.k), torch.int32)
+            self.select_workspace = select_pages_workspace(desc, device)
+        if mass:
+            self.mass = new((B, H, desc.capacity // block), torch.float32)
+        self.workspace = kv8_attend_workspace(desc, self.cache, mass, device)
+
+    def prefill(self, qkv, new_len=None):
+        """Writes the keys and values of a prompt (or of its next piece): qkv [B, T, Hq + 2 Hkv, D], of which
+        sequence b has its first new_len[b] tokens.  Returns the rotated queries [B, T, Hq, D]."""
+        Hq, H = self.desc.num_q_heads, self.desc.num_kv_heads
+        B, T = qkv.shape[:2]
+        step = torch.arange(T, dtype=torch.int32, device=qkv.device)
+        pos = self.positions[:, None] + step
+        if new_len is not None:
+            pos = torch.where(step < new_len[:, None], pos, -1)  # padding is skipped
+        flat = qkv.view(B * T, Hq + 2 * H, qkv.shape[-1])
+        q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:Hq + H], pos.reshape(-1), self.q_weight, self.k_weight)
+        kv8_append(self.desc, self.cache, k.view(B, T, H, -1), qkv[:, :, Hq + H:], self.ctx_len, new_len=new_len,
+                   kmin=self.kmin, kmax=self.kmax, mass=self.mass)
+        self.positions += T if new_len is None else new_len.clamp(0, T)
+        return q.view(B, T, Hq, -1)
+
+    def __call__(self, qkv, sink=None):
+        """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
+        d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
+        qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.positions, self.q_weight, self.k_weight,
+                     q_out=self.q, k_out=self.k_new)
+        kv8_append(d, self.cache, self.k_new[:, None], qkv[:, None, Hq + H:], self.ctx_len, kmin=self.kmin,
+                   kmax=self.kmax, mass=self.mass)
+        self.positions += 1
+        if self.k:
+            select_pages(d, self.q, self.kmin, self.kmax, self.ctx_len, self.k, self.n_sink, self.n_local,
+                         out=self.page_idx, workspace=self.select_workspace)
+        return kv8_decode_attend(d, self.cache, self.q, self.ctx_len, page_idx=self.page_idx, sink=sink,
+                                 mass_in=self.mass, mass_out=self.mass, out=self.out, lse=self.lse,
+                                 workspace=self.workspace)
+
+    def evict(self, keep: int, n_sink_blocks: int = 0, n_recent_blocks: int = 0):
+        """Cuts every sequence to its keep heaviest complete blocks (kv8_evict in place).  Returns their numbers."""
+        if self.mass is None:
+            raise ValueError("evict needs the weight sums (mass=True)")
+        return kv8_evict(self.desc, self.cache, self.ctx_len, self.mass, keep, n_sink_blocks, n_recent_blocks)[1]
