@@ -698,7 +698,8 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
   if (page_idx) {
     if (s.P < 16) return fail(SLS_EUNSUPPORTED, "page lists need pages of >= 16 tokens (P=%d)", s.P);
     if (idx_stride < 1) return fail(SLS_EINVAL, "idx_stride %d < 1", idx_stride);
-    if ((int64_t)idx_stride * s.P > INT32_MAX) return fail(SLS_EOVERFLOW, "idx_stride %d pages of %d tokens", idx_stride, s.P);
+    if ((int64_t)idx_stride * s.P > INT32_MAX || (int64_t)s.B * s.Hkv * idx_stride * (s.P / 16) > (1 << 30))
+      return fail(SLS_EOVERFLOW, "idx_stride %d pages of %d tokens", idx_stride, s.P);
     if (!count && (k_fixed < 0 || k_fixed > idx_stride))
       return fail(SLS_EINVAL, "k_fixed %d not in [0, idx_stride=%d]", k_fixed, idx_stride);
     if (mass_out) return fail(SLS_EUNSUPPORTED, "weight sums need dense attention (page_idx NULL)");

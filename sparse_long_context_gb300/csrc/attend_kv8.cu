@@ -1,208 +1,787 @@
-// Decode attention over the 8-bit cache: split-K online softmax, a CTA per
-// (row, slice of its token groups), then the merge of a row's slices.
+// Decode attention over the 8-bit cache (codes times a scale per block of
+// tokens and head; the newest, partial block in bf16 in its tail buffer).
+//
+// The G query heads of a KV head share every byte read.  A row's tokens are
+// taken in units of 16 SG positions (whole pages of a list, or the context in
+// order); the rows' units, concatenated, are cut into one nearly equal range
+// per CTA (one CTA per SM), so that rows of uneven length fill the GPU, and the
+// last CTA to finish a shared row merges its partials in CTA order.
+//
+// A unit is streamed by one warp through its own ring of shared-memory stages
+// (K codes, then V codes, one tensor-map box of 16 SG rows each, or SG boxes
+// where pages have 16 tokens), so a late copy holds up one warp only.  Both
+// products run on the fp16 tensor cores with the codes as exact operands:
+//   S^T = Q K^T    A = the heads' queries, scaled to at most 2^11 by a power of
+//                  two of their own (exact but for parts below 2^-35 of the
+//                  head's largest, which round to fp16's subnormals), B = codes
+//   x   = S * scale * s_k          fp32, one multiplication per score
+//   O^T += V^T W^T,  W = p s_v     rounded to fp16 (half a step, 2^-11)
+// The running maximum is that of x + e with 2^e <= s_v < 2^(e+1) the exponent of
+// the value scale: then W = exp2(x - m) s_v < 2 for blocks of any scale, nothing
+// overflows and what underflows is 2^-24 of the largest.  (e is held within
+// [-100, 121], so that exp2(x - m) and its sum stay finite as well; values below
+// 2^-100 add nothing.)  Sum and maximum are consistent, so the merge and the sink
+// need no other form.  Tail tokens go through the bf16 tensor cores with e = 0.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include <algorithm>
+#include <atomic>
 
 #include "attend_common.cuh"
 #include "kv8.cuh"
 #include "launch.h"
+#include "mma.cuh"
+#include "tma.cuh"
 
 namespace sls {
+
+constexpr int kKv8MaxGrid = 1024;  // CTAs whose ranges are kept in shared memory
+constexpr int kKv8MaxRows = 4096;  // rows whose first units are kept there
+// Least units of a CTA: a shorter job uses fewer CTAs.
+constexpr int kKv8MinUnits = 4;
+// Work of a row change (drain, merge, partial and refill) in tokens.
+constexpr int kKv8SegCost = 1024;
 
 struct Kv8Attend {
   Kv8 c;
   const bf16* q;
   const int32_t *page_idx, *count, *ctx_len;
-  int idx_stride, k_fixed, S, Hq, Hkv, G, Cap, P, pshift;
+  int idx_stride, k_fixed, rows, Hq, Hkv, G, Cap, P, pshift, boxes, test_wait;
   float qscale;  // softmax scale * log2(e)
   const float* sink;
   bf16* out;
   float* lse;
-  float *po, *pm, *pl;  // [B, Hq, S] partials
-  float2* grp;          // [rows, Cap/16, G] weight sums of 16-token groups and the max they are relative to, or null
-  float2* fin;          // [B, Hq] final max (base 2) and 1 / sum, or null
+  int32_t* tickets;     // [rows] arrival counters, zero between calls
+  float *po, *pm, *pl;  // [slot][G][D], [slot][G] partials, two slots per CTA, max in base-2 units
+  float2* grp;          // [rows, G, Cap/16] weight sums of 16-token groups and the max they are relative to
+  float2* fin;          // [B, Hq] final max (base 2) and 1 / sum
   const float* mass_in;
   float* mass_out;
 };
 
-// Number of 16-token groups of a row (list entries of P >= 16 tokens each, or
-// the whole context).
-__device__ __forceinline__ int kv8_groups(const Kv8Attend& a, int row, int N) {
-  if (!a.page_idx) return (N + 15) >> 4;
-  const int cnt = a.count ? a.count[row] : a.k_fixed;
-  return min(max(cnt, 0), a.idx_stride) << (a.pshift - 4);
+__device__ __forceinline__ float kv8_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void kv8_mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t kv8_h2(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Four codes as two fp16x2 of their exact values.  int8: the code plus 128 in
+// the low byte under the exponent 0x64 reads as 1152 + code.
+template <int FMT>
+__device__ __forceinline__ void kv8_unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (FMT == kKv8Int8) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 k = __float2half2_rn(1152.f);
+    uint32_t x = __byte_perm(u, 0x64646464u, 0x4140u), y = __byte_perm(u, 0x64646464u, 0x4342u);
+    lo = kv8_h2(__hsub2(*reinterpret_cast<__half2*>(&x), k));
+    hi = kv8_h2(__hsub2(*reinterpret_cast<__half2*>(&y), k));
+  } else {
+    asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
 }
 
+// exponent of a value scale, within [-100, 121] (0 gives -100; NaN and inf 121)
+__device__ __forceinline__ float kv8_exponent(float s) {
+  const int e = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
+  return (float)min(max(e, -100), 121);
+}
+
+template <int D, int SG, int W, int S>
+struct Kv8Layout {
+  static constexpr int GROUP = 16 * D;                    // bytes of a group's K (or V) codes
+  static constexpr int STAGE = 2 * SG * GROUP;            // K of the unit's groups, then V
+  static constexpr size_t RING = (size_t)W * S * STAGE;
+  static constexpr size_t MERGE = (size_t)W * 8 * D * sizeof(float);
+  static constexpr size_t REGION = RING > MERGE ? RING : MERGE;
+};
+
+// Shared-memory offset of 16-byte chunk c of row t of a box (the copy
+// engine's 128-byte swizzle for 128-byte rows, 64-byte swizzle for 64-byte rows:
+// eight consecutive rows' same chunk lies in eight different bank groups).
+template <int D>
+__device__ __forceinline__ int kv8_chunk(int t, int c) {
+  return D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+}
+
+// Scores of one stored group: lane (r, m) gets head r, tokens 2m, 2m+1 (sc[0])
+// and 8+2m, 9+2m (sc[1]).  The k slots of step c hold channels 16c + 4m .. + 3
+// of lane m (the order of a sum is free), so one ldmatrix register is the four
+// codes of both B registers.
 template <int D, int FMT>
-__global__ void __launch_bounds__(256)
-kv8_attend_kernel(const Kv8Attend a) {
+__device__ __forceinline__ void kv8_scores(uint32_t k, const uint32_t (&qa)[D / 16][2], float (&sc)[2][4], int lane) {
+  const int j = lane >> 3, tok = 8 * (j & 1) + (lane & 7);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 16; c += 2) {
+    uint32_t w[4];
+    ldsm_x4(k + kv8_chunk<D>(tok, c + (j >> 1)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t b0, b1;
+      kv8_unpack4<FMT>(w[i], b0, b1);
+      kv8_mma_f16(sc[i & 1], qa[c + (i >> 1)][0], 0u, qa[c + (i >> 1)][1], 0u, b0, b1);
+    }
+  }
+}
+
+// O^T += V^T W^T of one stored group.  Lane (r, m) reads channels
+// [r D/8, (r+1) D/8) of tokens 2m, 2m+1, 8+2m, 9+2m; m-tile t takes its channels
+// 2t (row r) and 2t + 1 (row r + 8).
+template <int D, int FMT>
+__device__ __forceinline__ void kv8_pv(uint32_t v, float (&o)[D / 16][4], uint32_t p0, uint32_t p1, int lane) {
+  constexpr int NW = D / 32;  // 32-bit words of a lane's channels
+  const int r = lane >> 2, m = lane & 3;
+  uint32_t w[4][NW];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 2 * m + (i & 1) + 8 * (i >> 1);
+    if constexpr (D == 128) {
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                   : "r"(v + kv8_chunk<D>(t, r)));
+    } else {
+      asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                   : "=r"(w[i][0]), "=r"(w[i][1])
+                   : "r"(v + kv8_chunk<D>(t, r >> 1) + 8 * (r & 1)));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NW; ++k) {
+    uint32_t a[2][4];  // [token pair][byte]: the two tokens' values of one channel
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      kv8_unpack4<FMT>(__byte_perm(w[2 * u][k], w[2 * u + 1][k], 0x5140u), a[u][0], a[u][1]);
+      kv8_unpack4<FMT>(__byte_perm(w[2 * u][k], w[2 * u + 1][k], 0x7362u), a[u][2], a[u][3]);
+    }
+    kv8_mma_f16(o[2 * k], a[0][0], a[0][1], a[1][0], a[1][1], p0, p1);
+    kv8_mma_f16(o[2 * k + 1], a[0][2], a[0][3], a[1][2], a[1][3], p0, p1);
+  }
+}
+
+// The same for a group of the tail buffer (bf16, `lim` valid tokens; others
+// are not read and count as zero).
+template <int D>
+__device__ __forceinline__ void kv8_tail_scores(const bf16* k, const bf16* qh, bool head, int lim, float (&sc)[2][4],
+                                                int lane) {
+  const int r = lane >> 2, m = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
+#pragma unroll 2
+  for (int c = 0; c < D / 16; ++c) {
+    const uint2 qv = head ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const int t = r + 8 * nt;
+      const uint2 kv = t < lim ? *reinterpret_cast<const uint2*>(k + (size_t)t * D + 16 * c + 4 * m) : make_uint2(0u, 0u);
+      mma_bf16(sc[nt], qv.x, 0u, qv.y, 0u, kv.x, kv.y);
+    }
+  }
+}
+template <int D>
+__device__ __forceinline__ void kv8_tail_pv(const bf16* v, int lim, float (&o)[D / 16][4], uint32_t p0, uint32_t p1,
+                                            int lane) {
+  const int r = lane >> 2, m = lane & 3;
+#pragma unroll
+  for (int t = 0; t < D / 16; ++t) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int tok = 2 * m + (i & 1) + 8 * (i >> 1);
+      w[i] = tok < lim ? *reinterpret_cast<const uint32_t*>(v + (size_t)tok * D + r * (D / 8) + 2 * t) : 0u;
+    }
+    mma_bf16(o[t], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x5410),
+             __byte_perm(w[2], w[3], 0x7632), p0, p1);
+  }
+}
+
+struct Kv8Smem {
+  int s_lo[kKv8MaxGrid + 1];  // first unit of every CTA's range, and the total
+  int s_slot[kKv8MaxGrid];
+  int s_tmp[32];
+  int s_fail, s_ncontrib, s_last, s_total;
+  float s_w[8][64], s_m[8], s_inv[8];
+};
+
+// Final output of head g, channel d: accumulator av and sum lv relative to
+// exp2(M); the sink joins the sum.
+template <int D>
+__device__ __forceinline__ void kv8_finish(const Kv8Attend& a, size_t hq, int head, float M, float lv, float av, int d) {
+  const float sk = a.sink ? a.sink[head] * kLog2e : kNegInf;
+  const float Mx = fmaxf(M, sk);
+  float f = 0.f, Lt = 0.f;
+  if (Mx != kNegInf) {
+    f = M == kNegInf ? 0.f : exp2f(M - Mx);
+    Lt = lv * f + (a.sink ? exp2f(sk - Mx) : 0.f);
+  }
+  // a NaN sum (a NaN block, or a wait that gave up) stays NaN in the output and lse
+  a.out[hq * D + d] = __float2bfloat16_rn(Lt == 0.f ? 0.f : av * f / Lt);
+  if (d == 0) {
+    if (a.lse) a.lse[hq] = Lt == 0.f ? kNegInf : Mx * kLn2 + logf(Lt);
+    if (a.fin) a.fin[hq] = make_float2(Mx, Lt == 0.f ? 0.f : 1.f / Lt);
+  }
+}
+
+template <int D, int FMT, int SG, int W, int S, bool LIST, bool MASS>
+__global__ void __launch_bounds__(W * 32, 1)
+kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Kv8Attend a) {
+  using L = Kv8Layout<D, SG, W, S>;
+  constexpr int KS = D / 16, NT = W * 32, UT = 16 * SG;
+  constexpr int BATCH = 32 - (S - 1);  // units between two loads of a warp's page ids and scales
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* ring =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  int* s_pref = reinterpret_cast<int*>(ring + L::REGION);  // [rows + 1] first unit of each row
+  __shared__ Kv8Smem sh;
+  __shared__ uint64_t full[W][S];
+  __shared__ float sM[W][8], sL[W][8], sF[W][8], sHm[8], sHl[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, m = lane & 3;
+  const int G = a.G, rows = a.rows, cta = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int w = 0; w < W; ++w)
+      for (int s = 0; s < S; ++s) mbar_init(&full[w][s], 1);
+    mbar_fence_init();
+    tma_prefetch_map(&tk);
+    tma_prefetch_map(&tv);
+    sh.s_fail = 0;
+  }
   pdl_wait_then_release();
-  constexpr int E = D / 32;
-  const int row = blockIdx.x / a.S, split = blockIdx.x % a.S, b = row / a.Hkv, h = row % a.Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int N = clamp_len(a.ctx_len[b], a.Cap);
-  const int ng = kv8_groups(a, row, N), per = (ng + a.S - 1) / a.S;
-  const int g0 = min(split * per, ng), g1 = min(g0 + per, ng);
-  const int32_t* list = a.page_idx ? a.page_idx + (size_t)row * a.idx_stride : nullptr;
-  if (list && warp == 0) {
-    unsigned bad = 0;
-    for (int e = (g0 >> (a.pshift - 4)) + lane; e < (g1 + (a.P >> 4) - 1) >> (a.pshift - 4); e += 32)
-      bad += ((e << (a.pshift - 4)) >= g0) && bad_page_id(list[e], a.Cap >> a.pshift) ? 1u : 0u;
-    note_bad_pages(bad);
-  }
-  float q[8][E], o[8][E], m[8], l[8];
+
+  // groups and units of a row
+  auto groups_of = [&](int row) {
+    if constexpr (!LIST) return (clamp_len(a.ctx_len[row / a.Hkv], a.Cap) + 15) >> 4;
+    const int cnt = a.count ? a.count[row] : a.k_fixed;
+    return min(max(cnt, 0), a.idx_stride) << (a.pshift - 4);
+  };
+  auto units_of = [&](int row) { return (groups_of(row) + SG - 1) / SG; };
+
+  // s_pref: exclusive prefix sum of the rows' units
+  {
+    const int rpt = (rows + NT - 1) / NT, r0 = threadIdx.x * rpt;
+    int sum = 0;
+    for (int i = 0; i < rpt; ++i)
+      if (r0 + i < rows) sum += units_of(r0 + i);
+    int x = sum;
 #pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    m[g] = kNegInf;
-    l[g] = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      o[g][i] = 0.f;
-      q[g][i] = g < a.G ? to_f32(a.q[((size_t)b * a.Hq + h * a.G + g) * D + lane * E + i]) * a.qscale : 0.f;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-  }
-  const int newest = N >> a.c.bshift;
-  for (int gi = g0 + warp; gi < g1; gi += 8) {
-    int base = gi << 4;
-    if (list) {
-      const int pg = list[base >> a.pshift];
-      if ((unsigned)pg >= (unsigned)(a.Cap >> a.pshift)) continue;
-      base = (pg << a.pshift) + (base & (a.P - 1));
+    if (lane == 31) sh.s_tmp[warp] = x;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      before += w < warp ? sh.s_tmp[w] : 0;
+      total += sh.s_tmp[w];
     }
-    const int lim = min(16, N - base);
-    if (lim <= 0) continue;
-    const int blk = base >> a.c.bshift;
-    const bool stored = blk < newest;
-    const size_t sc = (size_t)row * (a.Cap >> a.c.bshift) + blk;
-    const float ks = stored ? a.c.ks[sc] : 1.f, vs = stored ? a.c.vs[sc] : 1.f;
-    float gsum[8], gmax[8];
-#pragma unroll
-    for (int g = 0; g < 8; ++g) { gsum[g] = 0.f; gmax[g] = kNegInf; }
-    for (int t = 0; t < lim; ++t) {
-      const int pos = base + t;
-      float k[E], v[E];
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (stored) {
-          const size_t at = ((size_t)row * a.Cap + pos) * D + lane * E + i;
-          k[i] = kv8_value<FMT>(a.c.kc[at]) * ks;
-          v[i] = kv8_value<FMT>(a.c.vc[at]) * vs;
-        } else {
-          const size_t at = ((size_t)row * a.c.block + (pos & (a.c.block - 1))) * D + lane * E + i;
-          k[i] = to_f32(static_cast<const bf16*>(a.c.kt)[at]);
-          v[i] = to_f32(static_cast<const bf16*>(a.c.vt)[at]);
-        }
+    int acc = before + x - sum;
+    for (int i = 0; i < rpt; ++i)
+      if (r0 + i < rows) {
+        s_pref[r0 + i] = acc;
+        acc += units_of(r0 + i);
       }
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (g >= a.G) break;
-        float x = 0.f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) x = fmaf(q[g][i], k[i], x);
-        x = warp_sum(x);
-        const float mn = fmaxf(m[g], x);
-        const float al = mn == kNegInf ? 1.f : exp2f(m[g] - mn), p = x == kNegInf ? 0.f : exp2f(x - mn);
-        m[g] = mn;
-        l[g] = l[g] * al + p;
-        gsum[g] = gsum[g] * al + p;
-        gmax[g] = mn;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[g][i] = fmaf(o[g][i], al, p * v[i]);
-      }
-    }
-    if (a.grp && stored && lane == 0)
-      for (int g = 0; g < a.G; ++g)
-        a.grp[((size_t)row * (a.Cap >> 4) + (base >> 4)) * a.G + g] = make_float2(gsum[g], gmax[g]);
+    if (threadIdx.x == 0) s_pref[rows] = total;
+    __syncthreads();
   }
-  __shared__ float sm[8][8], sl[8][8], so[8][8][D];
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    if (lane == 0) { sm[warp][g] = m[g]; sl[warp][g] = l[g]; }
-#pragma unroll
-    for (int i = 0; i < E; ++i) so[warp][g][lane * E + i] = o[g][i];
+  const int T = s_pref[rows];
+  // the row holding unit x: the last row whose first unit (plus `beta` per
+  // earlier row) is <= x
+  auto row_at = [&](long long x, long long beta) {
+    int l = 0, u = rows - 1;
+    while (l < u) {
+      const int mid = (l + u + 1) >> 1;
+      if (s_pref[mid] + beta * mid <= x) l = mid;
+      else u = mid - 1;
+    }
+    return l;
+  };
+  // Every CTA's range: equal shares of a list in which each row start after
+  // the first counts kKv8SegCost tokens more.  Short jobs use fewer CTAs.
+  const int grid = min((int)gridDim.x, max(1, T / kKv8MinUnits));
+  {
+    const long long beta = kKv8SegCost / UT, Tp = T + beta * (rows - 1);
+    for (int k = threadIdx.x; k <= grid; k += NT) {
+      const long long at = Tp * k / grid;
+      const int l = row_at(at, beta);
+      sh.s_lo[k] = (int)min(at - beta * l, (long long)s_pref[l + 1]);
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.G * D; i += 256) {
-    const int g = i / D, d = i % D;
-    float M = kNegInf, L = 0.f, O = 0.f;
-    for (int w = 0; w < 8; ++w) M = fmaxf(M, sm[w][g]);
-    for (int w = 0; w < 8; ++w) {
-      const float f = sm[w][g] == kNegInf ? 0.f : exp2f(sm[w][g] - M);
-      L = fmaf(sl[w][g], f, L);
-      O = fmaf(so[w][g][d], f, O);
+  // rows without units: output 0, lse -inf (or the sink alone)
+  for (int row = cta; row < rows; row += gridDim.x) {
+    if (s_pref[row + 1] != s_pref[row]) continue;
+    for (int i = threadIdx.x; i < G * D; i += NT)
+      kv8_finish<D>(a, (size_t)row * G + i / D, (row % a.Hkv) * G + i / D, kNegInf, 0.f, 0.f, i % D);
+  }
+  if (cta >= grid) return;
+  const int lo = sh.s_lo[cta], hi = sh.s_lo[cta + 1];
+  if (lo >= hi) return;
+  int row = row_at(lo, 0);
+
+  const bool plant = a.test_wait && cta == 0 && warp == 0;  // the wait-timeout test hook
+  const uint32_t tries = plant ? kTestWaitTries : kWaitTries;
+  const uint32_t wring = smem_u32(ring) + (uint32_t)warp * S * L::STAGE;
+  uint32_t wseq = 0;  // this warp's ring position
+  for (int e = lo; e < hi;) {
+    const int seg_end = min(hi, s_pref[row + 1]), u0 = e - s_pref[row];
+    const int b = row / a.Hkv, h = row % a.Hkv;
+    const int N = clamp_len(a.ctx_len[b], a.Cap), ng = groups_of(row), newest = N >> a.c.bshift;
+    const int nseg = seg_end - e;
+    const int nk = nseg > warp ? (nseg - warp + W - 1) / W : 0;  // this warp's units: u0 + warp + W k
+    const bool failed = sh.s_fail != 0;                          // an earlier segment gave up: no more copies
+    const int32_t* list = LIST ? a.page_idx + (size_t)row * a.idx_stride : nullptr;
+    const size_t row_blk = (size_t)row * (a.Cap >> a.c.bshift);
+
+    // the heads' queries as fp16 with their largest channel in [2^10, 2^11)
+    uint32_t qa[KS][2];
+    float qmul;
+    const bf16* qh = a.q + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
+    {
+      uint2 raw[KS];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+        mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu));
+      }
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int ex = (int)(mx >> 7) - 127;  // 128 for infinity and NaN, -127 for zero and subnormals
+      const int sh2 = ex == 128 ? 0 : min(10 - ex, 100);
+      const float f = __uint_as_float((uint32_t)(sh2 + 127) << 23);
+      qmul = a.qscale * __uint_as_float((uint32_t)(127 - sh2) << 23);
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        qa[c][0] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].x) * f, bf16hi(raw[c].x) * f));
+        qa[c][1] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].y) * f, bf16hi(raw[c].y) * f));
+      }
     }
-    const size_t at = ((size_t)b * a.Hq + h * a.G + g) * a.S + split;
-    a.po[at * D + d] = O;
-    if (d == 0) { a.pm[at] = M; a.pl[at] = L; }
+    float o[KS][4], m_run = kNegInf, l_run = 0.f;
+#pragma unroll
+    for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+    // Of unit kb + lane: the positions of its groups (-1: nothing there) and
+    // the scales of those in complete blocks.
+    int base[SG];
+    float ksc[SG], vsc[SG];
+    auto load_batch = [&](int kb) {
+      const int k = kb + lane;
+      unsigned bad = 0;
+#pragma unroll
+      for (int s = 0; s < SG; ++s) {
+        base[s] = -1;
+        ksc[s] = vsc[s] = 1.f;
+        const int g = (u0 + warp + W * k) * SG + s;
+        if (k < nk && g < ng) {
+          int at = g << 4;
+          if constexpr (LIST) {
+            const int pg = __ldg(list + (at >> a.pshift)), in = at & (a.P - 1);
+            // counted once: by the unit holding the page's first group, when first loaded
+            bad += in == 0 && (kb == 0 || lane >= S - 1) && bad_page_id(pg, a.Cap >> a.pshift);
+            at = (unsigned)pg < (unsigned)(a.Cap >> a.pshift) ? (pg << a.pshift) + in : a.Cap;
+          }
+          if (at < N) {
+            base[s] = at;
+            if (at >> a.c.bshift < newest) {
+              ksc[s] = __ldg(a.c.ks + row_blk + (at >> a.c.bshift));
+              vsc[s] = __ldg(a.c.vs + row_blk + (at >> a.c.bshift));
+            }
+          }
+        }
+      }
+      if constexpr (LIST) note_bad_pages(bad);
+    };
+    // the copies of unit k (its batch entry in lane k - kb) into its stage
+    auto issue = [&](int k, int kb) {
+      int at[SG];
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int s = 0; s < SG; ++s) {
+        at[s] = __shfl_sync(0xffffffffu, base[s], k - kb);
+        if (at[s] >= 0 && at[s] >> a.c.bshift >= newest) at[s] = -1;  // tail tokens are not copied
+        if (at[s] >= 0) bytes += 2 * L::GROUP;
+      }
+      if (lane == 0) {
+        const uint32_t st = (wseq + k) % S;
+        uint64_t* bar = &full[warp][st];
+        unsigned char* dst = ring + ((size_t)warp * S + st) * L::STAGE;
+        if (plant && wseq + k == 0) {
+          mbar_arrive_expect_tx(bar, 16);  // no copy is issued: this phase never completes
+        } else if (bytes == 0) {
+          mbar_arrive(bar);
+        } else if (a.boxes == 1) {  // one box of the unit's 16 SG rows (at[0] >= 0 when any is)
+          mbar_arrive_expect_tx(bar, L::STAGE);
+          tma_load_2d(dst, &tk, 0, row * a.Cap + at[0], bar);
+          tma_load_2d(dst + SG * L::GROUP, &tv, 0, row * a.Cap + at[0], bar);
+        } else {
+          mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+          for (int s = 0; s < SG; ++s)
+            if (at[s] >= 0) {
+              tma_load_2d(dst + s * L::GROUP, &tk, 0, row * a.Cap + at[s], bar);
+              tma_load_2d(dst + (SG + s) * L::GROUP, &tv, 0, row * a.Cap + at[s], bar);
+            }
+        }
+      }
+    };
+
+    bool ok = !failed;
+    int k = 0;
+    if (ok && lane == 0) fence_proxy_async_smem();  // the merge's reads of the ring before the copies write it
+    for (int kb = 0; ok && kb < nk; kb += BATCH) {
+      load_batch(kb);
+      if (kb == 0)
+        for (int j = 0; j < min(S - 1, nk); ++j) issue(j, 0);
+      const int kend = min(nk, kb + BATCH);
+      for (; k < kend; ++k) {
+        if (k + S - 1 < nk) issue(k + S - 1, kb);  // into the stage unit k - 1 has left
+        const uint32_t st = (wseq + k) % S;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[warp][st], ((wseq + k) / S) & 1, tries))) {
+          ok = false;
+          break;
+        }
+        const uint32_t stage = wring + st * L::STAGE;
+        int at[SG];
+        float x[SG][4], vs[SG], gm = kNegInf;
+#pragma unroll
+        for (int s = 0; s < SG; ++s) {
+          at[s] = __shfl_sync(0xffffffffu, base[s], k - kb);
+          const float ks = __shfl_sync(0xffffffffu, ksc[s], k - kb);
+          vs[s] = __shfl_sync(0xffffffffu, vsc[s], k - kb);
+          if (at[s] < 0) {
+            x[s][0] = x[s][1] = x[s][2] = x[s][3] = kNegInf;
+            continue;
+          }
+          float sc[2][4];
+          if (at[s] >> a.c.bshift < newest) {
+            kv8_scores<D, FMT>(stage + s * L::GROUP, qa, sc, lane);
+            const float mul = qmul * ks;
+            x[s][0] = sc[0][0] * mul; x[s][1] = sc[0][1] * mul;
+            x[s][2] = sc[1][0] * mul; x[s][3] = sc[1][1] * mul;
+            const float e2 = kv8_exponent(vs[s]);
+            gm = fmaxf(gm, fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3])) + e2);
+          } else {
+            const int lim = min(16, N - at[s]), slot = at[s] & (a.c.block - 1);
+            kv8_tail_scores<D>(static_cast<const bf16*>(a.c.kt) + ((size_t)row * a.c.block + slot) * D, qh, r < G, lim, sc,
+                               lane);
+            x[s][0] = 2 * m < lim ? sc[0][0] * a.qscale : kNegInf;
+            x[s][1] = 2 * m + 1 < lim ? sc[0][1] * a.qscale : kNegInf;
+            x[s][2] = 2 * m + 8 < lim ? sc[1][0] * a.qscale : kNegInf;
+            x[s][3] = 2 * m + 9 < lim ? sc[1][1] * a.qscale : kNegInf;
+            gm = fmaxf(gm, fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3])));
+          }
+        }
+        gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
+        gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+        const float mn = fmaxf(m_run, gm), mref = mn == kNegInf ? 0.f : mn;
+        const float alpha = kv8_ex2(m_run - mref);  // first unit: exp2(-inf) = 0 scales zeros
+        m_run = mn;
+        float psum[SG];
+#pragma unroll
+        for (int s = 0; s < SG; ++s) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[s][i] = kv8_ex2(x[s][i] - mref);
+          psum[s] = (x[s][0] + x[s][1]) + (x[s][2] + x[s][3]);
+        }
+        l_run *= alpha;
+#pragma unroll
+        for (int s = 0; s < SG; ++s) l_run += psum[s];
+        // accumulator columns are heads 2m and 2m + 1
+        const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * m), a_hi = __shfl_sync(0xffffffffu, alpha, 8 * m + 4);
+        if (!__all_sync(0xffffffffu, a_lo == 1.f && a_hi == 1.f)) {
+#pragma unroll
+          for (int t = 0; t < KS; ++t) {
+            o[t][0] *= a_lo; o[t][1] *= a_hi; o[t][2] *= a_lo; o[t][3] *= a_hi;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < SG; ++s) {
+          if (at[s] < 0) continue;
+          if (at[s] >> a.c.bshift < newest) {
+            const uint32_t p0 = kv8_h2(__floats2half2_rn(x[s][0] * vs[s], x[s][1] * vs[s]));
+            const uint32_t p1 = kv8_h2(__floats2half2_rn(x[s][2] * vs[s], x[s][3] * vs[s]));
+            kv8_pv<D, FMT>(stage + (SG + s) * L::GROUP, o, p0, p1, lane);
+            if constexpr (MASS) {
+              float ps = psum[s];
+              ps += __shfl_xor_sync(0xffffffffu, ps, 1);
+              ps += __shfl_xor_sync(0xffffffffu, ps, 2);
+              if (m == 0 && r < G)
+                a.grp[((size_t)row * G + r) * (a.Cap >> 4) + (at[s] >> 4)] = make_float2(ps, mref);
+            }
+          } else {
+            const int lim = min(16, N - at[s]), slot = at[s] & (a.c.block - 1);
+            kv8_tail_pv<D>(static_cast<const bf16*>(a.c.vt) + ((size_t)row * a.c.block + slot) * D, lim, o,
+                           pack_bf16(x[s][0], x[s][1]), pack_bf16(x[s][2], x[s][3]), lane);
+          }
+        }
+        // the stage is read before the copy engine may write it again
+        __syncwarp();
+        if (lane == 0) fence_proxy_async_smem();
+      }
+    }
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) {
+        note_wait_timeout();
+        sh.s_fail = 1;
+        // the copies still in flight land before the ring is reused or left
+        if (!failed)
+          for (int k2 = k; k2 < min(nk, k + S); ++k2)
+            mbar_wait(&full[warp][(wseq + k2) % S], ((wseq + k2) / S) & 1, tries);
+      }
+      // an infinite running max makes this warp's merge weight NaN at every later merge
+      m_run = __int_as_float(0x7f800000);
+    }
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 1);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 2);
+    if (m == 0) {
+      sM[warp][r] = m_run;
+      sL[warp][r] = l_run;
+    }
+    wseq += failed ? 0u : (uint32_t)nk;
+    __syncthreads();  // every warp's stages have been consumed (or drained): the rings become the merge area
+
+    float* sO = reinterpret_cast<float*>(ring);  // [W][8 heads][D]
+#pragma unroll
+    for (int t = 0; t < KS; ++t) {
+      const int ch = r * (D / 8) + 2 * t;
+      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m) * D + ch) = make_float2(o[t][0], o[t][2]);
+      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m + 1) * D + ch) = make_float2(o[t][1], o[t][3]);
+    }
+    if (threadIdx.x < 8) {
+      const int g = threadIdx.x;
+      float M = kNegInf, Lh = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, sM[w][g]);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        // a NaN sum without a maximum (every score NaN) is kept
+        const float f = sM[w][g] == kNegInf ? (sL[w][g] == 0.f ? 0.f : 1.f) : exp2f(sM[w][g] - M);
+        sF[w][g] = f;
+        Lh = fmaf(sL[w][g], f, Lh);
+      }
+      if (Lh != Lh && M == kNegInf) M = 0.f;
+      sHm[g] = M;
+      sHl[g] = Lh;
+    }
+    __syncthreads();
+    const bool whole = e == s_pref[row] && seg_end == s_pref[row + 1];
+    const int slot = e == lo ? 2 * cta : 2 * cta + 1;
+    for (int i = threadIdx.x; i < G * D; i += NT) {
+      const int g = i / D, d = i % D;
+      float av = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) av = fmaf(sO[(w * 8 + g) * D + d], sF[w][g], av);
+      if (whole) {
+        kv8_finish<D>(a, (size_t)row * G + g, h * G + g, sHm[g], sHl[g], av, d);
+      } else {
+        const size_t sg = (size_t)slot * G + g;
+        a.po[sg * D + d] = av;
+        if (d == 0) {
+          a.pm[sg] = sHm[g];
+          a.pl[sg] = sHl[g];
+        }
+      }
+    }
+    if (!whole) {
+      // the row's contributors are the CTAs from the one holding its first
+      // unit to the one holding its last (those with units); CTA k wrote slot
+      // 2k when its range starts inside the row, else 2k + 1
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        auto cta_of = [&](int x) {  // the last CTA whose range starts at or before unit x
+          int l = 0, u = grid - 1;
+          while (l < u) {
+            const int mid = (l + u + 1) >> 1;
+            if (sh.s_lo[mid] <= x) l = mid;
+            else u = mid - 1;
+          }
+          return l;
+        };
+        const int cf = cta_of(s_pref[row]), cl = cta_of(s_pref[row + 1] - 1);
+        int n = 0;
+        for (int c2 = cf; c2 <= cl; ++c2)
+          if (sh.s_lo[c2] < sh.s_lo[c2 + 1]) sh.s_slot[n++] = sh.s_lo[c2] >= s_pref[row] ? 2 * c2 : 2 * c2 + 1;
+        sh.s_ncontrib = n;
+        sh.s_last = atomicAdd(a.tickets + row, 1) == n - 1;
+      }
+      __syncthreads();
+      if (sh.s_last) {
+        __threadfence();
+        const int n = sh.s_ncontrib;
+        for (int g = warp; g < G; g += W) {
+          float M = kNegInf, Ls = 0.f;
+          for (int j = lane; j < n; j += 32) M = fmaxf(M, __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g));
+          M = warp_max(M);
+          const float sk = a.sink ? a.sink[h * G + g] * kLog2e : kNegInf;
+          M = fmaxf(M, sk);
+          for (int j = lane; j < n; j += 32) {
+            const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
+            const float w = (ms == kNegInf || M == kNegInf) ? 0.f : exp2f(ms - M);
+            Ls += __ldcg(a.pl + (size_t)sh.s_slot[j] * G + g) * w;
+            if (j < 64) sh.s_w[g][j] = w;
+          }
+          Ls = warp_sum(Ls);
+          if (a.sink && M != kNegInf) Ls += exp2f(sk - M);
+          if (lane == 0) {
+            const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
+            const size_t hq = (size_t)row * G + g;
+            sh.s_m[g] = M;
+            sh.s_inv[g] = inv;
+            if (a.lse) a.lse[hq] = Ls == 0.f ? kNegInf : M * kLn2 + logf(Ls);
+            if (a.fin) a.fin[hq] = make_float2(M, inv);
+          }
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < G * D / 4; i += NT) {
+          const int g = i / (D / 4), d4 = i % (D / 4);
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int j0 = 0; j0 < n; j0 += 8) {
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              v[u] = j0 + u < n
+                         ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[j0 + u] * G + g) * D) + d4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int j = j0 + u;
+              if (j >= n) break;
+              float w;
+              if (j < 64) {
+                w = sh.s_w[g][j];
+              } else {
+                const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
+                w = (ms == kNegInf || sh.s_m[g] == kNegInf) ? 0.f : exp2f(ms - sh.s_m[g]);
+              }
+              acc.x = fmaf(v[u].x, w, acc.x);
+              acc.y = fmaf(v[u].y, w, acc.y);
+              acc.z = fmaf(v[u].z, w, acc.z);
+              acc.w = fmaf(v[u].w, w, acc.w);
+            }
+          }
+          const float inv = sh.s_inv[g];
+          __nv_bfloat162* op = reinterpret_cast<__nv_bfloat162*>(a.out + ((size_t)row * G + g) * D + 4 * d4);
+          op[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+          op[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        }
+        if (threadIdx.x == 0) a.tickets[row] = 0;  // ready for the next call
+      }
+    }
+    __syncthreads();  // shared memory is reused by the next segment
+    e = seg_end;
+    ++row;
+    while (row < rows && s_pref[row + 1] == s_pref[row]) ++row;  // empty rows hold no units
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(D)
-kv8_combine_kernel(const Kv8Attend a) {
-  pdl_wait_then_release();
-  const int hq = blockIdx.x, d = threadIdx.x;  // b * Hq + head
-  const float sk = a.sink ? a.sink[hq % a.Hq] * kLog2e : kNegInf;
-  float M = sk, L = 0.f, O = 0.f;
-  for (int s = 0; s < a.S; ++s) M = fmaxf(M, a.pm[(size_t)hq * a.S + s]);
-  for (int s = 0; s < a.S; ++s) {
-    const size_t at = (size_t)hq * a.S + s;
-    const float f = a.pm[at] == kNegInf ? 0.f : exp2f(a.pm[at] - M);
-    L = fmaf(a.pl[at], f, L);
-    O = fmaf(a.po[at * D + d], f, O);
-  }
-  if (a.sink && M != kNegInf) L += exp2f(sk - M);
-  a.out[(size_t)hq * D + d] = __float2bfloat16_rn(L == 0.f ? 0.f : O / L);
-  if (d == 0) {
-    if (a.lse) a.lse[hq] = L == 0.f ? kNegInf : M * kLn2 + logf(L);
-    if (a.fin) a.fin[hq] = make_float2(M, L == 0.f ? 0.f : 1.f / L);
-  }
-}
-
-__global__ void __launch_bounds__(128)
+// mass_out = mass_in + the blocks' weight sums: a lane per 16-token group
+// (coalesced loads of each head's sums), the groups of a block added by shuffles.
+__global__ void __launch_bounds__(256)
 kv8_mass_kernel(const Kv8Attend a, int per_row) {
   pdl_wait_then_release();
-  const int row = blockIdx.x / per_row, blk = (blockIdx.x % per_row) * 128 + threadIdx.x;
-  const int b = row / a.Hkv, h = row % a.Hkv;
-  if (blk >= clamp_len(a.ctx_len[b], a.Cap) >> a.c.bshift) return;
+  const int row = blockIdx.x / per_row, g16 = (blockIdx.x % per_row) * 256 + threadIdx.x;
+  const int gshift = a.c.bshift - 4, blk = g16 >> gshift;
+  const bool live = blk < clamp_len(a.ctx_len[row / a.Hkv], a.Cap) >> a.c.bshift;
   float sum = 0.f;
-  const int gpb = a.c.block >> 4;
-  for (int g = 0; g < a.G; ++g) {
-    const float2 f = a.fin[(size_t)b * a.Hq + h * a.G + g];
-    for (int i = 0; i < gpb; ++i) {
-      const float2 x = a.grp[((size_t)row * (a.Cap >> 4) + blk * gpb + i) * a.G + g];
-      if (x.y != kNegInf) sum += x.x * exp2f(x.y - f.x) * f.y;
+  if (live)
+    for (int g = 0; g < a.G; ++g) {
+      const float2 f = a.fin[(size_t)row * a.G + g];
+      const float2 x = __ldcg(a.grp + ((size_t)row * a.G + g) * (a.Cap >> 4) + g16);
+      sum += x.x * exp2f(x.y - f.x) * f.y;
     }
+  for (int o = 1; o < (1 << gshift); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (live && (g16 & ((1 << gshift) - 1)) == 0) {
+    const size_t at = (size_t)row * (a.Cap >> a.c.bshift) + blk;
+    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
   }
-  const size_t at = (size_t)row * (a.Cap >> a.c.bshift) + blk;
-  a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
+}
+
+// ------------------------------------------------------------------- launches
+
+// The driver's tensor-map encoder, looked up once.
+static PFN_cuTensorMapEncodeTiled_v12000 kv8_encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    return nullptr;
+  }();
+  return fn;
+}
+
+// Codes as [rows * Cap] rows of D bytes, boxes of `box_rows` whole rows.
+static bool kv8_map(CUtensorMap* map, const void* base, uint64_t rows, int D, int box_rows) {
+  auto fn = kv8_encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {(cuuint64_t)D};
+  cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool kv8_attend_supported(const Shape& s) {
-  return s.dtype == 1 && s.B * (long long)s.Hkv <= 4096 && (long long)s.B * s.Hkv * s.Cap < (1ll << 31);
+  return s.dtype == 1 && s.B * (long long)s.Hkv <= kKv8MaxRows && (long long)s.B * s.Hkv * s.Cap < (1ll << 31);
 }
 
+static int kv8_grid() { return std::min(sm_count(), kKv8MaxGrid); }
 static size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
-static int kv8_splits(const Shape& s) {
-  return std::max(1, std::min((s.Cap + 511) / 512, 4 * sm_count() / (s.B * s.Hkv) + 1));
-}
 
 size_t kv8_attend_workspace(const Shape& s, const Kv8&, bool with_mass) {
-  const size_t parts = (size_t)s.B * s.Hq * kv8_splits(s);
-  return a256(parts * s.D * 4) + 2 * a256(parts * 4) +
-         (with_mass ? a256((size_t)s.B * s.Hkv * (s.Cap / 16 + 1) * s.G * 8) + a256((size_t)s.B * s.Hq * 8) : 0);
+  const size_t rows = (size_t)s.B * s.Hkv, slots = 2 * (size_t)kv8_grid();
+  return a256(rows * 4) + a256(slots * s.G * s.D * 4) + 2 * a256(slots * s.G * 4) +
+         (with_mass ? a256(rows * s.G * 8) + a256(rows * s.G * (s.Cap >> 4) * 8) : 0);
+}
+
+template <int D, int FMT, bool LIST, bool MASS>
+static cudaError_t kv8_launch(Kv8Attend a, cudaStream_t st) {
+  constexpr int SG = 2, W = 12, S = D == 128 ? 2 : 4;
+  using L = Kv8Layout<D, SG, W, S>;
+  a.boxes = LIST && a.P < 16 * SG ? SG : 1;
+  CUtensorMap tk, tv;
+  const uint64_t tokens = (uint64_t)a.rows * a.Cap;
+  if (!kv8_map(&tk, a.c.kc, tokens, D, 16 * SG / a.boxes) || !kv8_map(&tv, a.c.vc, tokens, D, 16 * SG / a.boxes))
+    return cudaErrorInvalidValue;
+  const size_t smem = L::REGION + (size_t)(a.rows + 1) * sizeof(int) + 1024;
+  // the kernel's limit, raised once per device to the most any call needs
+  static std::atomic<bool> raised[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
+    e = cudaFuncSetAttribute(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(L::REGION + (kKv8MaxRows + 1) * sizeof(int) + 1024));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) raised[dev].store(true, std::memory_order_relaxed);
+  }
+  return launch_pdl(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS>, dim3(kv8_grid()), dim3(W * 32), smem, st, tk, tv, a);
 }
 
 template <int D>
-static cudaError_t kv8_launch(const Kv8Attend& a, int rows, cudaStream_t st) {
-  cudaError_t e = a.c.format == kKv8Int8
-                      ? launch_pdl(kv8_attend_kernel<D, kKv8Int8>, dim3(rows * a.S), dim3(256), 0, st, a)
-                      : launch_pdl(kv8_attend_kernel<D, kKv8E4m3>, dim3(rows * a.S), dim3(256), 0, st, a);
-  if (e == cudaSuccess) e = launch_pdl(kv8_combine_kernel<D>, dim3(rows * a.G), dim3(D), 0, st, a);
-  if (e == cudaSuccess && a.mass_out) {
-    const int per_row = ((a.Cap >> a.c.bshift) + 127) / 128;
-    e = launch_pdl(kv8_mass_kernel, dim3((unsigned)rows * per_row), dim3(128), 0, st, a, per_row);
-  }
-  return e;
+static cudaError_t kv8_dispatch(const Kv8Attend& a, cudaStream_t st) {
+  if (a.page_idx)
+    return a.c.format == kKv8Int8 ? kv8_launch<D, kKv8Int8, true, false>(a, st) : kv8_launch<D, kKv8E4m3, true, false>(a, st);
+  if (a.mass_out)
+    return a.c.format == kKv8Int8 ? kv8_launch<D, kKv8Int8, false, true>(a, st) : kv8_launch<D, kKv8E4m3, false, true>(a, st);
+  return a.c.format == kKv8Int8 ? kv8_launch<D, kKv8Int8, false, false>(a, st) : kv8_launch<D, kKv8E4m3, false, false>(a, st);
 }
 
 cudaError_t launch_kv8_attend(const Shape& s, const Kv8& c, const void* q, const int32_t* page_idx, int idx_stride,
@@ -217,29 +796,35 @@ cudaError_t launch_kv8_attend(const Shape& s, const Kv8& c, const void* q, const
   a.ctx_len = ctx_len;
   a.idx_stride = idx_stride;
   a.k_fixed = k_fixed;
-  a.S = kv8_splits(s);
+  a.rows = s.B * s.Hkv;
   a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift;
+  a.test_wait = (s.flags & kFlagTestWaitTimeout) ? 1 : 0;
   a.qscale = s.scale * kLog2e;
   a.sink = sink;
   a.out = static_cast<bf16*>(out);
   a.lse = lse;
-  const size_t parts = (size_t)s.B * s.Hq * a.S;
+  const size_t rows = (size_t)a.rows, slots = 2 * (size_t)kv8_grid();
   char* w = static_cast<char*>(ws);
-  a.po = reinterpret_cast<float*>(w);
-  w += a256(parts * s.D * 4);
-  a.pm = reinterpret_cast<float*>(w);
-  w += a256(parts * 4);
-  a.pl = reinterpret_cast<float*>(w);
-  w += a256(parts * 4);
+  auto take = [&](size_t bytes) {
+    char* p = w;
+    w += a256(bytes);
+    return p;
+  };
+  a.tickets = reinterpret_cast<int32_t*>(take(rows * 4));
+  a.po = reinterpret_cast<float*>(take(slots * s.G * s.D * 4));
+  a.pm = reinterpret_cast<float*>(take(slots * s.G * 4));
+  a.pl = reinterpret_cast<float*>(take(slots * s.G * 4));
   if (mass_out) {
-    a.grp = reinterpret_cast<float2*>(w);
-    w += a256((size_t)s.B * s.Hkv * (s.Cap / 16 + 1) * s.G * 8);
-    a.fin = reinterpret_cast<float2*>(w);
+    a.fin = reinterpret_cast<float2*>(take(rows * s.G * 8));
+    a.grp = reinterpret_cast<float2*>(take(rows * s.G * (s.Cap >> 4) * 8));
     a.mass_in = mass_in;
     a.mass_out = mass_out;
   }
-  const int rows = s.B * s.Hkv;
-  cudaError_t e = s.D == 64 ? kv8_launch<64>(a, rows, st) : kv8_launch<128>(a, rows, st);
+  cudaError_t e = s.D == 64 ? kv8_dispatch<64>(a, st) : kv8_dispatch<128>(a, st);
+  if (e == cudaSuccess && mass_out) {
+    const int per_row = ((s.Cap >> 4) + 255) / 256;
+    e = launch_pdl(kv8_mass_kernel, dim3((unsigned)a.rows * per_row), dim3(256), 0, st, a, per_row);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
