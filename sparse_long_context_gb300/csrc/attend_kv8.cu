@@ -22,6 +22,7 @@
 // [-100, 121], so that exp2(x - m) and its sum stay finite as well; values below
 // 2^-100 add nothing.)  Sum and maximum are consistent, so the merge and the sink
 // need no other form.  Tail tokens go through the bf16 tensor cores with e = 0.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -37,9 +38,16 @@
 namespace sls {
 
 constexpr int kKv8MaxGrid = 1024;  // CTAs whose ranges are kept in shared memory
+constexpr int kKv8MaxCluster = 16;
 constexpr int kKv8MaxRows = 4096;  // rows whose first units are kept there
+constexpr int kKv8PerSm = 1;       // resident CTAs of an SM
 // Least units of a CTA: a shorter job uses fewer CTAs.
 constexpr int kKv8MinUnits = 4;
+// Rows of at most so many tokens (capacity, or the longest list) go to the
+// cluster kernel: rows that are known to be of one length (a single sequence,
+// lists of a fixed length), and others, of which a long one may then keep one
+// cluster busy after the rest.
+constexpr long long kKv8ClusterEven = 32768, kKv8ClusterUneven = 8192;
 // Work of a row change (drain, merge, partial and refill) in tokens.
 constexpr int kKv8SegCost = 1024;
 
@@ -47,7 +55,7 @@ struct Kv8Attend {
   Kv8 c;
   const bf16* q;
   const int32_t *page_idx, *count, *ctx_len;
-  int idx_stride, k_fixed, rows, Hq, Hkv, G, Cap, P, pshift, boxes, test_wait;
+  int idx_stride, k_fixed, rows, Hq, Hkv, G, Cap, P, pshift, boxes, test_wait, cluster;
   float qscale;  // softmax scale * log2(e)
   const float* sink;
   bf16* out;
@@ -102,7 +110,10 @@ struct Kv8Layout {
   static constexpr int GROUP = 16 * D;                    // bytes of a group's K (or V) codes
   static constexpr int STAGE = 2 * SG * GROUP;            // K of the unit's groups, then V
   static constexpr size_t RING = (size_t)W * S * STAGE;
-  static constexpr size_t MERGE = (size_t)W * 8 * D * sizeof(float);
+  // The warps' accumulators, [warp][head][D + 4]: the lanes of a warp then
+  // write to different banks (kv8_channel gives the order of the channels).
+  static constexpr int MROW = D + 4;
+  static constexpr size_t MERGE = (size_t)W * 8 * MROW * sizeof(float);
   static constexpr size_t REGION = RING > MERGE ? RING : MERGE;
 };
 
@@ -112,6 +123,14 @@ struct Kv8Layout {
 template <int D>
 __device__ __forceinline__ int kv8_chunk(int t, int c) {
   return D == 128 ? t * 128 + ((c ^ (t & 7)) << 4) : t * 64 + ((c ^ ((t >> 1) & 3)) << 4);
+}
+
+// Channel held at place p of an accumulator row in shared memory and in the
+// partials: m-tile t's rows r and r + 8 are channels r D/8 + 2t and + 1, at
+// places 16 t + 2 r and + 1.
+template <int D>
+__device__ __forceinline__ int kv8_channel(int p) {
+  return ((p & 15) >> 1) * (D / 8) + 2 * (p >> 4) + (p & 1);
 }
 
 // Scores of one stored group: lane (r, m) gets head r, tokens 2m, 2m+1 (sc[0])
@@ -178,7 +197,7 @@ __device__ __forceinline__ void kv8_tail_scores(const bf16* k, const bf16* qh, b
   const int r = lane >> 2, m = lane & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
-#pragma unroll 2
+#pragma unroll  // its loads in flight together
   for (int c = 0; c < D / 16; ++c) {
     const uint2 qv = head ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
 #pragma unroll
@@ -206,9 +225,10 @@ __device__ __forceinline__ void kv8_tail_pv(const bf16* v, int lim, float (&o)[D
   }
 }
 
+template <bool CL>
 struct Kv8Smem {
-  int s_lo[kKv8MaxGrid + 1];  // first unit of every CTA's range, and the total
-  int s_slot[kKv8MaxGrid];
+  int s_lo[CL ? 1 : kKv8MaxGrid + 1];  // first unit of every CTA's range, and the total
+  int s_slot[CL ? 1 : kKv8MaxGrid];
   int s_tmp[32];
   int s_fail, s_ncontrib, s_last, s_total;
   float s_w[8][64], s_m[8], s_inv[8];
@@ -233,8 +253,19 @@ __device__ __forceinline__ void kv8_finish(const Kv8Attend& a, size_t hq, int he
   }
 }
 
-template <int D, int FMT, int SG, int W, int S, bool LIST, bool MASS>
-__global__ void __launch_bounds__(W * 32, 1)
+// What the CTAs of a row's cluster send each other: rank r merges its share of
+// the G x D outputs, a multiple of 4 values.
+template <int D>
+struct __align__(16) Kv8Inbox {
+  float o[8 * D + 4 * kKv8MaxCluster];
+  float m[kKv8MaxCluster * 8], l[kKv8MaxCluster * 8];
+};
+
+// CL: the CTAs of a cluster take one row's units in equal shares and merge
+// through distributed shared memory; otherwise every CTA takes a range of all
+// rows' units.
+template <int D, int FMT, int SG, int W, int S, bool LIST, bool MASS, bool CL>
+__global__ void __launch_bounds__(W * 32, kKv8PerSm)
 kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Kv8Attend a) {
   using L = Kv8Layout<D, SG, W, S>;
   constexpr int KS = D / 16, NT = W * 32, UT = 16 * SG;
@@ -243,7 +274,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   unsigned char* ring =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   int* s_pref = reinterpret_cast<int*>(ring + L::REGION);  // [rows + 1] first unit of each row
-  __shared__ Kv8Smem sh;
+  __shared__ Kv8Smem<CL> sh;
   __shared__ uint64_t full[W][S];
   __shared__ float sM[W][8], sL[W][8], sF[W][8], sHm[8], sHl[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, m = lane & 3;
@@ -256,6 +287,8 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     tma_prefetch_map(&tv);
     sh.s_fail = 0;
   }
+  // pairs with the wait before the cluster's first remote store: every peer runs by then
+  if constexpr (CL) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait_then_release();
 
   // groups and units of a row
@@ -266,6 +299,14 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   };
   auto units_of = [&](int row) { return (groups_of(row) + SG - 1) / SG; };
 
+  int row = 0, lo = 0, hi = 0, grid = 1;
+  if constexpr (CL) {
+    row = cta / a.cluster;
+    const int nu = units_of(row), split = cta % a.cluster;
+    lo = (int)((long long)nu * split / a.cluster);
+    hi = (int)((long long)nu * (split + 1) / a.cluster);
+    __syncthreads();  // barriers initialised
+  } else {
   // s_pref: exclusive prefix sum of the rows' units
   {
     const int rpt = (rows + NT - 1) / NT, r0 = threadIdx.x * rpt;
@@ -309,7 +350,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   };
   // Every CTA's range: equal shares of a list in which each row start after
   // the first counts kKv8SegCost tokens more.  Short jobs use fewer CTAs.
-  const int grid = min((int)gridDim.x, max(1, T / kKv8MinUnits));
+  grid = min((int)gridDim.x, max(1, T / kKv8MinUnits));
   {
     const long long beta = kKv8SegCost / UT, Tp = T + beta * (rows - 1);
     for (int k = threadIdx.x; k <= grid; k += NT) {
@@ -320,22 +361,24 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   }
   __syncthreads();
   // rows without units: output 0, lse -inf (or the sink alone)
-  for (int row = cta; row < rows; row += gridDim.x) {
-    if (s_pref[row + 1] != s_pref[row]) continue;
+  for (int er = cta; er < rows; er += gridDim.x) {
+    if (s_pref[er + 1] != s_pref[er]) continue;
     for (int i = threadIdx.x; i < G * D; i += NT)
-      kv8_finish<D>(a, (size_t)row * G + i / D, (row % a.Hkv) * G + i / D, kNegInf, 0.f, 0.f, i % D);
+      kv8_finish<D>(a, (size_t)er * G + i / D, (er % a.Hkv) * G + i / D, kNegInf, 0.f, 0.f, i % D);
   }
   if (cta >= grid) return;
-  const int lo = sh.s_lo[cta], hi = sh.s_lo[cta + 1];
+  lo = sh.s_lo[cta];
+  hi = sh.s_lo[cta + 1];
   if (lo >= hi) return;
-  int row = row_at(lo, 0);
+  row = row_at(lo, 0);
+  }
 
   const bool plant = a.test_wait && cta == 0 && warp == 0;  // the wait-timeout test hook
   const uint32_t tries = plant ? kTestWaitTries : kWaitTries;
   const uint32_t wring = smem_u32(ring) + (uint32_t)warp * S * L::STAGE;
   uint32_t wseq = 0;  // this warp's ring position
-  for (int e = lo; e < hi;) {
-    const int seg_end = min(hi, s_pref[row + 1]), u0 = e - s_pref[row];
+  for (int e = lo; CL || e < hi;) {
+    const int seg_end = CL ? hi : min(hi, s_pref[row + 1]), u0 = CL ? lo : e - s_pref[row];
     const int b = row / a.Hkv, h = row % a.Hkv;
     const int N = clamp_len(a.ctx_len[b], a.Cap), ng = groups_of(row), newest = N >> a.c.bshift;
     const int nseg = seg_end - e;
@@ -344,34 +387,31 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const int32_t* list = LIST ? a.page_idx + (size_t)row * a.idx_stride : nullptr;
     const size_t row_blk = (size_t)row * (a.Cap >> a.c.bshift);
 
-    // the heads' queries as fp16 with their largest channel in [2^10, 2^11)
+    const bf16* qh = a.q + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
     uint32_t qa[KS][2];
     float qmul;
-    const bf16* qh = a.q + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
-    {
-      uint2 raw[KS];
-      uint32_t mx = 0;
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
-        mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu));
-      }
-      mx = max(mx & 0xffffu, mx >> 16);
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const int ex = (int)(mx >> 7) - 127;  // 128 for infinity and NaN, -127 for zero and subnormals
-      const int sh2 = ex == 128 ? 0 : min(10 - ex, 100);
-      const float f = __uint_as_float((uint32_t)(sh2 + 127) << 23);
-      qmul = a.qscale * __uint_as_float((uint32_t)(127 - sh2) << 23);
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        qa[c][0] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].x) * f, bf16hi(raw[c].x) * f));
-        qa[c][1] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].y) * f, bf16hi(raw[c].y) * f));
-      }
-    }
     float o[KS][4], m_run = kNegInf, l_run = 0.f;
 #pragma unroll
     for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+    // Takes the lane's new maximum into the running one and rescales sum and
+    // accumulators; returns the value the weights are relative to.
+    auto softmax_step = [&](float gm) {
+      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
+      gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
+      const float mn = fmaxf(m_run, gm), mref = mn == kNegInf ? 0.f : mn;
+      const float alpha = kv8_ex2(m_run - mref);  // before any token: exp2(-inf) = 0 scales zeros
+      m_run = mn;
+      l_run *= alpha;
+      // accumulator columns are heads 2m and 2m + 1
+      const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * m), a_hi = __shfl_sync(0xffffffffu, alpha, 8 * m + 4);
+      if (!__all_sync(0xffffffffu, a_lo == 1.f && a_hi == 1.f)) {
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+          o[t][0] *= a_lo; o[t][1] *= a_hi; o[t][2] *= a_lo; o[t][3] *= a_hi;
+        }
+      }
+      return mref;
+    };
 
     // Of unit kb + lane: the positions of its groups (-1: nothing there) and
     // the scales of those in complete blocks.
@@ -440,12 +480,61 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 
     bool ok = !failed;
     int k = 0;
-    if (ok && lane == 0) fence_proxy_async_smem();  // the merge's reads of the ring before the copies write it
+    if (ok) {
+      if (lane == 0) fence_proxy_async_smem();  // the merge's reads of the ring before the copies write it
+      load_batch(0);
+      for (int j = 0; j < min(S - 1, nk); ++j) issue(j, 0);
+    }
+    // the heads' queries as fp16 with their largest channel in [2^10, 2^11)
+    {
+      uint2 raw[KS];
+      uint32_t mx = 0;
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+        mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu));
+      }
+      mx = max(mx & 0xffffu, mx >> 16);
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      const int ex = (int)(mx >> 7) - 127;  // 128 for infinity and NaN, -127 for zero and subnormals
+      const int sh2 = ex == 128 ? 0 : min(10 - ex, 100);
+      const float f = __uint_as_float((uint32_t)(sh2 + 127) << 23);
+      qmul = a.qscale * __uint_as_float((uint32_t)(127 - sh2) << 23);
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        qa[c][0] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].x) * f, bf16hi(raw[c].x) * f));
+        qa[c][1] = kv8_h2(__floats2half2_rn(bf16lo(raw[c].y) * f, bf16hi(raw[c].y) * f));
+      }
+    }
     for (int kb = 0; ok && kb < nk; kb += BATCH) {
-      load_batch(kb);
-      if (kb == 0)
-        for (int j = 0; j < min(S - 1, nk); ++j) issue(j, 0);
+      if (kb) load_batch(kb);
       const int kend = min(nk, kb + BATCH);
+      // The batch's groups in the tail buffer (lanes below BATCH: their own
+      // units, not the ones looked ahead), outside the loop over stored units.
+#pragma unroll
+      for (int s = 0; s < SG; ++s) {
+        uint32_t todo = __ballot_sync(0xffffffffu, lane < BATCH && base[s] >= 0 && base[s] >> a.c.bshift >= newest);
+        while (todo) {
+          const int at = __shfl_sync(0xffffffffu, base[s], __ffs(todo) - 1);
+          todo &= todo - 1;
+          const int lim = min(16, N - at), slot = at & (a.c.block - 1);
+          const size_t tail = ((size_t)row * a.c.block + slot) * D;
+          float sc[2][4], x[4];
+          kv8_tail_scores<D>(static_cast<const bf16*>(a.c.kt) + tail, qh, r < G, lim, sc, lane);
+          x[0] = 2 * m < lim ? sc[0][0] * a.qscale : kNegInf;
+          x[1] = 2 * m + 1 < lim ? sc[0][1] * a.qscale : kNegInf;
+          x[2] = 2 * m + 8 < lim ? sc[1][0] * a.qscale : kNegInf;
+          x[3] = 2 * m + 9 < lim ? sc[1][1] * a.qscale : kNegInf;
+          const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
+          l_run += (x[0] + x[1]) + (x[2] + x[3]);
+          kv8_tail_pv<D>(static_cast<const bf16*>(a.c.vt) + tail, lim, o, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
+                         lane);
+        }
+        if (base[s] >= 0 && base[s] >> a.c.bshift >= newest) base[s] = -1;  // nothing to stream
+      }
       for (; k < kend; ++k) {
         if (k + S - 1 < nk) issue(k + S - 1, kb);  // into the stage unit k - 1 has left
         const uint32_t st = (wseq + k) % S;
@@ -456,75 +545,42 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         const uint32_t stage = wring + st * L::STAGE;
         int at[SG];
         float x[SG][4], vs[SG], gm = kNegInf;
+        bool any = false;
 #pragma unroll
         for (int s = 0; s < SG; ++s) {
           at[s] = __shfl_sync(0xffffffffu, base[s], k - kb);
           const float ks = __shfl_sync(0xffffffffu, ksc[s], k - kb);
           vs[s] = __shfl_sync(0xffffffffu, vsc[s], k - kb);
-          if (at[s] < 0) {
-            x[s][0] = x[s][1] = x[s][2] = x[s][3] = kNegInf;
-            continue;
-          }
-          float sc[2][4];
-          if (at[s] >> a.c.bshift < newest) {
+          if (at[s] >= 0) {
+            any = true;
+            float sc[2][4];
             kv8_scores<D, FMT>(stage + s * L::GROUP, qa, sc, lane);
             const float mul = qmul * ks;
             x[s][0] = sc[0][0] * mul; x[s][1] = sc[0][1] * mul;
             x[s][2] = sc[1][0] * mul; x[s][3] = sc[1][1] * mul;
-            const float e2 = kv8_exponent(vs[s]);
-            gm = fmaxf(gm, fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3])) + e2);
+            gm = fmaxf(gm, fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3])) + kv8_exponent(vs[s]));
           } else {
-            const int lim = min(16, N - at[s]), slot = at[s] & (a.c.block - 1);
-            kv8_tail_scores<D>(static_cast<const bf16*>(a.c.kt) + ((size_t)row * a.c.block + slot) * D, qh, r < G, lim, sc,
-                               lane);
-            x[s][0] = 2 * m < lim ? sc[0][0] * a.qscale : kNegInf;
-            x[s][1] = 2 * m + 1 < lim ? sc[0][1] * a.qscale : kNegInf;
-            x[s][2] = 2 * m + 8 < lim ? sc[1][0] * a.qscale : kNegInf;
-            x[s][3] = 2 * m + 9 < lim ? sc[1][1] * a.qscale : kNegInf;
-            gm = fmaxf(gm, fmaxf(fmaxf(x[s][0], x[s][1]), fmaxf(x[s][2], x[s][3])));
+            x[s][0] = x[s][1] = x[s][2] = x[s][3] = kNegInf;
           }
         }
-        gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 1));
-        gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 2));
-        const float mn = fmaxf(m_run, gm), mref = mn == kNegInf ? 0.f : mn;
-        const float alpha = kv8_ex2(m_run - mref);  // first unit: exp2(-inf) = 0 scales zeros
-        m_run = mn;
-        float psum[SG];
+        if (any) {
+          const float mref = softmax_step(gm);
 #pragma unroll
-        for (int s = 0; s < SG; ++s) {
+          for (int s = 0; s < SG; ++s) {
+            if (at[s] < 0) continue;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[s][i] = kv8_ex2(x[s][i] - mref);
-          psum[s] = (x[s][0] + x[s][1]) + (x[s][2] + x[s][3]);
-        }
-        l_run *= alpha;
-#pragma unroll
-        for (int s = 0; s < SG; ++s) l_run += psum[s];
-        // accumulator columns are heads 2m and 2m + 1
-        const float a_lo = __shfl_sync(0xffffffffu, alpha, 8 * m), a_hi = __shfl_sync(0xffffffffu, alpha, 8 * m + 4);
-        if (!__all_sync(0xffffffffu, a_lo == 1.f && a_hi == 1.f)) {
-#pragma unroll
-          for (int t = 0; t < KS; ++t) {
-            o[t][0] *= a_lo; o[t][1] *= a_hi; o[t][2] *= a_lo; o[t][3] *= a_hi;
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < SG; ++s) {
-          if (at[s] < 0) continue;
-          if (at[s] >> a.c.bshift < newest) {
+            for (int i = 0; i < 4; ++i) x[s][i] = kv8_ex2(x[s][i] - mref);
+            const float psum = (x[s][0] + x[s][1]) + (x[s][2] + x[s][3]);
+            l_run += psum;
             const uint32_t p0 = kv8_h2(__floats2half2_rn(x[s][0] * vs[s], x[s][1] * vs[s]));
             const uint32_t p1 = kv8_h2(__floats2half2_rn(x[s][2] * vs[s], x[s][3] * vs[s]));
             kv8_pv<D, FMT>(stage + (SG + s) * L::GROUP, o, p0, p1, lane);
             if constexpr (MASS) {
-              float ps = psum[s];
+              float ps = psum;
               ps += __shfl_xor_sync(0xffffffffu, ps, 1);
               ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-              if (m == 0 && r < G)
-                a.grp[((size_t)row * G + r) * (a.Cap >> 4) + (at[s] >> 4)] = make_float2(ps, mref);
+              if (m == 0 && r < G) a.grp[((size_t)row * G + r) * (a.Cap >> 4) + (at[s] >> 4)] = make_float2(ps, mref);
             }
-          } else {
-            const int lim = min(16, N - at[s]), slot = at[s] & (a.c.block - 1);
-            kv8_tail_pv<D>(static_cast<const bf16*>(a.c.vt) + ((size_t)row * a.c.block + slot) * D, lim, o,
-                           pack_bf16(x[s][0], x[s][1]), pack_bf16(x[s][2], x[s][3]), lane);
           }
         }
         // the stage is read before the copy engine may write it again
@@ -553,12 +609,12 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     wseq += failed ? 0u : (uint32_t)nk;
     __syncthreads();  // every warp's stages have been consumed (or drained): the rings become the merge area
 
-    float* sO = reinterpret_cast<float*>(ring);  // [W][8 heads][D]
+    float* sO = reinterpret_cast<float*>(ring);  // [W][8 heads][MROW]
 #pragma unroll
     for (int t = 0; t < KS; ++t) {
-      const int ch = r * (D / 8) + 2 * t;
-      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m) * D + ch) = make_float2(o[t][0], o[t][2]);
-      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m + 1) * D + ch) = make_float2(o[t][1], o[t][3]);
+      const int p = 16 * t + 2 * r;
+      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m) * L::MROW + p) = make_float2(o[t][0], o[t][2]);
+      *reinterpret_cast<float2*>(sO + (warp * 8 + 2 * m + 1) * L::MROW + p) = make_float2(o[t][1], o[t][3]);
     }
     if (threadIdx.x < 8) {
       const int g = threadIdx.x;
@@ -577,15 +633,57 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       sHl[g] = Lh;
     }
     __syncthreads();
+    if constexpr (CL) {
+      __shared__ Kv8Inbox<D> inbox;
+      namespace cg = cooperative_groups;
+      cg::cluster_group cl = cg::this_cluster();
+      const int C = a.cluster, split = cta % C, GD = G * D;
+      const int chunk = ((GD + C - 1) / C + 3) & ~3;
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      for (int i = 4 * threadIdx.x; i < GD; i += 4 * NT) {
+        const int g = i / D, d = i % D, owner = i / chunk;
+        float4 av = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(sO + (w * 8 + g) * L::MROW + d);
+          const float f = sF[w][g];
+          av.x = fmaf(x.x, f, av.x);
+          av.y = fmaf(x.y, f, av.y);
+          av.z = fmaf(x.z, f, av.z);
+          av.w = fmaf(x.w, f, av.w);
+        }
+        *reinterpret_cast<float4*>(cl.map_shared_rank(inbox.o, owner) + split * chunk + (i - owner * chunk)) = av;
+      }
+      if (threadIdx.x < C * G) {
+        const int owner = threadIdx.x / G, g = threadIdx.x % G;
+        cl.map_shared_rank(inbox.m, owner)[split * 8 + g] = sHm[g];
+        cl.map_shared_rank(inbox.l, owner)[split * 8 + g] = sHl[g];
+      }
+      cl.sync();  // nothing remote is touched after this
+      const int i1 = min(GD, (split + 1) * chunk);
+      for (int i = split * chunk + threadIdx.x; i < i1; i += NT) {
+        const int g = i / D, d = i % D;
+        float M = kNegInf, Lh = 0.f, av = 0.f;
+        for (int s = 0; s < C; ++s) M = fmaxf(M, inbox.m[s * 8 + g]);
+        for (int s = 0; s < C; ++s) {
+          const float ms = inbox.m[s * 8 + g];
+          const float f = ms == kNegInf ? 0.f : exp2f(ms - M);
+          Lh = fmaf(inbox.l[s * 8 + g], f, Lh);
+          av = fmaf(inbox.o[s * chunk + (i - split * chunk)], f, av);
+        }
+        kv8_finish<D>(a, (size_t)row * G + g, h * G + g, M, Lh, av, kv8_channel<D>(d));
+      }
+      return;
+    }
     const bool whole = e == s_pref[row] && seg_end == s_pref[row + 1];
     const int slot = e == lo ? 2 * cta : 2 * cta + 1;
     for (int i = threadIdx.x; i < G * D; i += NT) {
       const int g = i / D, d = i % D;
       float av = 0.f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) av = fmaf(sO[(w * 8 + g) * D + d], sF[w][g], av);
+      for (int w = 0; w < W; ++w) av = fmaf(sO[(w * 8 + g) * L::MROW + d], sF[w][g], av);
       if (whole) {
-        kv8_finish<D>(a, (size_t)row * G + g, h * G + g, sHm[g], sHl[g], av, d);
+        kv8_finish<D>(a, (size_t)row * G + g, h * G + g, sHm[g], sHl[g], av, kv8_channel<D>(d));
       } else {
         const size_t sg = (size_t)slot * G + g;
         a.po[sg * D + d] = av;
@@ -674,9 +772,10 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             }
           }
           const float inv = sh.s_inv[g];
-          __nv_bfloat162* op = reinterpret_cast<__nv_bfloat162*>(a.out + ((size_t)row * G + g) * D + 4 * d4);
-          op[0] = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-          op[1] = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+          bf16* op = a.out + ((size_t)row * G + g) * D;
+          *reinterpret_cast<__nv_bfloat162*>(op + kv8_channel<D>(4 * d4)) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+          *reinterpret_cast<__nv_bfloat162*>(op + kv8_channel<D>(4 * d4 + 2)) =
+              __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
         }
         if (threadIdx.x == 0) a.tickets[row] = 0;  // ready for the next call
       }
@@ -742,7 +841,7 @@ bool kv8_attend_supported(const Shape& s) {
   return s.dtype == 1 && s.B * (long long)s.Hkv <= kKv8MaxRows && (long long)s.B * s.Hkv * s.Cap < (1ll << 31);
 }
 
-static int kv8_grid() { return std::min(sm_count(), kKv8MaxGrid); }
+static int kv8_grid() { return std::min(sm_count() * kKv8PerSm, kKv8MaxGrid); }
 static size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 size_t kv8_attend_workspace(const Shape& s, const Kv8&, bool with_mass) {
@@ -751,28 +850,95 @@ size_t kv8_attend_workspace(const Shape& s, const Kv8&, bool with_mass) {
          (with_mass ? a256(rows * s.G * 8) + a256(rows * s.G * (s.Cap >> 4) * 8) : 0);
 }
 
+// What a launch of one kernel needs once per device: the limit of its dynamic
+// shared memory raised, and the number of clusters of each size that fit.
+struct Kv8Device {
+  std::atomic<int> clusters[kKv8MaxCluster + 1];  // 0: not asked yet, else 1 + the number
+  std::atomic<bool> raised;
+};
+
+template <int D>
+struct Kv8Config {
+  static constexpr int SG = 2, W = 12, S = D == 128 ? 2 : 4;
+  using L = Kv8Layout<D, SG, W, S>;
+  static constexpr size_t smem(int rows) { return L::REGION + (size_t)(rows + 1) * sizeof(int) + 1024; }
+};
+
+template <int D, int FMT, bool LIST, bool MASS, bool CL>
+static cudaError_t kv8_prepare(Kv8Device** out) {
+  using F = Kv8Config<D>;
+  static Kv8Device devices[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  Kv8Device& d = devices[dev];
+  if (!d.raised.load(std::memory_order_acquire)) {
+    auto kern = kv8_attend_kernel<D, FMT, F::SG, F::W, F::S, LIST, MASS, CL>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F::smem(CL ? 0 : kKv8MaxRows));
+    if (e == cudaSuccess && CL) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    d.raised.store(true, std::memory_order_release);
+  }
+  *out = &d;
+  return cudaSuccess;
+}
+
+// CTAs per row of the cluster kernel: the most that let all rows' clusters run
+// at once; 0 when not even clusters of two do.
+template <int D, int FMT, bool LIST, bool MASS>
+static int kv8_cluster(int rows, Kv8Device* d) {
+  using F = Kv8Config<D>;
+  for (int c = std::min(kKv8MaxCluster, sm_count() / rows); c >= 2; --c) {
+    int n = d->clusters[c].load(std::memory_order_relaxed);
+    if (n == 0) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(c);
+      cfg.blockDim = dim3(F::W * 32);
+      cfg.dynamicSmemBytes = F::smem(0);
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = c;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      int got = 0;
+      auto kern = kv8_attend_kernel<D, FMT, F::SG, F::W, F::S, LIST, MASS, true>;
+      if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        got = 0;
+      }
+      n = 1 + got;
+      d->clusters[c].store(n, std::memory_order_relaxed);
+    }
+    if (n - 1 >= rows) return c;
+  }
+  return 0;
+}
+
 template <int D, int FMT, bool LIST, bool MASS>
 static cudaError_t kv8_launch(Kv8Attend a, cudaStream_t st) {
-  constexpr int SG = 2, W = 12, S = D == 128 ? 2 : 4;
-  using L = Kv8Layout<D, SG, W, S>;
+  using F = Kv8Config<D>;
+  constexpr int SG = F::SG, W = F::W, S = F::S;
   a.boxes = LIST && a.P < 16 * SG ? SG : 1;
   CUtensorMap tk, tv;
   const uint64_t tokens = (uint64_t)a.rows * a.Cap;
   if (!kv8_map(&tk, a.c.kc, tokens, D, 16 * SG / a.boxes) || !kv8_map(&tv, a.c.vc, tokens, D, 16 * SG / a.boxes))
     return cudaErrorInvalidValue;
-  const size_t smem = L::REGION + (size_t)(a.rows + 1) * sizeof(int) + 1024;
-  // the kernel's limit, raised once per device to the most any call needs
-  static std::atomic<bool> raised[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64 || !raised[dev].load(std::memory_order_relaxed)) {
-    e = cudaFuncSetAttribute(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(L::REGION + (kKv8MaxRows + 1) * sizeof(int) + 1024));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) raised[dev].store(true, std::memory_order_relaxed);
+  Kv8Device* d;
+  cudaError_t e;
+  const long long most = LIST ? (long long)(a.count ? a.idx_stride : a.k_fixed) << a.pshift : a.Cap;  // tokens of a row
+  const bool even = a.rows == a.Hkv || (LIST && !a.count);
+  if (most <= (even ? kKv8ClusterEven : kKv8ClusterUneven) && a.rows * 2 <= sm_count()) {
+    if ((e = kv8_prepare<D, FMT, LIST, MASS, true>(&d)) != cudaSuccess) return e;
+    a.cluster = kv8_cluster<D, FMT, LIST, MASS>(a.rows, d);
+    if (a.cluster)
+      return launch_pdl_cluster(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS, true>, dim3(a.rows * a.cluster),
+                                dim3(W * 32), F::smem(0), a.cluster, st, tk, tv, a);
   }
-  return launch_pdl(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS>, dim3(kv8_grid()), dim3(W * 32), smem, st, tk, tv, a);
+  if ((e = kv8_prepare<D, FMT, LIST, MASS, false>(&d)) != cudaSuccess) return e;
+  return launch_pdl(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS, false>, dim3(kv8_grid()), dim3(W * 32),
+                    F::smem(a.rows), st, tk, tv, a);
 }
 
 template <int D>
