@@ -138,5 +138,7 @@ def check(fn_name: str, status: int) -> None:
 
 def call(name: str, *args) -> None:
     """Calls the named C entry point and raises SlsError on a non-zero status."""
-    lib = load()
-    check(name, getattr(lib, name)(*args))
+    lib = _lib if _lib is not None else load()
+    status = getattr(lib, name)(*args)
+    if status != SLS_OK:
+        check(name, status)

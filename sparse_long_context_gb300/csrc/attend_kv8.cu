@@ -49,7 +49,7 @@ constexpr int kKv8MinUnits = 4;
 // cluster busy after the rest.
 constexpr long long kKv8ClusterEven = 32768, kKv8ClusterUneven = 8192;
 // Work of a row change (drain, merge, partial and refill) in tokens.
-constexpr int kKv8SegCost = 1024;
+constexpr int kKv8SegCost = 2048;
 
 struct Kv8Attend {
   Kv8 c;
@@ -189,41 +189,58 @@ __device__ __forceinline__ void kv8_pv(uint32_t v, float (&o)[D / 16][4], uint32
   }
 }
 
-// The same for a group of the tail buffer (bf16, `lim` valid tokens; others
-// are not read and count as zero).
+// A group of the tail buffer (bf16, `lim` valid tokens; the others are not
+// read and count as zero).  All of its loads are issued together: a CTA meets
+// it once per row, with the memory system busy.
 template <int D>
-__device__ __forceinline__ void kv8_tail_scores(const bf16* k, const bf16* qh, bool head, int lim, float (&sc)[2][4],
-                                                int lane) {
-  const int r = lane >> 2, m = lane & 3;
+struct Kv8Tail {
+  uint2 k[2][D / 16], q[D / 16];
+  uint32_t v[4][D / 16];
+  int lim;
+  __device__ __forceinline__ void load(const bf16* kt, const bf16* vt, const bf16* qh, bool head, int n, int lane) {
+    const int r = lane >> 2, m = lane & 3;
+    lim = n;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
-#pragma unroll  // its loads in flight together
-  for (int c = 0; c < D / 16; ++c) {
-    const uint2 qv = head ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+    for (int c = 0; c < D / 16; ++c) {
+      q[c] = head ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const int t = r + 8 * nt;
-      const uint2 kv = t < lim ? *reinterpret_cast<const uint2*>(k + (size_t)t * D + 16 * c + 4 * m) : make_uint2(0u, 0u);
-      mma_bf16(sc[nt], qv.x, 0u, qv.y, 0u, kv.x, kv.y);
+      for (int nt = 0; nt < 2; ++nt) {
+        const int t = r + 8 * nt;
+        k[nt][c] = t < lim ? *reinterpret_cast<const uint2*>(kt + (size_t)t * D + 16 * c + 4 * m) : make_uint2(0u, 0u);
+      }
     }
-  }
-}
-template <int D>
-__device__ __forceinline__ void kv8_tail_pv(const bf16* v, int lim, float (&o)[D / 16][4], uint32_t p0, uint32_t p1,
-                                            int lane) {
-  const int r = lane >> 2, m = lane & 3;
-#pragma unroll
-  for (int t = 0; t < D / 16; ++t) {
-    uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int tok = 2 * m + (i & 1) + 8 * (i >> 1);
-      w[i] = tok < lim ? *reinterpret_cast<const uint32_t*>(v + (size_t)tok * D + r * (D / 8) + 2 * t) : 0u;
+      const int t = 2 * m + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+      for (int u = 0; u < D / 64; ++u) {  // the lane's D/8 channels in 16-byte loads
+        const uint4 x = t < lim ? *reinterpret_cast<const uint4*>(vt + (size_t)t * D + r * (D / 8) + 8 * u)
+                                : make_uint4(0u, 0u, 0u, 0u);
+        v[i][4 * u] = x.x; v[i][4 * u + 1] = x.y; v[i][4 * u + 2] = x.z; v[i][4 * u + 3] = x.w;
+      }
     }
-    mma_bf16(o[t], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x5410),
-             __byte_perm(w[2], w[3], 0x7632), p0, p1);
   }
-}
+  __device__ __forceinline__ void scores(float mul, float (&x)[4], int lane) const {
+    const int m = lane & 3;
+    float sc[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sc[0][i] = sc[1][i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) mma_bf16(sc[nt], q[c].x, 0u, q[c].y, 0u, k[nt][c].x, k[nt][c].y);
+    x[0] = 2 * m < lim ? sc[0][0] * mul : kNegInf;
+    x[1] = 2 * m + 1 < lim ? sc[0][1] * mul : kNegInf;
+    x[2] = 2 * m + 8 < lim ? sc[1][0] * mul : kNegInf;
+    x[3] = 2 * m + 9 < lim ? sc[1][1] * mul : kNegInf;
+  }
+  __device__ __forceinline__ void pv(float (&o)[D / 16][4], uint32_t p0, uint32_t p1) const {
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t)
+      mma_bf16(o[t], __byte_perm(v[0][t], v[1][t], 0x5410), __byte_perm(v[0][t], v[1][t], 0x7632),
+               __byte_perm(v[2][t], v[3][t], 0x5410), __byte_perm(v[2][t], v[3][t], 0x7632), p0, p1);
+  }
+};
 
 template <bool CL>
 struct Kv8Smem {
@@ -291,13 +308,18 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   if constexpr (CL) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait_then_release();
 
-  // groups and units of a row
+  // Groups and units of a row.  Dense: the groups of its complete blocks; the
+  // tail's go with the last unit (a row with nothing but a tail has one unit).
   auto groups_of = [&](int row) {
-    if constexpr (!LIST) return (clamp_len(a.ctx_len[row / a.Hkv], a.Cap) + 15) >> 4;
+    if constexpr (!LIST)
+      return clamp_len(a.ctx_len[row / a.Hkv], a.Cap) >> a.c.bshift << (a.c.bshift - 4);
     const int cnt = a.count ? a.count[row] : a.k_fixed;
     return min(max(cnt, 0), a.idx_stride) << (a.pshift - 4);
   };
-  auto units_of = [&](int row) { return (groups_of(row) + SG - 1) / SG; };
+  auto units_of = [&](int row) {
+    const int n = (groups_of(row) + SG - 1) / SG;
+    return LIST || n > 0 ? n : (a.ctx_len[row / a.Hkv] > 0 ? 1 : 0);
+  };
 
   int row = 0, lo = 0, hi = 0, grid = 1;
   if constexpr (CL) {
@@ -378,7 +400,9 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   const uint32_t wring = smem_u32(ring) + (uint32_t)warp * S * L::STAGE;
   uint32_t wseq = 0;  // this warp's ring position
   for (int e = lo; CL || e < hi;) {
-    const int seg_end = CL ? hi : min(hi, s_pref[row + 1]), u0 = CL ? lo : e - s_pref[row];
+    // segment ends and row ends in the CTA's own counting of units
+    const int row_end = CL ? units_of(row) : s_pref[row + 1];
+    const int seg_end = CL ? hi : min(hi, row_end), u0 = CL ? lo : e - s_pref[row];
     const int b = row / a.Hkv, h = row % a.Hkv;
     const int N = clamp_len(a.ctx_len[b], a.Cap), ng = groups_of(row), newest = N >> a.c.bshift;
     const int nseg = seg_end - e;
@@ -411,6 +435,20 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         }
       }
       return mref;
+    };
+    // the 16 positions from `at` on, which lie in the tail buffer
+    auto tail_group = [&](int at) {
+      const size_t tail = ((size_t)row * a.c.block + (at & (a.c.block - 1))) * D;
+      Kv8Tail<D> g;
+      g.load(static_cast<const bf16*>(a.c.kt) + tail, static_cast<const bf16*>(a.c.vt) + tail, qh, r < G, min(16, N - at),
+             lane);
+      float x[4];
+      g.scores(a.qscale, x, lane);
+      const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
+      l_run += (x[0] + x[1]) + (x[2] + x[3]);
+      g.pv(o, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
     };
 
     // Of unit kb + lane: the positions of its groups (-1: nothing there) and
@@ -484,6 +522,11 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       if (lane == 0) fence_proxy_async_smem();  // the merge's reads of the ring before the copies write it
       load_batch(0);
       for (int j = 0; j < min(S - 1, nk); ++j) issue(j, 0);
+      if constexpr (!LIST) {
+        // the row's last CTA: its tail groups, one per warp from the last warp down
+        if (seg_end == row_end)
+          for (int at = (newest << a.c.bshift) + 16 * (W - 1 - warp); at < N; at += 16 * W) tail_group(at);
+      }
     }
     // the heads' queries as fp16 with their largest channel in [2^10, 2^11)
     {
@@ -510,30 +553,19 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     for (int kb = 0; ok && kb < nk; kb += BATCH) {
       if (kb) load_batch(kb);
       const int kend = min(nk, kb + BATCH);
-      // The batch's groups in the tail buffer (lanes below BATCH: their own
-      // units, not the ones looked ahead), outside the loop over stored units.
+      if constexpr (LIST) {
+        // The batch's groups in the tail buffer (lanes below BATCH: its own
+        // units, not the ones looked ahead), outside the loop over stored ones.
 #pragma unroll
-      for (int s = 0; s < SG; ++s) {
-        uint32_t todo = __ballot_sync(0xffffffffu, lane < BATCH && base[s] >= 0 && base[s] >> a.c.bshift >= newest);
-        while (todo) {
-          const int at = __shfl_sync(0xffffffffu, base[s], __ffs(todo) - 1);
-          todo &= todo - 1;
-          const int lim = min(16, N - at), slot = at & (a.c.block - 1);
-          const size_t tail = ((size_t)row * a.c.block + slot) * D;
-          float sc[2][4], x[4];
-          kv8_tail_scores<D>(static_cast<const bf16*>(a.c.kt) + tail, qh, r < G, lim, sc, lane);
-          x[0] = 2 * m < lim ? sc[0][0] * a.qscale : kNegInf;
-          x[1] = 2 * m + 1 < lim ? sc[0][1] * a.qscale : kNegInf;
-          x[2] = 2 * m + 8 < lim ? sc[1][0] * a.qscale : kNegInf;
-          x[3] = 2 * m + 9 < lim ? sc[1][1] * a.qscale : kNegInf;
-          const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
-          l_run += (x[0] + x[1]) + (x[2] + x[3]);
-          kv8_tail_pv<D>(static_cast<const bf16*>(a.c.vt) + tail, lim, o, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]),
-                         lane);
+        for (int s = 0; s < SG; ++s) {
+          const bool tail = base[s] >= 0 && base[s] >> a.c.bshift >= newest;
+          uint32_t todo = __ballot_sync(0xffffffffu, lane < BATCH && tail);
+          while (todo) {
+            tail_group(__shfl_sync(0xffffffffu, base[s], __ffs(todo) - 1));
+            todo &= todo - 1;
+          }
+          if (tail) base[s] = -1;  // nothing to stream
         }
-        if (base[s] >= 0 && base[s] >> a.c.bshift >= newest) base[s] = -1;  // nothing to stream
       }
       for (; k < kend; ++k) {
         if (k + S - 1 < nk) issue(k + S - 1, kb);  // into the stage unit k - 1 has left
@@ -697,7 +729,6 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       // the row's contributors are the CTAs from the one holding its first
       // unit to the one holding its last (those with units); CTA k wrote slot
       // 2k when its range starts inside the row, else 2k + 1
-      __threadfence();
       __syncthreads();
       if (threadIdx.x == 0) {
         auto cta_of = [&](int x) {  // the last CTA whose range starts at or before unit x
@@ -714,11 +745,14 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         for (int c2 = cf; c2 <= cl; ++c2)
           if (sh.s_lo[c2] < sh.s_lo[c2 + 1]) sh.s_slot[n++] = sh.s_lo[c2] >= s_pref[row] ? 2 * c2 : 2 * c2 + 1;
         sh.s_ncontrib = n;
+        // one thread's fences cover the CTA's stores before the barrier and
+        // its loads after the next one
+        __threadfence();
         sh.s_last = atomicAdd(a.tickets + row, 1) == n - 1;
+        __threadfence();
       }
       __syncthreads();
       if (sh.s_last) {
-        __threadfence();
         const int n = sh.s_ncontrib;
         for (int g = warp; g < G; g += W) {
           float M = kNegInf, Ls = 0.f;
@@ -796,12 +830,18 @@ kv8_mass_kernel(const Kv8Attend a, int per_row) {
   const int gshift = a.c.bshift - 4, blk = g16 >> gshift;
   const bool live = blk < clamp_len(a.ctx_len[row / a.Hkv], a.Cap) >> a.c.bshift;
   float sum = 0.f;
-  if (live)
-    for (int g = 0; g < a.G; ++g) {
-      const float2 f = a.fin[(size_t)row * a.G + g];
-      const float2 x = __ldcg(a.grp + ((size_t)row * a.G + g) * (a.Cap >> 4) + g16);
-      sum += x.x * exp2f(x.y - f.x) * f.y;
-    }
+  if (live) {
+    float2 x[8], f[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      if (g < a.G) {
+        x[g] = __ldcg(a.grp + ((size_t)row * a.G + g) * (a.Cap >> 4) + g16);
+        f[g] = a.fin[(size_t)row * a.G + g];
+      }
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      if (g < a.G) sum += x[g].x * exp2f(x[g].y - f[g].x) * f[g].y;
+  }
   for (int o = 1; o < (1 << gshift); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (live && (g16 & ((1 << gshift) - 1)) == 0) {
     const size_t at = (size_t)row * (a.Cap >> a.c.bshift) + blk;
@@ -857,16 +897,20 @@ struct Kv8Device {
   std::atomic<bool> raised;
 };
 
-template <int D>
+// Twelve warps (at most 170 registers a thread) whose rings of two 32-token
+// units fill the shared memory: 8, 10, 14 and 16 warps and units of 16 tokens
+// were slower.  At D = 64 int8 units of 64 tokens (half the softmax steps)
+// are 9% faster, but 7% slower for e4m3, whose conversions are the longer chain.
+template <int D, int FMT>
 struct Kv8Config {
-  static constexpr int SG = 2, W = 12, S = D == 128 ? 2 : 4;
+  static constexpr int SG = D == 64 && FMT == kKv8Int8 ? 4 : 2, W = 12, S = D == 128 || SG == 4 ? 2 : 4;
   using L = Kv8Layout<D, SG, W, S>;
   static constexpr size_t smem(int rows) { return L::REGION + (size_t)(rows + 1) * sizeof(int) + 1024; }
 };
 
 template <int D, int FMT, bool LIST, bool MASS, bool CL>
 static cudaError_t kv8_prepare(Kv8Device** out) {
-  using F = Kv8Config<D>;
+  using F = Kv8Config<D, FMT>;
   static Kv8Device devices[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -888,7 +932,7 @@ static cudaError_t kv8_prepare(Kv8Device** out) {
 // at once; 0 when not even clusters of two do.
 template <int D, int FMT, bool LIST, bool MASS>
 static int kv8_cluster(int rows, Kv8Device* d) {
-  using F = Kv8Config<D>;
+  using F = Kv8Config<D, FMT>;
   for (int c = std::min(kKv8MaxCluster, sm_count() / rows); c >= 2; --c) {
     int n = d->clusters[c].load(std::memory_order_relaxed);
     if (n == 0) {
@@ -918,7 +962,7 @@ static int kv8_cluster(int rows, Kv8Device* d) {
 
 template <int D, int FMT, bool LIST, bool MASS>
 static cudaError_t kv8_launch(Kv8Attend a, cudaStream_t st) {
-  using F = Kv8Config<D>;
+  using F = Kv8Config<D, FMT>;
   constexpr int SG = F::SG, W = F::W, S = F::S;
   a.boxes = LIST && a.P < 16 * SG ? SG : 1;
   CUtensorMap tk, tv;

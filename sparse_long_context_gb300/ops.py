@@ -21,7 +21,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current device's current stream, without building a torch.cuda.Stream (3 us of a call on the host)
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
@@ -357,20 +358,22 @@ def selection_recall(desc: L.AttnDesc, q, k_cache, page_idx, ctx_len, count=None
 
 # ------------------------------------------------- per-head norm and rotation
 
-def _local(t: torch.Tensor, name: str, dtype=None, shape=None, strided: bool = False):
-    """A tensor of the current device (whose stream the call goes to); strided: only the last dimension must be
-    contiguous."""
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _local(t: torch.Tensor, name: str, dtype, shape, strided: bool = False) -> int:
+    """Address of a tensor of the current device (whose stream the call goes to); strided: only the last dimension
+    must be contiguous."""
+    dev = t.get_device()  # -1 on the host
+    if t.dtype is dtype and t.shape == shape and dev >= 0 and dev == torch._C._cuda_getDevice() and (
+            t.is_contiguous() if not strided else t.stride(-1) == 1):
+        return t.data_ptr()
+    if not t.is_cuda or dev != torch.cuda.current_device():
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if strided:
-        if t.stride(-1) != 1 and t.numel():
-            raise ValueError(f"{name} must have contiguous channels")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.numel():
+        raise ValueError(f"{name} must have contiguous channels" if strided else f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def make_rope(num_q_heads: int, num_kv_heads: int, head_dim: int, dtype, rotary_dim: Optional[int] = None,
@@ -397,28 +400,23 @@ def qk_norm_rope(rope: L.RopeDesc, q, k, positions, q_weight=None, k_weight=None
     heads is passed as None.  Returns (q_out, k_out)."""
     n, d = int(positions.shape[0]), rope.head_dim
     dtype = torch.float32 if rope.dtype == L.SLS_DTYPE_F32 else torch.bfloat16
-    _local(positions, "positions", torch.int32, (n,))
-    args = []
-    outs = []
-    for name, heads, x, w, out in (("q", rope.num_q_heads, q, q_weight, q_out),
-                                   ("k", rope.num_kv_heads, k, k_weight, k_out)):
+    pos = _local(positions, "positions", torch.int32, (n,))
+
+    def side(name, heads, x, w, out):
         if heads == 0:
-            args.append((None, 0, 0, None, None, 0, 0))
-            outs.append(None)
-            continue
-        _local(x, name, dtype, (n, heads, d), strided=True)
+            return None, (None, 0, 0), None, (None, 0, 0)
+        shape = (n, heads, d)
         if out is None:
-            out = torch.empty((n, heads, d), dtype=dtype, device=x.device)
-        else:
-            _local(out, name + "_out", dtype, (n, heads, d), strided=True)
-        if w is not None:
-            _local(w, name + "_weight", dtype, (d,))
-        args.append((_ptr(x), x.stride(0), x.stride(1), _ptr(w), _ptr(out), out.stride(0), out.stride(1)))
-        outs.append(out)
-    a, b = args
-    L.call("sls_qk_norm_rope", ctypes.byref(rope), n, a[0], a[1], a[2], b[0], b[1], b[2], a[3], b[3], _ptr(positions),
-           a[4], a[5], a[6], b[4], b[5], b[6], _stream())
-    return outs[0], outs[1]
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+        xs, os = x.stride(), out.stride()
+        return (out, (_local(x, name, dtype, shape, True), xs[0], xs[1]),
+                None if w is None else _local(w, name + "_weight", dtype, (d,)),
+                (_local(out, name + "_out", dtype, shape, True), os[0], os[1]))
+
+    q_out, qi, wq, qo = side("q", rope.num_q_heads, q, q_weight, q_out)
+    k_out, ki, wk, ko = side("k", rope.num_kv_heads, k, k_weight, k_out)
+    L.call("sls_qk_norm_rope", ctypes.byref(rope), n, *qi, *ki, wq, wk, pos, *qo, *ko, _stream())
+    return q_out, k_out
 
 
 # -------------------------------------------------------------- 8-bit KV cache
@@ -449,6 +447,7 @@ class Kv8Cache:
         self.k_tail, self.v_tail = k_tail, v_tail
         self.c = L.Kv8CacheDesc(_KV8_FORMATS[fmt], block, *(t.data_ptr() for t in (
             k_codes, v_codes, k_scales, v_scales, k_tail, v_tail)))
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, desc: L.AttnDesc, fmt: str = "int8", block: int = 64, device="cuda") -> "Kv8Cache":
@@ -477,23 +476,25 @@ def kv8_append(desc: L.AttnDesc, cache: Kv8Cache, k_new, v_new, ctx_len, new_len
     B, H, D = desc.batch, desc.num_kv_heads, desc.head_dim
     if k_new.dim() != 4:
         raise ValueError(f"k_new must be [B, T, Hkv, D], got {tuple(k_new.shape)}")
-    T = int(k_new.shape[1])
-    for t, name in ((k_new, "k_new"), (v_new, "v_new")):
-        _local(t, name, torch.bfloat16, (B, T, H, D), strided=True)
-    ctx_out = ctx_len if ctx_out is None else ctx_out
-    for t, name in ((ctx_len, "ctx_len"), (new_len, "new_len"), (ctx_out, "ctx_out"), (pos_out, "pos_out")):
-        if t is not None:
-            _local(t, name, torch.int32, (B,))
-    for t, name in ((kmin, "kmin"), (kmax, "kmax")):
-        if t is not None:
-            _local(t, name, torch.bfloat16, (B, H, desc.capacity // desc.page_size, D))
-    if mass is not None:
-        _local(mass, "mass", torch.float32, (B, H, desc.capacity // cache.block))
+    T = k_new.shape[1]
+    shape = (B, T, H, D)
+    kp = _local(k_new, "k_new", torch.bfloat16, shape, True)
+    vp = _local(v_new, "v_new", torch.bfloat16, shape, True)
+    ctx = _local(ctx_len, "ctx_len", torch.int32, (B,))
+    to = ctx if ctx_out is None else _local(ctx_out, "ctx_out", torch.int32, (B,))
+    n = None if new_len is None else _local(new_len, "new_len", torch.int32, (B,))
+    at = None if pos_out is None else _local(pos_out, "pos_out", torch.int32, (B,))
+    lo = hi = None
+    if kmin is not None or kmax is not None:
+        if kmin is None or kmax is None:
+            raise ValueError("kmin and kmax: both or neither")
+        meta = (B, H, desc.capacity // desc.page_size, D)
+        lo, hi = _local(kmin, "kmin", torch.bfloat16, meta), _local(kmax, "kmax", torch.bfloat16, meta)
+    sums = None if mass is None else _local(mass, "mass", torch.float32, (B, H, desc.capacity // cache.block))
     ks, vs = k_new.stride(), v_new.stride()
-    L.call("sls_kv8_append", ctypes.byref(desc), ctypes.byref(cache.c), _ptr(k_new), ks[0], ks[1], ks[2], _ptr(v_new),
-           vs[0], vs[1], vs[2], T, _ptr(new_len), _ptr(kmin), _ptr(kmax), _ptr(mass), _ptr(ctx_len), _ptr(ctx_out),
-           _ptr(pos_out), _stream())
-    return ctx_out
+    L.call("sls_kv8_append", ctypes.byref(desc), cache.ref, kp, ks[0], ks[1], ks[2], vp, vs[0], vs[1], vs[2], T, n, lo,
+           hi, sums, ctx, to, at, _stream())
+    return ctx_len if ctx_out is None else ctx_out
 
 
 def kv8_attend_workspace(desc: L.AttnDesc, cache: Kv8Cache, mass: bool = False, device="cuda"):
@@ -509,36 +510,34 @@ def kv8_decode_attend(desc: L.AttnDesc, cache: Kv8Cache, q, ctx_len, page_idx=No
     mass_out, if given, receives every complete block's summed softmax weight added to mass_in.  Returns
     (out, lse)."""
     B, Hq, D = desc.batch, desc.num_q_heads, desc.head_dim
-    _local(q, "q", torch.bfloat16, (B, Hq, D))
-    _local(ctx_len, "ctx_len", torch.int32, (B,))
+    shape = (B, Hq, D)
+    qp = _local(q, "q", torch.bfloat16, shape)
+    ctx = _local(ctx_len, "ctx_len", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
-    else:
-        _local(out, "out", torch.bfloat16, (B, Hq, D))
-    if lse is not None:
-        _local(lse, "lse", torch.float32, (B, Hq))
-    elif want_lse:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+    op = _local(out, "out", torch.bfloat16, shape)
+    if lse is None and want_lse:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if sink is not None:
-        _local(sink, "sink", torch.float32, (Hq,))
+    lp = None if lse is None else _local(lse, "lse", torch.float32, (B, Hq))
+    sk = None if sink is None else _local(sink, "sink", torch.float32, (Hq,))
+    pages = cnt = None
     stride = kf = 0
     if page_idx is not None:
         rows = B * desc.num_kv_heads
-        stride = int(page_idx.shape[-1])
+        stride = page_idx.shape[-1]
         kf = stride if k_fixed is None else int(k_fixed)
-        _local(page_idx, "page_idx", torch.int32, (rows, stride))
-        if count is not None:
-            _local(count, "count", torch.int32, (rows,))
-    for t, name in ((mass_in, "mass_in"), (mass_out, "mass_out")):
-        if t is not None:
-            _local(t, name, torch.float32, (B, desc.num_kv_heads, desc.capacity // cache.block))
+        pages = _local(page_idx, "page_idx", torch.int32, (rows, stride))
+        cnt = None if count is None else _local(count, "count", torch.int32, (rows,))
+    mi = mo = None
+    if mass_out is not None or mass_in is not None:
+        sums = (B, desc.num_kv_heads, desc.capacity // cache.block)
+        mi = None if mass_in is None else _local(mass_in, "mass_in", torch.float32, sums)
+        mo = None if mass_out is None else _local(mass_out, "mass_out", torch.float32, sums)
     if workspace is None:
         workspace = kv8_attend_workspace(desc, cache, mass_out is not None, q.device)
-    else:
-        _local(workspace, "workspace", torch.uint8)
-    L.call("sls_kv8_decode_attend", ctypes.byref(desc), ctypes.byref(cache.c), _ptr(q), _ptr(page_idx), stride,
-           _ptr(count), kf, _ptr(ctx_len), _ptr(sink), _ptr(out), _ptr(lse), _ptr(mass_in), _ptr(mass_out),
-           _ptr(workspace), workspace.numel(), _stream())
+    ws = _local(workspace, "workspace", torch.uint8, workspace.shape)
+    L.call("sls_kv8_decode_attend", ctypes.byref(desc), cache.ref, qp, pages, stride, cnt, kf, ctx, sk, op, lp, mi, mo,
+           ws, workspace.numel(), _stream())
     return out, lse
 
 
@@ -565,20 +564,14 @@ def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sin
             ctx_out = torch.empty_like(ctx_len)
     if kept_idx is None:
         kept_idx = torch.empty((B * H, keep), dtype=torch.int32, device=ctx_len.device)
-    _local(kept_idx, "kept_idx", torch.int32, (B * H, keep))
-    for t, name in ((ctx_len, "ctx_len"), (ctx_out, "ctx_out")):
-        _local(t, name, torch.int32, (B,))
-    _local(mass, "mass", torch.float32, (B, H, cap // cache.block))
-    if mass_out is not None:
-        _local(mass_out, "mass_out", torch.float32, (B, H, dcap // cache.block))
-    for t, name, c in ((kmin, "kmin", cap), (kmax, "kmax", cap), (kmin_out, "kmin_out", dcap),
-                       (kmax_out, "kmax_out", dcap)):
-        if t is not None:
-            _local(t, name, torch.bfloat16, (B, H, c // P, D))
-    L.call("sls_kv8_evict", ctypes.byref(desc), ctypes.byref(cache.c), dcap,
-           None if dst is None else ctypes.byref(dst.c), int(keep), int(n_sink_blocks), int(n_recent_blocks),
-           _ptr(mass), _ptr(mass_out), _ptr(kmin), _ptr(kmax), _ptr(kmin_out), _ptr(kmax_out), _ptr(kept_idx),
-           _ptr(ctx_len), _ptr(ctx_out), _stream())
+    kept = _local(kept_idx, "kept_idx", torch.int32, (B * H, keep))
+    ctx, to = _local(ctx_len, "ctx_len", torch.int32, (B,)), _local(ctx_out, "ctx_out", torch.int32, (B,))
+    mi = _local(mass, "mass", torch.float32, (B, H, cap // cache.block))
+    mo = None if mass_out is None else _local(mass_out, "mass_out", torch.float32, (B, H, dcap // cache.block))
+    meta = [None if t is None else _local(t, name, torch.bfloat16, (B, H, c // P, D)) for t, name, c in (
+        (kmin, "kmin", cap), (kmax, "kmax", cap), (kmin_out, "kmin_out", dcap), (kmax_out, "kmax_out", dcap))]
+    L.call("sls_kv8_evict", ctypes.byref(desc), cache.ref, dcap, None if dst is None else dst.ref, int(keep),
+           int(n_sink_blocks), int(n_recent_blocks), mi, mo, *meta, kept, ctx, to, _stream())
     return ctx_out, kept_idx
 
 
