@@ -604,13 +604,27 @@ sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens, const
   if (Hkv && (r = side("k", Hkv, k, k_token_stride, k_head_stride, k_weight, k_out, k_out_token_stride,
                        k_out_head_stride)))
     return r;
-  for (int i = 0; i < R / 2; ++i) {
-    const double f = rope->inv_freq ? rope->inv_freq[i] : std::pow(rope->theta, -2.0 * i / R);
-    if (!std::isfinite(f)) return fail(SLS_EINVAL, "frequency %d is not finite", i);
-    const double turns = f / 6.283185307179586476925286766559;
-    double frac = turns - std::floor(turns);  // in [0, 1]
-    if (frac >= 1.0) frac = 0.0;
-    a.freq[i] = (uint64_t)std::ldexp(frac, 64);
+  // The frequencies of theta, kept from call to call by their value: R / 2
+  // calls of pow are half of a small call's time on the host.
+  thread_local double known_theta = 0.0;
+  thread_local int known_R = 0;
+  thread_local uint64_t known[64];
+  if (!rope->inv_freq && rope->theta == known_theta && R == known_R) {
+    std::memcpy(a.freq, known, sizeof(known));
+  } else {
+    for (int i = 0; i < R / 2; ++i) {
+      const double f = rope->inv_freq ? rope->inv_freq[i] : std::pow(rope->theta, -2.0 * i / R);
+      if (!std::isfinite(f)) return fail(SLS_EINVAL, "frequency %d is not finite", i);
+      const double turns = f / 6.283185307179586476925286766559;
+      double frac = turns - std::floor(turns);  // in [0, 1]
+      if (frac >= 1.0) frac = 0.0;
+      a.freq[i] = (uint64_t)std::ldexp(frac, 64);
+    }
+    if (!rope->inv_freq) {
+      known_theta = rope->theta;
+      known_R = R;
+      std::memcpy(known, a.freq, sizeof(known));
+    }
   }
   a.q = q; a.k = k; a.wq = q_weight; a.wk = k_weight; a.qo = q_out; a.ko = k_out; a.pos = positions;
   a.q_t = q_token_stride; a.q_h = q_head_stride; a.k_t = k_token_stride; a.k_h = k_head_stride;

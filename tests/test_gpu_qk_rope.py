@@ -105,6 +105,17 @@ def test_zero_rows_infinities_and_nan_stay_in_their_head():
     assert q.cpu()[~bad].isfinite().all()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+def test_channels_that_are_not_rotated_pass_an_infinity_alone(inter):
+    x = torch.ones((2, 1, 64), dtype=torch.bfloat16)
+    x[0, 0, 37] = float("inf")
+    x[1, 0, 33] = float("nan")
+    rope = ops.make_rope(1, 0, 64, torch.bfloat16, rotary_dim=32, interleaved=inter)
+    y = ops.qk_norm_rope(rope, x.cuda(), None, torch.tensor([3, 0], dtype=torch.int32, device="cuda"))[0].cpu()
+    assert torch.equal(y[0, 0, 32:], x[0, 0, 32:]) and y[0, 0, :32].isfinite().all()
+    assert y[1, 0, 33].isnan() and y[1].isnan().sum() == 1
+
+
 def test_other_stream_and_graph():
     qkv, (wq, wk) = draw(11, 33, 4, 2, 128, torch.bfloat16)
     rope = ops.make_rope(4, 2, 128, torch.bfloat16)
