@@ -644,6 +644,7 @@ static sls_status check_kv8(const sls::Shape& s, const sls_kv8_cache* c, int cap
     return fail(SLS_EINVAL, "%s block %d must be a power of two in [16, 256]", name, c->block);
   if (capacity < c->block || capacity % c->block)
     return fail(SLS_EINVAL, "%s capacity %d not a multiple of its block %d", name, capacity, c->block);
+  if (capacity > (1 << 30)) return fail(SLS_EUNSUPPORTED, "%s capacity %d above 2^30", name, capacity);
   if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales || !c->k_tail || !c->v_tail)
     return fail(SLS_EINVAL, "%s has a NULL pointer", name);
   if (((uintptr_t)c->k_codes | (uintptr_t)c->v_codes | (uintptr_t)c->k_tail | (uintptr_t)c->v_tail) & 15)
@@ -677,7 +678,7 @@ sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
     REQUIRE16(kmin); REQUIRE16(kmax);
     if (s.P == 1) return fail(SLS_EINVAL, "page_size 1: an 8-bit cache has no page summaries of single keys (pass NULL)");
   }
-  const int64_t units = (int64_t)(max_new / std::min(c.block, s.P)) + 2;
+  const int64_t units = (int64_t)(max_new / c.block) + 2;
   int64_t ctas;
   if (!checked_mul((int64_t)s.B * s.Hkv * 2, units, &ctas) || ctas > INT32_MAX)
     return fail(SLS_EOVERFLOW, "grid too large");
@@ -750,7 +751,7 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
   const bool same = e.dst.kc == e.src.kc;
   const int64_t rows = (int64_t)s.B * s.Hkv;
   int64_t ctas;
-  if (!checked_mul(rows, 64, &ctas) || ctas > INT32_MAX || rows * dst_capacity > (int64_t(1) << 41))
+  if (!checked_mul(rows, (int64_t)keep + 128, &ctas) || ctas > INT32_MAX || rows * dst_capacity > (int64_t(1) << 41))
     return fail(SLS_EOVERFLOW, "too many rows");
   if (same) {
     if (e.dst.vc != e.src.vc || e.dst.ks != e.src.ks || e.dst.vs != e.src.vs || e.dst.kt != e.src.kt ||

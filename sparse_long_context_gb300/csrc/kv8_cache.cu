@@ -1,5 +1,7 @@
 // The 8-bit cache's writers: appending tokens (quantising the blocks they
 // complete) and evicting blocks by accumulated attention weight.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kv8.cuh"
 #include "launch.h"
@@ -19,288 +21,581 @@ __device__ __forceinline__ AppendSpan append_span(const Kv8New& nw, const int32_
   return s;
 }
 
-// One CTA per (sequence, KV head, K or V, block touched): the
-// block's tokens, the earlier ones from the tail buffer and the new ones from
-// the caller, are read twice (largest magnitude, then the codes).  The CTA of
-// a sequence's first block also writes its newest, partial block to the
-// tail, after its own reads of it.
+// Page min/max of the new keys of one KV head: pages [p0, p1) of the row, by the
+// CTA's NT threads, a thread per page and 16-byte chunk of channels.  `src` is the
+// first new token.  A page that held tokens before is merged with what is stored.
+template <int NT>
+__device__ __forceinline__ void append_pagemeta(const bf16* src, int64_t st, bf16* kmin, bf16* kmax, size_t row, int Cap,
+                                                int D, int pshift, const AppendSpan& sp, int p0, int p1) {
+  const int cpr = D / 8;
+  for (int i = threadIdx.x; i < (p1 - p0) * cpr; i += NT) {
+    const int pg = p0 + i / cpr, ch = (i % cpr) * 8;
+    const int t0 = max(pg << pshift, sp.start) - sp.start, t1 = min((pg + 1) << pshift, sp.start + sp.n) - sp.start;
+    const size_t at = (row * (Cap >> pshift) + pg) * D + ch;
+    uint4 lo, hi;
+    if ((pg << pshift) < sp.start) {
+      lo = *reinterpret_cast<const uint4*>(kmin + at);
+      hi = *reinterpret_cast<const uint4*>(kmax + at);
+    } else {
+      lo = hi = *reinterpret_cast<const uint4*>(src + t0 * st + ch);
+    }
+    __nv_bfloat162* l2 = reinterpret_cast<__nv_bfloat162*>(&lo);
+    __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&hi);
+#pragma unroll 4
+    for (int t = t0; t < t1; ++t) {
+      const uint4 x = *reinterpret_cast<const uint4*>(src + t * st + ch);
+      const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l2[k] = __hmin2(l2[k], x2[k]);
+        h2[k] = __hmax2(h2[k], x2[k]);
+      }
+    }
+    *reinterpret_cast<uint4*>(kmin + at) = lo;
+    *reinterpret_cast<uint4*>(kmax + at) = hi;
+  }
+}
+
+// Codes of the eight bf16 values of a vector: rcp = top / amax once per block and
+// one multiplication each.  That product is within 2^-23 (relative) of the exact
+// quotient top x / amax, and the quotient of numbers of 8 significant bits is
+// either on a tie between two codes or at least 2^-13 (relative, e4m3) or
+// 1 / (510 2^k) (int8, x = 2^-k of amax: 64 times the product's error) away
+// from one: only products next to a tie, 1 vector in 30 or fewer, take the IEEE
+// division, so that every code is that of exact arithmetic (ties to even).
 template <int FMT>
-__global__ void __launch_bounds__(256)
-kv8_append_kernel(const Kv8 c, const Kv8New nw, float* mass, const int32_t* ctx_len, int Hkv, int Cap, int D,
-                  int units) {
+__device__ __forceinline__ uint2 kv8_codes8(const uint4& raw, float amax, float rcp) {
+  float x[8];
+  unpack_vec(raw, x);
+  uint32_t w[2];
+  bool near = false;
+  if constexpr (FMT == kKv8Int8) {
+    uint32_t c[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float y = x[k] * rcp, t = y + 12582912.f;  // 1.5 * 2^23: the nearest integer in the low bits
+      c[k] = __float_as_uint(t);
+      near |= fabsf(y - (t - 12582912.f)) > 0.5f - 1.f / 16384.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      w[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040u), __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040u),
+                         0x5410u);
+  } else {
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = x[k] * rcp;
+      const uint32_t u = __float_as_uint(y[k]);
+      // a tie has the 20 bits below e4m3's mantissa at 0x80000; subnormal codes are looked at one by one
+      near |= (u & 0xfffffu) - 0x7fff0u <= 0x20u || (fabsf(y[k]) < 0.015625f && y[k] != 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k], y[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2], y[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
+      w[k] = a | b << 16;
+    }
+  }
+  if (near) {
+    w[0] = w[1] = 0u;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k >> 2] |= kv8_code<FMT>(x[k], amax) << (8 * (k & 3));
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Largest magnitude of a vector's bf16 values as two bit patterns (NaN above
+// infinity above the numbers).
+__device__ __forceinline__ uint32_t abs_max2(const uint4& v) {
+  const uint32_t m = 0x7fff7fffu;
+  return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+}
+
+// Quantises a block whose vectors the CTA's threads hold, VPT each: vector v of
+// thread i is token v NT / (D / 8) + i / (D / 8).  Writes codes and scale.
+template <int FMT, int VPT, int NT>
+__device__ __forceinline__ void quantise_held(const uint4 (&x)[VPT], uint8_t* codes, float* scale, uint32_t* s_max) {
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) m2 = __vmaxu2(m2, abs_max2(x[v]));
+  uint32_t mx = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NT / 32; ++k) mx = max(mx, s_max[k]);
+  const float amax = __uint_as_float(mx << 16);
+  const bool finite = mx < 0x7f80u;
+  const float top = kv8_top<FMT>();
+  // a block of subnormals would overflow the reciprocal: the division then
+  const float rcp = __fdiv_rn(top, amax);
+  const bool fast = rcp < 1e38f;
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    uint2 w = make_uint2(0u, 0u);
+    if (finite && mx) {
+      if (fast) {
+        w = kv8_codes8<FMT>(x[v], amax, rcp);
+      } else {
+        float f[8];
+        unpack_vec(x[v], f);
+        uint32_t c[2] = {0u, 0u};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k >> 2] |= kv8_code<FMT>(f[k], amax) << (8 * (k & 3));
+        w = make_uint2(c[0], c[1]);
+      }
+    }
+    *reinterpret_cast<uint2*>(codes + ((size_t)v * NT + threadIdx.x) * 8) = w;
+  }
+  if (threadIdx.x == 0) *scale = finite ? __fdiv_rn(amax, top) : __int_as_float(0x7fffffff);
+}
+
+struct AppendOut {
+  bf16 *kmin, *kmax;  // or null
+  float* mass;        // or null
+  const int32_t* ctx_len;
+  int32_t *ctx_out, *pos_out;
+  int Hkv, Cap, pshift;
+  int advance;  // this kernel writes ctx_out and pos_out
+};
+
+// Prompts and chunks: one CTA per (sequence, block touched, KV head, K or V), the
+// heads of a block next to each other (they share DRAM pages of the projection).
+// A complete block's vectors are read once, all loads in flight together, the
+// earlier tokens from the tail buffer; the CTA of a sequence's first block also
+// writes its newest, partial block to the tail, after its own reads of it.
+template <int FMT, int D, int VPT, int NT>
+__global__ void __launch_bounds__(NT)
+kv8_append_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int units) {
   pdl_wait_then_release();
-  const int u = blockIdx.x % units, x = blockIdx.x / units;
-  const int isv = x & 1, h = (x >> 1) % Hkv, b = (x >> 1) / Hkv;
-  const AppendSpan sp = append_span(nw, ctx_len, b, Cap);
+  constexpr int CPR = D / 8;
+  __shared__ uint32_t s_max[NT / 32];
+  const int heads = 2 * o.Hkv;
+  const int hv = blockIdx.x % heads, h = hv >> 1, isv = hv & 1, u = (blockIdx.x / heads) % units,
+            b = blockIdx.x / heads / units;
+  const AppendSpan sp = append_span(nw, o.ctx_len, b, o.Cap);
+  if (o.advance && u == 0 && hv == 0 && threadIdx.x == 0) {
+    o.ctx_out[b] = sp.start + sp.n;
+    if (o.pos_out) o.pos_out[b] = sp.n ? sp.start : -1;
+  }
   if (sp.n == 0) return;
   const int first = sp.start >> c.bshift, last = (sp.start + sp.n) >> c.bshift;  // `last`: the newest, partial block
   const int j = first + u;
-  const int row = b * Hkv + h;
+  const size_t row = (size_t)b * o.Hkv + h;
   const bf16* src = static_cast<const bf16*>(isv ? nw.v : nw.k) + b * (isv ? nw.vb : nw.kb) + h * (isv ? nw.vh : nw.kh);
   const int64_t st = isv ? nw.vt : nw.kt;
-  bf16* tail = static_cast<bf16*>(isv ? c.vt : c.kt) + (size_t)row * c.block * D;
-  const int cpr = D / 8, nvec = c.block * cpr;  // 16-byte vectors of a block
+  bf16* tail = static_cast<bf16*>(isv ? c.vt : c.kt) + row * c.block * D;
+  const int ch = ((int)threadIdx.x % CPR) * 8;
   if (j < last) {
-    auto vec = [&](int i) {
-      const int t = i / cpr, ch = (i % cpr) * 8, pos = (j << c.bshift) + t;
-      const bf16* p = pos < sp.start ? tail + (size_t)t * D + ch : src + (pos - sp.start) * st + ch;
-      return *reinterpret_cast<const uint4*>(p);
-    };
-    __shared__ uint32_t s_max[8];
-    uint32_t mx = 0;  // magnitudes as bit patterns: NaN above infinity above the numbers
-    for (int i = threadIdx.x; i < nvec; i += 256) {
-      const uint4 v = vec(i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint4 x[VPT];
+    const int from = (j << c.bshift) - sp.start;  // the block's first token, counted from the first new one
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+    for (int v = 0; v < VPT; ++v) {
+      const int t = v * (NT / CPR) + (int)threadIdx.x / CPR;
+      x[v] = *reinterpret_cast<const uint4*>(from + t < 0 ? tail + (size_t)t * D + ch : src + (from + t) * st + ch);
     }
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 8; ++k) mx = max(mx, s_max[k]);
-    const float amax = __uint_as_float(mx << 16);
-    const bool finite = mx < 0x7f80u;
-    const size_t blk = (size_t)row * (Cap >> c.bshift) + j;
-    uint8_t* codes = (isv ? c.vc : c.kc) + blk * c.block * D;
-    for (int i = threadIdx.x; i < nvec; i += 256) {
-      float x[8];
-      unpack_vec(vec(i), x);
-      uint32_t w[2] = {0u, 0u};
-      if (finite && mx)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) w[k >> 2] |= kv8_code<FMT>(x[k], amax) << (8 * (k & 3));
-      *reinterpret_cast<uint2*>(codes + (size_t)i * 8) = make_uint2(w[0], w[1]);
-    }
-    if (threadIdx.x == 0) {
-      (isv ? c.vs : c.ks)[blk] = finite ? __fdiv_rn(amax, kv8_top<FMT>()) : __int_as_float(0x7fffffff);
-      if (mass && !isv) mass[blk] = 0.f;
-    }
+    const size_t blk = row * (o.Cap >> c.bshift) + j;
+    quantise_held<FMT, VPT, NT>(x, (isv ? c.vc : c.kc) + blk * c.block * D, (isv ? c.vs : c.ks) + blk, s_max);
+    if (o.mass && !isv && threadIdx.x == 0) o.mass[blk] = 0.f;
+  }
+  if (o.kmin && !isv && j <= last) {
+    // the pages that begin in this block, and for the first block the one before: the new tokens
+    // are in the cache from the reads above
+    const int pages = (sp.start + sp.n - 1) >> o.pshift;  // the last page
+    const int p0 = u == 0 ? sp.start >> o.pshift : ((j << c.bshift) + (1 << o.pshift) - 1) >> o.pshift;
+    const int p1 = min(((j + 1) << c.bshift) + (1 << o.pshift) - 1, INT32_MAX) >> o.pshift;
+    append_pagemeta<NT>(src, st, o.kmin, o.kmax, row, o.Cap, D, o.pshift, sp, p0, min(p1, pages + 1));
   }
   if (u == 0) {
     __syncthreads();  // the block just quantised has read the tail
     const int t0 = last == first ? sp.start - (first << c.bshift) : 0;
     const int t1 = (sp.start + sp.n) - (last << c.bshift);
-    for (int i = threadIdx.x + t0 * cpr; i < t1 * cpr; i += 256) {
-      const int t = i / cpr, ch = (i % cpr) * 8, pos = (last << c.bshift) + t;
-      *reinterpret_cast<uint4*>(tail + (size_t)t * D + ch) =
-          *reinterpret_cast<const uint4*>(src + (pos - sp.start) * st + ch);
+    const int from = (last << c.bshift) - sp.start;
+#pragma unroll 4
+    for (int t = t0 + (int)threadIdx.x / CPR; t < t1; t += NT / CPR)
+      *reinterpret_cast<uint4*>(tail + (size_t)t * D + ch) = *reinterpret_cast<const uint4*>(src + (from + t) * st + ch);
+  }
+}
+
+// Single tokens: a cluster per sequence, its CTAs taking the KV heads in turn, so
+// that ctx_len may be advanced in place (rank 0 writes it when every CTA has read
+// it).  Half of a CTA's threads take K, half V.  Only a token that completes its
+// block reads the tail and quantises it.
+template <int FMT, int D>
+__global__ void __launch_bounds__(256)
+kv8_append_one_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int cluster) {
+  constexpr int CPR = D / 8, NT = 128;
+  __shared__ uint32_t s_max[2][NT / 32];
+  pdl_wait_then_release();
+  const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
+  const int isv = threadIdx.x / NT, tid = threadIdx.x % NT, ch = (tid % CPR) * 8;
+  const AppendSpan sp = append_span(nw, o.ctx_len, b, o.Cap);
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // ctx_len has been read
+  const int blk = sp.start >> c.bshift, slot = sp.start & (c.block - 1);
+  const bool done = slot == c.block - 1;
+  if (sp.n) {
+    for (int h = rank; h < o.Hkv; h += cluster) {
+      const size_t row = (size_t)b * o.Hkv + h;
+      const bf16* src = static_cast<const bf16*>(isv ? nw.v : nw.k) + b * (isv ? nw.vb : nw.kb) + h * (isv ? nw.vh : nw.kh);
+      bf16* tail = static_cast<bf16*>(isv ? c.vt : c.kt) + row * c.block * D;
+      if (!done) {
+        if (tid < CPR) *reinterpret_cast<uint4*>(tail + (size_t)slot * D + ch) = *reinterpret_cast<const uint4*>(src + ch);
+      } else {
+        const size_t at = row * (o.Cap >> c.bshift) + blk;
+        uint8_t* codes = (isv ? c.vc : c.kc) + at * c.block * D;
+        auto vec = [&](int t) {
+          return *reinterpret_cast<const uint4*>(t < slot ? tail + (size_t)t * D + ch : src + ch);
+        };
+        uint32_t m2 = 0;
+#pragma unroll 8
+        for (int t = tid / CPR; t < c.block; t += NT / CPR) m2 = __vmaxu2(m2, abs_max2(vec(t)));
+        uint32_t mx = __reduce_max_sync(0xffffffffu, max(m2 & 0xffffu, m2 >> 16));
+        __syncthreads();  // the head before has been read
+        if ((tid & 31) == 0) s_max[isv][tid >> 5] = mx;
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NT / 32; ++k) mx = max(mx, s_max[isv][k]);
+        const float amax = __uint_as_float(mx << 16);
+        const bool finite = mx < 0x7f80u;
+#pragma unroll 4
+        for (int t = tid / CPR; t < c.block; t += NT / CPR) {
+          float x[8];
+          unpack_vec(vec(t), x);
+          uint32_t w[2] = {0u, 0u};
+          if (finite && mx)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k >> 2] |= kv8_code<FMT>(x[k], amax) << (8 * (k & 3));
+          *reinterpret_cast<uint2*>(codes + (size_t)t * D + ch) = make_uint2(w[0], w[1]);
+        }
+        if (tid == 0) {
+          (isv ? c.vs : c.ks)[at] = finite ? __fdiv_rn(amax, kv8_top<FMT>()) : __int_as_float(0x7fffffff);
+          if (o.mass && !isv) o.mass[at] = 0.f;
+        }
+      }
+      // page min/max by the last warp of K's threads
+      if (o.kmin && !isv && tid >= NT - CPR) {
+        const int ch2 = (tid - (NT - CPR)) * 8;
+        const size_t at = (row * (o.Cap >> o.pshift) + (sp.start >> o.pshift)) * D + ch2;
+        const uint4 x = *reinterpret_cast<const uint4*>(src + ch2);
+        uint4 lo = x, hi = x;
+        if (sp.start & ((1 << o.pshift) - 1)) {
+          lo = *reinterpret_cast<const uint4*>(o.kmin + at);
+          hi = *reinterpret_cast<const uint4*>(o.kmax + at);
+          const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x);
+          __nv_bfloat162 *l2 = reinterpret_cast<__nv_bfloat162*>(&lo), *h2 = reinterpret_cast<__nv_bfloat162*>(&hi);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            l2[k] = __hmin2(l2[k], x2[k]);
+            h2[k] = __hmax2(h2[k], x2[k]);
+          }
+        }
+        *reinterpret_cast<uint4*>(o.kmin + at) = lo;
+        *reinterpret_cast<uint4*>(o.kmax + at) = hi;
+      }
     }
   }
-}
-
-// Page min/max of the new keys: one CTA per (page touched, KV head, sequence).
-__global__ void __launch_bounds__(128)
-kv8_pagemeta_kernel(const Kv8New nw, bf16* kmin, bf16* kmax, const int32_t* ctx_len, int Hkv, int Cap, int D,
-                    int pshift, int units) {
-  pdl_wait_then_release();
-  const int x = blockIdx.x / units, h = x % Hkv, b = x / Hkv;
-  const AppendSpan sp = append_span(nw, ctx_len, b, Cap);
-  const int pg = (sp.start >> pshift) + blockIdx.x % units;
-  if (sp.n == 0 || pg > (sp.start + sp.n - 1) >> pshift) return;
-  const int d = threadIdx.x;
-  if (d >= D) return;
-  const bf16* src = static_cast<const bf16*>(nw.k) + b * nw.kb + h * nw.kh + d;
-  const int p0 = max(pg << pshift, sp.start), p1 = min((pg + 1) << pshift, sp.start + sp.n);
-  const size_t at = ((size_t)(b * Hkv + h) * (Cap >> pshift) + pg) * D + d;
-  const bool going = (pg << pshift) < sp.start;
-  float lo = going ? to_f32(kmin[at]) : to_f32(src[(p0 - sp.start) * nw.kt]);
-  float hi = going ? to_f32(kmax[at]) : lo;
-  for (int p = p0; p < p1; ++p) {
-    const float x = to_f32(src[(p - sp.start) * nw.kt]);
-    lo = fminf(lo, x);
-    hi = fmaxf(hi, x);
+  if (cluster > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  else __syncthreads();
+  if (rank == 0 && threadIdx.x == 0) {
+    o.ctx_out[b] = sp.start + sp.n;
+    if (o.pos_out) o.pos_out[b] = sp.n ? sp.start : -1;
   }
-  kmin[at] = __float2bfloat16_rn(lo);
-  kmax[at] = __float2bfloat16_rn(hi);
 }
 
-__global__ void kv8_advance_kernel(const Kv8New nw, const int32_t* ctx_len, int32_t* ctx_out, int32_t* pos_out, int B,
-                                   int Cap) {
+__global__ void kv8_advance_kernel(const Kv8New nw, const AppendOut o, int B) {
   pdl_wait_then_release();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
-  const AppendSpan sp = append_span(nw, ctx_len, b, Cap);
-  ctx_out[b] = sp.start + sp.n;
-  if (pos_out) pos_out[b] = sp.n ? sp.start : -1;
+  const AppendSpan sp = append_span(nw, o.ctx_len, b, o.Cap);
+  o.ctx_out[b] = sp.start + sp.n;
+  if (o.pos_out) o.pos_out[b] = sp.n ? sp.start : -1;
+}
+
+template <int FMT, int D, int BLOCK>
+static cudaError_t append_chunk(const Kv8& c, const Kv8New& n, const AppendOut& o, int units, int B, cudaStream_t st) {
+  // a block's 16-byte vectors, at most eight a thread
+  constexpr int NV = BLOCK * D / 8, NT = NV / 8 > 128 ? NV / 8 : 128, VPT = NV / NT;
+  return launch_pdl(kv8_append_kernel<FMT, D, VPT, NT>, dim3((unsigned)units * 2 * o.Hkv * B), dim3(NT), 0, st, c, n, o,
+                    units);
+}
+
+template <int FMT, int D>
+static cudaError_t append_launch(const Kv8& c, const Kv8New& n, const AppendOut& o, int B, cudaStream_t st) {
+  if (n.max_new == 1) {
+    const int cl = std::min(o.Hkv, 8);
+    return launch_pdl_cluster(kv8_append_one_kernel<FMT, D>, dim3((unsigned)B * cl), dim3(256), 0, cl, st, c, n, o, cl);
+  }
+  const int units = (n.max_new >> c.bshift) + 2;
+  switch (c.block) {
+    case 16: return append_chunk<FMT, D, 16>(c, n, o, units, B, st);
+    case 32: return append_chunk<FMT, D, 32>(c, n, o, units, B, st);
+    case 64: return append_chunk<FMT, D, 64>(c, n, o, units, B, st);
+    case 128: return append_chunk<FMT, D, 128>(c, n, o, units, B, st);
+    default: return append_chunk<FMT, D, 256>(c, n, o, units, B, st);
+  }
 }
 
 cudaError_t launch_kv8_append(const Shape& s, const Kv8& c, const Kv8New& n, void* kmin, void* kmax, float* mass,
                               const int32_t* ctx_len, int32_t* ctx_out, int32_t* pos_out, cudaStream_t st) {
+  AppendOut o = {static_cast<bf16*>(kmin), static_cast<bf16*>(kmax), mass, ctx_len, ctx_out, pos_out, s.Hkv, s.Cap,
+                 s.pshift, 0};
+  // The lengths may be written by the CTAs that still read them only where they
+  // are other memory; in place a launch of its own follows a chunk's.
+  auto apart = [&](const int32_t* p) {
+    const uintptr_t x = (uintptr_t)p, y = (uintptr_t)ctx_len, n4 = (uintptr_t)s.B * 4;
+    return !p || x + n4 <= y || y + n4 <= x;
+  };
+  o.advance = apart(ctx_out) && apart(pos_out);
   cudaError_t e = cudaSuccess;
   if (n.max_new > 0) {
-    const int units = (n.max_new >> c.bshift) + 2, pages = (n.max_new >> s.pshift) + 2;
-    const dim3 grid((unsigned)units * 2 * s.Hkv * s.B);
-    e = c.format == kKv8Int8 ? launch_pdl(kv8_append_kernel<kKv8Int8>, grid, dim3(256), 0, st, c, n, mass, ctx_len,
-                                          s.Hkv, s.Cap, s.D, units)
-                             : launch_pdl(kv8_append_kernel<kKv8E4m3>, grid, dim3(256), 0, st, c, n, mass, ctx_len,
-                                          s.Hkv, s.Cap, s.D, units);
-    if (e == cudaSuccess && kmin)
-      e = launch_pdl(kv8_pagemeta_kernel, dim3((unsigned)pages * s.Hkv * s.B), dim3(128), 0, st, n,
-                     static_cast<bf16*>(kmin), static_cast<bf16*>(kmax), ctx_len, s.Hkv, s.Cap, s.D, s.pshift, pages);
+    if (c.format == kKv8Int8)
+      e = s.D == 64 ? append_launch<kKv8Int8, 64>(c, n, o, s.B, st) : append_launch<kKv8Int8, 128>(c, n, o, s.B, st);
+    else
+      e = s.D == 64 ? append_launch<kKv8E4m3, 64>(c, n, o, s.B, st) : append_launch<kKv8E4m3, 128>(c, n, o, s.B, st);
   }
-  if (e == cudaSuccess)
-    e = launch_pdl(kv8_advance_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, n, ctx_len, ctx_out, pos_out, s.B,
-                   s.Cap);
+  if (e == cudaSuccess && (n.max_new == 0 || (n.max_new > 1 && !o.advance)))
+    e = launch_pdl(kv8_advance_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, n, o, s.B);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- eviction
 
+constexpr int kChooseThreads = 256;
+constexpr int kChooseStaged = 4096;  // keys of a row kept in shared memory; longer rows read them again
+
+// Exclusive scan of one int per thread over the CTA.
+template <int NT>
+__device__ __forceinline__ int cta_scan(int v, int* tmp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    before += w < warp ? tmp[w] : 0;
+    total += tmp[w];
+  }
+  __syncthreads();
+  return before + x - v;
+}
+
 // The blocks row `row` keeps, one CTA per row: a forced block's key is the
-// largest, another's is its mass (order-preserving bits); the keep-th largest
-// key T comes from four 8-bit radix passes, keys above T are kept, and keys
-// equal to T from the lowest block up until the list is full.
-__global__ void __launch_bounds__(256)
-kv8_choose_kernel(const Kv8Evict e, int Hkv) {
+// largest, another's is its mass (order-preserving bits).  The keep-th largest
+// key T comes from four 8-bit radix passes over the keys in shared memory (the
+// bins are summed by a scan over the threads, a bin each); keys above T are
+// kept, and keys equal to T from the lowest block up until the list is full.  Bound
+// by the latency of its dozen barriers.
+__global__ void __launch_bounds__(kChooseThreads)
+kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
+  constexpr int NT = kChooseThreads;
+  __shared__ uint32_t s_key[kChooseStaged];
+  __shared__ int s_hist[256], s_tmp[NT / 32], s_bin, s_above;
   pdl_wait_then_release();
-  const int row = blockIdx.x, bsh = e.src.bshift;
-  const int nb = clamp_len(e.ctx_len[row / Hkv], e.cap) >> bsh;
+  const int row = blockIdx.x, bsh = e.src.bshift, tid = threadIdx.x;
+  const int N = clamp_len(e.ctx_len[row / Hkv], e.cap), nb = N >> bsh;
   int32_t* kept = e.kept + (size_t)row * e.keep;
   const float* mass = e.mass + (size_t)row * (e.cap >> bsh);
+  if (write_len && row % Hkv == 0 && tid == 0)
+    e.ctx_out[row / Hkv] = min(nb, e.keep) * e.src.block + (N & (e.src.block - 1));
   if (nb <= e.keep) {
-    for (int i = threadIdx.x; i < e.keep; i += 256) kept[i] = i < nb ? i : -1;
+    for (int i = tid; i < e.keep; i += NT) kept[i] = i < nb ? i : -1;
     return;
   }
-  auto key = [&](int i) -> uint32_t {
+  auto key_of = [&](int i) -> uint32_t {
     if (i < e.n_sink || i >= nb - e.n_recent) return 0xffffffffu;
     const float m = mass[i] + 0.f;  // -0 counts as 0
     return m != m ? 0xfffffffeu : min(float_key(m), 0xfffffffdu);
   };
-  __shared__ int s_hist[256];
-  __shared__ uint32_t s_prefix;
-  __shared__ int s_left, s_warp[8], s_warp_eq[8], s_base, s_base_eq;
-  if (threadIdx.x == 0) { s_prefix = 0; s_left = e.keep; }
+  const int staged = min(nb, kChooseStaged);
+#pragma unroll 4
+  for (int i = tid; i < staged; i += NT) s_key[i] = key_of(i);
+  auto key = [&](int i) { return i < kChooseStaged ? s_key[i] : key_of(i); };
+  uint32_t prefix = 0;
+  int left = e.keep;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[threadIdx.x] = 0;
+    s_hist[tid] = 0;
     __syncthreads();
-    const uint32_t prefix = s_prefix, mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-    for (int i = threadIdx.x; i < nb; i += 256) {
+    const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
+    for (int i = tid; i < nb; i += NT) {
       const uint32_t k = key(i);
       if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-      int left = s_left, d = 255;
-      while (d > 0 && s_hist[d] < left) left -= s_hist[d--];
-      s_left = left;
-      s_prefix = prefix | ((uint32_t)d << shift);
+    // thread i holds bin 255 - i; the bin in which the count from the top reaches `left`
+    const int n = s_hist[255 - tid];
+    int total;
+    const int above = cta_scan<NT>(n, s_tmp, total);
+    if (above < left && above + n >= left) {
+      s_bin = 255 - tid;
+      s_above = above;
     }
     __syncthreads();
+    left -= s_above;
+    prefix |= (uint32_t)s_bin << shift;
   }
-  const uint32_t T = s_prefix;
-  const int take_eq = s_left;  // keys equal to T that are kept
-  if (threadIdx.x == 0) { s_base = 0; s_base_eq = 0; }
-  __syncthreads();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i0 = 0; i0 < nb; i0 += 256) {
-    const int i = i0 + threadIdx.x;
+  // ascending output: `left` of the keys equal to T (= prefix) are kept
+  int base = 0, base_eq = 0;
+  for (int i0 = 0; i0 < nb; i0 += NT) {
+    const int i = i0 + tid;
     const uint32_t k = i < nb ? key(i) : 0u;
-    const bool eq = i < nb && k == T, gt = i < nb && k > T;
-    const uint32_t beq = __ballot_sync(0xffffffffu, eq), bgt = __ballot_sync(0xffffffffu, gt);
-    if (lane == 0) { s_warp_eq[warp] = __popc(beq); s_warp[warp] = __popc(bgt); }
-    __syncthreads();
-    int before = s_base, before_eq = s_base_eq;
-    for (int w = 0; w < warp; ++w) { before += s_warp[w]; before_eq += s_warp_eq[w]; }
-    const uint32_t lt = (1u << lane) - 1u;
-    before += __popc(bgt & lt);
-    before_eq += __popc(beq & lt);
-    if (gt || (eq && before_eq < take_eq)) kept[before + min(before_eq, take_eq)] = i;
-    __syncthreads();
-    if (threadIdx.x == 0)
-      for (int w = 0; w < 8; ++w) { s_base += s_warp[w]; s_base_eq += s_warp_eq[w]; }
-    __syncthreads();
+    const bool eq = i < nb && k == prefix, gt = i < nb && k > prefix;
+    int total;
+    const int at = cta_scan<NT>((int)gt | (int)eq << 16, s_tmp, total);  // at most NT of each: no carry
+    const int g = base + (at & 0xffff), q = base_eq + (at >> 16);
+    if (gt || (eq && q < left)) kept[g + min(q, left)] = i;
+    base += total & 0xffff;
+    base_eq += total >> 16;
   }
 }
 
-// Moves 16-byte columns [col0, col0 + cols) of one row's kept items of
-// `bytes` bytes each: item i of the destination is item kept[i] of the
-// source.  The CTA goes up the items and reads a round of them before it writes
-// any, so that in place nothing is overwritten before it has been read: item i
-// goes to i <= kept[i], and what later rounds read lies above what this one
-// writes.
-__device__ __forceinline__ void move_column(const uint8_t* src, uint8_t* dst, const int32_t* kept, int n, int bytes,
-                                            int col0, int cols) {
-  constexpr int U = 4;
-  const int total = n * cols;
-  for (int i0 = 0; i0 < total; i0 += 256 * U) {
-    uint4 v[U];
-    bool go[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 256 + threadIdx.x;
-      const int it = i / cols, cl = col0 + i % cols;
-      go[u] = i < total && (src != dst || kept[it] != it);
-      if (go[u]) v[u] = *reinterpret_cast<const uint4*>(src + (size_t)kept[it] * bytes + (size_t)cl * 16);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * 256 + threadIdx.x;
-      const int it = i / cols, cl = col0 + i % cols;
-      if (go[u]) *reinterpret_cast<uint4*>(dst + (size_t)it * bytes + (size_t)cl * 16) = v[u];
-    }
-    __syncthreads();
-  }
-}
-
-// Part x < 2 * slices of a row: a slice of the columns of K's or V's blocks;
-// then one CTA for the scales, sums, tails and the length, and one each for
-// kmin and kmax.
+// Into another cache: a CTA moves `per` kept blocks of a row, eight loads of a
+// thread in flight together; the row's first CTA also the tails.
+constexpr int kMoveBytes = 16384;  // of K (and as many of V) per CTA
 __global__ void __launch_bounds__(256)
+kv8_copy_kernel(const Kv8Evict e, int Hkv, int D, int P, int per, int parts) {
+  pdl_wait_then_release();
+  const int row = blockIdx.x / parts, part = blockIdx.x % parts, block = e.src.block, bsh = e.src.bshift;
+  const int N = clamp_len(e.ctx_len[row / Hkv], e.cap);
+  const int nb = N >> bsh, n = min(nb, e.keep), rest = N & (block - 1), tid = threadIdx.x;
+  const size_t srow = (size_t)row * (e.cap >> bsh), drow = (size_t)row * (e.dcap >> bsh);
+  const int32_t* kept = e.kept + (size_t)row * e.keep;
+  const int vecs = block * D / 16, vsh = __ffs(vecs) - 1;  // 16-byte vectors of a block's codes, a power of two
+  // items [i0, i1) of the list, `vecs` vectors each
+  const int i0 = part * per, i1 = min(n, i0 + per);
+  constexpr int U = 4;
+  for (int x0 = 0; x0 < (i1 - i0) * vecs; x0 += 256 * U) {
+    uint4 k[U], v[U];
+    size_t to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int x = x0 + u * 256 + tid;
+      if (x < (i1 - i0) * vecs) {
+        const int it = i0 + (x >> vsh), w = x & (vecs - 1);
+        const size_t from = (srow + kept[it]) * vecs + w;
+        to[u] = (drow + it) * vecs + w;
+        k[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.kc) + from);
+        v[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.vc) + from);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (x0 + u * 256 + tid < (i1 - i0) * vecs) {
+        reinterpret_cast<uint4*>(e.dst.kc)[to[u]] = k[u];
+        reinterpret_cast<uint4*>(e.dst.vc)[to[u]] = v[u];
+      }
+  }
+  for (int i = i0 + tid; i < i1; i += 256) {
+    const size_t from = srow + kept[i], to = drow + i;
+    e.dst.ks[to] = e.src.ks[from];
+    e.dst.vs[to] = e.src.vs[from];
+    if (e.mass_out) e.mass_out[to] = e.mass[from];
+  }
+  if (e.kmin) {
+    const int item = block / P * D / 8;  // 16-byte vectors of a block's page summaries
+    const uint4 *smin = static_cast<const uint4*>(e.kmin) + srow * item, *smax = static_cast<const uint4*>(e.kmax) + srow * item;
+    uint4 *dmin = static_cast<uint4*>(e.kmin_out) + drow * item, *dmax = static_cast<uint4*>(e.kmax_out) + drow * item;
+#pragma unroll 2
+    for (int x = tid; x < (i1 - i0) * item; x += 256) {
+      const int it = i0 + x / item, w = x % item;
+      const size_t from = (size_t)kept[it] * item + w, to = (size_t)it * item + w;
+      dmin[to] = smin[from];
+      dmax[to] = smax[from];
+    }
+    if (part == 0)  // the pages of the newest, partial block
+      for (int x = tid; x < (rest + P - 1) / P * D / 8; x += 256) {
+        dmin[(size_t)n * item + x] = smin[(size_t)nb * item + x];
+        dmax[(size_t)n * item + x] = smax[(size_t)nb * item + x];
+      }
+  }
+  if (part == 0) {
+    const size_t t0 = (size_t)row * block * D / 8;
+    for (int i = tid; i < rest * D / 8; i += 256) {
+      static_cast<uint4*>(e.dst.kt)[t0 + i] = static_cast<const uint4*>(e.src.kt)[t0 + i];
+      static_cast<uint4*>(e.dst.vt)[t0 + i] = static_cast<const uint4*>(e.src.vt)[t0 + i];
+    }
+  }
+}
+
+// In place: moves 16-byte columns [col0, col0 + cols) of one row's kept items of
+// `bytes` bytes each: item i becomes item kept[i].  The CTA goes up the items and
+// reads a round of them before it writes any, so that nothing is overwritten before
+// it has been read: item i goes to i <= kept[i], and what later rounds read lies
+// above what this one writes.
+constexpr int kMoveThreads = 512;
+__device__ __forceinline__ void move_column(uint8_t* base, const int32_t* kept, int n, int bytes, int col0, int cols) {
+  constexpr int U = 8, NT = kMoveThreads;
+  const int sh = __ffs(cols) - 1;  // a power of two, as blocks, pages and D are
+  const long long total = (long long)n << sh;
+  for (long long i0 = 0; i0 < total; i0 += NT * U) {
+    uint4 v[U];
+    int from[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long i = i0 + u * NT + threadIdx.x;
+      const int it = (int)(i >> sh), col = col0 + (int)(i & (cols - 1));
+      from[u] = i < total ? kept[it] : -1;
+      if (from[u] == it) from[u] = -1;  // in its place already
+      if (from[u] >= 0) v[u] = *reinterpret_cast<const uint4*>(base + (size_t)from[u] * bytes + col * 16);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long i = i0 + u * NT + threadIdx.x;
+      const int it = (int)(i >> sh), col = col0 + (int)(i & (cols - 1));
+      if (from[u] >= 0) *reinterpret_cast<uint4*>(base + (size_t)it * bytes + col * 16) = v[u];
+    }
+    __syncthreads();
+  }
+}
+
+// Part x < 2 slices of a row: a slice of the columns of K's or V's blocks; then
+// one CTA for the scales and sums, and one each for kmin and kmax.
+__global__ void __launch_bounds__(kMoveThreads)
 kv8_move_kernel(const Kv8Evict e, int Hkv, int D, int P, int slices, int parts) {
   pdl_wait_then_release();
-  const int row = blockIdx.x / parts, b = row / Hkv, block = e.src.block, bsh = e.src.bshift;
-  const int N = clamp_len(e.ctx_len[b], e.cap);
-  const int nb = N >> bsh, n = min(nb, e.keep), rest = N & (block - 1);
-  const int nsrc = e.cap >> bsh, ndst = e.dcap >> bsh;
+  const int row = blockIdx.x / parts, x = blockIdx.x % parts, block = e.src.block, bsh = e.src.bshift;
+  const int N = clamp_len(e.ctx_len[row / Hkv], e.cap);
+  const int nb = N >> bsh, rest = N & (block - 1);
+  if (nb <= e.keep) return;  // nothing moves
+  const int n = e.keep;
+  const size_t row0 = (size_t)row * (e.cap >> bsh);
   const int32_t* kept = e.kept + (size_t)row * e.keep;
-  const int x = blockIdx.x % parts;
   if (x < 2 * slices) {
-    const size_t bytes = (size_t)block * D;
-    const int cols = (int)(bytes / 16) / slices, col0 = (x >> 1) * cols;
-    const uint8_t* s = ((x & 1) ? e.src.vc : e.src.kc) + (size_t)row * nsrc * bytes;
-    uint8_t* d = ((x & 1) ? e.dst.vc : e.dst.kc) + (size_t)row * ndst * bytes;
-    move_column(s, d, kept, n, (int)bytes, col0, cols);
+    const int bytes = block * D, cols = bytes / 16 / slices;
+    move_column(((x & 1) ? e.src.vc : e.src.kc) + row0 * bytes, kept, n, bytes, (x >> 1) * cols, cols);
   } else if (x == 2 * slices) {
-    for (int i0 = 0; i0 < n; i0 += 256) {
+    float* const mass = e.mass_out;  // the caller's sums, which the choice has read
+    for (int i0 = 0; i0 < n; i0 += kMoveThreads) {
       const int i = i0 + threadIdx.x;
       float a = 0.f, v = 0.f, m = 0.f;
       if (i < n) {
-        const size_t at = (size_t)row * nsrc + kept[i];
+        const size_t at = row0 + kept[i];
         a = e.src.ks[at];
         v = e.src.vs[at];
-        m = e.mass[at];
+        m = mass[at];
       }
       __syncthreads();
       if (i < n) {
-        const size_t at = (size_t)row * ndst + i;
-        e.dst.ks[at] = a;
-        e.dst.vs[at] = v;
-        if (e.mass_out) e.mass_out[at] = m;
+        e.src.ks[row0 + i] = a;
+        e.src.vs[row0 + i] = v;
+        mass[row0 + i] = m;
       }
-    }
-    if (!e.in_place) {
-      const size_t t0 = (size_t)row * block * D;
-      for (int i = threadIdx.x; i < rest * D / 8; i += 256) {
-        reinterpret_cast<uint4*>(static_cast<bf16*>(e.dst.kt) + t0)[i] =
-            reinterpret_cast<const uint4*>(static_cast<const bf16*>(e.src.kt) + t0)[i];
-        reinterpret_cast<uint4*>(static_cast<bf16*>(e.dst.vt) + t0)[i] =
-            reinterpret_cast<const uint4*>(static_cast<const bf16*>(e.src.vt) + t0)[i];
-      }
+      __syncthreads();
     }
   } else {
-    const bool mx = x == 2 * slices + 2;
-    const int ppb = block / P;
-    const int item = ppb * D * 2;  // bytes of a block's page summaries
-    const uint8_t* s = static_cast<const uint8_t*>(mx ? e.kmax : e.kmin) + (size_t)row * nsrc * item;
-    uint8_t* d = static_cast<uint8_t*>(mx ? e.kmax_out : e.kmin_out) + (size_t)row * ndst * item;
-    move_column(s, d, kept, n, item, 0, item / 16);
-    // the pages of the newest, partial block
-    const int vecs = (rest + P - 1) / P * D * 2 / 16;
-    if (s + (size_t)nb * item != d + (size_t)n * item)
-      for (int i = threadIdx.x; i < vecs; i += 256)
-        reinterpret_cast<uint4*>(d + (size_t)n * item)[i] = reinterpret_cast<const uint4*>(s + (size_t)nb * item)[i];
+    const int item = block / P * D * 2;  // bytes of a block's page summaries
+    uint8_t* m = static_cast<uint8_t*>(x == 2 * slices + 1 ? e.kmin_out : e.kmax_out) + row0 * item;
+    move_column(m, kept, n, item, 0, item / 16);
+    // the pages of the newest, partial block (nb > n: no overlap)
+    for (int i = threadIdx.x; i < (rest + P - 1) / P * D * 2 / 16; i += kMoveThreads)
+      reinterpret_cast<uint4*>(m + (size_t)n * item)[i] = reinterpret_cast<const uint4*>(m + (size_t)nb * item)[i];
   }
 }
 
@@ -314,12 +609,26 @@ __global__ void kv8_evicted_len_kernel(const Kv8Evict e, int B) {
 
 cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st) {
   const int rows = s.B * s.Hkv;
-  cudaError_t r = launch_pdl(kv8_choose_kernel, dim3(rows), dim3(256), 0, st, e, s.Hkv);
+  // the lengths are written with the choice where they are other memory than
+  // the ones that are read, else last
+  const uintptr_t x = (uintptr_t)e.ctx_out, y = (uintptr_t)e.ctx_len, n4 = (uintptr_t)s.B * 4;
+  const bool apart = x + n4 <= y || y + n4 <= x;
+  cudaError_t r = launch_pdl(kv8_choose_kernel, dim3(rows), dim3(kChooseThreads), 0, st, e, s.Hkv, (int)apart);
   if (r != cudaSuccess) return r;
-  const int slices = 4, parts = 2 * slices + (e.kmin ? 3 : 1);
-  r = launch_pdl(kv8_move_kernel, dim3((unsigned)rows * parts), dim3(256), 0, st, e, s.Hkv, s.D, s.P, slices, parts);
-  if (r != cudaSuccess) return r;
-  r = launch_pdl(kv8_evicted_len_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, e, s.B);
+  const int bytes = e.src.block * s.D;
+  if (e.in_place) {
+    // enough CTAs for the GPU, each at least 64 bytes wide
+    int slices = 1;
+    while (rows * 2 * slices < 2 * sm_count() && bytes / 16 / (2 * slices) >= 4) slices *= 2;
+    const int parts = 2 * slices + (e.kmin ? 3 : 1);
+    r = launch_pdl(kv8_move_kernel, dim3((unsigned)rows * parts), dim3(kMoveThreads), 0, st, e, s.Hkv, s.D, s.P, slices,
+                   parts);
+  } else {
+    const int per = std::max(1, kMoveBytes / bytes), parts = (e.keep + per - 1) / per;
+    r = launch_pdl(kv8_copy_kernel, dim3((unsigned)rows * parts), dim3(256), 0, st, e, s.Hkv, s.D, s.P, per, parts);
+  }
+  if (r == cudaSuccess && !apart)
+    r = launch_pdl(kv8_evicted_len_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, e, s.B);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
 

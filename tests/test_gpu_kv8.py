@@ -144,6 +144,42 @@ def test_append_of_zero_infinite_nan_and_tiny_blocks(fmt):
     p.check()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_codes_of_every_magnitude_and_tie(fmt):
+    """Every ratio of two 8-bit significands, powers of two and ties among them, in blocks with largest values of all
+    significands: each code is that of exact arithmetic."""
+    blocks = []
+    for a in range(128, 256):
+        x = [float(a)] + [s * v * 2.0 ** -k for k in range(10) for v in range(128, 256, 1 + k) for s in (1, -1)]
+        x = [v for v in x if abs(v) <= a]
+        blocks.append((x + [0.0] * 1024)[:1024])
+    x = torch.tensor(blocks, dtype=torch.bfloat16).view(1, 128 * 16, 1, 64)
+    assert (x.double().view(128, 1024).abs().max(1).values == torch.arange(128, 256)).all()
+    desc = ops.make_desc(1, 1, 1, 64, 16, 128 * 16, torch.bfloat16)
+    cache = ops.Kv8Cache.empty(desc, fmt, 16)
+    ops.kv8_append(desc, cache, x.cuda(), (-x * 2.0 ** 60).cuda(), ints([0]))
+    for codes, scales, ref in ((cache.k_codes, cache.k_scales, x), (cache.v_codes, cache.v_scales, -x * 2.0 ** 60)):
+        codes, ref = codes.cpu().numpy().reshape(128, 16, 64), ref.double().numpy().reshape(128, 16, 64)
+        for j in range(128):
+            want, s = plain.quantise(ref[j], fmt)
+            assert (plain.value(codes[j], fmt) == plain.value(want, fmt)).all(), j
+            assert float(scales[0, 0, j]) == s
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_lengths_in_place_or_apart(in_place):
+    p = Pair(3, 1, 1, 64, 256, "int8", 16, seed=9)
+    x = bf16(np.random.default_rng(0), (3, 40, 2, 64)).cuda()
+    ctx = ints([0, 5, 240])
+    out = ctx if in_place else torch.full_like(ctx, -9)
+    pos = torch.full_like(ctx, -9)
+    got = ops.kv8_append(p.desc, p.cache, x[:, :, :1], x[:, :, 1:], ctx, new_len=ints([40, 0, 17]), ctx_out=out, pos_out=pos)
+    assert got is out and out.tolist() == [40, 5, 240] and pos.tolist() == [0, -1, -1]
+    none = x[:, :0]
+    ops.kv8_append(p.desc, p.cache, none[:, :, :1], none[:, :, 1:], out, pos_out=pos)  # no tokens at all
+    assert out.tolist() == [40, 5, 240] and pos.tolist() == [-1, -1, -1]
+
+
 # ---------------------------------------------------------------- attention
 
 def attention(p, q, pages=None, sink=None, mass_in=None, **kw):
