@@ -41,7 +41,7 @@ __device__ __forceinline__ void append_pagemeta(const bf16* src, int64_t st, bf1
     }
     __nv_bfloat162* l2 = reinterpret_cast<__nv_bfloat162*>(&lo);
     __nv_bfloat162* h2 = reinterpret_cast<__nv_bfloat162*>(&hi);
-#pragma unroll 4
+#pragma unroll 8
     for (int t = t0; t < t1; ++t) {
       const uint4 x = *reinterpret_cast<const uint4*>(src + t * st + ch);
       const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(&x);
@@ -56,51 +56,48 @@ __device__ __forceinline__ void append_pagemeta(const bf16* src, int64_t st, bf1
   }
 }
 
-// Codes of the eight bf16 values of a vector: rcp = top / amax once per block and
-// one multiplication each.  That product is within 2^-23 (relative) of the exact
-// quotient top x / amax, and the quotient of numbers of 8 significant bits is
-// either on a tie between two codes or at least 2^-13 (relative, e4m3) or
-// 1 / (510 2^k) (int8, x = 2^-k of amax: 64 times the product's error) away
-// from one: only products next to a tie, 1 vector in 30 or fewer, take the IEEE
-// division, so that every code is that of exact arithmetic (ties to even).
+// Codes of eight bf16 values by the IEEE division, one after the other: for blocks
+// of subnormals, out of line so that the others' code stays short.
 template <int FMT>
-__device__ __forceinline__ uint2 kv8_codes8(const uint4& raw, float amax, float rcp) {
-  float x[8];
-  unpack_vec(raw, x);
+__device__ __noinline__ uint2 kv8_codes8_exact(uint4 raw, float amax) {
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll 1
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t h = (k < 4 ? (k < 2 ? raw.x : raw.y) : (k < 6 ? raw.z : raw.w)) >> (16 * (k & 1)) << 16;
+    const uint32_t c = kv8_code<FMT>(__uint_as_float(h), amax) << (8 * (k & 3));
+    if (k < 4) w[0] |= c;
+    else w[1] |= c;
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// Codes of eight bf16 values from products with rcp = top / amax; a division per
+// value is three times the work, and a chunk's append is then bound by issue.  The
+// product is within 2^-23 (relative) of the quotient top x / amax of numbers of at
+// most 8 significant bits, which is either exactly on a tie between two codes or at
+// least 2^-16 (int8; e4m3 2^-13) away from one: the tie (2n + 1) a 2^k = 2 top x has
+// factors of at most 16 bits.  Rounded to 18 mantissa bits (within 2^-19), a product
+// next to a tie becomes the tie itself, whose rounding to even then is that of exact
+// arithmetic, and no other product crosses one.
+template <int FMT>
+__device__ __forceinline__ uint2 kv8_codes8(const uint4& raw, float rcp) {
+  float y[8];
+  unpack_vec(raw, y);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = __uint_as_float((__float_as_uint(y[k] * rcp) + 16u) & ~31u);
   uint32_t w[2];
-  bool near = false;
-  if constexpr (FMT == kKv8Int8) {
-    uint32_t c[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float y = x[k] * rcp, t = y + 12582912.f;  // 1.5 * 2^23: the nearest integer in the low bits
-      c[k] = __float_as_uint(t);
-      near |= fabsf(y - (t - 12582912.f)) > 0.5f - 1.f / 16384.f;
-    }
+  for (int k = 0; k < 2; ++k) {
+    if constexpr (FMT == kKv8Int8) {
+      uint32_t c[4];  // 1.5 * 2^23 brings the nearest integer into the low bits
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      w[k] = __byte_perm(__byte_perm(c[4 * k], c[4 * k + 1], 0x0040u), __byte_perm(c[4 * k + 2], c[4 * k + 3], 0x0040u),
-                         0x5410u);
-  } else {
-    float y[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      y[k] = x[k] * rcp;
-      const uint32_t u = __float_as_uint(y[k]);
-      // a tie has the 20 bits below e4m3's mantissa at 0x80000; subnormal codes are looked at one by one
-      near |= (u & 0xfffffu) - 0x7fff0u <= 0x20u || (fabsf(y[k]) < 0.015625f && y[k] != 0.f);
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
+      for (int u = 0; u < 4; ++u) c[u] = __float_as_uint(y[4 * k + u] + 12582912.f);
+      w[k] = __byte_perm(__byte_perm(c[0], c[1], 0x0040u), __byte_perm(c[2], c[3], 0x0040u), 0x5410u);
+    } else {
       const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k], y[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
       const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(y[4 * k + 2], y[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
       w[k] = a | b << 16;
     }
-  }
-  if (near) {
-    w[0] = w[1] = 0u;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[k >> 2] |= kv8_code<FMT>(x[k], amax) << (8 * (k & 3));
   }
   return make_uint2(w[0], w[1]);
 }
@@ -126,28 +123,15 @@ __device__ __forceinline__ void quantise_held(const uint4 (&x)[VPT], uint8_t* co
   for (int k = 0; k < NT / 32; ++k) mx = max(mx, s_max[k]);
   const float amax = __uint_as_float(mx << 16);
   const bool finite = mx < 0x7f80u;
-  const float top = kv8_top<FMT>();
-  // a block of subnormals would overflow the reciprocal: the division then
-  const float rcp = __fdiv_rn(top, amax);
-  const bool fast = rcp < 1e38f;
+  const float rcp = __fdiv_rn(kv8_top<FMT>(), amax);
+  const bool fast = rcp < 1e38f;  // a block of subnormals overflows the reciprocal
 #pragma unroll
   for (int v = 0; v < VPT; ++v) {
     uint2 w = make_uint2(0u, 0u);
-    if (finite && mx) {
-      if (fast) {
-        w = kv8_codes8<FMT>(x[v], amax, rcp);
-      } else {
-        float f[8];
-        unpack_vec(x[v], f);
-        uint32_t c[2] = {0u, 0u};
-#pragma unroll
-        for (int k = 0; k < 8; ++k) c[k >> 2] |= kv8_code<FMT>(f[k], amax) << (8 * (k & 3));
-        w = make_uint2(c[0], c[1]);
-      }
-    }
+    if (finite && mx) w = fast ? kv8_codes8<FMT>(x[v], rcp) : kv8_codes8_exact<FMT>(x[v], amax);
     *reinterpret_cast<uint2*>(codes + ((size_t)v * NT + threadIdx.x) * 8) = w;
   }
-  if (threadIdx.x == 0) *scale = finite ? __fdiv_rn(amax, top) : __int_as_float(0x7fffffff);
+  if (threadIdx.x == 0) *scale = finite ? __fdiv_rn(amax, kv8_top<FMT>()) : __int_as_float(0x7fffffff);
 }
 
 struct AppendOut {
