@@ -1,4 +1,5 @@
-"""Builds libsls.so in-tree from csrc/*.cu with nvcc for sm_103a.
+"""Builds libsls.so in-tree from csrc/*.cu with nvcc for sm_103a, and the tensor
+binding _binding.so from csrc/binding.cpp with g++ against the installed torch.
 
 Each translation unit compiles in its own nvcc process (in parallel); the
 objects are linked into ``sparse_long_context_gb300/libsls.so`` against the
@@ -20,6 +21,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsls.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
                 "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
@@ -30,6 +32,30 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libsls.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile the tensor binding (a CPython extension over torch's C++ tensors); returns its path."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = _newest([src, os.path.join(INCLUDE, "sls.h"), torch.__file__, __file__])
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > newest:
+        return BINDING
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [INCLUDE, os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    tmp = f"{BINDING}.{os.getpid()}.tmp"
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc), src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def _newest(paths):
@@ -59,8 +85,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=max(len(sources), 1)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, sources))
+        binding.result()
     if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
         cmd = [cc, *ARCH, "-shared", "-cudart=static", "-o", LIB + ".tmp", *objs]
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -358,22 +358,18 @@ def selection_recall(desc: L.AttnDesc, q, k_cache, page_idx, ctx_len, count=None
 
 # ------------------------------------------------- per-head norm and rotation
 
-def _local(t: torch.Tensor, name: str, dtype, shape, strided: bool = False) -> int:
-    """Address of a tensor of the current device (whose stream the call goes to); strided: only the last dimension
-    must be contiguous."""
-    dev = t.get_device()  # -1 on the host
-    if t.dtype is dtype and t.shape == shape and dev >= 0 and dev == torch._C._cuda_getDevice() and (
-            t.is_contiguous() if not strided else t.stride(-1) == 1):
-        return t.data_ptr()
-    if not t.is_cuda or dev != torch.cuda.current_device():
-        raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.numel():
-        raise ValueError(f"{name} must have contiguous channels" if strided else f"{name} must be contiguous")
-    return t.data_ptr()
+_fast = None
+
+
+def _binding():
+    """The tensor binding of the calls below (csrc/binding.cpp), bound to the loaded library."""
+    global _fast
+    if _fast is None:
+        L.load()
+        from . import _binding as fast  # raises when it has not been built
+        fast.bind(L.LIB_PATH)
+        _fast = fast
+    return _fast
 
 
 def make_rope(num_q_heads: int, num_kv_heads: int, head_dim: int, dtype, rotary_dim: Optional[int] = None,
@@ -398,25 +394,14 @@ def qk_norm_rope(rope: L.RopeDesc, q, k, positions, q_weight=None, k_weight=None
     q [N, Hq, D] and k [N, Hkv, D] may be strided views of one projection's output; positions [N] int32, negative
     ones skipped.  The outputs default to new contiguous tensors and may be q and k themselves.  A side with no
     heads is passed as None.  Returns (q_out, k_out)."""
-    n, d = int(positions.shape[0]), rope.head_dim
-    dtype = torch.float32 if rope.dtype == L.SLS_DTYPE_F32 else torch.bfloat16
-    pos = _local(positions, "positions", torch.int32, (n,))
-
-    def side(name, heads, x, w, out):
-        if heads == 0:
-            return None, (None, 0, 0), None, (None, 0, 0)
-        shape = (n, heads, d)
-        if out is None:
-            out = torch.empty(shape, dtype=dtype, device=x.device)
-        xs, os = x.stride(), out.stride()
-        return (out, (_local(x, name, dtype, shape, True), xs[0], xs[1]),
-                None if w is None else _local(w, name + "_weight", dtype, (d,)),
-                (_local(out, name + "_out", dtype, shape, True), os[0], os[1]))
-
-    q_out, qi, wq, qo = side("q", rope.num_q_heads, q, q_weight, q_out)
-    k_out, ki, wk, ko = side("k", rope.num_kv_heads, k, k_weight, k_out)
-    L.call("sls_qk_norm_rope", ctypes.byref(rope), n, *qi, *ki, wq, wk, pos, *qo, *ko, _stream())
-    return q_out, k_out
+    if rope.num_q_heads and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if rope.num_kv_heads and k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    status = (_fast or _binding()).qk_norm_rope(rope, q, k, positions, q_weight, k_weight, q_out, k_out)
+    if status:
+        L.check("sls_qk_norm_rope", status)
+    return q_out if rope.num_q_heads else None, k_out if rope.num_kv_heads else None
 
 
 # -------------------------------------------------------------- 8-bit KV cache
@@ -437,17 +422,19 @@ class Kv8Cache:
         if block < 1 or Cap % block:
             raise ValueError(f"block {block} must divide the capacity {Cap}")
         for t, name in ((k_codes, "k_codes"), (v_codes, "v_codes")):
-            _local(t, name, torch.uint8, (B, H, Cap, D))
+            _need(t, name, torch.uint8, (B, H, Cap, D))
         for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
-            _local(t, name, torch.float32, (B, H, Cap // block))
+            _need(t, name, torch.float32, (B, H, Cap // block))
         for t, name in ((k_tail, "k_tail"), (v_tail, "v_tail")):
-            _local(t, name, torch.bfloat16, (B, H, block, D))
+            _need(t, name, torch.bfloat16, (B, H, block, D))
+        self.index = k_codes.get_device()
+        if any(t.get_device() != self.index for t in (v_codes, k_scales, v_scales, k_tail, v_tail)):
+            raise ValueError("the cache's tensors must be on one device")
         self.fmt, self.block = fmt, block
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.k_tail, self.v_tail = k_tail, v_tail
         self.c = L.Kv8CacheDesc(_KV8_FORMATS[fmt], block, *(t.data_ptr() for t in (
             k_codes, v_codes, k_scales, v_scales, k_tail, v_tail)))
-        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, desc: L.AttnDesc, fmt: str = "int8", block: int = 64, device="cuda") -> "Kv8Cache":
@@ -457,6 +444,12 @@ class Kv8Cache:
         return cls(desc, fmt, block, new((B, H, Cap, D), torch.uint8), new((B, H, Cap, D), torch.uint8),
                    new((B, H, Cap // block), torch.float32), new((B, H, Cap // block), torch.float32),
                    new((B, H, block, D), torch.bfloat16), new((B, H, block, D), torch.bfloat16))
+
+    def _beside(self, t: torch.Tensor) -> L.Kv8CacheDesc:
+        """The C structure, for a call on t's device."""
+        if t.get_device() != self.index:
+            raise ValueError("the cache must be on the device of the other tensors")
+        return self.c
 
     def values(self):
         """The complete blocks' K and V as fp32 [B, H, Cap, D] (codes times scales; for inspection)."""
@@ -473,27 +466,10 @@ def kv8_append(desc: L.AttnDesc, cache: Kv8Cache, k_new, v_new, ctx_len, new_len
     """Appends the first new_len[b] (None: all) tokens of k_new, v_new [B, T, Hkv, D] to every sequence
     (sls_kv8_append): complete blocks are quantised, the rest waits in the tail.  ctx_out defaults to ctx_len
     (advanced in place).  The new tensors may be strided views with contiguous channels."""
-    B, H, D = desc.batch, desc.num_kv_heads, desc.head_dim
-    if k_new.dim() != 4:
-        raise ValueError(f"k_new must be [B, T, Hkv, D], got {tuple(k_new.shape)}")
-    T = k_new.shape[1]
-    shape = (B, T, H, D)
-    kp = _local(k_new, "k_new", torch.bfloat16, shape, True)
-    vp = _local(v_new, "v_new", torch.bfloat16, shape, True)
-    ctx = _local(ctx_len, "ctx_len", torch.int32, (B,))
-    to = ctx if ctx_out is None else _local(ctx_out, "ctx_out", torch.int32, (B,))
-    n = None if new_len is None else _local(new_len, "new_len", torch.int32, (B,))
-    at = None if pos_out is None else _local(pos_out, "pos_out", torch.int32, (B,))
-    lo = hi = None
-    if kmin is not None or kmax is not None:
-        if kmin is None or kmax is None:
-            raise ValueError("kmin and kmax: both or neither")
-        meta = (B, H, desc.capacity // desc.page_size, D)
-        lo, hi = _local(kmin, "kmin", torch.bfloat16, meta), _local(kmax, "kmax", torch.bfloat16, meta)
-    sums = None if mass is None else _local(mass, "mass", torch.float32, (B, H, desc.capacity // cache.block))
-    ks, vs = k_new.stride(), v_new.stride()
-    L.call("sls_kv8_append", ctypes.byref(desc), cache.ref, kp, ks[0], ks[1], ks[2], vp, vs[0], vs[1], vs[2], T, n, lo,
-           hi, sums, ctx, to, at, _stream())
+    status = (_fast or _binding()).kv8_append(desc, cache._beside(k_new), k_new, v_new, ctx_len, new_len, kmin, kmax,
+                                              mass, ctx_out, pos_out)
+    if status:
+        L.check("sls_kv8_append", status)
     return ctx_len if ctx_out is None else ctx_out
 
 
@@ -509,35 +485,16 @@ def kv8_decode_attend(desc: L.AttnDesc, cache: Kv8Cache, q, ctx_len, page_idx=No
     """Decode attention over an 8-bit cache (sls_kv8_decode_attend): dense, or over page lists [rows, stride].
     mass_out, if given, receives every complete block's summed softmax weight added to mass_in.  Returns
     (out, lse)."""
-    B, Hq, D = desc.batch, desc.num_q_heads, desc.head_dim
-    shape = (B, Hq, D)
-    qp = _local(q, "q", torch.bfloat16, shape)
-    ctx = _local(ctx_len, "ctx_len", torch.int32, (B,))
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-    op = _local(out, "out", torch.bfloat16, shape)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
     if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    lp = None if lse is None else _local(lse, "lse", torch.float32, (B, Hq))
-    sk = None if sink is None else _local(sink, "sink", torch.float32, (Hq,))
-    pages = cnt = None
-    stride = kf = 0
-    if page_idx is not None:
-        rows = B * desc.num_kv_heads
-        stride = page_idx.shape[-1]
-        kf = stride if k_fixed is None else int(k_fixed)
-        pages = _local(page_idx, "page_idx", torch.int32, (rows, stride))
-        cnt = None if count is None else _local(count, "count", torch.int32, (rows,))
-    mi = mo = None
-    if mass_out is not None or mass_in is not None:
-        sums = (B, desc.num_kv_heads, desc.capacity // cache.block)
-        mi = None if mass_in is None else _local(mass_in, "mass_in", torch.float32, sums)
-        mo = None if mass_out is None else _local(mass_out, "mass_out", torch.float32, sums)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = kv8_attend_workspace(desc, cache, mass_out is not None, q.device)
-    ws = _local(workspace, "workspace", torch.uint8, workspace.shape)
-    L.call("sls_kv8_decode_attend", ctypes.byref(desc), cache.ref, qp, pages, stride, cnt, kf, ctx, sk, op, lp, mi, mo,
-           ws, workspace.numel(), _stream())
+    status = (_fast or _binding()).kv8_decode_attend(desc, cache._beside(q), q, ctx_len, page_idx, count, k_fixed, sink,
+                                                     mass_in, mass_out, out, lse, workspace)
+    if status:
+        L.check("sls_kv8_decode_attend", status)
     return out, lse
 
 
@@ -547,31 +504,29 @@ def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sin
     """Keeps at most `keep` complete blocks of every row by accumulated attention weight (sls_kv8_evict), in place
     (dst None) or into another cache of dst_desc's capacity.  The outputs default to the inputs' buffers in place,
     and ctx_out to ctx_len in place only.  Returns (ctx_out, kept_idx)."""
-    B, H, D, P = desc.batch, desc.num_kv_heads, desc.head_dim, desc.page_size
     if (dst is None) != (dst_desc is None):
         raise ValueError("dst and dst_desc: both or neither")
-    cap, dcap = desc.capacity, desc.capacity if dst is None else dst_desc.capacity
     if dst is None:
+        dcap, to = desc.capacity, None
         mass_out = mass if mass_out is None else mass_out
         kmin_out = kmin if kmin_out is None else kmin_out
         kmax_out = kmax if kmax_out is None else kmax_out
         ctx_out = ctx_len if ctx_out is None else ctx_out
     else:
+        dcap, to = dst_desc.capacity, dst._beside(ctx_len)
         if (dst_desc.batch, dst_desc.num_kv_heads, dst_desc.head_dim, dst_desc.page_size, dst_desc.dtype) != (
-                B, H, D, P, desc.dtype):
+                desc.batch, desc.num_kv_heads, desc.head_dim, desc.page_size, desc.dtype):
             raise ValueError("dst_desc must describe the same rows and pages as desc")
         if ctx_out is None:
             ctx_out = torch.empty_like(ctx_len)
     if kept_idx is None:
-        kept_idx = torch.empty((B * H, keep), dtype=torch.int32, device=ctx_len.device)
-    kept = _local(kept_idx, "kept_idx", torch.int32, (B * H, keep))
-    ctx, to = _local(ctx_len, "ctx_len", torch.int32, (B,)), _local(ctx_out, "ctx_out", torch.int32, (B,))
-    mi = _local(mass, "mass", torch.float32, (B, H, cap // cache.block))
-    mo = None if mass_out is None else _local(mass_out, "mass_out", torch.float32, (B, H, dcap // cache.block))
-    meta = [None if t is None else _local(t, name, torch.bfloat16, (B, H, c // P, D)) for t, name, c in (
-        (kmin, "kmin", cap), (kmax, "kmax", cap), (kmin_out, "kmin_out", dcap), (kmax_out, "kmax_out", dcap))]
-    L.call("sls_kv8_evict", ctypes.byref(desc), cache.ref, dcap, None if dst is None else dst.ref, int(keep),
-           int(n_sink_blocks), int(n_recent_blocks), mi, mo, *meta, kept, ctx, to, _stream())
+        kept_idx = torch.empty((desc.batch * desc.num_kv_heads, max(int(keep), 0)), dtype=torch.int32,
+                               device=ctx_len.device)
+    status = (_fast or _binding()).kv8_evict(desc, cache._beside(ctx_len), dcap, to, keep, n_sink_blocks,
+                                             n_recent_blocks, mass, mass_out, kmin, kmax, kmin_out, kmax_out, kept_idx,
+                                             ctx_len, ctx_out)
+    if status:
+        L.check("sls_kv8_evict", status)
     return ctx_out, kept_idx
 
 
