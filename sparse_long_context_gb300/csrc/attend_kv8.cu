@@ -62,7 +62,8 @@ struct Kv8Attend {
   float* lse;
   int32_t* tickets;     // [rows] arrival counters, zero between calls
   float *po, *pm, *pl;  // [slot][G][D], [slot][G] partials, two slots per CTA, max in base-2 units
-  float2* grp;          // [rows, G, Cap/16] weight sums of 16-token groups and the max they are relative to
+  float2* grp;          // [rows, G, Cap >> gshift] weight sums of 2^gshift tokens and the max they are relative to
+  int gshift;           // a unit's tokens, or a block's where blocks are smaller
   float2* fin;          // [B, Hq] final max (base 2) and 1 / sum
   const float* mass_in;
   float* mass_out;
@@ -597,6 +598,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         }
         if (any) {
           const float mref = softmax_step(gm);
+          [[maybe_unused]] float entry = 0.f;
 #pragma unroll
           for (int s = 0; s < SG; ++s) {
             if (at[s] < 0) continue;
@@ -608,10 +610,15 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
             const uint32_t p1 = kv8_h2(__floats2half2_rn(x[s][2] * vs[s], x[s][3] * vs[s]));
             kv8_pv<D, FMT>(stage + (SG + s) * L::GROUP, o, p0, p1, lane);
             if constexpr (MASS) {
-              float ps = psum;
-              ps += __shfl_xor_sync(0xffffffffu, ps, 1);
-              ps += __shfl_xor_sync(0xffffffffu, ps, 2);
-              if (m == 0 && r < G) a.grp[((size_t)row * G + r) * (a.Cap >> 4) + (at[s] >> 4)] = make_float2(ps, mref);
+              // groups that share an entry add up to the entry's last one
+              entry += psum;
+              if (((at[s] + 16) & ((1 << a.gshift) - 1)) == 0) {
+                entry += __shfl_xor_sync(0xffffffffu, entry, 1);
+                entry += __shfl_xor_sync(0xffffffffu, entry, 2);
+                if (m == 0 && r < G)
+                  a.grp[((size_t)row * G + r) * (a.Cap >> a.gshift) + (at[s] >> a.gshift)] = make_float2(entry, mref);
+                entry = 0.f;
+              }
             }
           }
         }
@@ -821,13 +828,14 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   }
 }
 
-// mass_out = mass_in + the blocks' weight sums: a lane per 16-token group
-// (coalesced loads of each head's sums), the groups of a block added by shuffles.
+// mass_out = mass_in + the blocks' weight sums: a lane per entry of each head's
+// sums (coalesced loads, all heads' in flight together), the entries of a block
+// added by shuffles in a fixed order.
 __global__ void __launch_bounds__(256)
 kv8_mass_kernel(const Kv8Attend a, int per_row) {
   pdl_wait_then_release();
-  const int row = blockIdx.x / per_row, g16 = (blockIdx.x % per_row) * 256 + threadIdx.x;
-  const int gshift = a.c.bshift - 4, blk = g16 >> gshift;
+  const int row = blockIdx.x / per_row, at = (blockIdx.x % per_row) * 256 + threadIdx.x;
+  const int eshift = a.c.bshift - a.gshift, blk = at >> eshift;  // 2^eshift <= 16 entries per block
   const bool live = blk < clamp_len(a.ctx_len[row / a.Hkv], a.Cap) >> a.c.bshift;
   float sum = 0.f;
   if (live) {
@@ -835,17 +843,17 @@ kv8_mass_kernel(const Kv8Attend a, int per_row) {
 #pragma unroll
     for (int g = 0; g < 8; ++g)
       if (g < a.G) {
-        x[g] = __ldcg(a.grp + ((size_t)row * a.G + g) * (a.Cap >> 4) + g16);
+        x[g] = __ldcg(a.grp + ((size_t)row * a.G + g) * (a.Cap >> a.gshift) + at);
         f[g] = a.fin[(size_t)row * a.G + g];
       }
 #pragma unroll
     for (int g = 0; g < 8; ++g)
       if (g < a.G) sum += x[g].x * exp2f(x[g].y - f[g].x) * f[g].y;
   }
-  for (int o = 1; o < (1 << gshift); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (live && (g16 & ((1 << gshift) - 1)) == 0) {
-    const size_t at = (size_t)row * (a.Cap >> a.c.bshift) + blk;
-    a.mass_out[at] = (a.mass_in ? a.mass_in[at] : 0.f) + sum;
+  for (int o = 1; o < (1 << eshift); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (live && (at & ((1 << eshift) - 1)) == 0) {
+    const size_t b = (size_t)row * (a.Cap >> a.c.bshift) + blk;
+    a.mass_out[b] = (a.mass_in ? a.mass_in[b] : 0.f) + sum;
   }
 }
 
@@ -877,26 +885,6 @@ static bool kv8_map(CUtensorMap* map, const void* base, uint64_t rows, int D, in
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool kv8_attend_supported(const Shape& s) {
-  return s.dtype == 1 && s.B * (long long)s.Hkv <= kKv8MaxRows && (long long)s.B * s.Hkv * s.Cap < (1ll << 31);
-}
-
-static int kv8_grid() { return std::min(sm_count() * kKv8PerSm, kKv8MaxGrid); }
-static size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
-
-size_t kv8_attend_workspace(const Shape& s, const Kv8&, bool with_mass) {
-  const size_t rows = (size_t)s.B * s.Hkv, slots = 2 * (size_t)kv8_grid();
-  return a256(rows * 4) + a256(slots * s.G * s.D * 4) + 2 * a256(slots * s.G * 4) +
-         (with_mass ? a256(rows * s.G * 8) + a256(rows * s.G * (s.Cap >> 4) * 8) : 0);
-}
-
-// What a launch of one kernel needs once per device: the limit of its dynamic
-// shared memory raised, and the number of clusters of each size that fit.
-struct Kv8Device {
-  std::atomic<int> clusters[kKv8MaxCluster + 1];  // 0: not asked yet, else 1 + the number
-  std::atomic<bool> raised;
-};
-
 // Twelve warps (at most 170 registers a thread) whose rings of two 32-token
 // units fill the shared memory: 8, 10, 14 and 16 warps and units of 16 tokens
 // were slower.  At D = 64 int8 units of 64 tokens (half the softmax steps)
@@ -906,6 +894,34 @@ struct Kv8Config {
   static constexpr int SG = D == 64 && FMT == kKv8Int8 ? 4 : 2, W = 12, S = D == 128 || SG == 4 ? 2 : 4;
   using L = Kv8Layout<D, SG, W, S>;
   static constexpr size_t smem(int rows) { return L::REGION + (size_t)(rows + 1) * sizeof(int) + 1024; }
+};
+
+bool kv8_attend_supported(const Shape& s) {
+  return s.dtype == 1 && s.B * (long long)s.Hkv <= kKv8MaxRows && (long long)s.B * s.Hkv * s.Cap < (1ll << 31);
+}
+
+static int kv8_grid() { return std::min(sm_count() * kKv8PerSm, kKv8MaxGrid); }
+static size_t a256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// log2 of the tokens of one entry of the weight sums (a unit of the kernel that runs,
+// or a block if that is smaller).
+static int kv8_entry_shift(const Shape& s, const Kv8& c) {
+  const int unit = 16 * (s.D == 128 ? (c.format == kKv8Int8 ? Kv8Config<128, kKv8Int8>::SG : Kv8Config<128, kKv8E4m3>::SG)
+                                    : (c.format == kKv8Int8 ? Kv8Config<64, kKv8Int8>::SG : Kv8Config<64, kKv8E4m3>::SG));
+  return __builtin_ctz((unsigned)std::min(unit, c.block));
+}
+
+size_t kv8_attend_workspace(const Shape& s, const Kv8& c, bool with_mass) {
+  const size_t rows = (size_t)s.B * s.Hkv, slots = 2 * (size_t)kv8_grid();
+  return a256(rows * 4) + a256(slots * s.G * s.D * 4) + 2 * a256(slots * s.G * 4) +
+         (with_mass ? a256(rows * s.G * 8) + a256(rows * s.G * (s.Cap >> kv8_entry_shift(s, c)) * 8) : 0);
+}
+
+// What a launch of one kernel needs once per device: the limit of its dynamic
+// shared memory raised, and the number of clusters of each size that fit.
+struct Kv8Device {
+  std::atomic<int> clusters[kKv8MaxCluster + 1];  // 0: not asked yet, else 1 + the number
+  std::atomic<bool> raised;
 };
 
 template <int D, int FMT, bool LIST, bool MASS, bool CL>
@@ -1026,13 +1042,14 @@ cudaError_t launch_kv8_attend(const Shape& s, const Kv8& c, const void* q, const
   a.pl = reinterpret_cast<float*>(take(slots * s.G * 4));
   if (mass_out) {
     a.fin = reinterpret_cast<float2*>(take(rows * s.G * 8));
-    a.grp = reinterpret_cast<float2*>(take(rows * s.G * (s.Cap >> 4) * 8));
+    a.gshift = kv8_entry_shift(s, c);
+    a.grp = reinterpret_cast<float2*>(take(rows * s.G * (s.Cap >> a.gshift) * 8));
     a.mass_in = mass_in;
     a.mass_out = mass_out;
   }
   cudaError_t e = s.D == 64 ? kv8_dispatch<64>(a, st) : kv8_dispatch<128>(a, st);
   if (e == cudaSuccess && mass_out) {
-    const int per_row = ((s.Cap >> 4) + 255) / 256;
+    const int per_row = ((s.Cap >> a.gshift) + 255) / 256;
     e = launch_pdl(kv8_mass_kernel, dim3((unsigned)a.rows * per_row), dim3(256), 0, st, a, per_row);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
