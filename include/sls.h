@@ -576,7 +576,7 @@ sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens,
  *   codes 0; an infinity or NaN in the block gives s = NaN and codes 0, so
  *   that it shows in every output that attends to the block.
  *   format    SLS_KV8_INT8 or SLS_KV8_E4M3
- *   block     power of two in [16, 256], Cap % block == 0
+ *   block     power of two in [16, 256], Cap % block == 0, Cap <= 2^30
  *   k_codes, v_codes    [B, Hkv, Cap, D] one byte each
  *   k_scales, v_scales  [B, Hkv, Cap/block] float
  *   k_tail, v_tail      [B, Hkv, block, D] bf16
@@ -609,10 +609,10 @@ typedef struct sls_kv8_cache {
  *                 NULL
  *   mass          [B, Hkv, Cap/block] float: set to 0 for every block that
  *                 becomes complete, or NULL
- *   ctx_len       [B] int32 (read); ctx_out [B] int32 (written; may be
- *                 ctx_len itself)
+ *   ctx_len       [B] int32 (read, clamped to [0, Cap]); ctx_out [B] int32
+ *                 (written; ctx_len itself or memory of its own)
  *   pos_out       [B] int32 receiving the first written position (-1 when
- *                 nothing was written), or NULL
+ *                 nothing was written), or NULL; memory of its own
  * max_new 0 appends nothing (ctx_out and pos_out are still written).
  */
 sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
@@ -638,13 +638,14 @@ size_t sls_kv8_decode_attend_workspace_size(const sls_attn_desc* desc, const sls
  *   page_idx, idx_stride, count, k_fixed   as in sls_sparse_decode_attend
  *             (-1 entries are skipped, bad ones counted for
  *             sls_pipeline_check and skipped)
- *   sink      [Hq] float or NULL;  out [B, Hq, D] bf16;  lse [B, Hq] float
- *             or NULL
+ *   sink      [Hq] float or NULL;  out [B, Hq, D] bf16 (not q's memory);
+ *             lse [B, Hq] float or NULL
  *   mass_in, mass_out  [B, Hkv, Cap/block] float, or mass_out NULL: every
  *             complete block of the context gets mass_out = mass_in (NULL: 0)
  *             + the sum over the group's query heads and the block's tokens
  *             of the softmax weight; the other blocks' entries are left as
- *             they were.  mass_in may be mass_out.  Only without page_idx.
+ *             they were.  mass_in may be mass_out itself.  Only without
+ *             page_idx.
  *             The sums do not depend on the order in which CTAs finish.
  *   workspace >= sls_kv8_decode_attend_workspace_size() bytes, 16-byte
  *             aligned, zero-filled before its first use (every call leaves
@@ -682,7 +683,8 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
  *                 buffers); needs P <= block and P dividing dst_capacity
  *   kept_idx      [B*Hkv, keep] int32 (written): the kept blocks' old
  *                 numbers, ascending, -1 padded when the row has fewer
- *   ctx_len [B] (read), ctx_out [B] (written; may be ctx_len itself)
+ *   ctx_len [B] (read), ctx_out [B] (written; ctx_len itself or memory of
+ *             its own)
  */
 sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, int32_t dst_capacity,
                          const sls_kv8_cache* dst, int32_t keep, int32_t n_sink_blocks,
@@ -737,7 +739,8 @@ typedef struct sls_stats {
   uint64_t attend_stream_k;           /* stream-K attends over block lists with bf16 keys */
   uint64_t attend_refined;            /* ... with the refined (2-bit + 8-bit) keys */
   uint64_t combine;                   /* separate combine launches */
-  uint64_t metadata;                  /* page min/max, thumbnail, residual and append launches */
+  uint64_t metadata;                  /* page min/max, thumbnail, residual and append calls, and those of
+                                         the norm/rotation and the 8-bit cache's append and eviction */
   uint64_t recall;                    /* selection-recall launches */
   uint64_t select_rows_all_keys;      /* rows wider than 8192 pages whose sls_select_pages top-k
                                          ranked all of the row's keys (the candidate check failed) */

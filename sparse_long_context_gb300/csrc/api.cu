@@ -585,10 +585,10 @@ sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens, const
     if (!in || !out) return fail(SLS_EINVAL, "%s or its output is NULL", name);
     if (((uintptr_t)in | (uintptr_t)out | (uintptr_t)w) & 15)
       return fail(SLS_EINVAL, "%s, its weight and its output must be 16-byte aligned", name);
-    const int64_t lim = int64_t(1) << 40;
+    const int64_t lim = INT32_MAX;  // tokens * stride stays within 62 bits
     if (it < 0 || ih < 0 || ot < 0 || oh < 0 || it > lim || ih > lim || ot > lim || oh > lim || it % vec || ih % vec ||
         ot % vec || oh % vec)
-      return fail(SLS_EINVAL, "strides of %s must be multiples of %d elements in [0, 2^40]", name, vec);
+      return fail(SLS_EINVAL, "strides of %s must be multiples of %d elements in [0, 2^31)", name, vec);
     // no two output vectors overlap: one of the two axes steps past the whole extent of the other
     const bool one_t = num_tokens == 1, one_h = heads == 1;
     const bool t_out = (one_h || oh >= D) && (one_t || ot >= (heads - 1) * oh + D);
@@ -635,6 +635,12 @@ sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens, const
   return cuda_status(sls::launch_qk_norm_rope(a, (cudaStream_t)stream), "sls_qk_norm_rope");
 }
 
+// Whether two ranges of device memory share a byte (a null range shares none).
+static bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+  return a && b && na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 static sls_status check_kv8(const sls::Shape& s, const sls_kv8_cache* c, int capacity, const char* name, sls::Kv8* out) {
   if (!c) return fail(SLS_EINVAL, "%s is NULL", name);
   if (s.dtype != SLS_DTYPE_BF16) return fail(SLS_EUNSUPPORTED, "the 8-bit cache takes bf16 descriptors only");
@@ -673,6 +679,10 @@ sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
   for (int64_t st : {k_seq_stride, k_token_stride, k_head_stride, v_seq_stride, v_token_stride, v_head_stride})
     if (st < 0 || st > (int64_t(1) << 40) || st % 8)
       return fail(SLS_EINVAL, "strides of the new tokens must be multiples of 8 elements in [0, 2^40]");
+  const int64_t n4 = (int64_t)s.B * 4;
+  if ((ctx_out != ctx_len && overlap(ctx_out, n4, ctx_len, n4)) || overlap(ctx_out, n4, new_len, n4) ||
+      overlap(pos_out, n4, ctx_len, n4) || overlap(pos_out, n4, new_len, n4) || overlap(pos_out, n4, ctx_out, n4))
+    return fail(SLS_EINVAL, "ctx_out must be ctx_len itself or memory of its own, and pos_out memory of its own");
   if ((kmin == nullptr) != (kmax == nullptr)) return fail(SLS_EINVAL, "kmin and kmax: both or neither");
   if (kmin) {
     REQUIRE16(kmin); REQUIRE16(kmax);
@@ -720,6 +730,10 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
     if (mass_out) return fail(SLS_EUNSUPPORTED, "weight sums need dense attention (page_idx NULL)");
   }
   if (mass_in && !mass_out) return fail(SLS_EINVAL, "mass_in without mass_out");
+  const int64_t sums = (int64_t)s.B * s.Hkv * (s.Cap / c.block) * 4, heads = (int64_t)s.B * s.Hq;
+  if (mass_in != mass_out && overlap(mass_in, sums, mass_out, sums))
+    return fail(SLS_EINVAL, "mass_out must be mass_in itself or memory of its own");
+  if (overlap(q, heads * s.D * 2, out, heads * s.D * 2)) return fail(SLS_EINVAL, "out shares memory with q");
   const size_t need = sls::kv8_attend_workspace(s, c, mass_out != nullptr);
   if (!workspace || workspace_bytes < need)
     return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
@@ -766,9 +780,11 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
     REQUIRE16(kmin); REQUIRE16(kmax); REQUIRE16(kmin_out); REQUIRE16(kmax_out);
     if (s.P > e.src.block) return fail(SLS_EUNSUPPORTED, "page summaries move with blocks: page %d > block %d", s.P, e.src.block);
   }
+  if (ctx_out != ctx_len && overlap(ctx_out, (int64_t)s.B * 4, ctx_len, (int64_t)s.B * 4))
+    return fail(SLS_EINVAL, "ctx_out must be ctx_len itself or memory of its own");
   if (!same) {  // no destination may share memory with what is read
-    struct Range { uintptr_t a; int64_t n; };
-    auto at = [](const void* p, int64_t n) { return Range{(uintptr_t)p, p ? n : 0}; };
+    struct Range { const void* p; int64_t n; };
+    auto at = [](const void* p, int64_t n) { return Range{p, n}; };
     const int64_t st = rows * s.Cap, dt = rows * dst_capacity, bl = e.src.block;
     const Range in[] = {at(e.src.kc, st * s.D), at(e.src.vc, st * s.D), at(e.src.ks, st / bl * 4), at(e.src.vs, st / bl * 4),
                         at(e.src.kt, rows * bl * s.D * 2), at(e.src.vt, rows * bl * s.D * 2), at(mass, st / bl * 4),
@@ -778,7 +794,7 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
                         at(kmin_out, dt / s.P * s.D * 2), at(kmax_out, dt / s.P * s.D * 2)};
     for (const Range& x : in)
       for (const Range& y : to)
-        if (x.n && y.n && x.a < y.a + y.n && y.a < x.a + x.n)
+        if (overlap(x.p, x.n, y.p, y.n))
           return fail(SLS_EINVAL, "source and destination share memory without being the same cache");
   }
   e.cap = s.Cap; e.dcap = dst_capacity; e.keep = keep; e.n_sink = n_sink_blocks; e.n_recent = n_recent_blocks;

@@ -106,6 +106,9 @@ class Args {
   int device_ = -1;
 };
 
+// Stride of a dimension in elements (of a single entry: none is ever taken).
+int64_t step(const at::Tensor& t, int dim) { return t.size(dim) > 1 ? t.stride(dim) : 0; }
+
 void* stream() { return c10::cuda::getCurrentCUDAStream().stream(); }
 
 template <typename F>
@@ -148,7 +151,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* args, Py_ssize_t n) {
       s.in = x.data_ptr();
       s.out = y.data_ptr();
       s.w = a.data(w, nw, dt, {D});
-      s.it = x.stride(0); s.ih = x.stride(1); s.ot = y.stride(0); s.oh = y.stride(1);
+      s.it = step(x, 0); s.ih = step(x, 1); s.ot = step(y, 0); s.oh = step(y, 1);
       return s;
     };
     const Side q = side(r->num_q_heads, 1, 4, 6, "q", "q_weight", "q_out");
@@ -181,8 +184,8 @@ PyObject* kv8_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     float* mass = a.data<float>(8, "mass", F32, {B, H, blocks});
     int32_t* to = a.none(9) ? ctx : a.data<int32_t>(9, "ctx_out", I32, {B});
     int32_t* pos = a.data<int32_t>(10, "pos_out", I32, {B});
-    return calls.append(d.get(), c.get(), k.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.data_ptr(), v.stride(0),
-                        v.stride(1), v.stride(2), (int32_t)T, len, lo, hi, mass, ctx, to, pos, stream());
+    return calls.append(d.get(), c.get(), k.data_ptr(), step(k, 0), step(k, 1), step(k, 2), v.data_ptr(), step(v, 0),
+                        step(v, 1), step(v, 2), (int32_t)T, len, lo, hi, mass, ctx, to, pos, stream());
   });
 }
 

@@ -671,8 +671,9 @@ class Kv8Decode:
         self.q_weight, self.k_weight = q_weight, k_weight
         self.cache = Kv8Cache.empty(desc, fmt, block, device)
         new = lambda shape, dt=torch.bfloat16: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
-        self.ctx_len = new(B, torch.int32)      # tokens held (less than the positions seen, after an eviction)
-        self.positions = new(B, torch.int32)    # position of the next token
+        self.ctx_len = new(B, torch.int32)      # tokens held
+        self.evicted = new(B, torch.int32)      # tokens evicted before them: position = evicted + index held
+        self.positions = new(B, torch.int32)    # position of the step's token
         self.q, self.k_new = new((B, Hq, D)), new((B, H, D))
         self.out, self.lse = new((B, Hq, D)), new((B, Hq), torch.float32)
         self.kmin = self.kmax = self.page_idx = self.select_workspace = self.mass = None
@@ -690,24 +691,23 @@ class Kv8Decode:
         Hq, H = self.desc.num_q_heads, self.desc.num_kv_heads
         B, T = qkv.shape[:2]
         step = torch.arange(T, dtype=torch.int32, device=qkv.device)
-        pos = self.positions[:, None] + step
+        pos = (self.ctx_len + self.evicted)[:, None] + step
         if new_len is not None:
             pos = torch.where(step < new_len[:, None], pos, -1)  # padding is skipped
         flat = qkv.view(B * T, Hq + 2 * H, qkv.shape[-1])
         q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:Hq + H], pos.reshape(-1), self.q_weight, self.k_weight)
         kv8_append(self.desc, self.cache, k.view(B, T, H, -1), qkv[:, :, Hq + H:], self.ctx_len, new_len=new_len,
                    kmin=self.kmin, kmax=self.kmax, mass=self.mass)
-        self.positions += T if new_len is None else new_len.clamp(0, T)
         return q.view(B, T, Hq, -1)
 
     def __call__(self, qkv, sink=None):
         """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
         d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
+        torch.add(self.ctx_len, self.evicted, out=self.positions)
         qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.positions, self.q_weight, self.k_weight,
                      q_out=self.q, k_out=self.k_new)
         kv8_append(d, self.cache, self.k_new[:, None], qkv[:, None, Hq + H:], self.ctx_len, kmin=self.kmin,
                    kmax=self.kmax, mass=self.mass)
-        self.positions += 1
         if self.k:
             select_pages(d, self.q, self.kmin, self.kmax, self.ctx_len, self.k, self.n_sink, self.n_local,
                          out=self.page_idx, workspace=self.select_workspace)
@@ -719,4 +719,7 @@ class Kv8Decode:
         """Cuts every sequence to its keep heaviest complete blocks (kv8_evict in place).  Returns their numbers."""
         if self.mass is None:
             raise ValueError("evict needs the weight sums (mass=True)")
-        return kv8_evict(self.desc, self.cache, self.ctx_len, self.mass, keep, n_sink_blocks, n_recent_blocks)[1]
+        self.evicted += self.ctx_len
+        kept = kv8_evict(self.desc, self.cache, self.ctx_len, self.mass, keep, n_sink_blocks, n_recent_blocks)[1]
+        self.evicted -= self.ctx_len
+        return kept

@@ -568,7 +568,7 @@ def test_prompt_steps_eviction_and_replayed_loop_together():
             want = choose(before[b, h].cpu().numpy(), lens[b] // block, 6, 1, 2)
             assert kept[b][h] == want
             rows[b][h].blocks = [rows[b][h].blocks[j] for j in want]
-    assert step.ctx_len.tolist() == [6 * block + n % block for n in lens] and step.positions.tolist() == seen
+    assert step.ctx_len.tolist() == [6 * block + n % block for n in lens] and (step.ctx_len + step.evicted).tolist() == seen
     loop.capture()
     for _ in range(25):  # blocks are completed on the way
         loop.qkv.copy_(bf16(rng, (B, Hq + 2 * H, D)))

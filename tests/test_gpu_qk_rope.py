@@ -84,6 +84,10 @@ def test_in_place_strided_skipped_and_empty():
     ops.qk_norm_rope(rope, qkv.cuda()[:, :hq], qkv.cuda()[:, hq:hq + hkv], pos.clamp(min=0).cuda(), wq.cuda(), wk.cuda(),
                      q_out=out.transpose(0, 1))
     assert torch.equal(out.transpose(0, 1), q)
+    # a single token's or head's stride does not matter, whatever the view says
+    odd = torch.as_strided(qkv.cuda()[0], (1, hq, d), (13, d, 1))
+    one, _ = ops.qk_norm_rope(rope, odd, qkv.cuda()[:1, hq:hq + hkv], pos[:1].clamp(min=0).cuda(), wq.cuda(), wk.cuda())
+    assert torch.equal(one[0], q[0])
     none = torch.zeros(0, dtype=torch.int32, device="cuda")
     q0, k0 = ops.qk_norm_rope(rope, dev[:0, :hq], dev[:0, hq:hq + hkv], none)
     assert q0.shape == (0, hq, d) and k0.shape == (0, hkv, d)

@@ -75,11 +75,11 @@ def test_cache_refusals_in_every_call(lib, d, c, code):
                              None, A, A, A, None) == code
 
 
-def append(lib, dd=None, st=(2048, 256, 128), new=4, k=A, kmin=None, kmax=None, ctx=A, out=A, v=A):
+def append(lib, dd=None, st=(2048, 256, 128), new=4, k=A, kmin=None, kmax=None, ctx=A, out=A, v=A, n=None, pos=None):
     dd = dd or desc()
     c = cache()
-    return lib.sls_kv8_append(ctypes.byref(dd), ctypes.byref(c), k, *st, v, *st, new, None, kmin, kmax, None, ctx, out,
-                              None, None)
+    return lib.sls_kv8_append(ctypes.byref(dd), ctypes.byref(c), k, *st, v, *st, new, n, kmin, kmax, None, ctx, out,
+                              pos, None)
 
 
 def test_append_refusals(lib):
@@ -93,9 +93,14 @@ def test_append_refusals(lib):
     assert append(lib, kmin=A) == L.SLS_EINVAL
     assert append(lib, dd=desc(page_size=1), kmin=A, kmax=A) == L.SLS_EINVAL
     assert append(lib, dd=desc(batch=1 << 20), new=1 << 20) == L.SLS_EOVERFLOW
+    assert append(lib, dd=desc(batch=1, num_q_heads=1, num_kv_heads=1, capacity=(1 << 30) + 64)) == L.SLS_EUNSUPPORTED
+    assert append(lib, out=P(0x10004)) == L.SLS_EINVAL                     # partly ctx_len's memory
+    assert append(lib, out=P(0x20000), n=P(0x20004)) == L.SLS_EINVAL
+    assert append(lib, pos=A) == L.SLS_EINVAL
+    assert append(lib, out=P(0x20000), pos=P(0x20004)) == L.SLS_EINVAL
 
 
-def attend(lib, dd=None, q=A, idx=None, stride=0, count=None, k=0, ctx=A, out=A, mi=None, mo=None, ws=A, wsb=1 << 40):
+def attend(lib, dd=None, q=A, idx=None, stride=0, count=None, k=0, ctx=A, out=P(0x80000), mi=None, mo=None, ws=A, wsb=1 << 40):
     dd = dd or desc()
     c = cache()
     return lib.sls_kv8_decode_attend(ctypes.byref(dd), ctypes.byref(c), q, idx, stride, count, k, ctx, None, out, None, mi,
@@ -116,6 +121,8 @@ def test_attend_refusals(lib):
     assert attend(lib, idx=A, stride=1 << 28, k=1) == L.SLS_EOVERFLOW
     assert attend(lib, idx=A, stride=4, k=4, mo=A) == L.SLS_EUNSUPPORTED
     assert attend(lib, mi=A) == L.SLS_EINVAL
+    assert attend(lib, mi=P(0x100000), mo=P(0x100004)) == L.SLS_EINVAL     # partly the same memory
+    assert attend(lib, q=P(0x100000), out=P(0x100010)) == L.SLS_EINVAL
     need = lib.sls_kv8_decode_attend_workspace_size(ctypes.byref(desc()), ctypes.byref(cache()), 0)
     with_mass = lib.sls_kv8_decode_attend_workspace_size(ctypes.byref(desc()), ctypes.byref(cache()), 1)
     assert 0 < need < with_mass
@@ -135,7 +142,7 @@ def evict(lib, dst=None, dcap=1024, keep=4, sink=1, recent=1, mass=A, mass_out=A
 def test_evict_refusals(lib):
     far = 1 << 30
     for kw in (dict(keep=0), dict(sink=-1), dict(keep=4, sink=2, recent=3), dict(keep=16), dict(mass=None), dict(kept=None),
-               dict(ctx=None), dict(out=None), dict(mass_out=P(0x20000)), dict(mass_out=None), dict(dcap=512),
+               dict(ctx=None), dict(out=None), dict(out=P(0x10004)), dict(mass_out=P(0x20000)), dict(mass_out=None), dict(dcap=512),
                dict(km=(A, None, None, None)), dict(km=(A, A, P(0x30000), A)),
                dict(dst=cache(fmt=1), dcap=1024), dict(dst=cache(far, block=32)), dict(dst=cache(far), dcap=1000),
                dict(dst=cache(far), dcap=256, keep=4),
