@@ -195,21 +195,19 @@ __device__ __forceinline__ void kv8_pv(uint32_t v, float (&o)[D / 16][4], uint32
 // it once per row, with the memory system busy.
 template <int D>
 struct Kv8Tail {
-  uint2 k[2][D / 16], q[D / 16];
+  uint2 k[2][D / 16];
   uint32_t v[4][D / 16];
   int lim;
-  __device__ __forceinline__ void load(const bf16* kt, const bf16* vt, const bf16* qh, bool head, int n, int lane) {
+  __device__ __forceinline__ void load(const bf16* kt, const bf16* vt, int n, int lane) {
     const int r = lane >> 2, m = lane & 3;
     lim = n;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-      q[c] = head ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+    for (int c = 0; c < D / 16; ++c)
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
         const int t = r + 8 * nt;
         k[nt][c] = t < lim ? *reinterpret_cast<const uint2*>(kt + (size_t)t * D + 16 * c + 4 * m) : make_uint2(0u, 0u);
       }
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int t = 2 * m + (i & 1) + 8 * (i >> 1);
@@ -221,7 +219,8 @@ struct Kv8Tail {
       }
     }
   }
-  __device__ __forceinline__ void scores(float mul, float (&x)[4], int lane) const {
+  // q: channels 16 c + 4 m .. + 3 of the lane's head
+  __device__ __forceinline__ void scores(const uint2 (&q)[D / 16], float mul, float (&x)[4], int lane) const {
     const int m = lane & 3;
     float sc[2][4];
 #pragma unroll
@@ -413,6 +412,12 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const size_t row_blk = (size_t)row * (a.Cap >> a.c.bshift);
 
     const bf16* qh = a.q + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
+    // the lane's part of its head's query
+    auto load_q = [&](uint2 (&raw)[KS]) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c)
+        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+    };
     uint32_t qa[KS][2];
     float qmul;
     float o[KS][4], m_run = kNegInf, l_run = 0.f;
@@ -439,12 +444,13 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     };
     // the 16 positions from `at` on, which lie in the tail buffer
     auto tail_group = [&](int at) {
+      uint2 q[KS];
+      load_q(q);
       const size_t tail = ((size_t)row * a.c.block + (at & (a.c.block - 1))) * D;
       Kv8Tail<D> g;
-      g.load(static_cast<const bf16*>(a.c.kt) + tail, static_cast<const bf16*>(a.c.vt) + tail, qh, r < G, min(16, N - at),
-             lane);
+      g.load(static_cast<const bf16*>(a.c.kt) + tail, static_cast<const bf16*>(a.c.vt) + tail, min(16, N - at), lane);
       float x[4];
-      g.scores(a.qscale, x, lane);
+      g.scores(q, a.qscale, x, lane);
       const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
@@ -519,6 +525,8 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 
     bool ok = !failed;
     int k = 0;
+    uint2 raw[KS];
+    if constexpr (LIST) load_q(raw);  // in flight with the list (the dense kernels start their copies first)
     if (ok) {
       if (lane == 0) fence_proxy_async_smem();  // the merge's reads of the ring before the copies write it
       load_batch(0);
@@ -529,15 +537,12 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           for (int at = (newest << a.c.bshift) + 16 * (W - 1 - warp); at < N; at += 16 * W) tail_group(at);
       }
     }
+    if constexpr (!LIST) load_q(raw);
     // the heads' queries as fp16 with their largest channel in [2^10, 2^11)
     {
-      uint2 raw[KS];
       uint32_t mx = 0;
 #pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
-        mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu));
-      }
+      for (int c = 0; c < KS; ++c) mx = __vmaxu2(mx, __vmaxu2(raw[c].x & 0x7fff7fffu, raw[c].y & 0x7fff7fffu));
       mx = max(mx & 0xffffu, mx >> 16);
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
       mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
