@@ -765,7 +765,7 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
   const bool same = e.dst.kc == e.src.kc;
   const int64_t rows = (int64_t)s.B * s.Hkv;
   int64_t ctas;
-  if (!checked_mul(rows, (int64_t)keep + 128, &ctas) || ctas > INT32_MAX || rows * dst_capacity > (int64_t(1) << 41))
+  if (!checked_mul(rows, 2 * (int64_t)keep + 128, &ctas) || ctas > INT32_MAX || rows * dst_capacity > (int64_t(1) << 41))
     return fail(SLS_EOVERFLOW, "too many rows");
   if (same) {
     if (e.dst.vc != e.src.vc || e.dst.ks != e.src.ks || e.dst.vs != e.src.vs || e.dst.kt != e.src.kt ||

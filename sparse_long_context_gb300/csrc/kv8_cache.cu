@@ -213,6 +213,11 @@ kv8_append_one_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int clust
   pdl_wait_then_release();
   const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
   const int isv = threadIdx.x / NT, tid = threadIdx.x % NT, ch = (tid % CPR) * 8;
+  auto source = [&](int h) {
+    return static_cast<const bf16*>(isv ? nw.v : nw.k) + b * (isv ? nw.vb : nw.kb) + h * (isv ? nw.vh : nw.kh);
+  };
+  // the lane's channels of the first head's new token, in flight with the lengths
+  uint4 token = *reinterpret_cast<const uint4*>(source(rank) + ch);
   const AppendSpan sp = append_span(nw, o.ctx_len, b, o.Cap);
   if (cluster > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // ctx_len has been read
   const int blk = sp.start >> c.bshift, slot = sp.start & (c.block - 1);
@@ -220,16 +225,14 @@ kv8_append_one_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int clust
   if (sp.n) {
     for (int h = rank; h < o.Hkv; h += cluster) {
       const size_t row = (size_t)b * o.Hkv + h;
-      const bf16* src = static_cast<const bf16*>(isv ? nw.v : nw.k) + b * (isv ? nw.vb : nw.kb) + h * (isv ? nw.vh : nw.kh);
+      if (h != rank) token = *reinterpret_cast<const uint4*>(source(h) + ch);
       bf16* tail = static_cast<bf16*>(isv ? c.vt : c.kt) + row * c.block * D;
       if (!done) {
-        if (tid < CPR) *reinterpret_cast<uint4*>(tail + (size_t)slot * D + ch) = *reinterpret_cast<const uint4*>(src + ch);
+        if (tid < CPR) *reinterpret_cast<uint4*>(tail + (size_t)slot * D + ch) = token;
       } else {
         const size_t at = row * (o.Cap >> c.bshift) + blk;
         uint8_t* codes = (isv ? c.vc : c.kc) + at * c.block * D;
-        auto vec = [&](int t) {
-          return *reinterpret_cast<const uint4*>(t < slot ? tail + (size_t)t * D + ch : src + ch);
-        };
+        auto vec = [&](int t) { return t < slot ? *reinterpret_cast<const uint4*>(tail + (size_t)t * D + ch) : token; };
         uint32_t m2 = 0;
 #pragma unroll 8
         for (int t = tid / CPR; t < c.block; t += NT / CPR) m2 = __vmaxu2(m2, abs_max2(vec(t)));
@@ -241,15 +244,13 @@ kv8_append_one_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int clust
         for (int k = 0; k < NT / 32; ++k) mx = max(mx, s_max[isv][k]);
         const float amax = __uint_as_float(mx << 16);
         const bool finite = mx < 0x7f80u;
-#pragma unroll 4
+        const float rcp = __fdiv_rn(kv8_top<FMT>(), amax);
+        const bool fast = rcp < 1e38f;  // a block of subnormals overflows the reciprocal
+#pragma unroll 8
         for (int t = tid / CPR; t < c.block; t += NT / CPR) {
-          float x[8];
-          unpack_vec(vec(t), x);
-          uint32_t w[2] = {0u, 0u};
-          if (finite && mx)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k >> 2] |= kv8_code<FMT>(x[k], amax) << (8 * (k & 3));
-          *reinterpret_cast<uint2*>(codes + (size_t)t * D + ch) = make_uint2(w[0], w[1]);
+          uint2 w = make_uint2(0u, 0u);
+          if (finite && mx) w = fast ? kv8_codes8<FMT>(vec(t), rcp) : kv8_codes8_exact<FMT>(vec(t), amax);
+          *reinterpret_cast<uint2*>(codes + (size_t)t * D + ch) = w;
         }
         if (tid == 0) {
           (isv ? c.vs : c.ks)[at] = finite ? __fdiv_rn(amax, kv8_top<FMT>()) : __int_as_float(0x7fffffff);
@@ -258,9 +259,8 @@ kv8_append_one_kernel(const Kv8 c, const Kv8New nw, const AppendOut o, int clust
       }
       // page min/max by the last warp of K's threads
       if (o.kmin && !isv && tid >= NT - CPR) {
-        const int ch2 = (tid - (NT - CPR)) * 8;
-        const size_t at = (row * (o.Cap >> o.pshift) + (sp.start >> o.pshift)) * D + ch2;
-        const uint4 x = *reinterpret_cast<const uint4*>(src + ch2);
+        const size_t at = (row * (o.Cap >> o.pshift) + (sp.start >> o.pshift)) * D + ch;
+        const uint4 x = token;
         uint4 lo = x, hi = x;
         if (sp.start & ((1 << o.pshift) - 1)) {
           lo = *reinterpret_cast<const uint4*>(o.kmin + at);
@@ -439,71 +439,86 @@ kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
   }
 }
 
-// Into another cache: a CTA moves `per` kept blocks of a row, eight loads of a
-// thread in flight together; the row's first CTA also the tails.
+// Into another cache, in CTAs of three kinds per row, so that the waits of one
+// kind's loads do not add to another's: `parts` of them move `per` kept blocks each
+// (K and V, eight loads of a thread in flight together), then `sums` move kSumItems
+// blocks' scales and sums (the first also the tails), then the rest the page
+// summaries of `meta_items` blocks each.
 constexpr int kMoveBytes = 16384;  // of K (and as many of V) per CTA
+constexpr int kSumItems = 1024;
 __global__ void __launch_bounds__(256)
-kv8_copy_kernel(const Kv8Evict e, int Hkv, int D, int P, int per, int parts) {
+kv8_copy_kernel(const Kv8Evict e, int Hkv, int D, int P, int per, int parts, int sums, int metas, int meta_items) {
   pdl_wait_then_release();
-  const int row = blockIdx.x / parts, part = blockIdx.x % parts, block = e.src.block, bsh = e.src.bshift;
+  const int kinds = parts + sums + metas;
+  const int row = blockIdx.x / kinds, x = blockIdx.x % kinds, block = e.src.block, bsh = e.src.bshift;
   const int N = clamp_len(e.ctx_len[row / Hkv], e.cap);
   const int nb = N >> bsh, n = min(nb, e.keep), rest = N & (block - 1), tid = threadIdx.x;
   const size_t srow = (size_t)row * (e.cap >> bsh), drow = (size_t)row * (e.dcap >> bsh);
   const int32_t* kept = e.kept + (size_t)row * e.keep;
-  const int vecs = block * D / 16, vsh = __ffs(vecs) - 1;  // 16-byte vectors of a block's codes, a power of two
-  // items [i0, i1) of the list, `vecs` vectors each
-  const int i0 = part * per, i1 = min(n, i0 + per);
-  constexpr int U = 4;
-  for (int x0 = 0; x0 < (i1 - i0) * vecs; x0 += 256 * U) {
-    uint4 k[U], v[U];
-    size_t to[U];
+  if (x < parts) {
+    const int vecs = block * D / 16, vsh = __ffs(vecs) - 1;  // 16-byte vectors of a block's codes, a power of two
+    const int i0 = x * per, i1 = min(n, i0 + per);
+    constexpr int U = 4;
+    for (int x0 = 0; x0 < (i1 - i0) * vecs; x0 += 256 * U) {
+      uint4 k[U], v[U];
+      size_t to[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int x = x0 + u * 256 + tid;
-      if (x < (i1 - i0) * vecs) {
-        const int it = i0 + (x >> vsh), w = x & (vecs - 1);
-        const size_t from = (srow + kept[it]) * vecs + w;
-        to[u] = (drow + it) * vecs + w;
-        k[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.kc) + from);
-        v[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.vc) + from);
+      for (int u = 0; u < U; ++u) {
+        const int w = x0 + u * 256 + tid;
+        if (w < (i1 - i0) * vecs) {
+          const int it = i0 + (w >> vsh), c = w & (vecs - 1);
+          const size_t from = (srow + kept[it]) * vecs + c;
+          to[u] = (drow + it) * vecs + c;
+          k[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.kc) + from);
+          v[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.vc) + from);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (x0 + u * 256 + tid < (i1 - i0) * vecs) {
+          reinterpret_cast<uint4*>(e.dst.kc)[to[u]] = k[u];
+          reinterpret_cast<uint4*>(e.dst.vc)[to[u]] = v[u];
+        }
+    }
+  } else if (x < parts + sums) {
+    const int i0 = (x - parts) * kSumItems, i1 = min(n, i0 + kSumItems);
+#pragma unroll 4
+    for (int i = i0 + tid; i < i1; i += 256) {
+      const size_t from = srow + kept[i], to = drow + i;
+      const float a = e.src.ks[from], b = e.src.vs[from], m = e.mass_out ? e.mass[from] : 0.f;
+      e.dst.ks[to] = a;
+      e.dst.vs[to] = b;
+      if (e.mass_out) e.mass_out[to] = m;
+    }
+    if (x == parts) {
+      const size_t t0 = (size_t)row * block * D / 8;
+#pragma unroll 2
+      for (int i = tid; i < rest * D / 8; i += 256) {
+        const uint4 a = static_cast<const uint4*>(e.src.kt)[t0 + i], b = static_cast<const uint4*>(e.src.vt)[t0 + i];
+        static_cast<uint4*>(e.dst.kt)[t0 + i] = a;
+        static_cast<uint4*>(e.dst.vt)[t0 + i] = b;
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (x0 + u * 256 + tid < (i1 - i0) * vecs) {
-        reinterpret_cast<uint4*>(e.dst.kc)[to[u]] = k[u];
-        reinterpret_cast<uint4*>(e.dst.vc)[to[u]] = v[u];
-      }
-  }
-  for (int i = i0 + tid; i < i1; i += 256) {
-    const size_t from = srow + kept[i], to = drow + i;
-    e.dst.ks[to] = e.src.ks[from];
-    e.dst.vs[to] = e.src.vs[from];
-    if (e.mass_out) e.mass_out[to] = e.mass[from];
-  }
-  if (e.kmin) {
-    const int item = block / P * D / 8;  // 16-byte vectors of a block's page summaries
+  } else {
+    const int item = block / P * D / 8;  // 16-byte vectors of a block's page summaries, a power of two
+    const int ish = __ffs(item) - 1;
     const uint4 *smin = static_cast<const uint4*>(e.kmin) + srow * item, *smax = static_cast<const uint4*>(e.kmax) + srow * item;
     uint4 *dmin = static_cast<uint4*>(e.kmin_out) + drow * item, *dmax = static_cast<uint4*>(e.kmax_out) + drow * item;
-#pragma unroll 2
-    for (int x = tid; x < (i1 - i0) * item; x += 256) {
-      const int it = i0 + x / item, w = x % item;
-      const size_t from = (size_t)kept[it] * item + w, to = (size_t)it * item + w;
-      dmin[to] = smin[from];
-      dmax[to] = smax[from];
+    const int i0 = (x - parts - sums) * meta_items, i1 = min(n, i0 + meta_items);
+#pragma unroll 4
+    for (int w = tid; w < (i1 - i0) << ish; w += 256) {
+      const int it = i0 + (w >> ish), c = w & (item - 1);
+      const size_t from = (size_t)kept[it] * item + c, to = (size_t)it * item + c;
+      const uint4 a = smin[from], b = smax[from];
+      dmin[to] = a;
+      dmax[to] = b;
     }
-    if (part == 0)  // the pages of the newest, partial block
-      for (int x = tid; x < (rest + P - 1) / P * D / 8; x += 256) {
-        dmin[(size_t)n * item + x] = smin[(size_t)nb * item + x];
-        dmax[(size_t)n * item + x] = smax[(size_t)nb * item + x];
+    if (i0 == 0)  // the pages of the newest, partial block
+      for (int w = tid; w < (rest + P - 1) / P * D / 8; w += 256) {
+        const uint4 a = smin[(size_t)nb * item + w], b = smax[(size_t)nb * item + w];
+        dmin[(size_t)n * item + w] = a;
+        dmax[(size_t)n * item + w] = b;
       }
-  }
-  if (part == 0) {
-    const size_t t0 = (size_t)row * block * D / 8;
-    for (int i = tid; i < rest * D / 8; i += 256) {
-      static_cast<uint4*>(e.dst.kt)[t0 + i] = static_cast<const uint4*>(e.src.kt)[t0 + i];
-      static_cast<uint4*>(e.dst.vt)[t0 + i] = static_cast<const uint4*>(e.src.vt)[t0 + i];
-    }
   }
 }
 
@@ -609,7 +624,12 @@ cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st)
                    parts);
   } else {
     const int per = std::max(1, kMoveBytes / bytes), parts = (e.keep + per - 1) / per;
-    r = launch_pdl(kv8_copy_kernel, dim3((unsigned)rows * parts), dim3(256), 0, st, e, s.Hkv, s.D, s.P, per, parts);
+    const int sums = (e.keep + kSumItems - 1) / kSumItems;
+    // four vectors of kmin and of kmax a thread
+    const int meta_items = e.kmin ? std::max(1, 1024 / (e.src.block / s.P * s.D / 8)) : 1;
+    const int metas = e.kmin ? (e.keep + meta_items - 1) / meta_items : 0;
+    r = launch_pdl(kv8_copy_kernel, dim3((unsigned)rows * (parts + sums + metas)), dim3(256), 0, st, e, s.Hkv, s.D, s.P,
+                   per, parts, sums, metas, meta_items);
   }
   if (r == cudaSuccess && !apart)
     r = launch_pdl(kv8_evicted_len_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, e, s.B);
