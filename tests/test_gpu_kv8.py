@@ -356,6 +356,47 @@ def test_attend_long_rows_many_rows_and_reused_workspace():
     assert all(torch.equal(r[0], a[0]) and torch.equal(r[1], a[1]) for r in runs)  # the same bits every time
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,block", [(64, 16), (64, 32), (128, 16), (128, 64)])
+def test_attend_long_uneven_rows(fmt, d, block):
+    """Capacities past the cluster kernel's: every CTA takes a range of all rows' tokens, most of them cross rows."""
+    lens = [9000, 0, 31, 8001, 1, 257, 4096, 17]
+    p = Pair(8, 10, 2, d, 9216, fmt, block, seed=d + block)
+    p.append(lens)
+    ws = ops.kv8_attend_workspace(p.desc, p.cache, mass=True)
+    for seed in range(2):
+        attention(p, query(p, seed), mass_in=torch.rand_like(p.mass), workspace=ws)
+    sink = torch.from_numpy(np.random.default_rng(6).standard_normal(10)).float()
+    attention(p, query(p, 7), sink=sink, workspace=ws)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d,page,block", [(64, 16, 32), (64, 32, 16), (64, 64, 64), (128, 16, 64), (128, 32, 16)])
+@pytest.mark.parametrize("batch,hkv", [(2, 2), (45, 2)])  # one cluster per row; more rows than half the GPU's SMs
+def test_attend_page_lists_of_few_and_many_rows(fmt, d, page, block, batch, hkv):
+    rng = np.random.default_rng(d + page)
+    lens = [int(x) for x in rng.integers(0, 321, batch)]
+    lens[0] = 320
+    p = Pair(batch, 3 * hkv, hkv, d, 320, fmt, block, page, seed=page)
+    p.append(lens)
+    npg = 320 // page
+    idx = np.full((batch * hkv, npg + 2), -1)
+    for r in range(batch * hkv):
+        some = rng.permutation(npg)[:rng.integers(0, npg + 1)]
+        idx[r, rng.permutation(npg + 2)[:len(some)]] = some
+    attention(p, query(p, 1), pages=(ints(idx), None))
+    attention(p, query(p, 2), pages=(ints(idx), ints(rng.integers(-1, npg + 4, batch * hkv))))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_attend_more_rows_than_a_cluster_each(fmt):
+    rng = np.random.default_rng(3)
+    lens = [int(x) for x in rng.integers(0, 400, 50)]
+    p = Pair(50, 16, 2, 64, 400, fmt, 16, seed=8)
+    p.append(lens)
+    attention(p, query(p, 1), mass_in=torch.rand_like(p.mass))
+
+
 def test_attend_sums_are_the_same_every_time_and_in_place():
     p = Pair(2, 12, 2, 128, 4096, "e4m3", 64, seed=5)
     p.append([4000, 1111])
