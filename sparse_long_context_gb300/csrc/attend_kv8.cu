@@ -259,11 +259,11 @@ __device__ __forceinline__ void kv8_finish(const Kv8Attend& a, size_t hq, int he
   const float Mx = fmaxf(M, sk);
   float f = 0.f, Lt = 0.f;
   if (Mx != kNegInf) {
-    f = M == kNegInf ? 0.f : exp2f(M - Mx);
-    Lt = lv * f + (a.sink ? exp2f(sk - Mx) : 0.f);
+    f = M == kNegInf ? 0.f : kv8_ex2(M - Mx);
+    Lt = lv * f + (a.sink ? kv8_ex2(sk - Mx) : 0.f);
   }
   // a NaN sum (a NaN block, or a wait that gave up) stays NaN in the output and lse
-  a.out[hq * D + d] = __float2bfloat16_rn(Lt == 0.f ? 0.f : av * f / Lt);
+  a.out[hq * D + d] = __float2bfloat16_rn(Lt == 0.f ? 0.f : __fdividef(av * f, Lt));  // Lt < 2^126: two ulp
   if (d == 0) {
     if (a.lse) a.lse[hq] = Lt == 0.f ? kNegInf : Mx * kLn2 + logf(Lt);
     if (a.fin) a.fin[hq] = make_float2(Mx, Lt == 0.f ? 0.f : 1.f / Lt);
@@ -668,7 +668,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         // a NaN sum without a maximum (every score NaN) is kept
-        const float f = sM[w][g] == kNegInf ? (sL[w][g] == 0.f ? 0.f : 1.f) : exp2f(sM[w][g] - M);
+        const float f = sM[w][g] == kNegInf ? (sL[w][g] == 0.f ? 0.f : 1.f) : kv8_ex2(sM[w][g] - M);
         sF[w][g] = f;
         Lh = fmaf(sL[w][g], f, Lh);
       }
@@ -711,7 +711,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         for (int s = 0; s < C; ++s) M = fmaxf(M, inbox.m[s * 8 + g]);
         for (int s = 0; s < C; ++s) {
           const float ms = inbox.m[s * 8 + g];
-          const float f = ms == kNegInf ? 0.f : exp2f(ms - M);
+          const float f = ms == kNegInf ? 0.f : kv8_ex2(ms - M);
           Lh = fmaf(inbox.l[s * 8 + g], f, Lh);
           av = fmaf(inbox.o[s * chunk + (i - split * chunk)], f, av);
         }
@@ -774,12 +774,12 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           M = fmaxf(M, sk);
           for (int j = lane; j < n; j += 32) {
             const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
-            const float w = (ms == kNegInf || M == kNegInf) ? 0.f : exp2f(ms - M);
+            const float w = (ms == kNegInf || M == kNegInf) ? 0.f : kv8_ex2(ms - M);
             Ls += __ldcg(a.pl + (size_t)sh.s_slot[j] * G + g) * w;
             if (j < 64) sh.s_w[g][j] = w;
           }
           Ls = warp_sum(Ls);
-          if (a.sink && M != kNegInf) Ls += exp2f(sk - M);
+          if (a.sink && M != kNegInf) Ls += kv8_ex2(sk - M);
           if (lane == 0) {
             const float inv = Ls == 0.f ? 0.f : 1.f / Ls;  // NaN stays NaN
             const size_t hq = (size_t)row * G + g;
@@ -809,7 +809,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
                 w = sh.s_w[g][j];
               } else {
                 const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
-                w = (ms == kNegInf || sh.s_m[g] == kNegInf) ? 0.f : exp2f(ms - sh.s_m[g]);
+                w = (ms == kNegInf || sh.s_m[g] == kNegInf) ? 0.f : kv8_ex2(ms - sh.s_m[g]);
               }
               acc.x = fmaf(v[u].x, w, acc.x);
               acc.y = fmaf(v[u].y, w, acc.y);
@@ -853,7 +853,7 @@ kv8_mass_kernel(const Kv8Attend a, int per_row) {
       }
 #pragma unroll
     for (int g = 0; g < 8; ++g)
-      if (g < a.G) sum += x[g].x * exp2f(x[g].y - f[g].x) * f[g].y;
+      if (g < a.G) sum += x[g].x * kv8_ex2(x[g].y - f[g].x) * f[g].y;
   }
   for (int o = 1; o < (1 << eshift); o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (live && (at & ((1 << eshift) - 1)) == 0) {
