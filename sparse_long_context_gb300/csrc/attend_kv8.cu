@@ -332,9 +332,9 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   // s_pref: exclusive prefix sum of the rows' units
   {
     const int rpt = (rows + NT - 1) / NT, r0 = threadIdx.x * rpt;
-    int sum = 0;
+    int sum = 0, one = 0;  // one: the units of a thread's only row, read once
     for (int i = 0; i < rpt; ++i)
-      if (r0 + i < rows) sum += units_of(r0 + i);
+      if (r0 + i < rows) sum += one = units_of(r0 + i);
     int x = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -353,7 +353,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     for (int i = 0; i < rpt; ++i)
       if (r0 + i < rows) {
         s_pref[r0 + i] = acc;
-        acc += units_of(r0 + i);
+        acc += rpt == 1 ? one : units_of(r0 + i);
       }
     if (threadIdx.x == 0) s_pref[rows] = total;
     __syncthreads();
@@ -766,17 +766,41 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       __syncthreads();
       if (sh.s_last) {
         const int n = sh.s_ncontrib;
+        // a thread per four channels of a head; the first eight contributors'
+        // values are in flight while the weights are formed
+        static_assert(8 * D / 4 <= NT, "one float4 of the output a thread");
+        const int g4 = threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
+        auto part = [&](int jj) {
+          return jj < n && g4 < G ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[jj] * G + g4) * D) + d4)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = part(u);
         for (int g = warp; g < G; g += W) {
-          float M = kNegInf, Ls = 0.f;
-          for (int j = lane; j < n; j += 32) M = fmaxf(M, __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g));
+          // the first 64 contributors' max and sum in registers, loaded at once
+          float pm[2], pl[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int jj = lane + 32 * u;
+            pm[u] = jj < n ? __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g) : kNegInf;
+            pl[u] = jj < n ? __ldcg(a.pl + (size_t)sh.s_slot[jj] * G + g) : 0.f;
+          }
+          float M = fmaxf(pm[0], pm[1]), Ls = 0.f;
+          for (int jj = lane + 64; jj < n; jj += 32) M = fmaxf(M, __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g));
           M = warp_max(M);
           const float sk = a.sink ? a.sink[h * G + g] * kLog2e : kNegInf;
           M = fmaxf(M, sk);
-          for (int j = lane; j < n; j += 32) {
-            const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
-            const float w = (ms == kNegInf || M == kNegInf) ? 0.f : kv8_ex2(ms - M);
-            Ls += __ldcg(a.pl + (size_t)sh.s_slot[j] * G + g) * w;
-            if (j < 64) sh.s_w[g][j] = w;
+          auto weight = [&](float ms) { return (ms == kNegInf || M == kNegInf) ? 0.f : kv8_ex2(ms - M); };
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float w = weight(pm[u]);
+            Ls += pl[u] * w;
+            if (lane + 32 * u < n) sh.s_w[g][lane + 32 * u] = w;
+          }
+          for (int jj = lane + 64; jj < n; jj += 32) {
+            const size_t at = (size_t)sh.s_slot[jj] * G + g;
+            Ls += __ldcg(a.pl + at) * weight(__ldcg(a.pm + at));
           }
           Ls = warp_sum(Ls);
           if (a.sink && M != kNegInf) Ls += kv8_ex2(sk - M);
@@ -790,26 +814,22 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < G * D / 4; i += NT) {
-          const int g = i / (D / 4), d4 = i % (D / 4);
+        if (g4 < G) {
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int j0 = 0; j0 < n; j0 += 8) {
-            float4 v[8];
+            if (j0)
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              v[u] = j0 + u < n
-                         ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[j0 + u] * G + g) * D) + d4)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int u = 0; u < 8; ++u) v[u] = part(j0 + u);
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              const int j = j0 + u;
-              if (j >= n) break;
+              const int jj = j0 + u;
+              if (jj >= n) break;
               float w;
-              if (j < 64) {
-                w = sh.s_w[g][j];
+              if (jj < 64) {
+                w = sh.s_w[g4][jj];
               } else {
-                const float ms = __ldcg(a.pm + (size_t)sh.s_slot[j] * G + g);
-                w = (ms == kNegInf || sh.s_m[g] == kNegInf) ? 0.f : kv8_ex2(ms - sh.s_m[g]);
+                const float ms = __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g4);
+                w = (ms == kNegInf || sh.s_m[g4] == kNegInf) ? 0.f : kv8_ex2(ms - sh.s_m[g4]);
               }
               acc.x = fmaf(v[u].x, w, acc.x);
               acc.y = fmaf(v[u].y, w, acc.y);
@@ -817,8 +837,8 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
               acc.w = fmaf(v[u].w, w, acc.w);
             }
           }
-          const float inv = sh.s_inv[g];
-          bf16* op = a.out + ((size_t)row * G + g) * D;
+          const float inv = sh.s_inv[g4];
+          bf16* op = a.out + ((size_t)row * G + g4) * D;
           *reinterpret_cast<__nv_bfloat162*>(op + kv8_channel<D>(4 * d4)) = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
           *reinterpret_cast<__nv_bfloat162*>(op + kv8_channel<D>(4 * d4 + 2)) =
               __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
