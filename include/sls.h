@@ -11,7 +11,13 @@
  *                                       with the optional sink
  *
  * plus the selector metadata kept next to the KV cache (page min/max keys,
- * 2-bit thumbnails), built in bulk or updated on append.
+ * 2-bit thumbnails), built in bulk or updated on append; and, around a cache
+ * held in 8 bits, what fills, reads and bounds it:
+ *
+ *   sls_qk_norm_rope        per-head norm and rotation of the projected heads
+ *   sls_kv8_append          tokens into the 8-bit cache
+ *   sls_kv8_decode_attend   decode attention over it, dense or over page lists
+ *   sls_kv8_evict           the blocks with the most attention weight kept
  *
  * Conventions shared by every call
  * --------------------------------

@@ -1,5 +1,11 @@
 // The 8-bit cache's writers: appending tokens (quantising the blocks they
 // complete) and evicting blocks by accumulated attention weight.
+//
+// Both are bound by memory on prompts: four prompts of up to 32k tokens, 8 heads of
+// 128 channels, with page min/max: 122 us for 813 MB (98% of the measured copy); 8 x 4
+// rows cut from 32k tokens to 16k: 50 us for 269 MB, of which the copies take 41 (97%)
+// and the choice before them the rest.  Single tokens and small caches are launches:
+// 3.8 us for 32 sequences' tokens, 7 us for a small eviction.
 #include <algorithm>
 
 #include "common.cuh"
