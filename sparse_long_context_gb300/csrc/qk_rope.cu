@@ -2,20 +2,23 @@
 // token's position in one pass over the projected heads:
 //   y = x w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin).
 // Bound by memory: every element is read and written once.  32768 tokens of 28 + 4
-// heads of 128 channels take 90 us (5.95 TB/s, 88% of the measured copy); 32
-// tokens of 12 + 2 heads 3 us, the launch.  Rings of asynchronous copies or of
-// registers in place of the plain loads were slower (115 and 109 us): what is
-// in flight was enough, resident warps were not.
+// heads of 128 channels take 92 us (5.8 TB/s, 86% of the measured copy), 16384 in
+// fp32 with half of the channels rotated 85 us (93%), 1000 tokens 6.2 us, 32 tokens of
+// 12 + 2 heads 3 us, the launch.
 //
-// A head is D/8 lanes of eight channels each, so a warp takes 256 / D heads at a
-// time.  A lane's channels are two vectors of four that form whole pairs (channels
-// 4l and R/2 + 4l when halves are paired), so a pair never leaves the lane and a
-// lane needs four angles.  With the norm's weights the rotation of a pair is
+// A lane holds two 16-byte vectors of a head whose channels form whole pairs (vector
+// l and vector R/2 further on when halves are paired), so a pair never leaves the
+// lane; at D = 128 in bf16 a head is 8 lanes and a warp takes 4 heads at a time.  With
+// the norm's weights the rotation of a pair is
 //   y_a = inv (x_a w_a cos - x_b w_b sin),  y_b = inv (x_b w_b cos + x_a w_a sin),
 // whose four products of weight, cosine and sine are formed once per token for all
 // of its query heads and once for its key heads; channels that are not rotated
 // have cos = 1, sin = 0.  Issue slots come next after memory, so the arithmetic is
-// in two-float instructions.  The loads of four steps are in flight together.
+// in two-float instructions and the sines are shared by the lanes that need the same.
+// The loads of four steps are in flight together.  Measured against it: vectors of 8
+// bytes (half as wide steps; 90 us on the bf16 prompt, but 7.8 on 1000 tokens and 95 in
+// fp32), rings of asynchronous copies (115) and of registers (109), L2 prefetches of the
+// next token (110).
 //
 // Angles are kept in turns: positions[t] * f_i modulo one turn is the low 64
 // bits of the product with the frequency as a 64-bit fixed-point fraction
@@ -28,24 +31,16 @@
 
 namespace sls {
 
-constexpr int kRopeThreads = 128, kRopePerSm = 7;  // 4 to 8 CTAs per SM: 100 to 90 us on 32768 tokens
+constexpr int kRopeThreads = 128, kRopePerSm = 4;  // more CTAs per SM spill: 118 us at 7
 constexpr int kRopeUnroll = 4;  // warp steps whose loads are in flight together
 
-template <typename T> struct Vec4;
-template <> struct Vec4<float> { using type = uint4; };
-template <> struct Vec4<bf16> { using type = uint2; };
-
-// Four channels, not kept in L1 (plain loads: the outputs may be the inputs).
-__device__ __forceinline__ uint4 rope_load(const float* p) {
+// A 16-byte vector, not kept in L1 (plain loads: the outputs may be the inputs).
+__device__ __forceinline__ uint4 rope_load(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
-__device__ __forceinline__ uint2 rope_load(const bf16* p) {
-  uint2 r;
-  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
+
 // Two floats in one 64-bit register: products and sums of both at once.
 using F2 = unsigned long long;
 __device__ __forceinline__ F2 f2(float lo, float hi) {
@@ -66,77 +61,91 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-
-__device__ __forceinline__ void rope_unpack(uint4 v, F2& a, F2& b) {
-  a = f2(__uint_as_float(v.x), __uint_as_float(v.y));
-  b = f2(__uint_as_float(v.z), __uint_as_float(v.w));
-}
-__device__ __forceinline__ void rope_unpack(uint2 v, F2& a, F2& b) {
-  a = f2(bf16lo(v.x), bf16hi(v.x));
-  b = f2(bf16lo(v.y), bf16hi(v.y));
-}
-__device__ __forceinline__ void rope_store(float* p, F2 a, F2 b) {
-  float4 y;
-  f2_split(a, y.x, y.y);
-  f2_split(b, y.z, y.w);
-  *reinterpret_cast<float4*>(p) = y;
-}
-__device__ __forceinline__ void rope_store(bf16* p, F2 a, F2 b) {
-  float4 y;
-  f2_split(a, y.x, y.y);
-  f2_split(b, y.z, y.w);
-  __nv_bfloat162 u = __floats2bfloat162_rn(y.x, y.y), v = __floats2bfloat162_rn(y.z, y.w);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&u), *reinterpret_cast<uint32_t*>(&v));
-}
-
-// What one side's heads are multiplied by for a token: the lane's eight channels
-// are x = (x0 x1 | x2 x3) and z, and
-//   paired halves:  y = x A + z B,  v = z C + x E        (pair i: x_i with z_i)
-//   interleaved:    y = x A + swap(x) B,  v = z C + swap(z) E
-struct RopeCoef {
-  F2 A[2], B[2], C[2], E[2];
-};
-template <typename T, bool INTER>
-__device__ __forceinline__ RopeCoef rope_coef(const T* w, int c0, int c1, const float (&cs)[4], const float (&sn)[4]) {
-  float wx[4], wz[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    wx[i] = w ? to_f32(w[c0 + i]) : 1.f;
-    wz[i] = w ? to_f32(w[c1 + i]) : 1.f;
-  }
-  RopeCoef r;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if constexpr (INTER) {
-      r.A[i] = f2(wx[2 * i] * cs[i], wx[2 * i + 1] * cs[i]);
-      r.B[i] = f2(-wx[2 * i + 1] * sn[i], wx[2 * i] * sn[i]);
-      r.C[i] = f2(wz[2 * i] * cs[i + 2], wz[2 * i + 1] * cs[i + 2]);
-      r.E[i] = f2(-wz[2 * i + 1] * sn[i + 2], wz[2 * i] * sn[i + 2]);
-    } else {
-      const int a = 2 * i, b = a + 1;
-      r.A[i] = f2(wx[a] * cs[a], wx[b] * cs[b]);
-      r.B[i] = f2(-wz[a] * sn[a], -wz[b] * sn[b]);
-      r.C[i] = f2(wz[a] * cs[a], wz[b] * cs[b]);
-      r.E[i] = f2(wx[a] * sn[a], wx[b] * sn[b]);
-    }
-  }
-  return r;
-}
 __device__ __forceinline__ F2 f2_swap(F2 v) {
   float a, b;
   f2_split(v, a, b);
   return f2(b, a);
 }
 
+__device__ __forceinline__ void rope_unpack(const float*, uint4 v, F2 (&x)[2]) {
+  x[0] = f2(__uint_as_float(v.x), __uint_as_float(v.y));
+  x[1] = f2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+__device__ __forceinline__ void rope_unpack(const bf16*, uint4 v, F2 (&x)[4]) {
+  x[0] = f2(bf16lo(v.x), bf16hi(v.x));
+  x[1] = f2(bf16lo(v.y), bf16hi(v.y));
+  x[2] = f2(bf16lo(v.z), bf16hi(v.z));
+  x[3] = f2(bf16lo(v.w), bf16hi(v.w));
+}
+__device__ __forceinline__ void rope_store(float* p, const F2 (&x)[2]) {
+  float4 y;
+  f2_split(x[0], y.x, y.y);
+  f2_split(x[1], y.z, y.w);
+  *reinterpret_cast<float4*>(p) = y;
+}
+__device__ __forceinline__ void rope_store(bf16* p, const F2 (&x)[4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f2_split(x[i], a, b);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    w[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// What one side's heads are multiplied by for a token.  The lane's channels are
+// two vectors x and z of 2 NF, in float pairs, and
+//   paired halves:  y = x A + z B,  v = z C + x E        (pair i: x_i with z_i)
+//   interleaved:    y = x A + swap(x) B,  v = z C + swap(z) E
+template <int NF>
+struct RopeCoef {
+  F2 A[NF], B[NF], C[NF], E[NF];
+};
+template <typename T, bool INTER, int NF>
+__device__ __forceinline__ void rope_coef(RopeCoef<NF>& r, const T* w, int c0, int c1, const float (&cs)[2 * NF],
+                                          const float (&sn)[2 * NF]) {
+  float wx[2 * NF], wz[2 * NF];
+#pragma unroll
+  for (int i = 0; i < 2 * NF; ++i) {
+    wx[i] = w ? to_f32(w[c0 + i]) : 1.f;
+    wz[i] = w ? to_f32(w[c1 + i]) : 1.f;
+  }
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    const int a = 2 * i, b = a + 1;
+    if constexpr (INTER) {  // angle i turns pair (a, b) of x, angle NF + i that of z
+      r.A[i] = f2(wx[a] * cs[i], wx[b] * cs[i]);
+      r.B[i] = f2(-wx[b] * sn[i], wx[a] * sn[i]);
+      r.C[i] = f2(wz[a] * cs[NF + i], wz[b] * cs[NF + i]);
+      r.E[i] = f2(-wz[b] * sn[NF + i], wz[a] * sn[NF + i]);
+    } else {
+      r.A[i] = f2(wx[a] * cs[a], wx[b] * cs[b]);
+      r.B[i] = f2(-wz[a] * sn[a], -wz[b] * sn[b]);
+      r.C[i] = f2(wz[a] * cs[a], wz[b] * cs[b]);
+      r.E[i] = f2(wx[a] * sn[a], wx[b] * sn[b]);
+    }
+  }
+}
+
+// The lanes of a head, and the heads of a warp step.
+template <typename T, int D>
+struct RopeShape {
+  static constexpr int VC = 16 / sizeof(T);  // channels of a vector
+  static constexpr int L = D / (2 * VC), HS = 32 / L;
+};
+
 // Steps [s0, s1) of one side (queries or keys) of a token: step s holds heads
 // s HS .. s HS + HS - 1.  FULL: every channel is rotated.
 template <typename T, int D, bool INTER, bool FULL>
 __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int64_t out_h, const T* w, int heads, int s0,
-                                          int s1, int c0, int c1, const float (&cs)[4], const float (&sn)[4], float eps,
-                                          int sub, bool rot) {
-  constexpr int L = D / 8, HS = 32 / L, U = kRopeUnroll;
-  using V = typename Vec4<T>::type;
-  const RopeCoef k = rope_coef<T, INTER>(w, c0, c1, cs, sn);
+                                          int s1, int c0, int c1, const float (&cs)[16 / sizeof(T)],
+                                          const float (&sn)[16 / sizeof(T)], float eps, int sub, bool rot) {
+  using S = RopeShape<T, D>;
+  constexpr int L = S::L, HS = S::HS, NF = S::VC / 2, U = kRopeUnroll;
+  RopeCoef<NF> k;
+  rope_coef<T, INTER, NF>(k, w, c0, c1, cs, sn);
   int h = s0 * HS + sub;
   const int hend = min(heads, s1 * HS);
   in += h * in_h;
@@ -144,10 +153,10 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
   in_h *= HS;
   out_h *= HS;
   for (int s = s0; s < s1; s += U) {
-    V r0[U], r1[U];
+    uint4 r0[U], r1[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      r0[u] = r1[u] = V{};
+      r0[u] = r1[u] = make_uint4(0u, 0u, 0u, 0u);
       if (h + u * HS < hend) {
         r0[u] = rope_load(in + c0);
         r1[u] = rope_load(in + c1);
@@ -157,12 +166,16 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (s + u < s1) {
-        F2 x[2], z[2];
-        rope_unpack(r0[u], x[0], x[1]);
-        rope_unpack(r1[u], z[0], z[1]);
+        F2 x[NF], z[NF];
+        rope_unpack(in, r0[u], x);
+        rope_unpack(in, r1[u], z);
         float inv = 1.f;
         if (w) {
-          const F2 q = f2_fma(x[0], x[0], f2_fma(x[1], x[1], f2_fma(z[0], z[0], f2_mul(z[1], z[1]))));
+          F2 q = f2_mul(x[0], x[0]);
+#pragma unroll
+          for (int i = 1; i < NF; ++i) q = f2_fma(x[i], x[i], q);
+#pragma unroll
+          for (int i = 0; i < NF; ++i) q = f2_fma(z[i], z[i], q);
           float ss, hi;
           f2_split(q, ss, hi);
           ss += hi;
@@ -171,17 +184,17 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
           inv = rsqrtf(ss * (1.f / D) + eps);
         }
         const F2 iv = f2(inv, inv);
-        F2 y[2], v[2];
+        F2 y[NF], v[NF];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NF; ++i) {
           // channels that are not rotated do not see their neighbour (0 * inf)
           const F2 xo = INTER ? f2_swap(x[i]) : z[i], zo = INTER ? f2_swap(z[i]) : x[i];
           y[i] = f2_mul(f2_fma(FULL || rot ? xo : 0ull, k.B[i], f2_mul(x[i], k.A[i])), iv);
           v[i] = f2_mul(f2_fma(FULL || rot ? zo : 0ull, k.E[i], f2_mul(z[i], k.C[i])), iv);
         }
         if (h + u * HS < hend) {
-          rope_store(out + c0, y[0], y[1]);
-          rope_store(out + c1, v[0], v[1]);
+          rope_store(out + c0, y);
+          rope_store(out + c1, v);
         }
       }
       out += out_h;
@@ -190,18 +203,21 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
   }
 }
 
-// A warp takes items (a token, or one of its `chunks` shares of `per` steps).
+// A warp takes items (a token, or one of its `chunks` shares of `per` steps).  The
+// lanes that hold the same channels of the warp's HS heads share the sines'
+// work: each forms VC / HS (at least one) of the VC angles' and hands them on.
 template <typename T, int D, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
-  constexpr int L = D / 8, HS = 32 / L;
+  using S = RopeShape<T, D>;
+  constexpr int VC = S::VC, L = S::L, HS = S::HS, PER = VC / HS > 1 ? VC / HS : 1;
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
   const int half = FULL ? D / 2 : a.R >> 1;
-  const bool rot = FULL || 8 * l < a.R;  // R is a multiple of 16: a lane is rotated whole or not at all
-  const int c0 = INTER || !rot ? 8 * l : 4 * l, c1 = INTER || !rot ? 8 * l + 4 : half + 4 * l;
-  uint64_t f[4];
+  const bool rot = FULL || 2 * VC * l < a.R;  // R is a multiple of 16: a lane is rotated whole or not at all
+  const int c0 = INTER || !rot ? 2 * VC * l : VC * l, c1 = INTER || !rot ? c0 + VC : half + VC * l;
+  uint64_t f[PER];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = rot ? a.freq[4 * l + i] : 0ull;
+  for (int i = 0; i < PER; ++i) f[i] = rot ? a.freq[VC * l + (sub * PER + i) % VC] : 0ull;
   const int qsteps = (a.Hq + HS - 1) / HS, steps = qsteps + (a.Hkv + HS - 1) / HS;
   pdl_wait_then_release();
   const int64_t warps = (int64_t)gridDim.x * (kRopeThreads / 32), items = (int64_t)a.N * chunks;
@@ -210,11 +226,16 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
     const int s0 = chunks == 1 ? 0 : (int)(it - t * chunks) * per, s1 = min(s0 + per, steps);
     const int pos = a.pos[t];
     if (pos < 0) continue;
-    float cs[4], sn[4];
+    float mc[PER], ms[PER], cs[VC], sn[VC];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < PER; ++i) {
       const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * f[i]);
-      sincospif((float)turn * 1.0842021724855044e-19f, &sn[i], &cs[i]);  // 2^-63: half turns in [-1, 1]
+      sincospif((float)turn * 1.0842021724855044e-19f, &ms[i], &mc[i]);  // 2^-63: half turns in [-1, 1]
+    }
+#pragma unroll
+    for (int i = 0; i < VC; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, mc[i % PER], (i / PER) * L + l);
+      sn[i] = __shfl_sync(0xffffffffu, ms[i % PER], (i / PER) * L + l);
     }
     if (s0 < qsteps)
       rope_side<T, D, INTER, FULL>(static_cast<const T*>(a.q) + t * a.q_t, a.q_h, static_cast<T*>(a.qo) + t * a.qo_t,
@@ -229,7 +250,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
 
 template <typename T, int D, bool INTER>
 static cudaError_t rope_launch(const RopeArgs& a, cudaStream_t st) {
-  constexpr int HS = 256 / D, NW = kRopeThreads / 32;
+  constexpr int HS = RopeShape<T, D>::HS, NW = kRopeThreads / 32;
   const int steps = (a.Hq + HS - 1) / HS + (a.Hkv + HS - 1) / HS;
   // few tokens: a token's heads go to several warps, up to 8 warps per SM
   const int64_t sms = sm_count();
