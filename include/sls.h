@@ -86,7 +86,8 @@ typedef int sls_status;
 #define SLS_FLAG_NO_TMA 2
 /* Test hook of the bounded waits, not for production: in the tensor-map fed
  * kernels (sls_sparse_decode_attend[_combine] on bf16 pages of >= 16 tokens,
- * and the one-launch sls_quest_decode_step), the first CTA of the launch
+ * the one-launch sls_quest_decode_step, and sls_kv8_decode_attend), the first
+ * CTA of the launch
  * announces 16 bytes on its first attend stage that it never requests, and
  * that CTA's waits poll a short while only.  The waits on that stage
  * give up, the first row's outputs become NaN, and the next

@@ -259,7 +259,7 @@ struct Kv8Smem {
   int s_lo[CL ? 1 : kKv8MaxGrid + 1];  // first unit of every CTA's range, and the total
   int s_slot[CL ? 1 : kKv8MaxGrid];
   int s_tmp[32];
-  int s_fail, s_ncontrib, s_last, s_total;
+  int s_fail, s_ncontrib, s_last;
   float s_w[8][64], s_m[8], s_inv[8];
 };
 

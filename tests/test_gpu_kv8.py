@@ -1,5 +1,9 @@
 """The 8-bit cache on the GPU (append, decode attention, eviction and the step built of them) against the plain 64-bit
 forms of tests/kv8_plain.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -9,6 +13,7 @@ from sparse_long_context_gb300 import harness, ops
 from tests import kv8_plain as plain
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def bf16(rng, shape, gain=1.0):
@@ -617,6 +622,53 @@ def test_prompt_steps_eviction_and_replayed_loop_together():
         keys(loop.qkv[:, None], [1, 1])
         check(loop.qkv)
     ops.pipeline_check()
+
+
+FIRST_CALLS = """
+import torch
+from sparse_long_context_gb300 import ops
+torch.manual_seed(3)
+desc = ops.make_desc(3, 6, 2, 128, 16, 1024, torch.bfloat16)
+rope = ops.make_rope(6, 2, 128, torch.bfloat16)
+qkv = torch.randn((3, 400, 10, 128), device="cuda").to(torch.bfloat16)
+pos = torch.arange(400, dtype=torch.int32, device="cuda")
+idx = torch.tensor([[0, 5, 2, -1]] * 6, dtype=torch.int32, device="cuda")
+
+class State:
+    def __init__(self):
+        self.cache = ops.Kv8Cache.empty(desc, "e4m3", 32)
+        self.ctx = torch.zeros(3, dtype=torch.int32, device="cuda")
+        self.mass = torch.zeros((3, 2, 32), device="cuda")
+        self.ws = ops.kv8_attend_workspace(desc, self.cache, mass=True)
+
+    def run(self):
+        q, k = ops.qk_norm_rope(rope, qkv[0, :, :6], qkv[0, :, 6:8], pos)
+        ops.kv8_append(desc, self.cache, qkv[:, :, 6:8], qkv[:, :, 8:], self.ctx, mass=self.mass)
+        ops.kv8_append(desc, self.cache, qkv[:, :1, 6:8], qkv[:, :1, 8:], self.ctx, mass=self.mass)
+        a = ops.kv8_decode_attend(desc, self.cache, qkv[:, 0, :6].contiguous(), self.ctx, mass_in=self.mass,
+                                  mass_out=self.mass, workspace=self.ws)
+        b = ops.kv8_decode_attend(desc, self.cache, qkv[:, 1, :6].contiguous(), self.ctx, page_idx=idx, workspace=self.ws)
+        kept = ops.kv8_evict(desc, self.cache, self.ctx, self.mass, 5, 1, 1)[1]
+        return [q, k, *a, *b, kept]
+
+s, g = State(), torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g):        # the process's first calls
+    out = s.run()
+g.replay()
+torch.cuda.synchronize()
+other = State()
+for x, y in zip(out + [s.ctx, s.mass, s.cache.k_codes], other.run() + [other.ctx, other.mass, other.cache.k_codes]):
+    assert torch.equal(x, y)
+assert s.ctx.tolist() == [5 * 32 + 401 % 32] * 3
+ops.pipeline_check()
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_quest_selection_over_the_8_bit_cache():
