@@ -3,9 +3,9 @@
 //
 // Both are bound by memory on prompts: four prompts of up to 32k tokens, 8 heads of
 // 128 channels, with page min/max: 122 us for 813 MB (98% of the measured copy); 8 x 4
-// rows cut from 32k tokens to 16k: 50 us for 269 MB, of which the copies take 41 (97%)
-// and the choice before them the rest.  Single tokens and small caches are launches:
-// 3.8 us for 32 sequences' tokens, 7 us for a small eviction.
+// rows cut from 32k tokens to 16k: 49 us for 269 MB, of which the copies take 41 (97%)
+// and the choice before them the rest.  Single tokens and small caches are latency:
+// 3.8 us for 32 sequences' tokens, 5.3 us for a small eviction.
 #include <algorithm>
 
 #include "common.cuh"
@@ -376,28 +376,20 @@ __device__ __forceinline__ int cta_scan(int v, int* tmp, int& total) {
   return before + x - v;
 }
 
-// The blocks row `row` keeps, one CTA per row: a forced block's key is the
-// largest, another's is its mass (order-preserving bits).  The keep-th largest
-// key T comes from four 8-bit radix passes over the keys in shared memory (the
-// bins are summed by a scan over the threads, a bin each); keys above T are
-// kept, and keys equal to T from the lowest block up until the list is full.  Bound
-// by the latency of its dozen barriers.
-__global__ void __launch_bounds__(kChooseThreads)
-kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
+// The blocks a row with nb > keep complete blocks keeps: a forced block's key is the
+// largest, another's is its mass (order-preserving bits).  The keep-th largest key T
+// comes from four 8-bit radix passes over the keys in shared memory (the bins are
+// summed by a scan over the threads, a bin each); keys above T are kept, and keys equal
+// to T from the lowest block up until the list is full.  emit(place, block) is called
+// for every kept block, places ascending.  Bound by the latency of its barriers: 4 us.
+struct ChooseSmem {
+  uint32_t key[kChooseStaged];
+  int hist[256], tmp[kChooseThreads / 32], bin, above;
+};
+template <typename Emit>
+__device__ __forceinline__ void choose_blocks(const Kv8Evict& e, const float* mass, int nb, ChooseSmem& sh, Emit emit) {
   constexpr int NT = kChooseThreads;
-  __shared__ uint32_t s_key[kChooseStaged];
-  __shared__ int s_hist[256], s_tmp[NT / 32], s_bin, s_above;
-  pdl_wait_then_release();
-  const int row = blockIdx.x, bsh = e.src.bshift, tid = threadIdx.x;
-  const int N = clamp_len(e.ctx_len[row / Hkv], e.cap), nb = N >> bsh;
-  int32_t* kept = e.kept + (size_t)row * e.keep;
-  const float* mass = e.mass + (size_t)row * (e.cap >> bsh);
-  if (write_len && row % Hkv == 0 && tid == 0)
-    e.ctx_out[row / Hkv] = min(nb, e.keep) * e.src.block + (N & (e.src.block - 1));
-  if (nb <= e.keep) {
-    for (int i = tid; i < e.keep; i += NT) kept[i] = i < nb ? i : -1;
-    return;
-  }
+  const int tid = threadIdx.x;
   auto key_of = [&](int i) -> uint32_t {
     if (i < e.n_sink || i >= nb - e.n_recent) return 0xffffffffu;
     const float m = mass[i] + 0.f;  // -0 counts as 0
@@ -405,30 +397,30 @@ kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
   };
   const int staged = min(nb, kChooseStaged);
 #pragma unroll 4
-  for (int i = tid; i < staged; i += NT) s_key[i] = key_of(i);
-  auto key = [&](int i) { return i < kChooseStaged ? s_key[i] : key_of(i); };
+  for (int i = tid; i < staged; i += NT) sh.key[i] = key_of(i);
+  auto key = [&](int i) { return i < kChooseStaged ? sh.key[i] : key_of(i); };
   uint32_t prefix = 0;
   int left = e.keep;
   for (int shift = 24; shift >= 0; shift -= 8) {
-    s_hist[tid] = 0;
+    sh.hist[tid] = 0;
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
     for (int i = tid; i < nb; i += NT) {
       const uint32_t k = key(i);
-      if ((k & mask) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1);
+      if ((k & mask) == prefix) atomicAdd(&sh.hist[(k >> shift) & 255], 1);
     }
     __syncthreads();
     // thread i holds bin 255 - i; the bin in which the count from the top reaches `left`
-    const int n = s_hist[255 - tid];
+    const int n = sh.hist[255 - tid];
     int total;
-    const int above = cta_scan<NT>(n, s_tmp, total);
+    const int above = cta_scan<NT>(n, sh.tmp, total);
     if (above < left && above + n >= left) {
-      s_bin = 255 - tid;
-      s_above = above;
+      sh.bin = 255 - tid;
+      sh.above = above;
     }
     __syncthreads();
-    left -= s_above;
-    prefix |= (uint32_t)s_bin << shift;
+    left -= sh.above;
+    prefix |= (uint32_t)sh.bin << shift;
   }
   // ascending output: `left` of the keys equal to T (= prefix) are kept
   int base = 0, base_eq = 0;
@@ -437,90 +429,117 @@ kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
     const uint32_t k = i < nb ? key(i) : 0u;
     const bool eq = i < nb && k == prefix, gt = i < nb && k > prefix;
     int total;
-    const int at = cta_scan<NT>((int)gt | (int)eq << 16, s_tmp, total);  // at most NT of each: no carry
+    const int at = cta_scan<NT>((int)gt | (int)eq << 16, sh.tmp, total);  // at most NT of each: no carry
     const int g = base + (at & 0xffff), q = base_eq + (at >> 16);
-    if (gt || (eq && q < left)) kept[g + min(q, left)] = i;
+    if (gt || (eq && q < left)) emit(g + min(q, left), i);
     base += total & 0xffff;
     base_eq += total >> 16;
   }
 }
 
-// Into another cache, in CTAs of three kinds per row, so that the waits of one
-// kind's loads do not add to another's: `parts` of them move `per` kept blocks each
-// (K and V, eight loads of a thread in flight together), then `sums` move kSumItems
-// blocks' scales and sums (the first also the tails), then the rest the page
-// summaries of `meta_items` blocks each.
-constexpr int kMoveBytes = 16384;  // of K (and as many of V) per CTA
-constexpr int kSumItems = 1024;
-__global__ void __launch_bounds__(256)
-kv8_copy_kernel(const Kv8Evict e, int Hkv, int D, int P, int per, int parts, int sums, int metas, int meta_items) {
+__device__ __forceinline__ void evicted_len(const Kv8Evict& e, int b, int N) {
+  e.ctx_out[b] = min(N >> e.src.bshift, e.keep) * e.src.block + (N & (e.src.block - 1));
+}
+
+// The list alone, before blocks move in place: one CTA per row.
+__global__ void __launch_bounds__(kChooseThreads)
+kv8_choose_kernel(const Kv8Evict e, int Hkv, int write_len) {
+  __shared__ ChooseSmem sh;
   pdl_wait_then_release();
-  const int kinds = parts + sums + metas;
-  const int row = blockIdx.x / kinds, x = blockIdx.x % kinds, block = e.src.block, bsh = e.src.bshift;
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int N = clamp_len(e.ctx_len[row / Hkv], e.cap), nb = N >> e.src.bshift;
+  int32_t* kept = e.kept + (size_t)row * e.keep;
+  if (write_len && row % Hkv == 0 && tid == 0) evicted_len(e, row / Hkv, N);
+  if (nb <= e.keep) {
+    for (int i = tid; i < e.keep; i += kChooseThreads) kept[i] = i < nb ? i : -1;
+    return;
+  }
+  choose_blocks(e, e.mass + (size_t)row * (e.cap >> e.src.bshift), nb, sh, [&](int at, int i) { kept[at] = i; });
+}
+
+// Into another cache, choice and copies in one launch: every CTA of a row makes the
+// row's choice for itself (4 us side by side, against a launch between the two) and
+// copies the items [i0, i0 + per) of the list; the row's first CTA writes the list and
+// the length, and copies the tails.  Eight loads of a thread are in flight together.
+constexpr int kEvictSlice = 2048;  // list entries a CTA keeps
+constexpr int kEvictPerSm = 2;     // CTAs per SM of the launch (3 to 8: up to 10% slower on prompts, 50% on small caches)
+__global__ void __launch_bounds__(kChooseThreads)
+kv8_evict_copy_kernel(const Kv8Evict e, int Hkv, int D, int P, int per, int parts, int write_len) {
+  constexpr int NT = kChooseThreads, U = 4;
+  __shared__ ChooseSmem sh;
+  __shared__ int s_kept[kEvictSlice];
+  pdl_wait_then_release();
+  const int row = blockIdx.x / parts, part = blockIdx.x % parts, block = e.src.block, bsh = e.src.bshift;
+  const int tid = threadIdx.x;
   const int N = clamp_len(e.ctx_len[row / Hkv], e.cap);
-  const int nb = N >> bsh, n = min(nb, e.keep), rest = N & (block - 1), tid = threadIdx.x;
+  const int nb = N >> bsh, n = min(nb, e.keep), rest = N & (block - 1);
   const size_t srow = (size_t)row * (e.cap >> bsh), drow = (size_t)row * (e.dcap >> bsh);
-  const int32_t* kept = e.kept + (size_t)row * e.keep;
-  if (x < parts) {
-    const int vecs = block * D / 16, vsh = __ffs(vecs) - 1;  // 16-byte vectors of a block's codes, a power of two
-    const int i0 = x * per, i1 = min(n, i0 + per);
-    constexpr int U = 4;
-    for (int x0 = 0; x0 < (i1 - i0) * vecs; x0 += 256 * U) {
-      uint4 k[U], v[U];
-      size_t to[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int w = x0 + u * 256 + tid;
-        if (w < (i1 - i0) * vecs) {
-          const int it = i0 + (w >> vsh), c = w & (vecs - 1);
-          const size_t from = (srow + kept[it]) * vecs + c;
-          to[u] = (drow + it) * vecs + c;
-          k[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.kc) + from);
-          v[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.vc) + from);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (x0 + u * 256 + tid < (i1 - i0) * vecs) {
-          reinterpret_cast<uint4*>(e.dst.kc)[to[u]] = k[u];
-          reinterpret_cast<uint4*>(e.dst.vc)[to[u]] = v[u];
-        }
-    }
-  } else if (x < parts + sums) {
-    const int i0 = (x - parts) * kSumItems, i1 = min(n, i0 + kSumItems);
-#pragma unroll 4
-    for (int i = i0 + tid; i < i1; i += 256) {
-      const size_t from = srow + kept[i], to = drow + i;
-      const float a = e.src.ks[from], b = e.src.vs[from], m = e.mass_out ? e.mass[from] : 0.f;
-      e.dst.ks[to] = a;
-      e.dst.vs[to] = b;
-      if (e.mass_out) e.mass_out[to] = m;
-    }
-    if (x == parts) {
-      const size_t t0 = (size_t)row * block * D / 8;
+  const int i0 = part * per, i1 = min(n, i0 + per);
+  int32_t* kept = e.kept + (size_t)row * e.keep;
+  if (part == 0) {
+    if (write_len && row % Hkv == 0 && tid == 0) evicted_len(e, row / Hkv, N);
+    const size_t t0 = (size_t)row * block * D / 8;
 #pragma unroll 2
-      for (int i = tid; i < rest * D / 8; i += 256) {
-        const uint4 a = static_cast<const uint4*>(e.src.kt)[t0 + i], b = static_cast<const uint4*>(e.src.vt)[t0 + i];
-        static_cast<uint4*>(e.dst.kt)[t0 + i] = a;
-        static_cast<uint4*>(e.dst.vt)[t0 + i] = b;
+    for (int i = tid; i < rest * D / 8; i += NT) {
+      const uint4 a = static_cast<const uint4*>(e.src.kt)[t0 + i], b = static_cast<const uint4*>(e.src.vt)[t0 + i];
+      static_cast<uint4*>(e.dst.kt)[t0 + i] = a;
+      static_cast<uint4*>(e.dst.vt)[t0 + i] = b;
+    }
+    if (nb <= e.keep)
+      for (int i = tid; i < e.keep; i += NT) kept[i] = i < nb ? i : -1;
+  }
+  if (nb <= e.keep) {
+    for (int i = i0 + tid; i < i1; i += NT) s_kept[i - i0] = i;
+  } else {
+    choose_blocks(e, e.mass + srow, nb, sh, [&](int at, int i) {
+      if (at >= i0 && at < i1) s_kept[at - i0] = i;
+      if (part == 0) kept[at] = i;
+    });
+  }
+  __syncthreads();
+  for (int i = i0 + tid; i < i1; i += NT) {
+    const size_t from = srow + s_kept[i - i0], to = drow + i;
+    const float a = e.src.ks[from], b = e.src.vs[from], m = e.mass_out ? e.mass[from] : 0.f;
+    e.dst.ks[to] = a;
+    e.dst.vs[to] = b;
+    if (e.mass_out) e.mass_out[to] = m;
+  }
+  const int vecs = block * D / 16, vsh = __ffs(vecs) - 1;  // 16-byte vectors of a block's codes, a power of two
+  for (int x0 = 0; x0 < (i1 - i0) << vsh; x0 += NT * U) {
+    uint4 k[U], v[U];
+    size_t to[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int w = x0 + u * NT + tid;
+      if (w < (i1 - i0) << vsh) {
+        const int it = w >> vsh, c = w & (vecs - 1);
+        const size_t from = (srow + s_kept[it]) * vecs + c;
+        to[u] = (drow + i0 + it) * vecs + c;
+        k[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.kc) + from);
+        v[u] = ldg_stream(reinterpret_cast<const uint4*>(e.src.vc) + from);
       }
     }
-  } else {
-    const int item = block / P * D / 8;  // 16-byte vectors of a block's page summaries, a power of two
-    const int ish = __ffs(item) - 1;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (x0 + u * NT + tid < (i1 - i0) << vsh) {
+        reinterpret_cast<uint4*>(e.dst.kc)[to[u]] = k[u];
+        reinterpret_cast<uint4*>(e.dst.vc)[to[u]] = v[u];
+      }
+  }
+  if (e.kmin) {
+    const int item = block / P * D / 8, ish = __ffs(item) - 1;  // 16-byte vectors of a block's page summaries
     const uint4 *smin = static_cast<const uint4*>(e.kmin) + srow * item, *smax = static_cast<const uint4*>(e.kmax) + srow * item;
     uint4 *dmin = static_cast<uint4*>(e.kmin_out) + drow * item, *dmax = static_cast<uint4*>(e.kmax_out) + drow * item;
-    const int i0 = (x - parts - sums) * meta_items, i1 = min(n, i0 + meta_items);
 #pragma unroll 4
-    for (int w = tid; w < (i1 - i0) << ish; w += 256) {
-      const int it = i0 + (w >> ish), c = w & (item - 1);
-      const size_t from = (size_t)kept[it] * item + c, to = (size_t)it * item + c;
+    for (int w = tid; w < (i1 - i0) << ish; w += NT) {
+      const int it = w >> ish, c = w & (item - 1);
+      const size_t from = (size_t)s_kept[it] * item + c, to = (size_t)(i0 + it) * item + c;
       const uint4 a = smin[from], b = smax[from];
       dmin[to] = a;
       dmax[to] = b;
     }
-    if (i0 == 0)  // the pages of the newest, partial block
-      for (int w = tid; w < (rest + P - 1) / P * D / 8; w += 256) {
+    if (part == 0)  // the pages of the newest, partial block
+      for (int w = tid; w < (rest + P - 1) / P * D / 8; w += NT) {
         const uint4 a = smin[(size_t)nb * item + w], b = smax[(size_t)nb * item + w];
         dmin[(size_t)n * item + w] = a;
         dmax[(size_t)n * item + w] = b;
@@ -608,8 +627,7 @@ __global__ void kv8_evicted_len_kernel(const Kv8Evict e, int B) {
   pdl_wait_then_release();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b >= B) return;
-  const int N = clamp_len(e.ctx_len[b], e.cap);
-  e.ctx_out[b] = min(N >> e.src.bshift, e.keep) * e.src.block + (N & (e.src.block - 1));
+  evicted_len(e, b, clamp_len(e.ctx_len[b], e.cap));
 }
 
 cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st) {
@@ -618,24 +636,23 @@ cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st)
   // the ones that are read, else last
   const uintptr_t x = (uintptr_t)e.ctx_out, y = (uintptr_t)e.ctx_len, n4 = (uintptr_t)s.B * 4;
   const bool apart = x + n4 <= y || y + n4 <= x;
-  cudaError_t r = launch_pdl(kv8_choose_kernel, dim3(rows), dim3(kChooseThreads), 0, st, e, s.Hkv, (int)apart);
-  if (r != cudaSuccess) return r;
-  const int bytes = e.src.block * s.D;
+  cudaError_t r;
   if (e.in_place) {
+    r = launch_pdl(kv8_choose_kernel, dim3(rows), dim3(kChooseThreads), 0, st, e, s.Hkv, (int)apart);
+    if (r != cudaSuccess) return r;
     // enough CTAs for the GPU, each at least 64 bytes wide
+    const int bytes = e.src.block * s.D;
     int slices = 1;
     while (rows * 2 * slices < 2 * sm_count() && bytes / 16 / (2 * slices) >= 4) slices *= 2;
     const int parts = 2 * slices + (e.kmin ? 3 : 1);
     r = launch_pdl(kv8_move_kernel, dim3((unsigned)rows * parts), dim3(kMoveThreads), 0, st, e, s.Hkv, s.D, s.P, slices,
                    parts);
   } else {
-    const int per = std::max(1, kMoveBytes / bytes), parts = (e.keep + per - 1) / per;
-    const int sums = (e.keep + kSumItems - 1) / kSumItems;
-    // four vectors of kmin and of kmax a thread
-    const int meta_items = e.kmin ? std::max(1, 1024 / (e.src.block / s.P * s.D / 8)) : 1;
-    const int metas = e.kmin ? (e.keep + meta_items - 1) / meta_items : 0;
-    r = launch_pdl(kv8_copy_kernel, dim3((unsigned)rows * (parts + sums + metas)), dim3(256), 0, st, e, s.Hkv, s.D, s.P,
-                   per, parts, sums, metas, meta_items);
+    // one wave of CTAs, each with a slice of the list that fits its shared memory
+    const long long want = std::max(1, kEvictPerSm * sm_count() / rows);
+    const int per = (int)std::min<long long>(kEvictSlice, (e.keep + want - 1) / want), parts = (e.keep + per - 1) / per;
+    r = launch_pdl(kv8_evict_copy_kernel, dim3((unsigned)rows * parts), dim3(kChooseThreads), 0, st, e, s.Hkv, s.D, s.P,
+                   per, parts, (int)apart);
   }
   if (r == cudaSuccess && !apart)
     r = launch_pdl(kv8_evicted_len_kernel, dim3((s.B + 127) / 128), dim3(128), 0, st, e, s.B);
