@@ -134,18 +134,27 @@ template <typename T, int D>
 struct RopeShape {
   static constexpr int VC = 16 / sizeof(T);  // channels of a vector
   static constexpr int L = D / (2 * VC), HS = 32 / L;
+  static constexpr int PER = VC / HS > 1 ? VC / HS : 1;  // angles whose sines a lane forms
 };
 
 // Steps [s0, s1) of one side (queries or keys) of a token: step s holds heads
 // s HS .. s HS + HS - 1.  FULL: every channel is rotated.
 template <typename T, int D, bool INTER, bool FULL>
 __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int64_t out_h, const T* w, int heads, int s0,
-                                          int s1, int c0, int c1, const float (&cs)[16 / sizeof(T)],
-                                          const float (&sn)[16 / sizeof(T)], float eps, int sub, bool rot) {
+                                          int s1, int c0, int c1, const float (&mc)[RopeShape<T, D>::PER],
+                                          const float (&ms)[RopeShape<T, D>::PER], float eps, int sub, bool rot) {
   using S = RopeShape<T, D>;
-  constexpr int L = S::L, HS = S::HS, NF = S::VC / 2, U = kRopeUnroll;
+  constexpr int L = S::L, HS = S::HS, NF = S::VC / 2, U = kRopeUnroll, PER = S::PER;
   RopeCoef<NF> k;
-  rope_coef<T, INTER, NF>(k, w, c0, c1, cs, sn);
+  {
+    float cs[S::VC], sn[S::VC];
+#pragma unroll
+    for (int i = 0; i < S::VC; ++i) {
+      cs[i] = __shfl_sync(0xffffffffu, mc[i % PER], (i / PER) * L + (threadIdx.x & 31) % L);
+      sn[i] = __shfl_sync(0xffffffffu, ms[i % PER], (i / PER) * L + (threadIdx.x & 31) % L);
+    }
+    rope_coef<T, INTER, NF>(k, w, c0, c1, cs, sn);
+  }
   int h = s0 * HS + sub;
   const int hend = min(heads, s1 * HS);
   in += h * in_h;
@@ -210,7 +219,7 @@ template <typename T, int D, bool INTER, bool FULL>
 __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
   using S = RopeShape<T, D>;
-  constexpr int VC = S::VC, L = S::L, HS = S::HS, PER = VC / HS > 1 ? VC / HS : 1;
+  constexpr int VC = S::VC, L = S::L, HS = S::HS, PER = S::PER;
   const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
   const int half = FULL ? D / 2 : a.R >> 1;
   const bool rot = FULL || 2 * VC * l < a.R;  // R is a multiple of 16: a lane is rotated whole or not at all
@@ -226,25 +235,20 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
     const int s0 = chunks == 1 ? 0 : (int)(it - t * chunks) * per, s1 = min(s0 + per, steps);
     const int pos = a.pos[t];
     if (pos < 0) continue;
-    float mc[PER], ms[PER], cs[VC], sn[VC];
+    float mc[PER], ms[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * f[i]);
       sincospif((float)turn * 1.0842021724855044e-19f, &ms[i], &mc[i]);  // 2^-63: half turns in [-1, 1]
     }
-#pragma unroll
-    for (int i = 0; i < VC; ++i) {
-      cs[i] = __shfl_sync(0xffffffffu, mc[i % PER], (i / PER) * L + l);
-      sn[i] = __shfl_sync(0xffffffffu, ms[i % PER], (i / PER) * L + l);
-    }
     if (s0 < qsteps)
       rope_side<T, D, INTER, FULL>(static_cast<const T*>(a.q) + t * a.q_t, a.q_h, static_cast<T*>(a.qo) + t * a.qo_t,
-                                   a.qo_h, static_cast<const T*>(a.wq), a.Hq, s0, min(s1, qsteps), c0, c1, cs, sn, a.eps,
+                                   a.qo_h, static_cast<const T*>(a.wq), a.Hq, s0, min(s1, qsteps), c0, c1, mc, ms, a.eps,
                                    sub, rot);
     if (s1 > qsteps)
       rope_side<T, D, INTER, FULL>(static_cast<const T*>(a.k) + t * a.k_t, a.k_h, static_cast<T*>(a.ko) + t * a.ko_t,
                                    a.ko_h, static_cast<const T*>(a.wk), a.Hkv, max(s0 - qsteps, 0), s1 - qsteps, c0, c1,
-                                   cs, sn, a.eps, sub, rot);
+                                   mc, ms, a.eps, sub, rot);
   }
 }
 
