@@ -51,13 +51,6 @@ constexpr int kKv8PerSm = 1;       // resident CTAs of an SM
 // Least units of a CTA: a shorter job uses fewer CTAs (1, 2, 4, 8 and 12 units: 14.4,
 // 12.7, 11.8, 13.1 and 13.6 us for 1000 tokens of 4 heads).
 constexpr int kKv8MinUnits = 4;
-// Rows of at most so many tokens (capacity, or the longest list) go to the
-// cluster kernel: rows that are known to be of one length (a single sequence,
-// lists of a fixed length), and others, of which a long one may then keep one
-// cluster busy after the rest.  Against the ranges over all rows, even rows:
-// 6.9 to 11.9 us at 1k tokens of 8 rows, 20.8 to 25.5 at 8k of 32, 30.3 to 34.5 at
-// 16k of 32, 17.6 to 22.4 at 32k of 8, 34.4 to 31.3 at 32k of 16.
-constexpr long long kKv8ClusterEven = 32768, kKv8ClusterUneven = 8192;
 // Work of a row change (drain, merge, partial and refill) in tokens: 512 to 4096
 // measured on seven shapes, 2048 the best or within 2% of it on six (64k x 32 dense
 // 142 us at 1024, 140 at 2048, 144 at 4096).
@@ -254,13 +247,14 @@ struct Kv8Tail {
   }
 };
 
+constexpr int kKv8Weights = 160;  // contributors of a row whose weights are kept (all SMs of a GB300)
 template <bool CL>
 struct Kv8Smem {
   int s_lo[CL ? 1 : kKv8MaxGrid + 1];  // first unit of every CTA's range, and the total
   int s_slot[CL ? 1 : kKv8MaxGrid];
   int s_tmp[32];
   int s_fail, s_ncontrib, s_last;
-  float s_w[8][64], s_m[8], s_inv[8];
+  float s_w[8][CL ? 1 : kKv8Weights], s_m[8], s_inv[8];
 };
 
 // Final output of head g, channel d: accumulator av and sum lv relative to
@@ -778,7 +772,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       __syncthreads();
       if (sh.s_last) {
         const int n = sh.s_ncontrib;
-        // a thread per four channels of a head; the first eight contributors'
+        // a thread per four channels of a head; the first sixteen contributors'
         // values are in flight while the weights are formed
         static_assert(8 * D / 4 <= NT, "one float4 of the output a thread");
         const int g4 = threadIdx.x / (D / 4), d4 = threadIdx.x % (D / 4);
@@ -786,31 +780,34 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           return jj < n && g4 < G ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[jj] * G + g4) * D) + d4)
                                   : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        float4 v[8];
+        constexpr int U = 16, H = kKv8Weights / 32;
+        float4 v[U];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = part(u);
+        for (int u = 0; u < U; ++u) v[u] = part(u);
         for (int g = warp; g < G; g += W) {
-          // the first 64 contributors' max and sum in registers, loaded at once
-          float pm[2], pl[2];
+          // the contributors' max and sum in registers, loaded at once
+          float pm[H], pl[H];
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < H; ++u) {
             const int jj = lane + 32 * u;
             pm[u] = jj < n ? __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g) : kNegInf;
             pl[u] = jj < n ? __ldcg(a.pl + (size_t)sh.s_slot[jj] * G + g) : 0.f;
           }
-          float M = fmaxf(pm[0], pm[1]), Ls = 0.f;
-          for (int jj = lane + 64; jj < n; jj += 32) M = fmaxf(M, __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g));
+          float M = pm[0], Ls = 0.f;
+#pragma unroll
+          for (int u = 1; u < H; ++u) M = fmaxf(M, pm[u]);
+          for (int jj = lane + kKv8Weights; jj < n; jj += 32) M = fmaxf(M, __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g));
           M = warp_max(M);
           const float sk = a.sink ? a.sink[h * G + g] * kLog2e : kNegInf;
           M = fmaxf(M, sk);
           auto weight = [&](float ms) { return (ms == kNegInf || M == kNegInf) ? 0.f : kv8_ex2(ms - M); };
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < H; ++u) {
             const float w = weight(pm[u]);
             Ls += pl[u] * w;
             if (lane + 32 * u < n) sh.s_w[g][lane + 32 * u] = w;
           }
-          for (int jj = lane + 64; jj < n; jj += 32) {
+          for (int jj = lane + kKv8Weights; jj < n; jj += 32) {
             const size_t at = (size_t)sh.s_slot[jj] * G + g;
             Ls += __ldcg(a.pl + at) * weight(__ldcg(a.pm + at));
           }
@@ -828,16 +825,16 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         __syncthreads();
         if (g4 < G) {
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j0 = 0; j0 < n; j0 += 8) {
+          for (int j0 = 0; j0 < n; j0 += U) {
             if (j0)
 #pragma unroll
-              for (int u = 0; u < 8; ++u) v[u] = part(j0 + u);
+              for (int u = 0; u < U; ++u) v[u] = part(j0 + u);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < U; ++u) {
               const int jj = j0 + u;
               if (jj >= n) break;
               float w;
-              if (jj < 64) {
+              if (jj < kKv8Weights) {
                 w = sh.s_w[g4][jj];
               } else {
                 const float ms = __ldcg(a.pm + (size_t)sh.s_slot[jj] * G + g4);
@@ -981,36 +978,60 @@ static cudaError_t kv8_prepare(Kv8Device** out) {
   return cudaSuccess;
 }
 
-// CTAs per row of the cluster kernel: the most that let all rows' clusters run
-// at once; 0 when not even clusters of two do.
+// Clusters of c CTAs of the cluster kernel that run at once (asked once per device).
 template <int D, int FMT, bool LIST, bool MASS>
-static int kv8_cluster(int rows, Kv8Device* d) {
+static int kv8_clusters(int c, Kv8Device* d) {
   using F = Kv8Config<D, FMT>;
-  for (int c = std::min(kKv8MaxCluster, sm_count() / rows); c >= 2; --c) {
-    int n = d->clusters[c].load(std::memory_order_relaxed);
-    if (n == 0) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(c);
-      cfg.blockDim = dim3(F::W * 32);
-      cfg.dynamicSmemBytes = F::smem(0);
-      cudaLaunchAttribute attr;
-      attr.id = cudaLaunchAttributeClusterDimension;
-      attr.val.clusterDim.x = c;
-      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-      cfg.attrs = &attr;
-      cfg.numAttrs = 1;
-      int got = 0;
-      auto kern = kv8_attend_kernel<D, FMT, F::SG, F::W, F::S, LIST, MASS, true>;
-      if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        got = 0;
-      }
-      n = 1 + got;
-      d->clusters[c].store(n, std::memory_order_relaxed);
+  int n = d->clusters[c].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(F::W * 32);
+    cfg.dynamicSmemBytes = F::smem(0);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    auto kern = kv8_attend_kernel<D, FMT, F::SG, F::W, F::S, LIST, MASS, true>;
+    if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      got = 0;
     }
-    if (n - 1 >= rows) return c;
+    n = 1 + got;
+    d->clusters[c].store(n, std::memory_order_relaxed);
   }
-  return 0;
+  return n - 1;
+}
+
+// CTAs per row of the cluster kernel, or 0 for ranges over all rows: whichever the
+// measured costs make faster.  A CTA takes t ns a token (4.9 at D = 128, 2.7 at
+// D = 64) and a cluster 5.5 us besides, in as many waves as the clusters need; the
+// ranges take 13 us, 6 per row beyond their equal shares, and 0.1 for each CTA that shares
+// a row.  Fitted to 50 shapes of 1
+// to 256 rows of 1k to 64k tokens, which it times within 10% or so: 96 rows of 4k at
+// D = 128 take 27 us with a CTA each and 30 in ranges, 16k 87 and 66; 64 rows of 16k at
+// D = 64 29 with two each and 32 in ranges, 64k 94 and 86.  `most` bounds a row's
+// tokens; where only the device knows them, rows are taken to hold three quarters
+// of it on average and a cluster to wait for one that is full.
+template <int D, int FMT, bool LIST, bool MASS>
+static int kv8_pick(int rows, double most, bool fixed, bool even, Kv8Device* d) {
+  const double t = D == 128 ? 4.9e-3 : 2.7e-3, sms = sm_count();
+  const double mean = fixed ? most : 0.75 * most, longest = even ? mean : most;
+  double best = 13.0 + rows / sms * (mean * t + 6.0) + 0.1 * sms / rows;
+  int pick = 0;
+  for (int c = 1; c <= kKv8MaxCluster; ++c) {
+    const int n = c == 1 ? sm_count() : kv8_clusters<D, FMT, LIST, MASS>(c, d);
+    if (n < 1) continue;
+    const double us = ((rows + n - 1) / n) * (5.5 + longest / c * t);
+    if (us < best) {
+      best = us;
+      pick = c;
+    }
+  }
+  return pick;
 }
 
 template <int D, int FMT, bool LIST, bool MASS>
@@ -1023,16 +1044,14 @@ static cudaError_t kv8_launch(Kv8Attend a, cudaStream_t st) {
   if (!kv8_map(&tk, a.c.kc, tokens, D, 16 * SG / a.boxes) || !kv8_map(&tv, a.c.vc, tokens, D, 16 * SG / a.boxes))
     return cudaErrorInvalidValue;
   Kv8Device* d;
-  cudaError_t e;
-  const long long most = LIST ? (long long)(a.count ? a.idx_stride : a.k_fixed) << a.pshift : a.Cap;  // tokens of a row
-  const bool even = a.rows == a.Hkv || (LIST && !a.count);
-  if (most <= (even ? kKv8ClusterEven : kKv8ClusterUneven) && a.rows * 2 <= sm_count()) {
-    if ((e = kv8_prepare<D, FMT, LIST, MASS, true>(&d)) != cudaSuccess) return e;
-    a.cluster = kv8_cluster<D, FMT, LIST, MASS>(a.rows, d);
-    if (a.cluster)
-      return launch_pdl_cluster(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS, true>, dim3(a.rows * a.cluster),
-                                dim3(W * 32), F::smem(0), a.cluster, st, tk, tv, a);
-  }
+  cudaError_t e = kv8_prepare<D, FMT, LIST, MASS, true>(&d);
+  if (e != cudaSuccess) return e;
+  const bool fixed = LIST && !a.count;  // lists of one length; one sequence's rows are of one length too
+  const double most = LIST ? (double)(a.count ? a.idx_stride : a.k_fixed) * a.P : a.Cap;
+  a.cluster = kv8_pick<D, FMT, LIST, MASS>(a.rows, most, fixed, fixed || (!LIST && a.rows == a.Hkv), d);
+  if (a.cluster)
+    return launch_pdl_cluster(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS, true>, dim3(a.rows * a.cluster),
+                              dim3(W * 32), F::smem(0), a.cluster, st, tk, tv, a);
   if ((e = kv8_prepare<D, FMT, LIST, MASS, false>(&d)) != cudaSuccess) return e;
   return launch_pdl(kv8_attend_kernel<D, FMT, SG, W, S, LIST, MASS, false>, dim3(kv8_grid()), dim3(W * 32),
                     F::smem(a.rows), st, tk, tv, a);

@@ -363,10 +363,11 @@ def test_attend_long_rows_many_rows_and_reused_workspace():
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
 @pytest.mark.parametrize("d,block", [(64, 16), (64, 32), (128, 16), (128, 64)])
-def test_attend_long_uneven_rows(fmt, d, block):
-    """Capacities past the cluster kernel's: every CTA takes a range of all rows' tokens, most of them cross rows."""
+@pytest.mark.parametrize("cap", [9216, 262144])  # clusters; ranges
+def test_attend_long_uneven_rows(fmt, d, block, cap):
+    """Capacities past the cluster kernel's: every CTA takes a range of all rows' tokens, many of them cross rows."""
     lens = [9000, 0, 31, 8001, 1, 257, 4096, 17]
-    p = Pair(8, 10, 2, d, 9216, fmt, block, seed=d + block)
+    p = Pair(8, 10, 2, d, cap, fmt, block, seed=d + block)
     p.append(lens)
     ws = ops.kv8_attend_workspace(p.desc, p.cache, mass=True)
     for seed in range(2):
@@ -391,6 +392,10 @@ def test_attend_page_lists_of_few_and_many_rows(fmt, d, page, block, batch, hkv)
         idx[r, rng.permutation(npg + 2)[:len(some)]] = some
     attention(p, query(p, 1), pages=(ints(idx), None))
     attention(p, query(p, 2), pages=(ints(idx), ints(rng.integers(-1, npg + 4, batch * hkv))))
+    # in long buffers of lists, of which only the counted entries are read: ranges over all rows
+    wide = np.full((batch * hkv, 400000 // page), 1 << 30)
+    wide[:, :npg + 2] = idx
+    attention(p, query(p, 3), pages=(ints(wide), ints(rng.integers(-1, npg + 3, batch * hkv))))
 
 
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])

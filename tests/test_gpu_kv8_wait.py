@@ -10,7 +10,7 @@ from sparse_long_context_gb300 import ops
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("cap", [4096, 16384])  # a cluster per row; ranges over all rows
+@pytest.mark.parametrize("cap", [4096, 1 << 20])  # a cluster per row; ranges over all rows
 def test_wait_timeout_poisons_the_first_row_only(cap):
     rng = np.random.default_rng(0)
     mk = lambda **kw: ops.make_desc(4, 6, 1, 128, 16, cap, torch.bfloat16, **kw)  # noqa: E731
