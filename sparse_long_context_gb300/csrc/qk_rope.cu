@@ -2,9 +2,11 @@
 // token's position in one pass over the projected heads:
 //   y = x w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin).
 // Bound by memory: every element is read and written once.  32768 tokens of 28 + 4
-// heads of 128 channels take 92 us (5.8 TB/s, 86% of the measured copy), 16384 in
+// heads of 128 channels take 91 us (5.9 TB/s, 87% of the measured copy), 16384 in
 // fp32 with half of the channels rotated 85 us (93%), 1000 tokens 6.2 us, 32 tokens of
-// 12 + 2 heads 3 us, the launch.
+// 12 + 2 heads 2.8 us, the launch.  Tokens of few heads are bound by the sines and
+// coefficients, which are a token's whatever its heads: 16384 tokens of 8 + 1 heads 20 us
+// (floor 11).
 //
 // A lane holds two 16-byte vectors of a head whose channels form whole pairs (vector
 // l and vector R/2 further on when halves are paired), so a pair never leaves the
@@ -38,6 +40,14 @@ constexpr int kRopeUnroll = 4;  // warp steps whose loads are in flight together
 __device__ __forceinline__ uint4 rope_load(const void* p) {
   uint4 r;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+// A vector of weights, which stays in L1.  Loaded at each token: 16 registers a side
+// that hold them for all tokens spill (97 us on the bf16 prompt).
+__device__ __forceinline__ uint4 rope_weights(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
 
@@ -107,10 +117,18 @@ template <typename T, bool INTER, int NF>
 __device__ __forceinline__ void rope_coef(RopeCoef<NF>& r, const T* w, int c0, int c1, const float (&cs)[2 * NF],
                                           const float (&sn)[2 * NF]) {
   float wx[2 * NF], wz[2 * NF];
+  if (w) {
+    F2 a[NF], b[NF];
+    rope_unpack(w, rope_weights(w + c0), a);
+    rope_unpack(w, rope_weights(w + c1), b);
 #pragma unroll
-  for (int i = 0; i < 2 * NF; ++i) {
-    wx[i] = w ? to_f32(w[c0 + i]) : 1.f;
-    wz[i] = w ? to_f32(w[c1 + i]) : 1.f;
+    for (int i = 0; i < NF; ++i) {
+      f2_split(a[i], wx[2 * i], wx[2 * i + 1]);
+      f2_split(b[i], wz[2 * i], wz[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * NF; ++i) wx[i] = wz[i] = 1.f;
   }
 #pragma unroll
   for (int i = 0; i < NF; ++i) {
@@ -137,24 +155,67 @@ struct RopeShape {
   static constexpr int PER = VC / HS > 1 ? VC / HS : 1;  // angles whose sines a lane forms
 };
 
+// The coefficients of one side for a token, from the sines that the warp's lanes formed.
+template <typename T, int D, bool INTER>
+__device__ __forceinline__ void rope_side_coef(RopeCoef<RopeShape<T, D>::VC / 2>& k, const T* w, int c0, int c1,
+                                               const float (&mc)[RopeShape<T, D>::PER],
+                                               const float (&ms)[RopeShape<T, D>::PER]) {
+  using S = RopeShape<T, D>;
+  float cs[S::VC], sn[S::VC];
+#pragma unroll
+  for (int i = 0; i < S::VC; ++i) {
+    cs[i] = __shfl_sync(0xffffffffu, mc[i % S::PER], (i / S::PER) * S::L + (threadIdx.x & 31) % S::L);
+    sn[i] = __shfl_sync(0xffffffffu, ms[i % S::PER], (i / S::PER) * S::L + (threadIdx.x & 31) % S::L);
+  }
+  rope_coef<T, INTER, S::VC / 2>(k, w, c0, c1, cs, sn);
+}
+
+// One step: the lane's two vectors of a head, normalised, rotated and stored (if `live`).
+template <typename T, int D, bool INTER, bool FULL>
+__device__ __forceinline__ void rope_step(T* out, uint4 r0, uint4 r1, const RopeCoef<RopeShape<T, D>::VC / 2>& k, bool norm,
+                                          int c0, int c1, float eps, bool rot, bool live) {
+  constexpr int L = RopeShape<T, D>::L, NF = RopeShape<T, D>::VC / 2;
+  F2 x[NF], z[NF];
+  rope_unpack(out, r0, x);
+  rope_unpack(out, r1, z);
+  float inv = 1.f;
+  if (norm) {
+    F2 q = f2_mul(x[0], x[0]);
+#pragma unroll
+    for (int i = 1; i < NF; ++i) q = f2_fma(x[i], x[i], q);
+#pragma unroll
+    for (int i = 0; i < NF; ++i) q = f2_fma(z[i], z[i], q);
+    float ss, hi;
+    f2_split(q, ss, hi);
+    ss += hi;
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    inv = rsqrtf(ss * (1.f / D) + eps);
+  }
+  const F2 iv = f2(inv, inv);
+  F2 y[NF], v[NF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    // channels that are not rotated do not see their neighbour (0 * inf)
+    const F2 xo = INTER ? f2_swap(x[i]) : z[i], zo = INTER ? f2_swap(z[i]) : x[i];
+    y[i] = f2_mul(f2_fma(FULL || rot ? xo : 0ull, k.B[i], f2_mul(x[i], k.A[i])), iv);
+    v[i] = f2_mul(f2_fma(FULL || rot ? zo : 0ull, k.E[i], f2_mul(z[i], k.C[i])), iv);
+  }
+  if (live) {
+    rope_store(out + c0, y);
+    rope_store(out + c1, v);
+  }
+}
+
 // Steps [s0, s1) of one side (queries or keys) of a token: step s holds heads
 // s HS .. s HS + HS - 1.  FULL: every channel is rotated.
 template <typename T, int D, bool INTER, bool FULL>
 __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int64_t out_h, const T* w, int heads, int s0,
                                           int s1, int c0, int c1, const float (&mc)[RopeShape<T, D>::PER],
                                           const float (&ms)[RopeShape<T, D>::PER], float eps, int sub, bool rot) {
-  using S = RopeShape<T, D>;
-  constexpr int L = S::L, HS = S::HS, NF = S::VC / 2, U = kRopeUnroll, PER = S::PER;
-  RopeCoef<NF> k;
-  {
-    float cs[S::VC], sn[S::VC];
-#pragma unroll
-    for (int i = 0; i < S::VC; ++i) {
-      cs[i] = __shfl_sync(0xffffffffu, mc[i % PER], (i / PER) * L + (threadIdx.x & 31) % L);
-      sn[i] = __shfl_sync(0xffffffffu, ms[i % PER], (i / PER) * L + (threadIdx.x & 31) % L);
-    }
-    rope_coef<T, INTER, NF>(k, w, c0, c1, cs, sn);
-  }
+  constexpr int HS = RopeShape<T, D>::HS, U = kRopeUnroll;
+  RopeCoef<RopeShape<T, D>::VC / 2> k;
+  rope_side_coef<T, D, INTER>(k, w, c0, c1, mc, ms);
   int h = s0 * HS + sub;
   const int hend = min(heads, s1 * HS);
   in += h * in_h;
@@ -174,38 +235,8 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s + u < s1) {
-        F2 x[NF], z[NF];
-        rope_unpack(in, r0[u], x);
-        rope_unpack(in, r1[u], z);
-        float inv = 1.f;
-        if (w) {
-          F2 q = f2_mul(x[0], x[0]);
-#pragma unroll
-          for (int i = 1; i < NF; ++i) q = f2_fma(x[i], x[i], q);
-#pragma unroll
-          for (int i = 0; i < NF; ++i) q = f2_fma(z[i], z[i], q);
-          float ss, hi;
-          f2_split(q, ss, hi);
-          ss += hi;
-#pragma unroll
-          for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          inv = rsqrtf(ss * (1.f / D) + eps);
-        }
-        const F2 iv = f2(inv, inv);
-        F2 y[NF], v[NF];
-#pragma unroll
-        for (int i = 0; i < NF; ++i) {
-          // channels that are not rotated do not see their neighbour (0 * inf)
-          const F2 xo = INTER ? f2_swap(x[i]) : z[i], zo = INTER ? f2_swap(z[i]) : x[i];
-          y[i] = f2_mul(f2_fma(FULL || rot ? xo : 0ull, k.B[i], f2_mul(x[i], k.A[i])), iv);
-          v[i] = f2_mul(f2_fma(FULL || rot ? zo : 0ull, k.E[i], f2_mul(z[i], k.C[i])), iv);
-        }
-        if (h + u * HS < hend) {
-          rope_store(out + c0, y);
-          rope_store(out + c1, v);
-        }
-      }
+      if (s + u < s1)
+        rope_step<T, D, INTER, FULL>(out, r0[u], r1[u], k, w != nullptr, c0, c1, eps, rot, h + u * HS < hend);
       out += out_h;
     }
     h += U * HS;
@@ -215,7 +246,12 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
 // A warp takes items (a token, or one of its `chunks` shares of `per` steps).  The
 // lanes that hold the same channels of the warp's HS heads share the sines'
 // work: each forms VC / HS (at least one) of the VC angles' and hands them on.
-template <typename T, int D, bool INTER, bool FULL>
+// FEW: all steps of a token's two sides fit in one group of kRopeUnroll.  Their loads go
+// out together before the sines, and the next token's position before that, so a
+// token waits for memory once and not three times: 16384 tokens of 8 + 1 heads of 128
+// 25.0 -> 19.8 us, 23029 of 7 + 1 heads of 64 28.5 -> 19.9.  (At two steps fewer registers
+// and five CTAs per SM gave 17.9, but 4.8 for 4.6 us on 2000 tokens.)
+template <typename T, int D, bool INTER, bool FULL, bool FEW>
 __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
   using S = RopeShape<T, D>;
@@ -230,25 +266,65 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
   const int qsteps = (a.Hq + HS - 1) / HS, steps = qsteps + (a.Hkv + HS - 1) / HS;
   pdl_wait_then_release();
   const int64_t warps = (int64_t)gridDim.x * (kRopeThreads / 32), items = (int64_t)a.N * chunks;
-  for (int64_t it = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5); it < items; it += warps) {
+  int64_t it = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);
+  int next = FEW && it < items ? a.pos[it] : 0;
+  for (; it < items; it += warps) {
     const int64_t t = chunks == 1 ? it : it / chunks;
     const int s0 = chunks == 1 ? 0 : (int)(it - t * chunks) * per, s1 = min(s0 + per, steps);
-    const int pos = a.pos[t];
+    const int pos = FEW ? next : a.pos[t];
+    if (FEW && it + warps < items) next = a.pos[it + warps];
     if (pos < 0) continue;
+    const T* qi = static_cast<const T*>(a.q) + t * a.q_t;
+    const T* ki = static_cast<const T*>(a.k) + t * a.k_t;
+    T* qo = static_cast<T*>(a.qo) + t * a.qo_t;
+    T* ko = static_cast<T*>(a.ko) + t * a.ko_t;
+    uint4 r0[kRopeUnroll], r1[kRopeUnroll];
+    if constexpr (FEW) {
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        const bool key = u >= qsteps;
+        const int h = (key ? u - qsteps : u) * HS + sub;
+        r0[u] = r1[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (h < (key ? a.Hkv : a.Hq)) {
+          const T* in = key ? ki + h * a.k_h : qi + h * a.q_h;
+          r0[u] = rope_load(in + c0);
+          r1[u] = rope_load(in + c1);
+        }
+      }
+    }
     float mc[PER], ms[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * f[i]);
       sincospif((float)turn * 1.0842021724855044e-19f, &ms[i], &mc[i]);  // 2^-63: half turns in [-1, 1]
     }
-    if (s0 < qsteps)
-      rope_side<T, D, INTER, FULL>(static_cast<const T*>(a.q) + t * a.q_t, a.q_h, static_cast<T*>(a.qo) + t * a.qo_t,
-                                   a.qo_h, static_cast<const T*>(a.wq), a.Hq, s0, min(s1, qsteps), c0, c1, mc, ms, a.eps,
-                                   sub, rot);
-    if (s1 > qsteps)
-      rope_side<T, D, INTER, FULL>(static_cast<const T*>(a.k) + t * a.k_t, a.k_h, static_cast<T*>(a.ko) + t * a.ko_t,
-                                   a.ko_h, static_cast<const T*>(a.wk), a.Hkv, max(s0 - qsteps, 0), s1 - qsteps, c0, c1,
-                                   mc, ms, a.eps, sub, rot);
+    if constexpr (FEW) {
+      RopeCoef<VC / 2> k;
+      if (qsteps) {
+        rope_side_coef<T, D, INTER>(k, static_cast<const T*>(a.wq), c0, c1, mc, ms);
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u)
+          if (u < qsteps)
+            rope_step<T, D, INTER, FULL>(qo + (u * HS + sub) * a.qo_h, r0[u], r1[u], k, a.wq != nullptr, c0, c1, a.eps, rot,
+                                         u * HS + sub < a.Hq);
+      }
+      if (steps > qsteps) {
+        rope_side_coef<T, D, INTER>(k, static_cast<const T*>(a.wk), c0, c1, mc, ms);
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u)
+          if (u >= qsteps && u < steps) {
+            const int h = (u - qsteps) * HS + sub;
+            rope_step<T, D, INTER, FULL>(ko + h * a.ko_h, r0[u], r1[u], k, a.wk != nullptr, c0, c1, a.eps, rot, h < a.Hkv);
+          }
+      }
+    } else {
+      if (s0 < qsteps)
+        rope_side<T, D, INTER, FULL>(qi, a.q_h, qo, a.qo_h, static_cast<const T*>(a.wq), a.Hq, s0, min(s1, qsteps), c0, c1,
+                                     mc, ms, a.eps, sub, rot);
+      if (s1 > qsteps)
+        rope_side<T, D, INTER, FULL>(ki, a.k_h, ko, a.ko_h, static_cast<const T*>(a.wk), a.Hkv, max(s0 - qsteps, 0),
+                                     s1 - qsteps, c0, c1, mc, ms, a.eps, sub, rot);
+    }
   }
 }
 
@@ -262,8 +338,15 @@ static cudaError_t rope_launch(const RopeArgs& a, cudaStream_t st) {
   const int per = (int)((steps + want - 1) / want), chunks = (steps + per - 1) / per;
   const int64_t ctas = std::min<int64_t>(((int64_t)a.N * chunks + NW - 1) / NW, sms * kRopePerSm);
   const dim3 grid((unsigned)ctas), block(kRopeThreads);
-  cudaError_t e = a.R == D ? launch_pdl(qk_norm_rope_kernel<T, D, INTER, true>, grid, block, 0, st, a, per, chunks)
-                           : launch_pdl(qk_norm_rope_kernel<T, D, INTER, false>, grid, block, 0, st, a, per, chunks);
+  // (calls whose tokens are split over warps keep the general form: 2.8 us against 3.0)
+  const bool few = chunks == 1 && steps <= kRopeUnroll;
+  cudaError_t e;
+  if (a.R == D)
+    e = few ? launch_pdl(qk_norm_rope_kernel<T, D, INTER, true, true>, grid, block, 0, st, a, per, chunks)
+            : launch_pdl(qk_norm_rope_kernel<T, D, INTER, true, false>, grid, block, 0, st, a, per, chunks);
+  else
+    e = few ? launch_pdl(qk_norm_rope_kernel<T, D, INTER, false, true>, grid, block, 0, st, a, per, chunks)
+            : launch_pdl(qk_norm_rope_kernel<T, D, INTER, false, false>, grid, block, 0, st, a, per, chunks);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -49,6 +49,30 @@ def test_matches_plain(dtype, d, rot, inter, n, hq, hkv):
     assert torch.equal(dev.cpu(), qkv)  # the projection is only read
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rot,inter", [(128, 128, False), (64, 64, True), (64, 16, False), (128, 0, True)])
+@pytest.mark.parametrize("hq,hkv", [(8, 1), (7, 1), (5, 0), (0, 3), (4, 4), (13, 2)])
+def test_many_tokens_of_few_heads(dtype, d, rot, inter, hq, hkv):
+    """Several tokens to a warp, skipped ones among them (the last too), results in place."""
+    n = 5003
+    qkv, (wq, wk) = draw(d + rot + hq, n, hq, hkv, d, dtype)
+    pos = torch.from_numpy(np.random.default_rng(d + hq).integers(0, 2 ** 31, n, dtype=np.int64).astype(np.int32))
+    pos[3::11] = -1
+    pos[-1] = -5
+    rope = ops.make_rope(hq, hkv, d, dtype, rotary_dim=rot, theta=5e5, interleaved=inter, eps=1e-5)
+    dev = qkv.cuda()
+    q, k = dev[:, :hq] if hq else None, dev[:, hq:hq + hkv] if hkv else None
+    ops.qk_norm_rope(rope, q, k, pos.cuda(), wq.cuda() if hq else None, wk.cuda() if hkv else None, q_out=q, k_out=k)
+    x = qkv.double().numpy()
+    live = pos.numpy() >= 0
+    for got, part, w in ((q, x[:, :hq], wq), (k, x[:, hq:hq + hkv], wk)):
+        if got is not None:
+            ref, size = plain.norm_rope(part[live], w.double().numpy(), pos.numpy()[live], rot, inter, freqs(rot, 5e5), 1e-5)
+            check(got.cpu()[live], ref, size, dtype)
+    assert torch.equal(dev.cpu()[~live], qkv[~live])
+    assert torch.equal(dev[:, hq + hkv:].cpu(), qkv[:, hq + hkv:])
+
+
 def test_without_norm_given_frequencies_and_one_side():
     qkv, (_, wk) = draw(5, 65, 4, 2, 128, torch.bfloat16)
     pos = torch.arange(65, dtype=torch.int32) * 977
