@@ -19,8 +19,8 @@
 // The running maximum is that of x + e with 2^e <= s_v < 2^(e+1) the exponent of
 // the value scale: then W = exp2(x - m) s_v < 2 for blocks of any scale, nothing
 // overflows and what underflows is 2^-24 of the largest.  (e is held within
-// [-100, 121], so that exp2(x - m) and its sum stay finite as well; values below
-// 2^-100 add nothing.)  Sum and maximum are consistent, so the merge and the sink
+// [-94, 121], so that exp2(x - m) and its sum over 2^31 tokens stay finite as well;
+// values below 2^-94 lose bits, those below 2^-118 add nothing.)  Sum and maximum are consistent, so the merge and the sink
 // need no other form.  Tail tokens go through the bf16 tensor cores with e = 0.
 //
 // Bound by memory on long contexts: 32 contexts of 49k to 64k tokens, 2 KV heads of 6
@@ -105,10 +105,10 @@ __device__ __forceinline__ void kv8_unpack4(uint32_t w, uint32_t& lo, uint32_t& 
   }
 }
 
-// exponent of a value scale, within [-100, 121] (0 gives -100; NaN and inf 121)
+// exponent of a value scale, within [-94, 121] (0 gives -94; NaN and inf 121)
 __device__ __forceinline__ float kv8_exponent(float s) {
   const int e = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
-  return (float)min(max(e, -100), 121);
+  return (float)min(max(e, -94), 121);
 }
 
 template <int D, int SG, int W, int S>
@@ -1010,9 +1010,8 @@ static int kv8_clusters(int c, Kv8Device* d) {
 // measured costs make faster.  A CTA takes t ns a token (4.9 at D = 128, 2.7 at
 // D = 64) and a cluster 5.5 us besides, in as many waves as the clusters need; the
 // ranges take 13 us, 6 per row beyond their equal shares, and 0.1 for each CTA that shares
-// a row.  Fitted to 50 shapes of 1
-// to 256 rows of 1k to 64k tokens, which it times within 10% or so: 96 rows of 4k at
-// D = 128 take 27 us with a CTA each and 30 in ranges, 16k 87 and 66; 64 rows of 16k at
+// a row.  Fitted to 50 shapes of 1 to 256 rows of 1k to 64k tokens, which it times
+// within 10% or so: 96 rows of 4k at D = 128 take 27 us with a CTA each and 30 in ranges, 16k 87 and 66; 64 rows of 16k at
 // D = 64 29 with two each and 32 in ranges, 64k 94 and 86.  `most` bounds a row's
 // tokens; where only the device knows them, rows are taken to hold three quarters
 // of it on average and a cluster to wait for one that is full.

@@ -331,6 +331,19 @@ def test_attend_extreme_scales_and_queries(fmt):
     attention(p, q, mass_in=torch.zeros_like(p.mass))
 
 
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch,cap,lens", [(1, 16, [16]), (1, 16, [5]), (2, 48, [48, 31]), (3, 16, [0, 16, 1])])
+def test_attend_caches_smaller_than_a_unit(fmt, d, batch, cap, lens):
+    """A whole cache that is smaller than what a warp copies at a time, full to the last slot."""
+    p = Pair(batch, 3, 1, d, cap, fmt, 16, page=16, seed=cap + d)
+    p.append(lens)
+    q = query(p, 8)
+    attention(p, q, mass_in=torch.rand_like(p.mass))
+    pages = torch.arange(cap // 16, dtype=torch.int32, device="cuda").expand(batch, -1).flip(1).contiguous()
+    attention(p, q, pages=(pages, None))
+
+
 def test_attend_shows_nan_blocks_in_their_row_only():
     p = Pair(2, 4, 2, 64, 128, "int8", 16, seed=3)
 
