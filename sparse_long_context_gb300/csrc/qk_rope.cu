@@ -3,10 +3,10 @@
 //   y = x w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin).
 // Bound by memory: every element is read and written once.  32768 tokens of 28 + 4
 // heads of 128 channels take 91 us (5.9 TB/s, 87% of the measured copy), 16384 in
-// fp32 with half of the channels rotated 85 us (93%), 1000 tokens 6.2 us, 32 tokens of
-// 12 + 2 heads 2.8 us, the launch.  Tokens of few heads are bound by the sines and
+// fp32 with half of the channels rotated 85 us (93%), 1000 tokens 5.7 us, 32 tokens of
+// 12 + 2 heads 1.8 us, the launch.  Tokens of few heads are bound by the sines and
 // coefficients, which are a token's whatever its heads: 16384 tokens of 8 + 1 heads 20 us
-// (floor 11).
+// (floor 11), 23029 of 7 + 1 heads of 64 channels 10.6 (floor 7).
 //
 // A lane holds two 16-byte vectors of a head whose channels form whole pairs (vector
 // l and vector R/2 further on when halves are paired), so a pair never leaves the
@@ -34,6 +34,7 @@
 namespace sls {
 
 constexpr int kRopeThreads = 128, kRopePerSm = 4;  // more CTAs per SM spill: 118 us at 7
+constexpr int kRopeOnePerSm = 5;  // of the kernel of single steps (4 and 6: 7% and 10% to 38% slower)
 constexpr int kRopeUnroll = 4;  // warp steps whose loads are in flight together
 
 // A 16-byte vector, not kept in L1 (plain loads: the outputs may be the inputs).
@@ -170,10 +171,11 @@ __device__ __forceinline__ void rope_side_coef(RopeCoef<RopeShape<T, D>::VC / 2>
   rope_coef<T, INTER, S::VC / 2>(k, w, c0, c1, cs, sn);
 }
 
-// One step: the lane's two vectors of a head, normalised, rotated and stored (if `live`).
+// One step: the lane's two vectors of a head, normalised (`norm` for the warp, `mine` for
+// the lane's head), rotated and stored (if `live`).
 template <typename T, int D, bool INTER, bool FULL>
 __device__ __forceinline__ void rope_step(T* out, uint4 r0, uint4 r1, const RopeCoef<RopeShape<T, D>::VC / 2>& k, bool norm,
-                                          int c0, int c1, float eps, bool rot, bool live) {
+                                          int c0, int c1, float eps, bool rot, bool live, bool mine = true) {
   constexpr int L = RopeShape<T, D>::L, NF = RopeShape<T, D>::VC / 2;
   F2 x[NF], z[NF];
   rope_unpack(out, r0, x);
@@ -190,7 +192,7 @@ __device__ __forceinline__ void rope_step(T* out, uint4 r0, uint4 r1, const Rope
     ss += hi;
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    inv = rsqrtf(ss * (1.f / D) + eps);
+    inv = mine ? rsqrtf(ss * (1.f / D) + eps) : 1.f;
   }
   const F2 iv = f2(inv, inv);
   F2 y[NF], v[NF];
@@ -249,8 +251,7 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
 // FEW: all steps of a token's two sides fit in one group of kRopeUnroll.  Their loads go
 // out together before the sines, and the next token's position before that, so a
 // token waits for memory once and not three times: 16384 tokens of 8 + 1 heads of 128
-// 25.0 -> 19.8 us, 23029 of 7 + 1 heads of 64 28.5 -> 19.9.  (At two steps fewer registers
-// and five CTAs per SM gave 17.9, but 4.8 for 4.6 us on 2000 tokens.)
+// 25.0 -> 19.8 us.
 template <typename T, int D, bool INTER, bool FULL, bool FEW>
 __global__ void __launch_bounds__(kRopeThreads, kRopePerSm)
 qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
@@ -328,17 +329,90 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
   }
 }
 
+// A warp step by itself: heads are numbered through queries and keys, and a lane keeps
+// to its head's side.  steps == 1: a token's heads are one step.  A warp takes tokens in
+// turn, with the next one's vectors and the position of the one after in flight: 23029
+// tokens of 7 + 1 heads of 64 channels 19.9 -> 10.6 us, 32484 of 3 + 1 of 128 30.8 -> 14.9.
+// steps > 1: few tokens, a warp each for every step, whose vectors are loaded together
+// with the position: 32 tokens of 12 + 2 heads 2.8 -> 1.8 us, 370 of 28 + 4 3.9 -> 3.4.
+template <typename T, int D, bool INTER, bool FULL>
+__global__ void __launch_bounds__(kRopeThreads, kRopeOnePerSm)
+qk_norm_rope_one_kernel(const __grid_constant__ RopeArgs a, int steps) {
+  using S = RopeShape<T, D>;
+  constexpr int VC = S::VC, L = S::L, HS = S::HS, PER = S::PER;
+  const int lane = threadIdx.x & 31, sub = lane / L, l = lane % L;
+  const int half = FULL ? D / 2 : a.R >> 1;
+  const bool rot = FULL || 2 * VC * l < a.R;
+  const int c0 = INTER || !rot ? 2 * VC * l : VC * l, c1 = INTER || !rot ? c0 + VC : half + VC * l;
+  uint64_t f[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) f[i] = rot ? a.freq[VC * l + (sub * PER + i) % VC] : 0ull;
+  int64_t t = (int64_t)blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5), stride = (int64_t)gridDim.x * (kRopeThreads / 32);
+  int h = sub;
+  if (steps > 1) {
+    h += (int)(t % steps) * HS;
+    t /= steps;
+    stride = a.N;
+  }
+  if (t >= a.N) return;
+  const bool key = h >= a.Hq, live = h < a.Hq + a.Hkv;
+  h -= key ? a.Hq : 0;
+  const T* in = static_cast<const T*>(key ? a.k : a.q) + h * (key ? a.k_h : a.q_h);
+  T* out = static_cast<T*>(key ? a.ko : a.qo) + h * (key ? a.ko_h : a.qo_h);
+  const int64_t in_t = key ? a.k_t : a.q_t, out_t = key ? a.ko_t : a.qo_t;
+  const T* w = static_cast<const T*>(key ? (a.Hkv ? a.wk : nullptr) : a.wq);
+  const bool norm = (a.Hq && a.wq) || (a.Hkv && a.wk);
+  pdl_wait_then_release();
+  int pos = a.pos[t], next = t + stride < a.N ? a.pos[t + stride] : 0;
+  uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0, n0 = r0, n1 = r0;
+  if (live) {
+    r0 = rope_load(in + t * in_t + c0);
+    r1 = rope_load(in + t * in_t + c1);
+  }
+  for (; t < a.N; t += stride) {
+    const int64_t t1 = t + stride;
+    if (live && t1 < a.N) {
+      n0 = rope_load(in + t1 * in_t + c0);
+      n1 = rope_load(in + t1 * in_t + c1);
+    }
+    const int after = t1 + stride < a.N ? a.pos[t1 + stride] : 0;
+    if (pos >= 0) {
+      float mc[PER], ms[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int64_t turn = (int64_t)((uint64_t)(int64_t)pos * f[i]);
+        sincospif((float)turn * 1.0842021724855044e-19f, &ms[i], &mc[i]);  // 2^-63: half turns in [-1, 1]
+      }
+      RopeCoef<VC / 2> k;
+      rope_side_coef<T, D, INTER>(k, w, c0, c1, mc, ms);
+      rope_step<T, D, INTER, FULL>(out + t * out_t, r0, r1, k, norm, c0, c1, a.eps, rot, live, w != nullptr);
+    }
+    pos = next;
+    next = after;
+    r0 = n0;
+    r1 = n1;
+  }
+}
+
 template <typename T, int D, bool INTER>
 static cudaError_t rope_launch(const RopeArgs& a, cudaStream_t st) {
   constexpr int HS = RopeShape<T, D>::HS, NW = kRopeThreads / 32;
   const int steps = (a.Hq + HS - 1) / HS + (a.Hkv + HS - 1) / HS;
-  // few tokens: a token's heads go to several warps, up to 8 warps per SM
   const int64_t sms = sm_count();
+  const int one = (a.Hq + a.Hkv + HS - 1) / HS;
+  // steps by themselves while they fit in one wave (500 tokens of 8 steps: 5.0 us against 4.3)
+  if (one == 1 || (int64_t)a.N * one <= sms * NW * kRopeOnePerSm) {
+    const int64_t ctas = ((int64_t)a.N * one + NW - 1) / NW;
+    const dim3 grid((unsigned)(one == 1 ? std::min(ctas, sms * kRopeOnePerSm) : ctas)), block(kRopeThreads);
+    const cudaError_t e = a.R == D ? launch_pdl(qk_norm_rope_one_kernel<T, D, INTER, true>, grid, block, 0, st, a, one)
+                                   : launch_pdl(qk_norm_rope_one_kernel<T, D, INTER, false>, grid, block, 0, st, a, one);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  // up to a few hundred tokens: a token's heads go to several warps, up to 8 warps per SM
   const int64_t want = std::min<int64_t>(steps, std::max<int64_t>(1, sms * 8 / a.N));
   const int per = (int)((steps + want - 1) / want), chunks = (steps + per - 1) / per;
   const int64_t ctas = std::min<int64_t>(((int64_t)a.N * chunks + NW - 1) / NW, sms * kRopePerSm);
   const dim3 grid((unsigned)ctas), block(kRopeThreads);
-  // (calls whose tokens are split over warps keep the general form: 2.8 us against 3.0)
   const bool few = chunks == 1 && steps <= kRopeUnroll;
   cudaError_t e;
   if (a.R == D)

@@ -88,6 +88,25 @@ def test_without_norm_given_frequencies_and_one_side():
     assert q2 is None and torch.equal(k2, k)
 
 
+@pytest.mark.parametrize("n", [3, 5003])
+@pytest.mark.parametrize("dtype,d,hq,hkv", [(torch.bfloat16, 64, 4, 2), (torch.bfloat16, 64, 3, 5), (torch.bfloat16, 64, 7, 6),
+                                            (torch.float32, 64, 3, 1), (torch.float32, 128, 1, 1), (torch.bfloat16, 128, 3, 2)])
+@pytest.mark.parametrize("norm_q,norm_k", [(True, False), (False, True), (False, False)])
+def test_sides_of_a_step_with_and_without_norm(n, dtype, d, hq, hkv, norm_q, norm_k):
+    """Queries and keys next to each other in a warp, one side normalised and the other not; heads first in memory."""
+    qkv, (wq, wk) = draw(n + d + hq, n, hq, hkv, d, dtype)
+    pos = torch.arange(n, dtype=torch.int32) * 401
+    rope = ops.make_rope(hq, hkv, d, dtype, rotary_dim=d // 2, theta=1e4, eps=1e-5)
+    dev = qkv.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    q, k = ops.qk_norm_rope(rope, dev[:, :hq], dev[:, hq:hq + hkv], pos.cuda(), wq.cuda() if norm_q else None,
+                            wk.cuda() if norm_k else None)
+    x = qkv.double().numpy()
+    for got, part, w in ((q, x[:, :hq], wq if norm_q else None), (k, x[:, hq:hq + hkv], wk if norm_k else None)):
+        ref, size = plain.norm_rope(part, None if w is None else w.double().numpy(), pos.numpy(), d // 2, False,
+                                    freqs(d // 2, 1e4), 1e-5)
+        check(got, ref, size, dtype)
+
+
 def test_in_place_strided_skipped_and_empty():
     hq, hkv, d, n = 6, 2, 64, 50
     qkv, (wq, wk) = draw(9, n, hq, hkv, d, torch.bfloat16)
