@@ -430,7 +430,7 @@ class Kv8Cache:
         self.index = k_codes.get_device()
         if any(t.get_device() != self.index for t in (v_codes, k_scales, v_scales, k_tail, v_tail)):
             raise ValueError("the cache's tensors must be on one device")
-        self.fmt, self.block = fmt, block
+        self.fmt, self.block, self.shape = fmt, block, (B, H, Cap, D)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.k_tail, self.v_tail = k_tail, v_tail
         self.c = L.Kv8CacheDesc(_KV8_FORMATS[fmt], block, *(t.data_ptr() for t in (
@@ -445,10 +445,12 @@ class Kv8Cache:
                    new((B, H, Cap // block), torch.float32), new((B, H, Cap // block), torch.float32),
                    new((B, H, block, D), torch.bfloat16), new((B, H, block, D), torch.bfloat16))
 
-    def _beside(self, t: torch.Tensor) -> L.Kv8CacheDesc:
-        """The C structure, for a call on t's device."""
+    def _beside(self, t: torch.Tensor, desc: L.AttnDesc) -> L.Kv8CacheDesc:
+        """The C structure, for a call with this descriptor on t's device."""
         if t.get_device() != self.index:
             raise ValueError("the cache must be on the device of the other tensors")
+        if (desc.batch, desc.num_kv_heads, desc.capacity, desc.head_dim) != self.shape:
+            raise ValueError(f"the descriptor's shape is not that of the cache, {self.shape}")
         return self.c
 
     def values(self):
@@ -466,7 +468,7 @@ def kv8_append(desc: L.AttnDesc, cache: Kv8Cache, k_new, v_new, ctx_len, new_len
     """Appends the first new_len[b] (None: all) tokens of k_new, v_new [B, T, Hkv, D] to every sequence
     (sls_kv8_append): complete blocks are quantised, the rest waits in the tail.  ctx_out defaults to ctx_len
     (advanced in place).  The new tensors may be strided views with contiguous channels."""
-    status = (_fast or _binding()).kv8_append(desc, cache._beside(k_new), k_new, v_new, ctx_len, new_len, kmin, kmax,
+    status = (_fast or _binding()).kv8_append(desc, cache._beside(k_new, desc), k_new, v_new, ctx_len, new_len, kmin, kmax,
                                               mass, ctx_out, pos_out)
     if status:
         L.check("sls_kv8_append", status)
@@ -491,7 +493,7 @@ def kv8_decode_attend(desc: L.AttnDesc, cache: Kv8Cache, q, ctx_len, page_idx=No
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = kv8_attend_workspace(desc, cache, mass_out is not None, q.device)
-    status = (_fast or _binding()).kv8_decode_attend(desc, cache._beside(q), q, ctx_len, page_idx, count, k_fixed, sink,
+    status = (_fast or _binding()).kv8_decode_attend(desc, cache._beside(q, desc), q, ctx_len, page_idx, count, k_fixed, sink,
                                                      mass_in, mass_out, out, lse, workspace)
     if status:
         L.check("sls_kv8_decode_attend", status)
@@ -513,7 +515,7 @@ def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sin
         kmax_out = kmax if kmax_out is None else kmax_out
         ctx_out = ctx_len if ctx_out is None else ctx_out
     else:
-        dcap, to = dst_desc.capacity, dst._beside(ctx_len)
+        dcap, to = dst_desc.capacity, dst._beside(ctx_len, dst_desc)
         if (dst_desc.batch, dst_desc.num_kv_heads, dst_desc.head_dim, dst_desc.page_size, dst_desc.dtype) != (
                 desc.batch, desc.num_kv_heads, desc.head_dim, desc.page_size, desc.dtype):
             raise ValueError("dst_desc must describe the same rows and pages as desc")
@@ -522,7 +524,7 @@ def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sin
     if kept_idx is None:
         kept_idx = torch.empty((desc.batch * desc.num_kv_heads, max(int(keep), 0)), dtype=torch.int32,
                                device=ctx_len.device)
-    status = (_fast or _binding()).kv8_evict(desc, cache._beside(ctx_len), dcap, to, keep, n_sink_blocks,
+    status = (_fast or _binding()).kv8_evict(desc, cache._beside(ctx_len, desc), dcap, to, keep, n_sink_blocks,
                                              n_recent_blocks, mass, mass_out, kmin, kmax, kmin_out, kmax_out, kept_idx,
                                              ctx_len, ctx_out)
     if status:

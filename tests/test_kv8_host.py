@@ -167,3 +167,23 @@ def test_binding_refuses_host_tensors_and_bad_shapes():
     rope = ops.make_rope(1, 1, 64, torch.bfloat16)
     with pytest.raises(ValueError):
         ops.qk_norm_rope(rope, torch.zeros(1, 1, 64), torch.zeros(1, 1, 64), torch.zeros(1, dtype=torch.int32))
+
+
+def test_cache_of_another_shape_is_refused():
+    """A cache is used with the shape it was made for: a larger descriptor would reach past its buffers."""
+    cache = object.__new__(ops.Kv8Cache)  # without a GPU there are no buffers; the check comes before they are used
+    cache.index, cache.shape, cache.c = -1, (2, 1, 64, 64), L.Kv8CacheDesc()
+    x = torch.zeros((2, 1, 1, 64), dtype=torch.bfloat16)
+    ctx = torch.zeros(2, dtype=torch.int32)
+    for b, h, cap, d in ((2, 1, 128, 64), (3, 1, 64, 64), (2, 2, 64, 64), (2, 1, 64, 128)):
+        wrong = ops.make_desc(b, 2, h, d, 16, cap, torch.bfloat16)
+        with pytest.raises(ValueError, match="shape is not that of the cache"):
+            ops.kv8_append(wrong, cache, x, x, ctx)
+        with pytest.raises(ValueError, match="shape is not that of the cache"):
+            ops.kv8_decode_attend(wrong, cache, x[:, 0], ctx, out=x, lse=ctx, workspace=ctx)
+        with pytest.raises(ValueError, match="shape is not that of the cache"):
+            ops.kv8_evict(wrong, cache, ctx, x, 1)
+        right = ops.make_desc(2, 2, 1, 64, 16, 64, torch.bfloat16)
+        if (b, h, d) == (2, 1, 64):
+            with pytest.raises(ValueError, match="shape is not that of the cache"):
+                ops.kv8_evict(right, cache, ctx, x, 1, dst_desc=wrong, dst=cache)
