@@ -21,7 +21,8 @@
 // overflows and what underflows is 2^-24 of the largest.  (e is held within
 // [-94, 121], so that exp2(x - m) and its sum over 2^31 tokens stay finite as well;
 // values below 2^-94 lose bits, those below 2^-118 add nothing.)  Sum and maximum are consistent, so the merge and the sink
-// need no other form.  Tail tokens go through the bf16 tensor cores with e = 0.
+// need no other form.  Tail tokens go through the bf16 tensor cores, a group of 16
+// with the exponent of the scale that its values would be stored with.
 //
 // Bound by memory on long contexts: 32 contexts of 49k to 64k tokens, 2 KV heads of 6
 // query heads and 128 channels, int8: 140 to 143 us for 943 MB (6.6 to 6.7 TB/s, the
@@ -223,6 +224,23 @@ struct Kv8Tail {
         v[i][4 * u] = x.x; v[i][4 * u + 1] = x.y; v[i][4 * u + 2] = x.z; v[i][4 * u + 3] = x.w;
       }
     }
+  }
+  // The exponent with which the group's values enter the running maximum: that of
+  // the scale they would be stored with, so that a token weighs the same in the
+  // tail and in a block.  Infinities and NaN are left out: they show in their own
+  // channels and must not push the others' weights down.
+  template <int FMT>
+  __device__ __forceinline__ float exponent() const {
+    uint32_t mx = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) {
+        const uint32_t a = v[i][c] & 0x7fff7fffu;
+        mx = __vmaxu2(mx, a & __vcmpltu2(a, 0x7f807f80u));
+      }
+    mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+    return kv8_exponent(__uint_as_float(mx << 16) * (1.f / kv8_top<FMT>()));
   }
   // q: channels 16 c + 4 m .. + 3 of the lane's head
   __device__ __forceinline__ void scores(const uint2 (&q)[D / 16], float mul, float (&x)[4], int lane) const {
@@ -457,7 +475,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
       g.load(static_cast<const bf16*>(a.c.kt) + tail, static_cast<const bf16*>(a.c.vt) + tail, min(16, N - at), lane);
       float x[4];
       g.scores(q, a.qscale, x, lane);
-      const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])));
+      const float mref = softmax_step(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) + g.template exponent<FMT>());
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
       l_run += (x[0] + x[1]) + (x[2] + x[3]);
