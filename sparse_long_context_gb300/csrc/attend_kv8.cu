@@ -16,13 +16,15 @@
 //                  head's largest, which round to fp16's subnormals), B = codes
 //   x   = S * scale * s_k          fp32, one multiplication per score
 //   O^T += V^T W^T,  W = p s_v     rounded to fp16 (half a step, 2^-11)
-// The running maximum is that of x + e with 2^e <= s_v < 2^(e+1) the exponent of
-// the value scale: then W = exp2(x - m) s_v < 2 for blocks of any scale, nothing
-// overflows and what underflows is 2^-24 of the largest.  (e is held within
-// [-94, 121], so that exp2(x - m) and its sum over 2^31 tokens stay finite as well;
-// values below 2^-94 lose bits, those below 2^-118 add nothing.)  Sum and maximum are consistent, so the merge and the sink
-// need no other form.  Tail tokens go through the bf16 tensor cores, a group of 16
-// with the exponent of the scale that its values would be stored with.
+// The running maximum is that of x + e - 14 with 2^e <= s_v < 2^(e+1) the exponent of
+// the value scale: then W = exp2(x - m) s_v < 2^15 for blocks of any scale, nothing
+// overflows, and the largest W is 2^14 or more, so that weights down to 2^-28 of it
+// keep their bits and what underflows is below 2^-38 of it.  (e is held within
+// [-80, 121], so that exp2(x - m) and its sum over 2^31 tokens stay finite as well;
+// scales below 2^-108 lose bits, those below 2^-119 add nothing.)  Sum and maximum are
+// consistent, so the merge and the sink need no other form.  Tail tokens go through the
+// bf16 tensor cores, a group of 16 with the exponent of the scale that its values would
+// be stored with.
 //
 // Bound by memory on long contexts: 32 contexts of 49k to 64k tokens, 2 KV heads of 6
 // query heads and 128 channels, int8: 140 to 143 us for 943 MB (6.6 to 6.7 TB/s, the
@@ -106,10 +108,12 @@ __device__ __forceinline__ void kv8_unpack4(uint32_t w, uint32_t& lo, uint32_t& 
   }
 }
 
-// exponent of a value scale, within [-94, 121] (0 gives -94; NaN and inf 121)
+// What a value scale adds to its scores in the running maximum: its exponent, within
+// [-80, 121] (0 gives -80; NaN and inf 121), less 14, so that the largest weight takes
+// fp16's upper range and those far below it stay clear of its subnormals.
 __device__ __forceinline__ float kv8_exponent(float s) {
   const int e = (int)((__float_as_uint(s) >> 23) & 255u) - 127;
-  return (float)min(max(e, -94), 121);
+  return (float)(min(max(e, -80), 121) - 14);
 }
 
 template <int D, int SG, int W, int S>

@@ -1,5 +1,5 @@
-"""Precision of the 8-bit attend's value product where values of any size stand next to a tail, against the plain 64-bit form
-with bounds that do not depend on the values' size."""
+"""Precision of the 8-bit attend's value product: values of any size next to a tail, and weights far below the largest,
+against the plain 64-bit form with bounds that do not depend on the values' size."""
 import numpy as np
 import pytest
 import torch
@@ -24,7 +24,7 @@ def bounds(q, k, v, scale, p, stored, size, tail_half):
     """Bounds of the kernel's errors from its formula's roundings, relative to the values' own size.
     Scores: as in plain.attend_bounds.  A stored token's weight is rounded to fp16: half a step is 2^-11 of it, or, among
     the subnormals, 2^-25 in units in which the token with the largest product of weight and value scale has
-    1 or more, so 2^-25 of the largest weight times value for each token.  A tail token's weight has the relative half
+    2^14 or more, so 2^-39 of the largest weight times value for each token.  A tail token's weight has the relative half
     step `tail_half`.  Sums: a warp adds its tokens' groups one after the other (a row is spread over 12 warps at least),
     then up to 200 partials are merged, each addition off by 2^-23 of at most sum p |v| (truncating adds), in
     the accumulators and in the weights' sum alike."""
@@ -33,7 +33,7 @@ def bounds(q, k, v, scale, p, stored, size, tail_half):
     pv = p @ np.abs(v)
     w = (p * np.where(stored, 2.0 ** -11, tail_half)) @ np.abs(v)
     adds = 2 * (n / 192 + 200) * 2.0 ** -23
-    return e, w + (2 * e[:, None] + 2.0 ** -20 + adds) * pv + n * 2.0 ** -25 * (p * size).max(1)[:, None]
+    return e, w + (2 * e[:, None] + 2.0 ** -20 + adds) * pv + n * 2.0 ** -39 * (p * size).max(1)[:, None]
 
 
 def check(p, q, pages=None, tail_half=2.0 ** -8, heads=None, **kw):
@@ -146,3 +146,25 @@ def test_infinite_tail_value_shows_in_its_channel_only():
         err = np.abs(out[b].double().numpy() - ref)
         err[:, ch] = 0
         assert (err <= slack + 2.0 ** -8 * (np.abs(ref) + slack)).all()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("gap,at", [(14, 5), (18, 5), (18, 6800), (22, 5)])
+def test_weights_far_below_a_dominant_token(fmt, d, gap, at):
+    """One token without a value of its own draws nearly all of the weight; the others have about e^-gap of it each, and all
+    of the output is theirs.  128 rows in a capacity of 6912, one CTA each: the dominant token's warp has a twelfth of
+    its row, whose weights are relative to it."""
+    lens = [6900, 6912, 6801] + [1] * 125
+    p = Pair(128, 2, 1, d, 6912, fmt, 64, seed=gap)
+    q = torch.zeros((128, 2, d), dtype=torch.bfloat16)
+    q[:, :, 0] = d ** 0.5  # the logit is the key's first channel, nearly (8 and 11.3125)
+
+    def edit(kv):
+        kv[:3, :, 0, 0] = torch.from_numpy(np.random.default_rng(1).standard_normal((3, 6912)) * 0.5).to(torch.bfloat16)
+        kv[:3, at, 0, 0] = gap
+        kv[:3, :, 1] = kv[:3, :, 1].abs()
+        kv[:3, at, 1] = 0
+
+    p.append(lens, edit)
+    check(p, q)
