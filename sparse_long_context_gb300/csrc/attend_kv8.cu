@@ -50,6 +50,9 @@ namespace sls {
 constexpr int kKv8MaxGrid = 1024;  // CTAs whose ranges are kept in shared memory
 constexpr int kKv8MaxCluster = 16;
 constexpr int kKv8MaxRows = 4096;  // rows whose first units are kept there
+// The arrival counters' place in a workspace, whatever the shape: no call's partials lie
+// where another one's counters are.
+constexpr size_t kKv8TicketBytes = kKv8MaxRows * sizeof(int32_t);
 constexpr int kKv8PerSm = 1;       // resident CTAs of an SM
 // Least units of a CTA: a shorter job uses fewer CTAs (1, 2, 4, 8 and 12 units: 14.4,
 // 12.7, 11.8, 13.1 and 13.6 us for 1000 tokens of 4 heads).
@@ -969,7 +972,7 @@ static int kv8_entry_shift(const Shape& s, const Kv8& c) {
 
 size_t kv8_attend_workspace(const Shape& s, const Kv8& c, bool with_mass) {
   const size_t rows = (size_t)s.B * s.Hkv, slots = 2 * (size_t)kv8_grid();
-  return a256(rows * 4) + a256(slots * s.G * s.D * 4) + 2 * a256(slots * s.G * 4) +
+  return kKv8TicketBytes + a256(slots * s.G * s.D * 4) + 2 * a256(slots * s.G * 4) +
          (with_mass ? a256(rows * s.G * 8) + a256(rows * s.G * (s.Cap >> kv8_entry_shift(s, c)) * 8) : 0);
 }
 
@@ -1113,7 +1116,7 @@ cudaError_t launch_kv8_attend(const Shape& s, const Kv8& c, const void* q, const
     w += a256(bytes);
     return p;
   };
-  a.tickets = reinterpret_cast<int32_t*>(take(rows * 4));
+  a.tickets = reinterpret_cast<int32_t*>(take(kKv8TicketBytes));
   a.po = reinterpret_cast<float*>(take(slots * s.G * s.D * 4));
   a.pm = reinterpret_cast<float*>(take(slots * s.G * 4));
   a.pl = reinterpret_cast<float*>(take(slots * s.G * 4));

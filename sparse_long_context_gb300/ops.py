@@ -476,7 +476,8 @@ def kv8_append(desc: L.AttnDesc, cache: Kv8Cache, k_new, v_new, ctx_len, new_len
 
 
 def kv8_attend_workspace(desc: L.AttnDesc, cache: Kv8Cache, mass: bool = False, device="cuda"):
-    """Zero-filled workspace of kv8_decode_attend (reusable); mass: for calls that sum the blocks' weights."""
+    """Zero-filled workspace of kv8_decode_attend (reusable, also by calls of other shapes that need no more bytes, one
+    after the other); mass: for calls that sum the blocks' weights."""
     n = L.load().sls_kv8_decode_attend_workspace_size(ctypes.byref(desc), ctypes.byref(cache.c), int(bool(mass)))
     return torch.zeros(max(int(n), 1), dtype=torch.uint8, device=device)
 
