@@ -23,8 +23,8 @@
 // [-80, 121], so that exp2(x - m) and its sum over 2^31 tokens stay finite as well;
 // scales below 2^-108 lose bits, those below 2^-119 add nothing.)  Sum and maximum are
 // consistent, so the merge and the sink need no other form.  Tail tokens go through the
-// bf16 tensor cores, a group of 16 with the exponent of the scale that its values would
-// be stored with.
+// bf16 tensor cores (weights in a high and a low part, half a step 2^-15), a group of
+// 16 with the exponent of the scale that its values would be stored with.
 //
 // Bound by memory on long contexts: 32 contexts of 49k to 64k tokens, 2 KV heads of 6
 // query heads and 128 channels, int8: 140 to 143 us for 943 MB (6.6 to 6.7 TB/s, the
@@ -264,11 +264,25 @@ struct Kv8Tail {
     x[2] = 2 * m + 8 < lim ? sc[1][0] * mul : kNegInf;
     x[3] = 2 * m + 9 < lim ? sc[1][1] * mul : kNegInf;
   }
-  __device__ __forceinline__ void pv(float (&o)[D / 16][4], uint32_t p0, uint32_t p1) const {
+  // O^T += V^T P^T with the weights as the sum of two bf16 (16 bits in all, half a step
+  // 2^-15: the tail may be a whole context, and the newest tokens draw much weight).  The
+  // high part is truncated, so the low one has its sign, and a low part of zero becomes
+  // 2^-126 next to a weight, so that no infinite value meets a zero or another sign.
+  __device__ __forceinline__ void pv(float (&o)[D / 16][4], const float (&p)[4]) const {
+    uint32_t hi[2], lo[2];
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t)
-      mma_bf16(o[t], __byte_perm(v[0][t], v[1][t], 0x5410), __byte_perm(v[0][t], v[1][t], 0x7632),
-               __byte_perm(v[2][t], v[3][t], 0x5410), __byte_perm(v[2][t], v[3][t], 0x7632), p0, p1);
+    for (int i = 0; i < 2; ++i) {
+      hi[i] = __byte_perm(__float_as_uint(p[2 * i]), __float_as_uint(p[2 * i + 1]), 0x7632);
+      lo[i] = pack_bf16(p[2 * i] - bf16lo(hi[i]), p[2 * i + 1] - bf16hi(hi[i]));
+      lo[i] = __vmaxu2(lo[i], 0x00800080u) & __vcmpgtu2(hi[i], 0u);
+    }
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      const uint32_t a0 = __byte_perm(v[0][t], v[1][t], 0x5410), a1 = __byte_perm(v[0][t], v[1][t], 0x7632);
+      const uint32_t a2 = __byte_perm(v[2][t], v[3][t], 0x5410), a3 = __byte_perm(v[2][t], v[3][t], 0x7632);
+      mma_bf16(o[t], a0, a1, a2, a3, hi[0], hi[1]);
+      mma_bf16(o[t], a0, a1, a2, a3, lo[0], lo[1]);
+    }
   }
 };
 
@@ -486,7 +500,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = kv8_ex2(x[i] - mref);
       l_run += (x[0] + x[1]) + (x[2] + x[3]);
-      g.pv(o, pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+      g.pv(o, x);
     };
 
     // Of unit kb + lane: the positions of its groups (-1: nothing there) and

@@ -1,5 +1,5 @@
-"""Precision of the 8-bit attend's value product: values of any size next to a tail, and weights far below the largest,
-against the plain 64-bit form with bounds that do not depend on the values' size."""
+"""Precision of the 8-bit attend's value product: values of any size next to a tail, weights far below the largest, and
+tail weights, against the plain 64-bit form with bounds that do not depend on the values' size."""
 import numpy as np
 import pytest
 import torch
@@ -20,23 +20,24 @@ def value_sizes(row, block, fmt):
     return np.concatenate([np.zeros(0)] + out)
 
 
-def bounds(q, k, v, scale, p, stored, size, tail_half):
+def bounds(q, k, v, scale, p, stored, size):
     """Bounds of the kernel's errors from its formula's roundings, relative to the values' own size.
     Scores: as in plain.attend_bounds.  A stored token's weight is rounded to fp16: half a step is 2^-11 of it, or, among
     the subnormals, 2^-25 in units in which the token with the largest product of weight and value scale has
-    2^14 or more, so 2^-39 of the largest weight times value for each token.  A tail token's weight has the relative half
-    step `tail_half`.  Sums: a warp adds its tokens' groups one after the other (a row is spread over 12 warps at least),
-    then up to 200 partials are merged, each addition off by 2^-23 of at most sum p |v| (truncating adds), in
-    the accumulators and in the weights' sum alike."""
+    2^14 or more, so 2^-39 of the largest weight times value for each token.  A tail token's weight is the sum of a
+    truncated bf16 (the rest is below 2^-7 of it) and that rest in bf16 (half a step is 2^-8 of it): 2^-15.
+    Sums: a warp adds its tokens' groups one after the other (a row is spread over 12 warps at least), then up to 200
+    partials are merged, each addition off by 2^-23 of at most sum p |v| (truncating adds), in the accumulators and
+    in the weights' sum alike."""
     d, n = q.shape[1], k.shape[0]
     e = d * 2.0 ** -23 * scale * (np.abs(q) @ np.abs(k).T).max(1)
     pv = p @ np.abs(v)
-    w = (p * np.where(stored, 2.0 ** -11, tail_half)) @ np.abs(v)
+    w = (p * np.where(stored, 2.0 ** -11, 2.0 ** -15)) @ np.abs(v)
     adds = 2 * (n / 192 + 200) * 2.0 ** -23
     return e, w + (2 * e[:, None] + 2.0 ** -20 + adds) * pv + n * 2.0 ** -39 * (p * size).max(1)[:, None]
 
 
-def check(p, q, pages=None, tail_half=2.0 ** -8, heads=None, **kw):
+def check(p, q, pages=None, **kw):
     d = p.desc
     G, scale = d.num_q_heads // d.num_kv_heads, d.head_dim ** -0.5
     out, lse = ops.kv8_decode_attend(d, p.cache, q.cuda(), p.ctx, page_idx=None if pages is None else pages[0],
@@ -61,7 +62,7 @@ def check(p, q, pages=None, tail_half=2.0 ** -8, heads=None, **kw):
             at = slice(h * G, (h + 1) * G)
             qq = q[b, at].double().numpy()
             ref, ref_lse, w = plain.attend(qq, k, v, scale)
-            e, slack = bounds(qq, k, v, scale, w, stored, size, tail_half)
+            e, slack = bounds(qq, k, v, scale, w, stored, size)
             err = np.abs(got[b, at] - ref)
             assert (err <= slack + 2.0 ** -8 * (np.abs(ref) + slack)).all(), (b, h, (err / (np.abs(ref) + slack)).max())
             assert (np.abs(got_lse[b, at] - ref_lse) <= e + 2.0 ** -18 + 2.0 ** -22 * np.abs(ref_lse)).all()
@@ -142,7 +143,7 @@ def test_infinite_tail_value_shows_in_its_channel_only():
         ref, _, w = plain.attend(qq, k, v, 128 ** -0.5)
         stored = np.arange(len(row)) < 2944
         row.tail_v = [np.where(np.isfinite(x), x, 0) for x in row.tail_v]
-        _, slack = bounds(qq, k, v, 128 ** -0.5, w, stored, value_sizes(row, 64, "int8"), 2.0 ** -8)
+        _, slack = bounds(qq, k, v, 128 ** -0.5, w, stored, value_sizes(row, 64, "int8"))
         err = np.abs(out[b].double().numpy() - ref)
         err[:, ch] = 0
         assert (err <= slack + 2.0 ** -8 * (np.abs(ref) + slack)).all()
@@ -168,3 +169,18 @@ def test_weights_far_below_a_dominant_token(fmt, d, gap, at):
 
     p.append(lens, edit)
     check(p, q)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tail_weights_near_cancellation(d):
+    """Rows that are nothing but tail, with values +1 and -1: the output is the difference of sums of weights."""
+    lens = [1, 2, 3, 15, 16, 17, 100, 255]
+    p = Pair(len(lens), 8, 1, d, 512, "int8", 256, seed=d + 5)
+
+    def edit(kv):
+        kv[:, 0::2, 1] = 1
+        kv[:, 1::2, 1] = -1
+        kv[:, 1::2, 0] = kv[:, 0::2, 0][:, :kv[:, 1::2].shape[1]] * 1.0078125  # logits in pairs almost alike
+
+    p.append(lens, edit)
+    check(p, query(p, 6, 0.25))
