@@ -691,17 +691,17 @@ class Kv8Decode:
     def prefill(self, qkv, new_len=None):
         """Writes the keys and values of a prompt (or of its next piece): qkv [B, T, Hq + 2 Hkv, D], of which
         sequence b has its first new_len[b] tokens.  Returns the rotated queries [B, T, Hq, D]."""
-        Hq, H = self.desc.num_q_heads, self.desc.num_kv_heads
+        Hq, H, D = self.desc.num_q_heads, self.desc.num_kv_heads, self.desc.head_dim
         B, T = qkv.shape[:2]
         step = torch.arange(T, dtype=torch.int32, device=qkv.device)
         pos = (self.ctx_len + self.evicted)[:, None] + step
         if new_len is not None:
             pos = torch.where(step < new_len[:, None], pos, -1)  # padding is skipped
-        flat = qkv.view(B * T, Hq + 2 * H, qkv.shape[-1])
+        flat = qkv.view(B * T, Hq + 2 * H, D)
         q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:Hq + H], pos.reshape(-1), self.q_weight, self.k_weight)
-        kv8_append(self.desc, self.cache, k.view(B, T, H, -1), qkv[:, :, Hq + H:], self.ctx_len, new_len=new_len,
+        kv8_append(self.desc, self.cache, k.view(B, T, H, D), qkv[:, :, Hq + H:], self.ctx_len, new_len=new_len,
                    kmin=self.kmin, kmax=self.kmax, mass=self.mass)
-        return q.view(B, T, Hq, -1)
+        return q.view(B, T, Hq, D)
 
     def __call__(self, qkv, sink=None):
         """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
