@@ -697,8 +697,8 @@ class Kv8Decode:
         pos = (self.ctx_len + self.evicted)[:, None] + step
         if new_len is not None:
             pos = torch.where(step < new_len[:, None], pos, -1)  # padding is skipped
-        flat = qkv.view(B * T, Hq + 2 * H, D)
-        q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:Hq + H], pos.reshape(-1), self.q_weight, self.k_weight)
+        flat = qkv[:, :, :Hq + H].reshape(B * T, Hq + H, D)  # a view, or a copy where qkv is a slice of a longer batch
+        q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:], pos.reshape(-1), self.q_weight, self.k_weight)
         kv8_append(self.desc, self.cache, k.view(B, T, H, D), qkv[:, :, Hq + H:], self.ctx_len, new_len=new_len,
                    kmin=self.kmin, kmax=self.kmax, mass=self.mass)
         return q.view(B, T, Hq, D)

@@ -28,3 +28,21 @@ def test_prefill_of_an_empty_piece():
     before = [x.clone() for x in held(s)]
     assert s.prefill(qkv[:, :0].contiguous(), ints([0, 3])).shape == (B, 0, HQ, D)
     assert s.ctx_len.tolist() == [40, 40] and all(same(x, y) for x, y in zip(held(s), before))
+
+
+def test_prefill_in_slices_of_one_batch_equals_the_whole():
+    """The pieces are strided views [B, T, heads, D] of one projection's output, ragged lengths among them."""
+    a, b = step(), step()
+    qkv = bf16(np.random.default_rng(1), (B, 90, HQ + 2 * H, D)).cuda()
+    whole = a.prefill(qkv)
+    parts = [b.prefill(qkv[:, lo:hi]) for lo, hi in ((0, 33), (33, 34), (34, 90))]
+    assert torch.equal(torch.cat(parts, 1), whole)
+    for x, y in zip(held(a)[:-2], held(b)[:-2]):
+        assert same(x, y)
+    assert same(a.cache.k_tail[:, :, :10], b.cache.k_tail[:, :, :10])
+    wide = torch.zeros((B, 7, HQ + 2 * H + 3, D), dtype=torch.bfloat16, device="cuda")
+    wide[:, :, 1:-2] = bf16(np.random.default_rng(2), (B, 7, HQ + 2 * H, D)).cuda()
+    x = a.prefill(wide[:, :, 1:-2], ints([7, 2]))  # heads that are a slice, too
+    y = b.prefill(wide[:, :, 1:-2].contiguous(), ints([7, 2]))
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1, :2], y[1, :2]) and a.ctx_len.tolist() == [97, 92]
+    assert same(a.cache.k_tail[:, :, :1], b.cache.k_tail[:, :, :1]) and same(a.cache.k_codes, b.cache.k_codes)
