@@ -668,6 +668,15 @@ class Kv8Decode:
             raise ValueError("rope and desc must describe the same heads")
         if mass and k_budget:
             raise ValueError("weight sums need dense attention (k_budget 0)")
+        if desc.flags & ~L.SLS_FLAG_TEST_WAIT_TIMEOUT:
+            raise ValueError("the 8-bit attend has one kernel: no path flags")
+        if k_budget:  # what the first step would refuse only after it has appended its token
+            if desc.page_size < 16:
+                raise ValueError(f"page lists over an 8-bit cache need pages of >= 16 tokens, got {desc.page_size}")
+            forced = n_sink_pages + (-(-n_local_tokens // desc.page_size) + 1 if n_local_tokens > 0 else 0)
+            if min(n_sink_pages, n_local_tokens) < 0 or not max(1, forced) <= k_budget <= desc.capacity // desc.page_size:
+                raise ValueError(f"k_budget {k_budget} must hold the forced pages (up to {forced}) and be at most the "
+                                 f"{desc.capacity // desc.page_size} pages of a row")
         B, Hq, H, D, P = desc.batch, desc.num_q_heads, desc.num_kv_heads, desc.head_dim, desc.page_size
         self.desc, self.rope = desc, rope
         self.k, self.n_sink, self.n_local = int(k_budget), int(n_sink_pages), int(n_local_tokens)
@@ -686,6 +695,8 @@ class Kv8Decode:
             self.select_workspace = select_pages_workspace(desc, device)
         if mass:
             self.mass = new((B, H, desc.capacity // block), torch.float32)
+        if not L.load().sls_kv8_decode_attend_workspace_size(ctypes.byref(desc), ctypes.byref(self.cache.c), int(mass)):
+            raise ValueError("the 8-bit attend does not take this descriptor or block")
         self.workspace = kv8_attend_workspace(desc, self.cache, mass, device)
 
     def prefill(self, qkv, new_len=None):

@@ -46,3 +46,11 @@ def test_prefill_in_slices_of_one_batch_equals_the_whole():
     y = b.prefill(wide[:, :, 1:-2].contiguous(), ints([7, 2]))
     assert torch.equal(x[0], y[0]) and torch.equal(x[1, :2], y[1, :2]) and a.ctx_len.tolist() == [97, 92]
     assert same(a.cache.k_tail[:, :, :1], b.cache.k_tail[:, :, :1]) and same(a.cache.k_codes, b.cache.k_codes)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=torch.float32), dict(batch=4097)])
+def test_step_of_a_shape_that_the_attend_does_not_take_is_refused(kw):
+    dt = kw.get("dtype", torch.bfloat16)
+    desc = ops.make_desc(kw.get("batch", 1), 2, 1, 64, 16, 16, dt)
+    with pytest.raises(ValueError, match="does not take"):
+        ops.Kv8Decode(desc, ops.make_rope(2, 1, 64, dt), "int8", 16)
