@@ -733,7 +733,7 @@ class Kv8Decode:
         """Cuts every sequence to its keep heaviest complete blocks (kv8_evict in place).  Returns their numbers."""
         if self.mass is None:
             raise ValueError("evict needs the weight sums (mass=True)")
-        self.evicted += self.ctx_len
+        held = self.ctx_len.clone()
         kept = kv8_evict(self.desc, self.cache, self.ctx_len, self.mass, keep, n_sink_blocks, n_recent_blocks)[1]
-        self.evicted -= self.ctx_len
+        self.evicted += held - self.ctx_len  # after the call: one that is refused moves no position
         return kept

@@ -54,3 +54,14 @@ def test_step_of_a_shape_that_the_attend_does_not_take_is_refused(kw):
     desc = ops.make_desc(kw.get("batch", 1), 2, 1, 64, 16, 16, dt)
     with pytest.raises(ValueError, match="does not take"):
         ops.Kv8Decode(desc, ops.make_rope(2, 1, 64, dt), "int8", 16)
+
+
+def test_refused_eviction_leaves_the_positions():
+    s = step(mass=True)
+    s.prefill(bf16(np.random.default_rng(4), (B, 100, HQ + 2 * H, D)).cuda(), ints([100, 20]))
+    for bad in ((0, 0, 0), (4, 3, 2), (16, 0, 0)):
+        with pytest.raises(ops.L.SlsError):
+            s.evict(*bad)
+        assert s.evicted.tolist() == [0, 0] and s.ctx_len.tolist() == [100, 20]
+    s.evict(3)
+    assert s.evicted.tolist() == [48, 0] and s.ctx_len.tolist() == [52, 20]
