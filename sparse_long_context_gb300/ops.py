@@ -717,6 +717,8 @@ class Kv8Decode:
     def __call__(self, qkv, sink=None):
         """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
         d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
+        if sink is not None:
+            _need(sink, "sink", torch.float32, (Hq,))  # before the token is appended
         torch.add(self.ctx_len, self.evicted, out=self.positions)
         qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.positions, self.q_weight, self.k_weight,
                      q_out=self.q, k_out=self.k_new)

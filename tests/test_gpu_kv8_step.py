@@ -65,3 +65,15 @@ def test_refused_eviction_leaves_the_positions():
         assert s.evicted.tolist() == [0, 0] and s.ctx_len.tolist() == [100, 20]
     s.evict(3)
     assert s.evicted.tolist() == [48, 0] and s.ctx_len.tolist() == [52, 20]
+
+
+def test_step_with_a_bad_argument_appends_nothing():
+    s = step()
+    qkv = bf16(np.random.default_rng(5), (B, HQ + 2 * H, D)).cuda()
+    sink = torch.zeros(HQ, device="cuda")
+    for args in ((qkv, sink[:-1]), (qkv, sink.double()), (qkv, sink.cpu()), (qkv[:1], None), (qkv[:, :-1], None)):
+        with pytest.raises(ValueError):
+            s(*args)
+        assert s.ctx_len.tolist() == [0, 0]
+    s(qkv, sink)
+    assert s.ctx_len.tolist() == [1, 1]
