@@ -34,6 +34,7 @@
 // 6.2 us for 1000 tokens of 4 heads, 12 us for 128 pages of 16 tokens in 64 rows.
 #include <cooperative_groups.h>
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <algorithm>

@@ -2,7 +2,6 @@
 // scale s (int8: s = amax / 127; e4m3: s = amax / 448).
 #pragma once
 
-#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -23,12 +22,6 @@ __device__ __forceinline__ uint32_t kv8_code(float x, float amax) {
   const float y = __fdiv_rn(x * kv8_top<FMT>(), amax);
   if constexpr (FMT == kKv8Int8) return (uint32_t)__float2int_rn(y) & 0xffu;
   return __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
-}
-
-template <int FMT>
-__device__ __forceinline__ float kv8_value(uint32_t code) {
-  if constexpr (FMT == kKv8Int8) return (float)(int8_t)(code & 0xffu);
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)(code & 0xffu), __NV_E4M3)));
 }
 
 }  // namespace sls
