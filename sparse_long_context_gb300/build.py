@@ -35,10 +35,14 @@ def nvcc() -> str:
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile the tensor binding (a CPython extension over torch's C++ tensors); returns its path."""
+    """Compile the tensor binding (a CPython extension over torch's C++ tensors); returns its path.  Raises
+    RuntimeError where torch, its headers or g++ are missing."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError as e:
+        raise RuntimeError("the tensor binding needs torch (the C library does not)") from e
     src = os.path.join(CSRC, "binding.cpp")
     newest = _newest([src, os.path.join(INCLUDE, "sls.h"), torch.__file__, __file__])
     if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) > newest:
@@ -51,7 +55,10 @@ def build_binding(force: bool = False) -> str:
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in inc), src, "-o", tmp,
            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-ldl"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except FileNotFoundError as e:
+        raise RuntimeError("the tensor binding needs g++ (the C library does not)") from e
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, BINDING)
@@ -63,7 +70,8 @@ def _newest(paths):
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link libsls.so; returns its path."""
+    """Compile and link libsls.so, and compile the tensor binding beside it; returns the library's path.  The library
+    needs neither g++ nor torch: where the binding cannot be built, it is linked all the same before the error."""
     os.makedirs(BUILD, exist_ok=True)
     sources = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
@@ -88,13 +96,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         binding = ex.submit(build_binding, force)
         objs = list(ex.map(compile_one, sources))
+        if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
+            cmd = [cc, *ARCH, "-shared", "-cudart=static", "-o", LIB + ".tmp", *objs]
+            r = subprocess.run(cmd, capture_output=True, text=True)
+            if r.returncode != 0:
+                raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+            os.replace(LIB + ".tmp", LIB)
         binding.result()
-    if force or not os.path.exists(LIB) or os.path.getmtime(LIB) < _newest(objs):
-        cmd = [cc, *ARCH, "-shared", "-cudart=static", "-o", LIB + ".tmp", *objs]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-        os.replace(LIB + ".tmp", LIB)
     return LIB
 
 

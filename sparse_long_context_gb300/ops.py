@@ -366,7 +366,11 @@ def _binding():
     global _fast
     if _fast is None:
         L.load()
-        from . import _binding as fast  # raises when it has not been built
+        try:
+            from . import _binding as fast
+        except ImportError as e:
+            raise RuntimeError("the tensor binding of the norm/rotation and 8-bit cache calls is missing or does not load: "
+                               f"build it first (python -m sparse_long_context_gb300.build): {e}") from e
         fast.bind(L.LIB_PATH)
         _fast = fast
     return _fast
