@@ -689,7 +689,8 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
  *                 kmax_out [B, Hkv, dst_capacity/P, D] (in place: the same
  *                 buffers); needs P <= block and P dividing dst_capacity
  *   kept_idx      [B*Hkv, keep] int32 (written): the kept blocks' old
- *                 numbers, ascending, -1 padded when the row has fewer
+ *                 numbers, ascending, -1 padded when the row has fewer;
+ *                 memory of its own, as are ctx_len and ctx_out
  *   ctx_len [B] (read), ctx_out [B] (written; ctx_len itself or memory of
  *             its own)
  */

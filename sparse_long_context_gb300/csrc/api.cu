@@ -662,6 +662,23 @@ static sls_status check_kv8(const sls::Shape& s, const sls_kv8_cache* c, int cap
   return SLS_OK;
 }
 
+// Memory that a call reads or writes, and its bytes.
+struct Span {
+  const void* p;
+  int64_t n;
+};
+static Span at(const void* p, int64_t n) { return Span{p, n}; }
+
+// A cache's buffers, for `rows` rows of `capacity` tokens of D channels.
+struct CacheSpans {
+  Span s[6];
+};
+static CacheSpans spans_of(const sls::Kv8& c, int64_t rows, int64_t capacity, int D) {
+  const int64_t t = rows * capacity;
+  return {{at(c.kc, t * D), at(c.vc, t * D), at(c.ks, t / c.block * 4), at(c.vs, t / c.block * 4),
+           at(c.kt, rows * c.block * D * 2), at(c.vt, rows * c.block * D * 2)}};
+}
+
 sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* k_new,
                           int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
                           int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t max_new,
@@ -782,21 +799,30 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
   }
   if (ctx_out != ctx_len && overlap(ctx_out, (int64_t)s.B * 4, ctx_len, (int64_t)s.B * 4))
     return fail(SLS_EINVAL, "ctx_out must be ctx_len itself or memory of its own");
-  if (!same) {  // no destination may share memory with what is read
-    struct Range { const void* p; int64_t n; };
-    auto at = [](const void* p, int64_t n) { return Range{p, n}; };
-    const int64_t st = rows * s.Cap, dt = rows * dst_capacity, bl = e.src.block;
-    const Range in[] = {at(e.src.kc, st * s.D), at(e.src.vc, st * s.D), at(e.src.ks, st / bl * 4), at(e.src.vs, st / bl * 4),
-                        at(e.src.kt, rows * bl * s.D * 2), at(e.src.vt, rows * bl * s.D * 2), at(mass, st / bl * 4),
-                        at(kmin, st / s.P * s.D * 2), at(kmax, st / s.P * s.D * 2)};
-    const Range to[] = {at(e.dst.kc, dt * s.D), at(e.dst.vc, dt * s.D), at(e.dst.ks, dt / bl * 4), at(e.dst.vs, dt / bl * 4),
-                        at(e.dst.kt, rows * bl * s.D * 2), at(e.dst.vt, rows * bl * s.D * 2), at(mass_out, dt / bl * 4),
-                        at(kmin_out, dt / s.P * s.D * 2), at(kmax_out, dt / s.P * s.D * 2)};
-    for (const Range& x : in)
-      for (const Range& y : to)
+  const int64_t st = rows * s.Cap, dt = rows * dst_capacity, bl = e.src.block, pg = (int64_t)s.D * 2;
+  const CacheSpans from = spans_of(e.src, rows, s.Cap, s.D), into = spans_of(e.dst, rows, dst_capacity, s.D);
+  const Span in[] = {from.s[0], from.s[1], from.s[2], from.s[3], from.s[4], from.s[5], at(mass, st / bl * 4),
+                     at(kmin, st / s.P * pg), at(kmax, st / s.P * pg)};
+  const Span to[] = {into.s[0], into.s[1], into.s[2], into.s[3], into.s[4], into.s[5], at(mass_out, dt / bl * 4),
+                     at(kmin_out, dt / s.P * pg), at(kmax_out, dt / s.P * pg)};
+  if (!same)  // no destination may share memory with what is read
+    for (const Span& x : in)
+      for (const Span& y : to)
         if (overlap(x.p, x.n, y.p, y.n))
           return fail(SLS_EINVAL, "source and destination share memory without being the same cache");
+  // The list and the lengths are read while blocks move (the list's entries as
+  // they are): nothing else may lie there.
+  const Span own[] = {at(kept_idx, rows * keep * 4), at(ctx_out, (int64_t)s.B * 4), at(ctx_len, (int64_t)s.B * 4)};
+  for (int i = 0; i < 9; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(in[i].p, in[i].n, in[j].p, in[j].n) || overlap(to[i].p, to[i].n, to[j].p, to[j].n))
+        return fail(SLS_EINVAL, "two buffers of a cache, its sums or page summaries share memory");
+    for (const Span& x : own)
+      if (overlap(in[i].p, in[i].n, x.p, x.n) || overlap(to[i].p, to[i].n, x.p, x.n))
+        return fail(SLS_EINVAL, "kept_idx, ctx_len and ctx_out must be memory of their own");
   }
+  if (overlap(own[0].p, own[0].n, own[1].p, own[1].n) || overlap(own[0].p, own[0].n, own[2].p, own[2].n))
+    return fail(SLS_EINVAL, "kept_idx must be memory of its own");
   e.cap = s.Cap; e.dcap = dst_capacity; e.keep = keep; e.n_sink = n_sink_blocks; e.n_recent = n_recent_blocks;
   e.in_place = same; e.mass = mass; e.mass_out = mass_out;
   e.kmin = kmin; e.kmax = kmax; e.kmin_out = kmin_out; e.kmax_out = kmax_out;
