@@ -587,7 +587,7 @@ sls_status sls_qk_norm_rope(const sls_rope_desc* rope, int32_t num_tokens,
  *   k_codes, v_codes    [B, Hkv, Cap, D] one byte each
  *   k_scales, v_scales  [B, Hkv, Cap/block] float
  *   k_tail, v_tail      [B, Hkv, block, D] bf16
- * All pointers 16-byte aligned but for the scales (4).
+ * All pointers 16-byte aligned but for the scales (4); six pieces of memory.
  */
 typedef struct sls_kv8_cache {
   int32_t format;
@@ -620,6 +620,7 @@ typedef struct sls_kv8_cache {
  *                 (written; ctx_len itself or memory of its own)
  *   pos_out       [B] int32 receiving the first written position (-1 when
  *                 nothing was written), or NULL; memory of its own
+ * What is written shares no memory with the cache or another output.
  * max_new 0 appends nothing (ctx_out and pos_out are still written).
  */
 sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,

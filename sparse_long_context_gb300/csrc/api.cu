@@ -679,6 +679,14 @@ static CacheSpans spans_of(const sls::Kv8& c, int64_t rows, int64_t capacity, in
            at(c.kt, rows * c.block * D * 2), at(c.vt, rows * c.block * D * 2)}};
 }
 
+// The buffers a cache is made of are six pieces of memory.
+static sls_status check_apart(const CacheSpans& c, const char* name) {
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(c.s[i].p, c.s[i].n, c.s[j].p, c.s[j].n)) return fail(SLS_EINVAL, "%s has buffers that share memory", name);
+  return SLS_OK;
+}
+
 sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* k_new,
                           int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
                           int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t max_new,
@@ -709,6 +717,17 @@ sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
   int64_t ctas;
   if (!checked_mul((int64_t)s.B * s.Hkv * 2, units, &ctas) || ctas > INT32_MAX)
     return fail(SLS_EOVERFLOW, "grid too large");
+  const int64_t rows = (int64_t)s.B * s.Hkv, meta = rows * (s.Cap >> s.pshift) * s.D * 2;
+  const CacheSpans cs = spans_of(c, rows, s.Cap, s.D);
+  if ((r = check_apart(cs, "cache"))) return r;
+  // what is written besides: memory of its own, and none of the cache's
+  const Span to[] = {at(kmin, meta), at(kmax, meta), at(mass, rows * (s.Cap / c.block) * 4), at(ctx_out, n4), at(pos_out, n4)};
+  for (int i = 0; i < 5; ++i) {
+    for (const Span& x : cs.s)
+      if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(SLS_EINVAL, "an output shares memory with the cache");
+    for (int j = 0; j < i; ++j)
+      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(SLS_EINVAL, "two outputs share memory");
+  }
   sls::Kv8New n = {k_new, v_new, k_seq_stride, k_token_stride, k_head_stride,
                    v_seq_stride, v_token_stride, v_head_stride, max_new, new_len};
   sls::stat_add(sls::kStatMetadata);

@@ -63,3 +63,24 @@ def test_evict_buffers_do_not_share_memory(lib, in_place):
     if not in_place:
         assert evict(lib, in_place, kmax_out=X["kmin_out"]) == L.SLS_EINVAL
         assert evict(lib, in_place, mass_out=TO["v_scales"] + 252) == L.SLS_EINVAL
+
+
+def append(lib, src=None, **kw):
+    x, c = {**X, **kw}, cache({**AT, **(src or {})})
+    st = [8 * 256, 256, 128]
+    status = lib.sls_kv8_append(ctypes.byref(DESC), ctypes.byref(c), P(x["k"]), *st, P(x["v"]), *st, 8, P(x["len"]),
+                                P(x["kmin"]), P(x["kmax"]), P(x["mass"]), P(x["ctx"]), P(x["ctx_out"]), P(x["pos"]), None)
+    assert b"memory" in lib.sls_last_error()
+    return status
+
+
+def test_append_buffers_do_not_share_memory(lib):
+    for i, a in enumerate(NAMES):
+        for b in NAMES[:i]:
+            assert append(lib, {a: AT[b]}) == L.SLS_EINVAL, (a, b)
+    for name in ("kmin", "kmax", "mass", "ctx_out", "pos"):
+        for n, at in AT.items():
+            assert append(lib, **{name: at + SIZES[n] - 16}) == L.SLS_EINVAL, (name, n)
+        for other in ("kmin", "kmax", "mass", "ctx_out", "pos"):
+            if other != name:
+                assert append(lib, **{name: X[other]}) == L.SLS_EINVAL, (name, other)
