@@ -659,6 +659,8 @@ size_t sls_kv8_decode_attend_workspace_size(const sls_attn_desc* desc, const sls
  *             aligned, zero-filled before its first use (every call leaves
  *             its arrival counters at zero).  Calls of any shapes may share
  *             one that is large enough for each, but not run concurrently
+ * Outputs and workspace share no memory with each other or with what is read
+ * (mass_in excepted).
  * Rows with no token: out = 0, lse = -inf (or the sink alone).
  */
 sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* q,

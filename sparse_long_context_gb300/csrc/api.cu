@@ -774,6 +774,21 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
   if (!workspace || workspace_bytes < need)
     return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
   REQUIRE16(workspace);
+  const int64_t rows = (int64_t)s.B * s.Hkv, n4 = (int64_t)s.B * 4;
+  const CacheSpans cs = spans_of(c, rows, s.Cap, s.D);
+  if ((r = check_apart(cs, "cache"))) return r;
+  // what is written: memory of its own, and none of what is read (but for mass_in, above)
+  const Span to[] = {at(out, heads * s.D * 2), at(lse, heads * 4), at(mass_out, sums), at(workspace, (int64_t)need)};
+  const Span in[] = {at(q, heads * s.D * 2), at(ctx_len, n4), at(page_idx, rows * idx_stride * 4), at(count, rows * 4),
+                     at(sink, (int64_t)s.Hq * 4), at(mass_in == mass_out ? nullptr : mass_in, sums)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& x : cs.s)
+      if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(SLS_EINVAL, "an output or the workspace shares memory with the cache");
+    for (const Span& x : in)
+      if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(SLS_EINVAL, "an output or the workspace shares memory with an input");
+    for (int j = 0; j < i; ++j)
+      if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(SLS_EINVAL, "two outputs (or one and the workspace) share memory");
+  }
   return cuda_status(sls::launch_kv8_attend(s, c, q, page_idx, idx_stride, count, k_fixed, ctx_len, sink, out, lse,
                                             mass_in, mass_out, workspace, (cudaStream_t)stream),
                      "sls_kv8_decode_attend");

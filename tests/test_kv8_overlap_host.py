@@ -84,3 +84,28 @@ def test_append_buffers_do_not_share_memory(lib):
         for other in ("kmin", "kmax", "mass", "ctx_out", "pos"):
             if other != name:
                 assert append(lib, **{name: X[other]}) == L.SLS_EINVAL, (name, other)
+
+
+def attend(lib, src=None, pages=False, **kw):
+    x, c = {**X, **kw}, cache({**AT, **(src or {})})
+    status = lib.sls_kv8_decode_attend(
+        ctypes.byref(DESC), ctypes.byref(c), P(x["q"]), P(x["idx"]) if pages else None, 8, P(x["count"]) if pages else None, 8,
+        P(x["ctx"]), P(x["sink"]), P(x["out"]), P(x["lse"]), None if pages else P(x["mass"]),
+        None if pages else P(x["mass_out"]), P(x["ws"]), 1 << 40, None)
+    assert b"memory" in lib.sls_last_error()
+    return status
+
+
+@pytest.mark.parametrize("pages", [False, True])
+def test_attend_buffers_do_not_share_memory(lib, pages):
+    for i, a in enumerate(NAMES):
+        for b in NAMES[:i]:
+            assert attend(lib, {a: AT[b]}, pages) == L.SLS_EINVAL, (a, b)
+    read = ["q", "ctx", "sink"] + (["idx", "count"] if pages else ["mass"])
+    written = ["out", "lse", "ws"] + ([] if pages else ["mass_out"])
+    for name in written:
+        for n, at in AT.items():
+            assert attend(lib, None, pages, **{name: at + SIZES[n] - 16}) == L.SLS_EINVAL, (name, n)
+        for other in read + written:
+            if other != name and (name, other) != ("mass_out", "mass"):  # sums in place are allowed
+                assert attend(lib, None, pages, **{name: X[other]}) == L.SLS_EINVAL, (name, other)
