@@ -157,10 +157,10 @@ struct RopeShape {
 };
 
 // The coefficients of one side for a token, from the sines that the warp's lanes formed.
-template <typename T, int D, bool INTER>
+template <typename T, int D, bool INTER, bool FULL>
 __device__ __forceinline__ void rope_side_coef(RopeCoef<RopeShape<T, D>::VC / 2>& k, const T* w, int c0, int c1,
                                                const float (&mc)[RopeShape<T, D>::PER],
-                                               const float (&ms)[RopeShape<T, D>::PER]) {
+                                               const float (&ms)[RopeShape<T, D>::PER], bool rot) {
   using S = RopeShape<T, D>;
   float cs[S::VC], sn[S::VC];
 #pragma unroll
@@ -169,6 +169,10 @@ __device__ __forceinline__ void rope_side_coef(RopeCoef<RopeShape<T, D>::VC / 2>
     sn[i] = __shfl_sync(0xffffffffu, ms[i % S::PER], (i / S::PER) * S::L + (threadIdx.x & 31) % S::L);
   }
   rope_coef<T, INTER, S::VC / 2>(k, w, c0, c1, cs, sn);
+  if (!FULL && !rot) {  // sin = 0, but an infinite weight times it is not
+#pragma unroll
+    for (int i = 0; i < S::VC / 2; ++i) k.B[i] = k.E[i] = 0ull;
+  }
 }
 
 // One step: the lane's two vectors of a head, normalised (`norm` for the warp, `mine` for
@@ -217,7 +221,7 @@ __device__ __forceinline__ void rope_side(const T* in, int64_t in_h, T* out, int
                                           const float (&ms)[RopeShape<T, D>::PER], float eps, int sub, bool rot) {
   constexpr int HS = RopeShape<T, D>::HS, U = kRopeUnroll;
   RopeCoef<RopeShape<T, D>::VC / 2> k;
-  rope_side_coef<T, D, INTER>(k, w, c0, c1, mc, ms);
+  rope_side_coef<T, D, INTER, FULL>(k, w, c0, c1, mc, ms, rot);
   int h = s0 * HS + sub;
   const int hend = min(heads, s1 * HS);
   in += h * in_h;
@@ -302,7 +306,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
     if constexpr (FEW) {
       RopeCoef<VC / 2> k;
       if (qsteps) {
-        rope_side_coef<T, D, INTER>(k, static_cast<const T*>(a.wq), c0, c1, mc, ms);
+        rope_side_coef<T, D, INTER, FULL>(k, static_cast<const T*>(a.wq), c0, c1, mc, ms, rot);
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u)
           if (u < qsteps)
@@ -310,7 +314,7 @@ qk_norm_rope_kernel(const __grid_constant__ RopeArgs a, int per, int chunks) {
                                          u * HS + sub < a.Hq);
       }
       if (steps > qsteps) {
-        rope_side_coef<T, D, INTER>(k, static_cast<const T*>(a.wk), c0, c1, mc, ms);
+        rope_side_coef<T, D, INTER, FULL>(k, static_cast<const T*>(a.wk), c0, c1, mc, ms, rot);
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u)
           if (u >= qsteps && u < steps) {
@@ -384,7 +388,7 @@ qk_norm_rope_one_kernel(const __grid_constant__ RopeArgs a, int steps) {
         sincospif((float)turn * 1.0842021724855044e-19f, &ms[i], &mc[i]);  // 2^-63: half turns in [-1, 1]
       }
       RopeCoef<VC / 2> k;
-      rope_side_coef<T, D, INTER>(k, w, c0, c1, mc, ms);
+      rope_side_coef<T, D, INTER, FULL>(k, w, c0, c1, mc, ms, rot);
       rope_step<T, D, INTER, FULL>(out + t * out_t, r0, r1, k, norm, c0, c1, a.eps, rot, live, w != nullptr);
     }
     pos = next;
