@@ -657,10 +657,16 @@ size_t sls_kv8_decode_attend_workspace_size(const sls_attn_desc* desc, const sls
  *             The sums do not depend on the order in which CTAs finish.
  *   workspace >= sls_kv8_decode_attend_workspace_size() bytes, 16-byte
  *             aligned, zero-filled before its first use (every call leaves
- *             its arrival counters at zero).  Calls of any shapes may share
- *             one that is large enough for each, but not run concurrently
+ *             its arrival counters at zero).  Calls of this function, of any
+ *             shapes, may share one that is large enough for each, but not
+ *             run concurrently
  * Outputs and workspace share no memory with each other or with what is read
  * (mass_in excepted).
+ * Roundings: scores, softmax statistics and sums are fp32.  In the value
+ * product a weight times its block's value scale has 11 bits (tail tokens'
+ * weights 16), down to 2^-28 of the largest such product that shares its sums;
+ * smaller ones lose bits, and those below 2^-38 of it are dropped.  The
+ * output is rounded to bf16.
  * Rows with no token: out = 0, lse = -inf (or the sink alone).
  */
 sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache* cache, const void* q,

@@ -15,7 +15,9 @@
 //                  two of their own (exact but for parts below 2^-35 of the
 //                  head's largest, which round to fp16's subnormals), B = codes
 //   x   = S * scale * s_k          fp32, one multiplication per score
-//   O^T += V^T W^T,  W = p s_v     rounded to fp16 (half a step, 2^-11)
+//   O^T += V^T W^T,  W = p s_v     rounded to fp16 (half a step, 2^-11: independent
+//                  errors of a row's weights, which add 2.6e-4 of the output to the 1.7e-3
+//                  of its own rounding to bf16; a second part would double the products)
 // The running maximum is that of x + e - 14 with 2^e <= s_v < 2^(e+1) the exponent of
 // the value scale: then W = exp2(x - m) s_v < 2^15 for blocks of any scale, nothing
 // overflows, and the largest W is 2^14 or more, so that weights down to 2^-28 of it
@@ -28,10 +30,14 @@
 //
 // Bound by memory on long contexts: 32 contexts of 49k to 64k tokens, 2 KV heads of 6
 // query heads and 128 channels, int8: 140 to 143 us for 943 MB (6.6 to 6.7 TB/s, the
-// measured copy rate); e4m3 is 5% slower, its conversion instruction the busiest
+// measured copy rate); e4m3 is 6% slower, its conversion instruction the busiest
 // pipe.  At D = 64 the work per token weighs twice as much: 81 us for 470 MB (85%).
 // Short rows are bound by a chain of latencies (lengths, list, scales, copies, merge):
 // 6.2 us for 1000 tokens of 4 heads, 12 us for 128 pages of 16 tokens in 64 rows.
+// Rows of middle length stay far from the copy rate: 26 us for 4 rows of 64k tokens (a
+// cluster of 16 CTAs each, floor 10), and the variant follows from the capacity, so 64
+// rows of 1000 tokens take 8 us in a capacity of 1024 and 14 in 65536.  (Times of the
+// device alone, calls replayed from a graph.)
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -55,8 +61,10 @@ constexpr int kKv8MaxRows = 4096;  // rows whose first units are kept there
 // where another one's counters are.
 constexpr size_t kKv8TicketBytes = kKv8MaxRows * sizeof(int32_t);
 constexpr int kKv8PerSm = 1;       // resident CTAs of an SM
-// Least units of a CTA: a shorter job uses fewer CTAs (1, 2, 4, 8 and 12 units: 14.4,
-// 12.7, 11.8, 13.1 and 13.6 us for 1000 tokens of 4 heads).
+// Least units of a CTA in ranges: a shorter job uses fewer CTAs.  2, 4 and 8 units: 10.8,
+// 11.5 and 13.1 us for 8 rows of 1000 tokens in a capacity of 131072, 10.8, 10.6 and 15.8
+// for 32 rows of 500 at D = 64; 64 rows of 100 tokens would be faster with 2 (7.4, 11.7
+// and 20.5), rows of 4000 take the same with each.
 constexpr int kKv8MinUnits = 4;
 // Work of a row change (drain, merge, partial and refill) in tokens: 512 to 4096
 // measured on seven shapes, 2048 the best or within 2% of it on six (64k x 32 dense
@@ -1050,10 +1058,12 @@ static int kv8_clusters(int c, Kv8Device* d) {
 // measured costs make faster.  A CTA takes t ns a token (4.9 at D = 128, 2.7 at
 // D = 64) and a cluster 5.5 us besides, in as many waves as the clusters need; the
 // ranges take 13 us, 6 per row beyond their equal shares, and 0.1 for each CTA that shares
-// a row.  Fitted to 50 shapes of 1 to 256 rows of 1k to 64k tokens, which it times
-// within 10% or so: 96 rows of 4k at D = 128 take 27 us with a CTA each and 30 in ranges, 16k 87 and 66; 64 rows of 16k at
-// D = 64 29 with two each and 32 in ranges, 64k 94 and 86.  `most` bounds a row's
-// tokens; where only the device knows them, rows are taken to hold three quarters
+// a row.  Measured on 50 shapes of 1 to 256 rows, full but for a tenth, of 1k to 64k tokens,
+// both sides each: 27.5 us with a CTA a row and 30.3 in ranges for 96 rows of 4k at D = 128,
+// 76 and 66 at 16k; 28.9 with two a row and 32.8 for 64 rows of 16k at D = 64, 94 and 87 at
+// 64k.  Where it takes the slower side it loses 9% at most (256 rows of 4k at D = 128: 57.9
+// us against 53.0).
+// `most` bounds a row's tokens; where only the device knows them, rows are taken to hold three quarters
 // of it on average and a cluster to wait for one that is full.
 template <int D, int FMT, bool LIST, bool MASS>
 static int kv8_pick(int rows, double most, bool fixed, bool even, Kv8Device* d) {

@@ -4,8 +4,11 @@
 // Both are bound by memory on prompts: four prompts of up to 32k tokens, 8 heads of
 // 128 channels, with page min/max: 122 us for 813 MB (98% of the measured copy); 8 x 4
 // rows cut from 32k tokens to 16k: 49 us for 269 MB, of which the copies take 41 (97%)
-// and the choice before them the rest.  Single tokens and small caches are latency:
-// 3.8 us for 32 sequences' tokens, 5.3 us for a small eviction.
+// and the choice before them the rest; in place, in two launches, 52 us for the 267 MB of the
+// blocks that move.  Single tokens and small caches are latency: 3.8 us for 32 sequences'
+// tokens, 5.3 us for a small eviction, 7.9 in place.  (Times of the device alone, calls
+// replayed from a graph, with lengths written to other memory; written in place they cost
+// a prompt's append 0.5 us and an eviction 1.1 us more, a launch of its own.)
 #include <algorithm>
 
 #include "common.cuh"

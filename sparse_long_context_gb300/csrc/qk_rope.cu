@@ -3,10 +3,12 @@
 //   y = x w / sqrt(mean(x^2) + eps),  (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin).
 // Bound by memory: every element is read and written once.  32768 tokens of 28 + 4
 // heads of 128 channels take 91 us (5.9 TB/s, 87% of the measured copy), 16384 in
-// fp32 with half of the channels rotated 85 us (93%), 1000 tokens 5.7 us, 32 tokens of
+// fp32 with half of the channels rotated 86 us (92%), 1000 tokens 6.2 us, 32 tokens of
 // 12 + 2 heads 1.8 us, the launch.  Tokens of few heads are bound by the sines and
 // coefficients, which are a token's whatever its heads: 16384 tokens of 8 + 1 heads 20 us
-// (floor 11), 23029 of 7 + 1 heads of 64 channels 10.6 (floor 7).
+// (floor 11), 23029 of 7 + 1 heads of 64 channels 10.7 (floor 7).  (Times of the device
+// alone, calls replayed from a graph.)  The arithmetic is fp32 throughout, the norm's
+// reciprocal root within 2 ulp; the one rounding to fewer bits is the output's.
 //
 // A lane holds two 16-byte vectors of a head whose channels form whole pairs (vector
 // l and vector R/2 further on when halves are paired), so a pair never leaves the

@@ -662,7 +662,12 @@ class Kv8Decode:
     (qk_norm_rope), append of the token (kv8_append), and the attention, dense or, with k_budget > 0, over the
     k_budget pages per KV head that Quest selection picks from page min/max kept of the unquantised keys.  The
     buffers are preallocated, so a step can be captured in a CUDA graph.  With mass=True every block's attention
-    weight is summed (dense only), and evict() cuts the cache to a budget of blocks by it."""
+    weight is summed (dense only), and evict() cuts the cache to a budget of blocks by it.
+
+    As with decode_append, a sequence at capacity is left unchanged: the step appends nothing to it and ctx_len
+    stays (its query attends to what is held), so a caller that counts tokens evicts, or stops, before that.  The
+    same holds for a piece of a prompt that does not fit.  The weight sums are those of decode steps: after a prefill
+    they are 0, and an eviction then keeps the first blocks."""
 
     def __init__(self, desc: L.AttnDesc, rope: L.RopeDesc, fmt: str = "int8", block: int = 64, k_budget: int = 0,
                  n_sink_pages: int = 0, n_local_tokens: int = 0, mass: bool = False, device="cuda",
