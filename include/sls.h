@@ -620,7 +620,8 @@ typedef struct sls_kv8_cache {
  *                 (written; ctx_len itself or memory of its own)
  *   pos_out       [B] int32 receiving the first written position (-1 when
  *                 nothing was written), or NULL; memory of its own
- * What is written shares no memory with the cache or another output.
+ * Lengths and outputs share no memory with the cache or each other (ctx_out
+ * excepted, as above).
  * max_new 0 appends nothing (ctx_out and pos_out are still written).
  */
 sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,

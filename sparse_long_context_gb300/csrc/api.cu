@@ -722,6 +722,12 @@ sls_status sls_kv8_append(const sls_attn_desc* desc, const sls_kv8_cache* cache,
   if ((r = check_apart(cs, "cache"))) return r;
   // what is written besides: memory of its own, and none of the cache's
   const Span to[] = {at(kmin, meta), at(kmax, meta), at(mass, rows * (s.Cap / c.block) * 4), at(ctx_out, n4), at(pos_out, n4)};
+  for (const Span& x : {at(ctx_len, n4), at(new_len, n4)}) {
+    for (const Span& y : cs.s)
+      if (overlap(x.p, x.n, y.p, y.n)) return fail(SLS_EINVAL, "the lengths share memory with the cache");
+    for (int i = 0; i < 3; ++i)
+      if (overlap(x.p, x.n, to[i].p, to[i].n)) return fail(SLS_EINVAL, "the lengths share memory with an output");
+  }
   for (int i = 0; i < 5; ++i) {
     for (const Span& x : cs.s)
       if (overlap(to[i].p, to[i].n, x.p, x.n)) return fail(SLS_EINVAL, "an output shares memory with the cache");

@@ -84,6 +84,9 @@ def test_append_buffers_do_not_share_memory(lib):
         for other in ("kmin", "kmax", "mass", "ctx_out", "pos"):
             if other != name:
                 assert append(lib, **{name: X[other]}) == L.SLS_EINVAL, (name, other)
+    for name in ("ctx", "len"):
+        for at in [*AT.values(), X["kmin"], X["kmax"], X["mass"]]:
+            assert append(lib, **{name: at}) == L.SLS_EINVAL, name
 
 
 def attend(lib, src=None, pages=False, **kw):
