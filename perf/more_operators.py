@@ -82,11 +82,12 @@ def draw(rng):
     if op == "append":
         new = 1 if rng.random() < 0.4 else _log(rng, 2, cap // 2)
         return c | dict(pool=batch * (cap // page) + rng.randint(1, 99), new=new, summaries=rng.random() < 0.5)
-    if op == "select":
-        k = min(cap // page, _log(rng, 16, 200) + 16)
-        forced = k >= 16
-        return c | dict(hq=group * hkv, low=low, high=high, k=k, first=rng.choice([0, 1, 2]) if forced else 0,
-                        last=rng.choice([0, 50, 64, 128]) if forced else 0)
+    if op == "select":  # a budget of at most half of the shortest context's pages
+        c["page"] = page = page if cap // page >= 32 else 16
+        k = min(220, _log(rng, 8, cap // page // 2))
+        low = rng.randint(2 * k * page, cap)
+        return c | dict(hq=group * hkv, low=low, high=rng.randint(low, cap), k=k, first=rng.choice([0, 1, 2]) if k > 11 else 0,
+                        last=rng.choice([0, 50, 64, 128]) if k > 11 else 0)
     if op == "fork":
         prompts = max(1, batch // rng.choice([2, 3, 4, 8]))
         return c | dict(prompts=prompts, low=low, high=high, summaries=rng.random() < 0.5, beams=rng.random() < 0.5)
