@@ -19,6 +19,14 @@
  *   sls_kv8_decode_attend   decode attention over it, dense or over page lists
  *   sls_kv8_evict           the blocks with the most attention weight kept
  *
+ * and a cache whose pages lie in a pool, handed out as sequences grow:
+ *
+ *   sls_paged_append         tokens into pages taken from the pool
+ *   sls_paged_select_pages   page bound + top-k over the pool's summaries
+ *   sls_paged_decode_attend  decode attention, dense or over page lists
+ *   sls_paged_fork           sequences shared, reordered, cut and freed
+ *   sls_paged_compact        the pool's used pages moved to its front
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Every pointer argument is a DEVICE pointer owned by the caller, unless
@@ -710,6 +718,162 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
                          const void* kmax, void* kmin_out, void* kmax_out, int32_t* kept_idx,
                          const int32_t* ctx_len, int32_t* ctx_out, void* stream);
 
+/* ---- the paged KV cache -------------------------------------------------- */
+
+/*
+ * A K/V cache whose pages lie anywhere in a pool and may be held by several
+ * sequences.  Of the descriptor, batch is the number of sequences, page_size P
+ * in [16, 256], and capacity the most tokens of one sequence (no memory is
+ * set aside for it but the table's row).  The struct lives on the host, the
+ * pointers are device memory of the caller.
+ *   num_pages   N pages of the pool, 1 <= N <= 2^24, N * Hkv * P < 2^31
+ *   k_pages, v_pages  [N, Hkv, P, D] dtype
+ *   kmin, kmax  [N, Hkv, D] dtype: min and max of every page's keys, kept
+ *               current by the calls below, or both NULL
+ *   ctx_len     [B] int32 tokens of each sequence
+ *   table       [B, Cap/P] int32 the pool's page that holds a logical page, -1
+ *               past the sequence's length
+ *   refs        [N] int32 sequences that hold each page (0: free)
+ *   state       [sls_paged_state_words()] int32, the free pages and scratch of
+ *               the calls; its contents are the library's
+ * k_pages, v_pages, kmin, kmax and state are 16-byte aligned; no two of the
+ * buffers share memory.  Before the first use of a cache (all ctx_len 0), and
+ * whenever table or ctx_len were written by the caller, sls_paged_init derives
+ * refs and state from them.
+ * A page that is not complete (the last one of a sequence whose length is not
+ * a multiple of P) belongs to one sequence; complete pages may be shared and are
+ * never written.  The calls keep to this; a table that the caller writes has to.
+ * Calls on one cache are ordered by the caller: none runs while another that
+ * changes it does.  At most 4096 sequences; another P returns
+ * SLS_EUNSUPPORTED.  Table entries of a sequence's length that are no page
+ * of the pool are counted for sls_pipeline_check() and skipped.
+ */
+typedef struct sls_paged_cache {
+  int32_t num_pages;
+  void* k_pages;
+  void* v_pages;
+  void* kmin;
+  void* kmax;
+  int32_t* ctx_len;
+  int32_t* table;
+  int32_t* refs;
+  int32_t* state;
+} sls_paged_cache;
+
+/* Words of a cache's state; 0 for an invalid descriptor or number of pages. */
+size_t sls_paged_state_words(const sls_attn_desc* desc, int32_t num_pages);
+
+/*
+ * Derives refs and state from table and ctx_len (read), and sets the table's
+ * entries past each length to -1.  The page summaries are the caller's.
+ */
+sls_status sls_paged_init(const sls_attn_desc* desc, const sls_paged_cache* cache, void* stream);
+
+/*
+ * Append new tokens of every sequence: one decoded token, a whole prompt or a
+ * piece of one.  Sequence b appends its first new_len[b] (clamped to
+ * [0, max_new]; NULL: max_new) tokens at positions ctx_len[b] and up.  It needs
+ * ceil((ctx_len[b] + n) / P) - ceil(ctx_len[b] / P) pages: the call takes the
+ * lowest-numbered free ones, in the order of sequences and their logical pages.
+ * A sequence whose tokens do not fit its capacity needs none and is left
+ * unchanged; so is one that needs pages when it and the sequences before it need
+ * more in all than are free (a later one that needs none still appends).
+ *   k_new, v_new  [B, max_new, Hkv, D] dtype (read), strides in elements
+ *                 between sequences, tokens and heads (>= 0, multiples of 8
+ *                 for bf16 and 4 for fp32; channels contiguous); no memory of the
+ *                 cache
+ *   kmin, kmax of the cache: a page's first token sets them, later ones fold in
+ *   pos_out       [B] int32 receiving the first written position (-1 when
+ *                 nothing was written), or NULL; memory of its own
+ * A sequence whose partial page is held by others too (a table the caller
+ * wrote) is left unchanged and counted as a bad entry.
+ */
+sls_status sls_paged_append(const sls_attn_desc* desc, const sls_paged_cache* cache,
+                            const void* k_new, int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride,
+                            const void* v_new, int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride,
+                            int32_t max_new, const int32_t* new_len, int32_t* pos_out, void* stream);
+
+/*
+ * sls_select_pages over a paged cache: the summaries are the cache's kmin and
+ * kmax (not NULL), found through its table; page_idx [B, Hkv, k] receives
+ * LOGICAL pages.  A page whose table entry is bad scores as a summary of zeros.
+ *   workspace  >= sls_select_pages_workspace_size() bytes, memory of its own
+ *              like page_idx
+ */
+sls_status sls_paged_select_pages(const sls_attn_desc* desc, const sls_paged_cache* cache, const void* q, int32_t k,
+                                  int32_t n_sink_pages, int32_t n_local_tokens, int32_t* page_idx, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace sls_paged_decode_attend needs; 0 for an invalid or
+ * unsupported descriptor. */
+size_t sls_paged_decode_attend_workspace_size(const sls_attn_desc* desc);
+
+/*
+ * Decode attention over a paged cache: softmax(scale q.k) v over the positions
+ * < ctx_len[b] (page_idx NULL) or over the valid tokens of the listed LOGICAL
+ * pages, with the sink as in sls_combine_splits.  Rows of uneven length are cut
+ * into equal ranges over the GPU.
+ *   desc      G <= 8, D 64 or 128, B*Hkv <= 4096; of the flags only
+ *             SLS_FLAG_TEST_WAIT_TIMEOUT
+ *   page_idx, idx_stride, count, k_fixed   as in sls_sparse_decode_attend
+ *             (-1 entries are skipped, bad ones counted and skipped)
+ *   q [B, Hq, D] dtype; sink [Hq] float or NULL; out [B, Hq, D] dtype; lse
+ *             [B, Hq] float or NULL
+ *   workspace >= sls_paged_decode_attend_workspace_size() bytes, 16-byte
+ *             aligned, zero-filled before its first use (every call leaves
+ *             its arrival counters at zero).  Calls of this function, of any
+ *             shapes, may share one that is large enough for each, but not
+ *             run concurrently
+ * Outputs and workspace share no memory with each other or with what is read.
+ * Roundings: scores, softmax statistics and sums are fp32; a bf16 cache's
+ * weights enter the value product with 16 bits; the output is rounded to dtype.
+ * Rows with no token: out = 0, lse = -inf (or the sink alone).
+ */
+sls_status sls_paged_decode_attend(const sls_attn_desc* desc, const sls_paged_cache* cache, const void* q,
+                                   const int32_t* page_idx, int32_t idx_stride, const int32_t* count, int32_t k_fixed,
+                                   const float* sink, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Bytes of workspace sls_paged_fork needs; 0 for an invalid descriptor. */
+size_t sls_paged_fork_workspace_size(const sls_attn_desc* desc);
+
+/*
+ * Make every sequence a prefix of an old one, all at once: sequence b becomes
+ * the first min(ctx_len[parent[b]], keep_len[b]) tokens of what sequence
+ * parent[b] was before the call (keep_len NULL: all of them).  parent[b] = b
+ * leaves it (or cuts it), -1 frees it, several sequences with one parent fork
+ * it, and a permutation reorders.  Complete pages are shared.  A partial last
+ * page, other than that of a sequence that stays as it is, is kept by the
+ * lowest-numbered sequence that needs it if no sequence holds it otherwise, and
+ * copied for the others to the lowest-numbered pages that were free before the
+ * call, in the order of sequences; its summary is formed anew.  Pages that no
+ * sequence holds any more are free after the call.
+ *   parent    [B] int32 (read); a value outside [-1, B) leaves the sequence as
+ *             it is and is counted for sls_pipeline_check()
+ *   keep_len  [B] int32 (read, negative ones count as 0) or NULL
+ *   done      [1] int32 or NULL: 1, or 0 when fewer pages were free than copies
+ *             are needed; then nothing has changed
+ *   workspace >= sls_paged_fork_workspace_size() bytes, 16-byte aligned
+ * parent, keep_len, done and workspace are memory of their own.
+ */
+sls_status sls_paged_fork(const sls_attn_desc* desc, const sls_paged_cache* cache, const int32_t* parent,
+                          const int32_t* keep_len, int32_t* done, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace sls_paged_compact needs; 0 for an invalid number of pages. */
+size_t sls_paged_compact_workspace_size(int32_t num_pages);
+
+/*
+ * Move the used pages to the front of the pool, so that with U of them the
+ * pages from U on are free: the used pages numbered U and up move, in order, to
+ * the free pages below U, with their summaries; table and refs follow.
+ *   moved     [N] int32: every page's new number, -1 for those that were free;
+ *             or NULL
+ *   workspace >= sls_paged_compact_workspace_size() bytes, 16-byte aligned
+ * moved and workspace are memory of their own.
+ */
+sls_status sls_paged_compact(const sls_attn_desc* desc, const sls_paged_cache* cache, int32_t* moved, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Message of the last failing call on this thread ("" if none). */
@@ -758,7 +922,8 @@ typedef struct sls_stats {
   uint64_t attend_refined;            /* ... with the refined (2-bit + 8-bit) keys */
   uint64_t combine;                   /* separate combine launches */
   uint64_t metadata;                  /* page min/max, thumbnail, residual and append calls, and those of
-                                         the norm/rotation and the 8-bit cache's append and eviction */
+                                         the norm/rotation, the 8-bit cache's append and eviction, and the
+                                         paged cache's append, fork and compaction */
   uint64_t recall;                    /* selection-recall launches */
   uint64_t select_rows_all_keys;      /* rows wider than 8192 pages whose sls_select_pages top-k
                                          ranked all of the row's keys (the candidate check failed) */

@@ -42,6 +42,12 @@ class Kv8CacheDesc(ctypes.Structure):
         (n, ctypes.c_void_p) for n in ("k_codes", "v_codes", "k_scales", "v_scales", "k_tail", "v_tail")]
 
 
+class PagedCacheDesc(ctypes.Structure):
+    """ctypes mirror of sls_paged_cache."""
+    _fields_ = [("num_pages", ctypes.c_int32)] + [
+        (n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "kmin", "kmax", "ctx_len", "table", "refs", "state")]
+
+
 class Stats(ctypes.Structure):
     """sls_stats: which paths the library took (include/sls.h)."""
     _fields_ = [(n, ctypes.c_uint64) for n in (
@@ -56,6 +62,8 @@ _I = ctypes.c_int32
 _L = ctypes.c_int64
 _D = ctypes.POINTER(AttnDesc)
 _C = ctypes.POINTER(Kv8CacheDesc)
+_G = ctypes.POINTER(PagedCacheDesc)
+_Z = ctypes.c_size_t
 SIGNATURES = {
     "sls_pagemeta_build": (_I, [_D, _P, _P, _P, _P, _P]),
     "sls_pagemeta_update": (_I, [_D, _P, _P, _P, _P, _P]),
@@ -92,6 +100,16 @@ SIGNATURES = {
     "sls_kv8_decode_attend_workspace_size": (ctypes.c_size_t, [_D, _C, _I]),
     "sls_kv8_decode_attend": (_I, [_D, _C, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "sls_kv8_evict": (_I, [_D, _C, _I, _C, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "sls_paged_state_words": (_Z, [_D, _I]),
+    "sls_paged_init": (_I, [_D, _G, _P]),
+    "sls_paged_append": (_I, [_D, _G, _P, _L, _L, _L, _P, _L, _L, _L, _I, _P, _P, _P]),
+    "sls_paged_select_pages": (_I, [_D, _G, _P, _I, _I, _I, _P, _P, _Z, _P]),
+    "sls_paged_decode_attend_workspace_size": (_Z, [_D]),
+    "sls_paged_decode_attend": (_I, [_D, _G, _P, _P, _I, _P, _I, _P, _P, _P, _P, _Z, _P]),
+    "sls_paged_fork_workspace_size": (_Z, [_D]),
+    "sls_paged_fork": (_I, [_D, _G, _P, _P, _P, _P, _Z, _P]),
+    "sls_paged_compact_workspace_size": (_Z, [_I]),
+    "sls_paged_compact": (_I, [_D, _G, _P, _P, _Z, _P]),
     "sls_pipeline_check": (_I, []),
     "sls_last_error": (ctypes.c_char_p, []),
     "sls_version": (_I, []),

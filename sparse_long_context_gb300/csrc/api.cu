@@ -6,6 +6,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 
 #include "launch.h"
 #include "sls.h"
@@ -154,7 +155,8 @@ sls_status sls_pipeline_check(void) {
   unsigned int timeouts = 0, bad = 0;
   for (auto take : {sls::take_status_attend_cc, sls::take_status_attend_mma, sls::take_status_attend_tma,
                     sls::take_status_attend_refined, sls::take_status_quest_step, sls::take_status_recall,
-                    sls::take_status_attend_kv8}) {
+                    sls::take_status_attend_kv8, sls::take_status_attend_paged, sls::take_status_paged_cache,
+                    sls::take_status_select_pages}) {
     const sls::DeviceStatus st = take();
     timeouts += st.wait_timeouts;
     bad += st.bad_page_ids;
@@ -267,14 +269,7 @@ size_t sls_select_pages_workspace_size(const sls_attn_desc* desc) {
   return sls::select_pages_workspace(s);
 }
 
-sls_status sls_select_pages(const sls_attn_desc* desc, const void* q, const void* kmin,
-                            const void* kmax, const int32_t* ctx_len, int32_t k,
-                            int32_t n_sink_pages, int32_t n_local_tokens, int32_t* page_idx,
-                            void* workspace, size_t workspace_bytes, void* stream) {
-  sls::Shape s;
-  sls_status r = check_desc(desc, &s);
-  if (r) return r;
-  REQUIRE16(q); REQUIRE16(kmin); REQUIRE16(kmax); REQUIRE(ctx_len); REQUIRE(page_idx);
+static sls_status check_select(const sls::Shape& s, int32_t k, int32_t n_sink_pages, int32_t n_local_tokens) {
   const int npcap = s.Cap >> s.pshift;
   if (k < 1 || k > npcap) return fail(SLS_EINVAL, "k=%d must be in [1, Cap/P=%d]", k, npcap);
   if (n_sink_pages < 0 || n_local_tokens < 0)
@@ -284,11 +279,23 @@ sls_status sls_select_pages(const sls_attn_desc* desc, const void* q, const void
   if (forced_max > k)
     return fail(SLS_EINVAL, "budget k=%d cannot hold the forced pages (up to %lld)", k,
                 (long long)forced_max);
-  if (s.P == 1 && kmin != kmax)
-    return fail(SLS_EINVAL, "page_size 1: pass the key cache as both kmin and kmax");
   if (npcap > sls::select_pages_max_pages())
     return fail(SLS_EUNSUPPORTED, "Cap/P=%d pages per row exceeds the supported %d", npcap,
                 sls::select_pages_max_pages());
+  return SLS_OK;
+}
+
+sls_status sls_select_pages(const sls_attn_desc* desc, const void* q, const void* kmin,
+                            const void* kmax, const int32_t* ctx_len, int32_t k,
+                            int32_t n_sink_pages, int32_t n_local_tokens, int32_t* page_idx,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  sls::Shape s;
+  sls_status r = check_desc(desc, &s);
+  if (r) return r;
+  REQUIRE16(q); REQUIRE16(kmin); REQUIRE16(kmax); REQUIRE(ctx_len); REQUIRE(page_idx);
+  if ((r = check_select(s, k, n_sink_pages, n_local_tokens))) return r;
+  if (s.P == 1 && kmin != kmax)
+    return fail(SLS_EINVAL, "page_size 1: pass the key cache as both kmin and kmax");
   const size_t need = sls::select_pages_workspace(s);
   if (!workspace || workspace_bytes < need)
     return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
@@ -869,6 +876,238 @@ sls_status sls_kv8_evict(const sls_attn_desc* desc, const sls_kv8_cache* src, in
   e.kept = kept_idx; e.ctx_len = ctx_len; e.ctx_out = ctx_out;
   sls::stat_add(sls::kStatMetadata);
   return cuda_status(sls::launch_kv8_evict(s, e, (cudaStream_t)stream), "sls_kv8_evict");
+}
+
+// ---- the paged cache
+
+// A paged cache's buffers; two of them share no memory.
+struct PagedSpans {
+  Span s[8];
+};
+
+static sls_status check_paged_pages(int32_t pages) {
+  if (pages < 1 || pages > (1 << 24)) return fail(SLS_EINVAL, "num_pages %d not in [1, 2^24]", pages);
+  return SLS_OK;
+}
+
+static sls_status check_paged_desc(const sls_attn_desc* desc, sls::Shape* s) {
+  const sls_status r = check_desc(desc, s);
+  if (r) return r;
+  if (s->P < 16) return fail(SLS_EUNSUPPORTED, "a paged cache has pages of >= 16 tokens (P=%d)", s->P);
+  if (s->B > 4096) return fail(SLS_EUNSUPPORTED, "a paged cache has at most 4096 sequences (B=%d)", s->B);
+  if ((int64_t)s->B * (s->Cap >> s->pshift) > INT32_MAX)
+    return fail(SLS_EOVERFLOW, "a table of %d rows of %d pages", s->B, s->Cap >> s->pshift);
+  return SLS_OK;
+}
+
+static size_t paged_state_words(int B, int32_t pages) {
+  const size_t words = ((size_t)pages + 31) / 32;
+  return 16 + ((words + 1) & ~(size_t)1) + 2 * (size_t)B;
+}
+
+static sls_status check_paged(const sls_attn_desc* desc, const sls_paged_cache* cache, sls::Shape* s, sls::Paged* c,
+                              PagedSpans* sp) {
+  sls_status r = check_paged_desc(desc, s);
+  if (r) return r;
+  if (!cache) return fail(SLS_EINVAL, "cache is NULL");
+  if ((r = check_paged_pages(cache->num_pages))) return r;
+  const int64_t pages = cache->num_pages, rows = pages * s->Hkv * s->P, e = s->dtype == SLS_DTYPE_F32 ? 4 : 2;
+  if (rows > INT32_MAX) return fail(SLS_EOVERFLOW, "a pool of %lld rows (num_pages * Hkv * P) above 2^31 - 1", (long long)rows);
+  if (!cache->k_pages || !cache->v_pages || !cache->ctx_len || !cache->table || !cache->refs || !cache->state)
+    return fail(SLS_EINVAL, "cache has a NULL pointer");
+  if (((uintptr_t)cache->k_pages | (uintptr_t)cache->v_pages | (uintptr_t)cache->kmin | (uintptr_t)cache->kmax |
+       (uintptr_t)cache->state) & 15)
+    return fail(SLS_EINVAL, "k_pages, v_pages, kmin, kmax and state must be 16-byte aligned");
+  if (((uintptr_t)cache->ctx_len | (uintptr_t)cache->table | (uintptr_t)cache->refs) & 3)
+    return fail(SLS_EINVAL, "ctx_len, table and refs must be 4-byte aligned");
+  if ((cache->kmin == nullptr) != (cache->kmax == nullptr)) return fail(SLS_EINVAL, "kmin and kmax: both or neither");
+  *c = sls::Paged{cache->num_pages, cache->k_pages, cache->v_pages, cache->kmin, cache->kmax,
+                  cache->ctx_len, cache->table, cache->refs, cache->state};
+  const int64_t pool = rows * s->D * e, meta = pages * s->Hkv * s->D * e;
+  *sp = PagedSpans{{at(c->k, pool), at(c->v, pool), at(c->kmin, meta), at(c->kmax, meta), at(c->ctx, (int64_t)s->B * 4),
+                    at(c->table, (int64_t)s->B * (s->Cap >> s->pshift) * 4), at(c->refs, pages * 4),
+                    at(c->state, (int64_t)paged_state_words(s->B, cache->num_pages) * 4)}};
+  for (int i = 0; i < 8; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(sp->s[i].p, sp->s[i].n, sp->s[j].p, sp->s[j].n))
+        return fail(SLS_EINVAL, "the cache has buffers that share memory");
+  return SLS_OK;
+}
+
+// Memory of a call besides the cache: aligned to its 4-byte words, none of the cache's, and (what is written, the
+// first `written` of them) none of each other's.
+static sls_status check_paged_apart(const PagedSpans& sp, std::initializer_list<Span> all, int written) {
+  const Span* x = all.begin();
+  for (int i = 0; i < (int)all.size(); ++i) {
+    if ((uintptr_t)x[i].p & 3) return fail(SLS_EINVAL, "an argument is not 4-byte aligned");
+    for (const Span& y : sp.s)
+      if (overlap(x[i].p, x[i].n, y.p, y.n)) return fail(SLS_EINVAL, "an argument shares memory with the cache");
+    for (int j = 0; j < i && j < written; ++j)
+      if (overlap(x[i].p, x[i].n, x[j].p, x[j].n)) return fail(SLS_EINVAL, "an output or the workspace shares memory with another argument");
+  }
+  return SLS_OK;
+}
+
+size_t sls_paged_state_words(const sls_attn_desc* desc, int32_t num_pages) {
+  sls::Shape s;
+  if (check_paged_desc(desc, &s) || check_paged_pages(num_pages)) return 0;
+  return paged_state_words(s.B, num_pages);
+}
+
+sls_status sls_paged_init(const sls_attn_desc* desc, const sls_paged_cache* cache, void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  const sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_paged_init(s, c, (cudaStream_t)stream), "sls_paged_init");
+}
+
+sls_status sls_paged_append(const sls_attn_desc* desc, const sls_paged_cache* cache, const void* k_new,
+                            int64_t k_seq_stride, int64_t k_token_stride, int64_t k_head_stride, const void* v_new,
+                            int64_t v_seq_stride, int64_t v_token_stride, int64_t v_head_stride, int32_t max_new,
+                            const int32_t* new_len, int32_t* pos_out, void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  if (max_new < 0) return fail(SLS_EINVAL, "max_new %d < 0", max_new);
+  if (max_new > 0) {
+    REQUIRE16(k_new); REQUIRE16(v_new);
+  }
+  const int size = s.dtype == SLS_DTYPE_F32 ? 4 : 2, vec = 16 / size;
+  for (int64_t st : {k_seq_stride, k_token_stride, k_head_stride, v_seq_stride, v_token_stride, v_head_stride})
+    if (st < 0 || st > (int64_t(1) << 40) || st % vec)
+      return fail(SLS_EINVAL, "strides of the new tokens must be multiples of %d elements in [0, 2^40]", vec);
+  // the last element of a strided tensor; tokens past a sequence's capacity are never read
+  auto extent = [&](int64_t b, int64_t t, int64_t h) -> int64_t {
+    const __int128 n = (__int128)(s.B - 1) * b + (__int128)(std::min(max_new, s.Cap) - 1) * t + (__int128)(s.Hkv - 1) * h + s.D;
+    return n > INT64_MAX / 8 ? INT64_MAX / 8 * size : (int64_t)n * size;
+  };
+  const int64_t n4 = (int64_t)s.B * 4;
+  const int64_t kn = extent(k_seq_stride, k_token_stride, k_head_stride), vn = extent(v_seq_stride, v_token_stride, v_head_stride);
+  if ((r = check_paged_apart(sp, {at(pos_out, n4), at(new_len, n4), at(max_new ? k_new : nullptr, kn),
+                                  at(max_new ? v_new : nullptr, vn)}, 1)))
+    return r;
+  if (((int64_t)std::min(max_new, s.Cap) / s.P + 2) * s.Hkv > INT32_MAX) return fail(SLS_EOVERFLOW, "grid too large");
+  const sls::PagedNew n = {k_new, v_new, k_seq_stride, k_token_stride, k_head_stride,
+                           v_seq_stride, v_token_stride, v_head_stride, max_new, new_len};
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_paged_append(s, c, n, pos_out, (cudaStream_t)stream), "sls_paged_append");
+}
+
+sls_status sls_paged_select_pages(const sls_attn_desc* desc, const sls_paged_cache* cache, const void* q, int32_t k,
+                                  int32_t n_sink_pages, int32_t n_local_tokens, int32_t* page_idx, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  if (!c.kmin) return fail(SLS_EINVAL, "the selection needs the cache's kmin and kmax");
+  REQUIRE16(q); REQUIRE(page_idx);
+  if ((r = check_select(s, k, n_sink_pages, n_local_tokens))) return r;
+  const size_t need = sls::select_pages_workspace(s);
+  if (!workspace || workspace_bytes < need)
+    return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  REQUIRE16(workspace);
+  if ((r = check_paged_apart(sp, {at(page_idx, (int64_t)s.B * s.Hkv * k * 4), at(workspace, (int64_t)need),
+                                  at(q, (int64_t)s.B * s.Hq * s.D * (s.dtype == SLS_DTYPE_F32 ? 4 : 2))}, 2)))
+    return r;
+  sls::stat_add(sls::kStatSelectPages);
+  return cuda_status(sls::launch_paged_select(s, c, q, k, n_sink_pages, n_local_tokens, page_idx, workspace,
+                                              (cudaStream_t)stream),
+                     "sls_paged_select_pages");
+}
+
+size_t sls_paged_decode_attend_workspace_size(const sls_attn_desc* desc) {
+  sls::Shape s;
+  sls::Paged c = {};
+  if (check_paged_desc(desc, &s) || !sls::paged_attend_supported(s, c)) return 0;
+  return sls::paged_attend_workspace(s);
+}
+
+sls_status sls_paged_decode_attend(const sls_attn_desc* desc, const sls_paged_cache* cache, const void* q,
+                                   const int32_t* page_idx, int32_t idx_stride, const int32_t* count, int32_t k_fixed,
+                                   const float* sink, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  if (s.flags & ~SLS_FLAG_TEST_WAIT_TIMEOUT)
+    return fail(SLS_EUNSUPPORTED, "the paged cache has one attend kernel: flags 0x%x", s.flags);
+  if (!sls::paged_attend_supported(s, c))
+    return fail(SLS_EUNSUPPORTED, "at most 4096 rows (B*Hkv) and 2^34 positions in all");
+  REQUIRE16(q); REQUIRE16(out);
+  if (page_idx) {
+    if (idx_stride < 1) return fail(SLS_EINVAL, "idx_stride %d < 1", idx_stride);
+    if ((int64_t)idx_stride * s.P > INT32_MAX || (int64_t)s.B * s.Hkv * idx_stride * (s.P / 16) > (1 << 30))
+      return fail(SLS_EOVERFLOW, "idx_stride %d pages of %d tokens", idx_stride, s.P);
+    if (!count && (k_fixed < 0 || k_fixed > idx_stride))
+      return fail(SLS_EINVAL, "k_fixed %d not in [0, idx_stride=%d]", k_fixed, idx_stride);
+  }
+  const size_t need = sls::paged_attend_workspace(s);
+  if (!workspace || workspace_bytes < need)
+    return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  REQUIRE16(workspace);
+  const int64_t rows = (int64_t)s.B * s.Hkv, heads = (int64_t)s.B * s.Hq, e = s.dtype == SLS_DTYPE_F32 ? 4 : 2;
+  if ((r = check_paged_apart(sp, {at(out, heads * s.D * e), at(lse, heads * 4), at(workspace, (int64_t)need),
+                                  at(q, heads * s.D * e), at(page_idx, rows * idx_stride * 4),
+                                  at(page_idx ? count : nullptr, rows * 4), at(sink, (int64_t)s.Hq * 4)}, 3)))
+    return r;
+  return cuda_status(sls::launch_paged_attend(s, c, q, page_idx, idx_stride, count, k_fixed, sink, out, lse, workspace,
+                                              (cudaStream_t)stream),
+                     "sls_paged_decode_attend");
+}
+
+size_t sls_paged_fork_workspace_size(const sls_attn_desc* desc) {
+  sls::Shape s;
+  return check_paged_desc(desc, &s) ? 0 : sls::paged_fork_workspace(s);
+}
+
+sls_status sls_paged_fork(const sls_attn_desc* desc, const sls_paged_cache* cache, const int32_t* parent,
+                          const int32_t* keep_len, int32_t* done, void* workspace, size_t workspace_bytes, void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  REQUIRE(parent);
+  const size_t need = sls::paged_fork_workspace(s);
+  if (!workspace || workspace_bytes < need)
+    return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  REQUIRE16(workspace);
+  const int64_t n4 = (int64_t)s.B * 4;
+  if ((r = check_paged_apart(sp, {at(done, 4), at(workspace, (int64_t)need), at(parent, n4), at(keep_len, n4)}, 2))) return r;
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_paged_fork(s, c, parent, keep_len, done, workspace, (cudaStream_t)stream), "sls_paged_fork");
+}
+
+size_t sls_paged_compact_workspace_size(int32_t num_pages) {
+  if (check_paged_pages(num_pages)) return 0;
+  sls::Paged c = {};
+  c.pages = num_pages;
+  return sls::paged_compact_workspace(c);
+}
+
+sls_status sls_paged_compact(const sls_attn_desc* desc, const sls_paged_cache* cache, int32_t* moved, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  sls::Shape s;
+  sls::Paged c;
+  PagedSpans sp;
+  sls_status r = check_paged(desc, cache, &s, &c, &sp);
+  if (r) return r;
+  const size_t need = sls::paged_compact_workspace(c);
+  if (!workspace || workspace_bytes < need)
+    return fail(SLS_EWORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace_bytes);
+  REQUIRE16(workspace);
+  if ((r = check_paged_apart(sp, {at(moved, (int64_t)c.pages * 4), at(workspace, (int64_t)need)}, 2))) return r;
+  sls::stat_add(sls::kStatMetadata);
+  return cuda_status(sls::launch_paged_compact(s, c, moved, workspace, (cudaStream_t)stream), "sls_paged_compact");
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
-// Python binding of the calls whose host time counts (the norm/rotation and the
-// 8-bit cache: a decode step makes them one after the other, each a few
-// microseconds on the device).  It does what the ctypes binding does, reading
+// Python binding of the calls whose host time counts (the norm/rotation, the
+// 8-bit cache and the paged cache: a decode step makes them one after the other, each a
+// few microseconds on the device).  It does what the ctypes binding does, reading
 // tensors through the C++ API: checks device, type, shape and strides, and passes
 // pointers and the current stream to the C ABI.  Every function returns the
 // sls_status; a tensor that does not fit raises ValueError.
@@ -24,6 +24,11 @@ struct Calls {
   decltype(&sls_kv8_append) append = nullptr;
   decltype(&sls_kv8_decode_attend) attend = nullptr;
   decltype(&sls_kv8_evict) evict = nullptr;
+  decltype(&sls_paged_append) paged_append = nullptr;
+  decltype(&sls_paged_select_pages) paged_select = nullptr;
+  decltype(&sls_paged_decode_attend) paged_attend = nullptr;
+  decltype(&sls_paged_fork) paged_fork = nullptr;
+  decltype(&sls_paged_compact) paged_compact = nullptr;
 } calls;
 
 [[noreturn]] void bad(const std::string& what) { throw std::invalid_argument(what); }
@@ -258,6 +263,110 @@ PyObject* kv8_evict(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+at::ScalarType type_of(const sls_attn_desc* d) { return d->dtype == SLS_DTYPE_F32 ? F32 : BF16; }
+
+// An int32 argument.
+int32_t word(const Args& a, int i, const char* name) {
+  const int64_t v = a.integer(i);
+  if (v < INT32_MIN || v > INT32_MAX) bad(std::string(name) + " is out of range");
+  return (int32_t)v;
+}
+
+// (desc, cache, k_new, v_new, new_len, pos_out)
+PyObject* paged_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 6);
+    Struct<sls_attn_desc> d(a.at(0), "desc");
+    Struct<sls_paged_cache> c(a.at(1), "cache");
+    const int64_t B = d->batch, H = d->num_kv_heads, D = d->head_dim;
+    const at::Tensor& first = a.any(2, "k_new");
+    if (first.dim() != 4) bad("k_new must be [B, T, Hkv, D], got " + text(first.sizes()));
+    const int64_t T = first.size(1);
+    if (T > INT32_MAX) bad("k_new holds too many tokens");
+    const at::Tensor& k = a.tensor(2, "k_new", type_of(d.get()), {B, T, H, D}, true);
+    const at::Tensor& v = a.tensor(3, "v_new", type_of(d.get()), {B, T, H, D}, true);
+    const int32_t* len = a.data<int32_t>(4, "new_len", I32, {B});
+    int32_t* pos = a.data<int32_t>(5, "pos_out", I32, {B});
+    return calls.paged_append(d.get(), c.get(), k.data_ptr(), step(k, 0), step(k, 1), step(k, 2), v.data_ptr(), step(v, 0),
+                              step(v, 1), step(v, 2), (int32_t)T, len, pos, stream());
+  });
+}
+
+// (desc, cache, q, k, n_sink_pages, n_local_tokens, page_idx, workspace)
+PyObject* paged_select_pages(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 8);
+    Struct<sls_attn_desc> d(a.at(0), "desc");
+    Struct<sls_paged_cache> c(a.at(1), "cache");
+    const int64_t B = d->batch, Hq = d->num_q_heads, H = d->num_kv_heads, D = d->head_dim;
+    const at::Tensor& q = a.tensor(2, "q", type_of(d.get()), {B, Hq, D});
+    const int32_t k = word(a, 3, "k"), sinks = word(a, 4, "n_sink_pages"), local = word(a, 5, "n_local_tokens");
+    int32_t* idx = static_cast<int32_t*>(a.tensor(6, "page_idx", I32, {B * H, (int64_t)k}).data_ptr());
+    const int64_t bytes = a.any(7, "workspace").numel();
+    void* ws = a.data(7, "workspace", at::kByte, {bytes});
+    return calls.paged_select(d.get(), c.get(), q.data_ptr(), k, sinks, local, idx, ws, (size_t)bytes, stream());
+  });
+}
+
+// (desc, cache, q, page_idx, count, k_fixed, sink, out, lse, workspace)
+PyObject* paged_decode_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 10);
+    Struct<sls_attn_desc> d(a.at(0), "desc");
+    Struct<sls_paged_cache> c(a.at(1), "cache");
+    const int64_t B = d->batch, Hq = d->num_q_heads, H = d->num_kv_heads, D = d->head_dim;
+    const auto dt = type_of(d.get());
+    const at::Tensor& q = a.tensor(2, "q", dt, {B, Hq, D});
+    const int32_t *pages = nullptr, *count = nullptr;
+    int64_t stride = 0;
+    int32_t fixed = 0;
+    if (!a.none(3)) {
+      const at::Tensor& p = a.any(3, "page_idx");
+      if (p.dim() != 2 || p.size(1) > INT32_MAX) bad("page_idx must be [B * Hkv, entries], got " + text(p.sizes()));
+      stride = p.size(1);
+      pages = a.data<int32_t>(3, "page_idx", I32, {B * H, stride});
+      count = a.data<int32_t>(4, "count", I32, {B * H});
+      fixed = a.none(5) ? (int32_t)stride : word(a, 5, "k_fixed");
+    }
+    const float* sink = a.data<float>(6, "sink", F32, {Hq});
+    void* out = a.tensor(7, "out", dt, {B, Hq, D}).data_ptr();
+    float* lse = a.data<float>(8, "lse", F32, {B, Hq});
+    const int64_t bytes = a.any(9, "workspace").numel();
+    void* ws = a.data(9, "workspace", at::kByte, {bytes});
+    return calls.paged_attend(d.get(), c.get(), q.data_ptr(), pages, (int32_t)stride, count, fixed, sink, out, lse, ws,
+                              (size_t)bytes, stream());
+  });
+}
+
+// (desc, cache, parent, keep_len, done, workspace)
+PyObject* paged_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 6);
+    Struct<sls_attn_desc> d(a.at(0), "desc");
+    Struct<sls_paged_cache> c(a.at(1), "cache");
+    const int64_t B = d->batch;
+    const int32_t* parent = static_cast<const int32_t*>(a.tensor(2, "parent", I32, {B}).data_ptr());
+    const int32_t* keep = a.data<int32_t>(3, "keep_len", I32, {B});
+    int32_t* done = a.data<int32_t>(4, "done", I32, {1});
+    const int64_t bytes = a.any(5, "workspace").numel();
+    void* ws = a.data(5, "workspace", at::kByte, {bytes});
+    return calls.paged_fork(d.get(), c.get(), parent, keep, done, ws, (size_t)bytes, stream());
+  });
+}
+
+// (desc, cache, moved, workspace)
+PyObject* paged_compact(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&] {
+    Args a(args, n, 4);
+    Struct<sls_attn_desc> d(a.at(0), "desc");
+    Struct<sls_paged_cache> c(a.at(1), "cache");
+    int32_t* moved = a.data<int32_t>(2, "moved", I32, {(int64_t)c->num_pages});
+    const int64_t bytes = a.any(3, "workspace").numel();
+    void* ws = a.data(3, "workspace", at::kByte, {bytes});
+    return calls.paged_compact(d.get(), c.get(), moved, ws, (size_t)bytes, stream());
+  });
+}
+
 // (path): looks the entry points up in the library the ctypes binding has loaded.
 PyObject* bind(PyObject*, PyObject* path) {
   const char* p = PyUnicode_AsUTF8(path);
@@ -272,8 +381,14 @@ PyObject* bind(PyObject*, PyObject* path) {
   c.append = reinterpret_cast<decltype(c.append)>(dlsym(lib, "sls_kv8_append"));
   c.attend = reinterpret_cast<decltype(c.attend)>(dlsym(lib, "sls_kv8_decode_attend"));
   c.evict = reinterpret_cast<decltype(c.evict)>(dlsym(lib, "sls_kv8_evict"));
-  if (!c.qk_norm_rope || !c.append || !c.attend || !c.evict) {
-    PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point of the 8-bit cache");
+  c.paged_append = reinterpret_cast<decltype(c.paged_append)>(dlsym(lib, "sls_paged_append"));
+  c.paged_select = reinterpret_cast<decltype(c.paged_select)>(dlsym(lib, "sls_paged_select_pages"));
+  c.paged_attend = reinterpret_cast<decltype(c.paged_attend)>(dlsym(lib, "sls_paged_decode_attend"));
+  c.paged_fork = reinterpret_cast<decltype(c.paged_fork)>(dlsym(lib, "sls_paged_fork"));
+  c.paged_compact = reinterpret_cast<decltype(c.paged_compact)>(dlsym(lib, "sls_paged_compact"));
+  if (!c.qk_norm_rope || !c.append || !c.attend || !c.evict || !c.paged_append || !c.paged_select || !c.paged_attend ||
+      !c.paged_fork || !c.paged_compact) {
+    PyErr_SetString(PyExc_RuntimeError, "the library lacks an entry point of the 8-bit or the paged cache");
     return nullptr;
   }
   calls = c;
@@ -287,9 +402,19 @@ PyMethodDef methods[] = {
     {"kv8_decode_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv8_decode_attend)), METH_FASTCALL,
      nullptr},
     {"kv8_evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv8_evict)), METH_FASTCALL, nullptr},
+    {"paged_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_append)), METH_FASTCALL,
+     nullptr},
+    {"paged_select_pages", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_select_pages)), METH_FASTCALL,
+     nullptr},
+    {"paged_decode_attend", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_decode_attend)), METH_FASTCALL,
+     nullptr},
+    {"paged_fork", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_fork)), METH_FASTCALL,
+     nullptr},
+    {"paged_compact", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_compact)), METH_FASTCALL,
+     nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Tensor binding of the 8-bit cache's calls.", -1, methods,
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Tensor binding of the 8-bit and the paged cache's calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

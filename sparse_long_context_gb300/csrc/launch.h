@@ -110,6 +110,9 @@ DeviceStatus take_status_attend_refined();
 DeviceStatus take_status_quest_step();
 DeviceStatus take_status_recall();
 DeviceStatus take_status_attend_kv8();
+DeviceStatus take_status_attend_paged();
+DeviceStatus take_status_paged_cache();
+DeviceStatus take_status_select_pages();
 
 // Fused Quest step (bf16, pages of >= 16 tokens): select + attend + combine
 // in one launch.  *handled is false (and nothing is enqueued) when the shape
@@ -168,6 +171,43 @@ struct Kv8Evict {
   int32_t* ctx_out;
 };
 cudaError_t launch_kv8_evict(const Shape& s, const Kv8Evict& e, cudaStream_t st);
+
+// The paged cache as the kernels see it (paged.cuh has the state's layout).
+struct Paged {
+  int pages;
+  void *k, *v, *kmin, *kmax;
+  int32_t *ctx, *table, *refs, *state;
+};
+struct PagedNew {
+  const void *k, *v;
+  int64_t kb, kt, kh, vb, vt, vh;  // strides in elements
+  int max_new;
+  const int32_t* new_len;
+};
+cudaError_t launch_paged_init(const Shape& s, const Paged& c, cudaStream_t st);
+cudaError_t launch_paged_append(const Shape& s, const Paged& c, const PagedNew& n, int32_t* pos_out, cudaStream_t st);
+struct PagedFork {
+  const int32_t *parent, *keep;
+  int32_t* done;
+  int4* copy;     // [B] of a changed sequence's partial page: source, destination, tokens; length before (-1: unchanged)
+  int32_t* rows;  // [B, Cap/P] new rows of the changed sequences
+};
+size_t paged_fork_workspace(const Shape& s);
+cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* parent, const int32_t* keep, int32_t* done,
+                              void* ws, cudaStream_t st);
+struct PagedCompact {
+  int32_t *count, *holes, *movers, *rank, *moved;
+};
+size_t paged_compact_workspace(const Paged& c);
+cudaError_t launch_paged_compact(const Shape& s, const Paged& c, int32_t* moved, void* ws, cudaStream_t st);
+bool paged_attend_supported(const Shape& s, const Paged& c);
+size_t paged_attend_workspace(const Shape& s);
+cudaError_t launch_paged_attend(const Shape& s, const Paged& c, const void* q, const int32_t* page_idx, int idx_stride,
+                                const int32_t* count, int k_fixed, const float* sink, void* out, float* lse, void* ws,
+                                cudaStream_t st);
+// sls_select_pages over a pool's summaries, found through the table (workspace as select_pages_workspace).
+cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, int k, int n_sink_pages, int n_local_tokens,
+                                int32_t* page_idx, void* ws, cudaStream_t st);
 
 // Selection quality: attention-mass recall of page lists (a diagnostic).
 size_t recall_workspace(const Shape& s);

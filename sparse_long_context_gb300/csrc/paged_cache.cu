@@ -1,0 +1,632 @@
+// The paged K/V cache's writers: appending tokens to pages taken from the pool, forking
+// (sharing, cutting and freeing) sequences, and compacting the pool.
+//
+// Free pages are bits in a map, and a call takes the lowest-numbered ones in the order of
+// its sequences and their logical pages, so what a call does follows from lengths,
+// table and counts alone and is the same every time.  A page that is not complete belongs to one
+// sequence: a fork shares complete pages and copies a partial one, so appends never meet a
+// shared page.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+#include "paged.cuh"
+#include "status.cuh"
+
+namespace sls {
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive scan of one int per thread over the CTA; `total` gets the sum.
+__device__ __forceinline__ int plan_scan(int v, int* tmp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();  // an earlier scan's reads of tmp
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    before += w < warp ? tmp[w] : 0;
+    total += tmp[w];
+  }
+  return before + x - v;
+}
+
+struct PlanShared {
+  uint32_t word[kPlanThreads];
+  int base[kPlanThreads], tmp[kPlanThreads / 32];
+};
+
+// Takes the `total` lowest-numbered free pages (there are as many): give(rank, page) for each, and
+// their bits cleared.  All threads of the one CTA call it.
+template <typename F>
+__device__ __forceinline__ void take_pages(const Paged& c, int total, PlanShared& sh, F give) {
+  uint32_t* bits = paged_bits(c);
+  const int words = paged_words(c.pages), tid = threadIdx.x, lane = tid & 31;
+  const int first = c.state[1];
+  int got = 0;
+  __syncthreads();  // every thread has read the head
+  for (int w0 = max(first, 0); got < total && w0 < words; w0 += kPlanThreads) {
+    const uint32_t word = w0 + tid < words ? bits[w0 + tid] : 0u;
+    int sum;
+    const int base = got + plan_scan(__popc(word), sh.tmp, sum);
+    sh.word[tid] = word;
+    sh.base[tid] = base;
+    __syncthreads();
+    for (int i = tid >> 5; i < kPlanThreads && sh.base[i] < total; i += kPlanThreads / 32) {
+      const uint32_t x = sh.word[i];
+      const int r = sh.base[i] + __popc(x & ((1u << lane) - 1u));
+      if ((x >> lane & 1u) && r < total) give(r, (w0 + i) * 32 + lane);
+    }
+    if (word && base < total) {
+      uint32_t left = word;
+      for (int k = base; k < total && left; ++k) left &= left - 1;
+      bits[w0 + tid] = left;
+      if (base + __popc(word) >= total) c.state[1] = w0 + tid;
+    }
+    got += sum;
+    __syncthreads();
+  }
+  if (tid == 0) c.state[0] -= total;
+}
+
+// ------------------------------------------------------------------- the state from the table
+
+__global__ void __launch_bounds__(256)
+paged_clear_kernel(const Paged c) {
+  pdl_wait_then_release();
+  const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < c.pages) c.refs[i] = 0;
+  if (i < kPagedHead) c.state[i] = 0;
+}
+
+// Counts every sequence's pages; entries past its length become -1.
+__global__ void __launch_bounds__(256)
+paged_count_kernel(const Paged c, int B, int Cap, int pshift) {
+  pdl_wait_then_release();
+  const int MP = Cap >> pshift;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)B * MP) return;
+  const int b = (int)(i / MP), l = (int)(i % MP);
+  const int n = clamp_len(c.ctx[b], Cap);
+  if (l >= (n + (1 << pshift) - 1) >> pshift) {
+    c.table[i] = -1;
+  } else {
+    const int p = c.table[i];
+    if (paged_page(p, c.pages)) atomicAdd(c.refs + p, 1);
+    else note_bad_pages(1);
+  }
+}
+
+__global__ void __launch_bounds__(256)
+paged_free_kernel(const Paged c) {
+  pdl_wait_then_release();
+  const int p = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t word = __ballot_sync(0xffffffffu, p < c.pages && c.refs[p] == 0);
+  if ((threadIdx.x & 31) == 0 && p < c.pages) {
+    paged_bits(c)[p >> 5] = word;
+    atomicAdd(c.state, __popc(word));
+  }
+}
+
+cudaError_t launch_paged_init(const Shape& s, const Paged& c, cudaStream_t st) {
+  const int ctas = (c.pages + 255) / 256;
+  const int64_t entries = (int64_t)s.B * (s.Cap >> s.pshift);
+  cudaError_t e = launch_pdl(paged_clear_kernel, dim3(ctas), dim3(256), 0, st, c);
+  if (e == cudaSuccess)
+    e = launch_pdl(paged_count_kernel, dim3((unsigned)((entries + 255) / 256)), dim3(256), 0, st, c, s.B, s.Cap, s.pshift);
+  if (e == cudaSuccess) e = launch_pdl(paged_free_kernel, dim3(ctas), dim3(256), 0, st, c);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ------------------------------------------------------------------- append
+
+// Which sequences append, and the pages they take.  A sequence needs the pages between those it has
+// and those its new length takes; it appends if its tokens fit its capacity and its and the earlier
+// sequences' pages are there (or it needs none), and its partial page is its own.
+__global__ void __launch_bounds__(kPlanThreads)
+paged_plan_kernel(const Paged c, const int32_t* new_len, int max_new, int32_t* pos_out, int B, int Cap, int pshift) {
+  __shared__ PlanShared sh;
+  __shared__ int s_first[kPagedMaxSeqs], s_had[kPagedMaxSeqs];
+  __shared__ int s_total;
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, P = 1 << pshift, MP = Cap >> pshift, free = c.state[0];
+  const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  constexpr int MOST = kPagedMaxSeqs / kPlanThreads;
+  int start[MOST], n[MOST], need[MOST], sum = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int b = b0 + i;
+    start[i] = n[i] = need[i] = 0;
+    if (b >= b1) continue;
+    start[i] = clamp_len(c.ctx[b], Cap);
+    n[i] = new_len ? min(max(new_len[b], 0), max_new) : max_new;
+    if (n[i] > Cap - start[i]) n[i] = 0;
+    if (n[i] && (start[i] & (P - 1))) {
+      const int p = c.table[(size_t)b * MP + (start[i] >> pshift)];
+      if (!paged_page(p, c.pages) || c.refs[p] != 1) {
+        note_bad_pages(1);
+        n[i] = 0;
+      }
+    }
+    const int had = (start[i] + P - 1) >> pshift;
+    if (n[i]) need[i] = (int)(((int64_t)start[i] + n[i] + P - 1) >> pshift) - had;
+    s_had[b] = had;
+    sum += need[i];
+  }
+  if (tid == 0) s_total = 0;
+  int all;
+  int first = plan_scan(sum, sh.tmp, all), most = 0;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int b = b0 + i;
+    if (b >= b1) continue;
+    s_first[b] = first;
+    first += need[i];
+    if (need[i] && first <= free) most = first;
+    else if (need[i]) n[i] = 0;
+    paged_spans(c)[b] = make_int2(start[i], n[i]);
+    if (n[i]) c.ctx[b] = start[i] + n[i];
+    if (pos_out) pos_out[b] = n[i] ? start[i] : -1;
+  }
+  // the pages of the sequences that append are the first ones in order
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&s_total, most);
+  __syncthreads();
+  const int total = s_total;
+  if (total == 0) return;
+  take_pages(c, total, sh, [&](int r, int page) {
+    int lo = 0, hi = B - 1;  // the last sequence whose first page is r or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_first[mid] <= r) lo = mid;
+      else hi = mid - 1;
+    }
+    c.table[(size_t)lo * MP + s_had[lo] + r - s_first[lo]] = page;
+    c.refs[page] = 1;
+  });
+}
+
+template <typename T>
+struct PagedLimits;
+template <>
+struct PagedLimits<bf16> {
+  static __device__ __forceinline__ void fold(uint4& lo, uint4& hi, const uint4& a, const uint4& b) {
+    __nv_bfloat162 *l = reinterpret_cast<__nv_bfloat162*>(&lo), *h = reinterpret_cast<__nv_bfloat162*>(&hi);
+    const __nv_bfloat162 *x = reinterpret_cast<const __nv_bfloat162*>(&a), *y = reinterpret_cast<const __nv_bfloat162*>(&b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l[k] = __hmin2(l[k], x[k]);
+      h[k] = __hmax2(h[k], y[k]);
+    }
+  }
+};
+template <>
+struct PagedLimits<float> {
+  static __device__ __forceinline__ void fold(uint4& lo, uint4& hi, const uint4& a, const uint4& b) {
+    float *l = reinterpret_cast<float*>(&lo), *h = reinterpret_cast<float*>(&hi);
+    const float *x = reinterpret_cast<const float*>(&a), *y = reinterpret_cast<const float*>(&b);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      l[k] = fminf(l[k], x[k]);
+      h[k] = fmaxf(h[k], y[k]);
+    }
+  }
+};
+
+// Folds the threads' limits of one head's keys (thread i: vector i % V of a row) and writes
+// the page's; `merge`: with what is stored.
+template <typename T, int NT>
+__device__ __forceinline__ void write_limits(uint4 lo, uint4 hi, bool any, bool merge, uint4* kmin, uint4* kmax, int V) {
+  __shared__ uint4 s_lo[NT], s_hi[NT];
+  __shared__ bool s_any[NT];
+  s_lo[threadIdx.x] = lo;
+  s_hi[threadIdx.x] = hi;
+  s_any[threadIdx.x] = any;
+  __syncthreads();
+  if (threadIdx.x < V) {
+    const int v = threadIdx.x;  // every page written has a row, whose vectors the first V threads hold
+    lo = s_lo[v];
+    hi = s_hi[v];
+    for (int i = v + V; i < NT && s_any[i]; i += V) PagedLimits<T>::fold(lo, hi, s_lo[i], s_hi[i]);
+    if (merge) PagedLimits<T>::fold(lo, hi, kmin[v], kmax[v]);
+    kmin[v] = lo;
+    kmax[v] = hi;
+  }
+}
+
+constexpr int kPagedThreads = 128, kPagedUnroll = 4;
+
+// A CTA writes the new tokens of one page and KV head.
+template <typename T>
+__global__ void __launch_bounds__(kPagedThreads)
+paged_write_kernel(const Paged c, const PagedNew nw, int Hkv, int Cap, int D, int pshift) {
+  constexpr int NT = kPagedThreads, U = kPagedUnroll, E = Vec16<T>::N;
+  pdl_wait_then_release();
+  const int b = blockIdx.y, h = blockIdx.x % Hkv, unit = blockIdx.x / Hkv;
+  const int2 span = paged_spans(c)[b];
+  const int l = (span.x >> pshift) + unit;
+  if (span.y == 0 || l > (span.x + span.y - 1) >> pshift) return;
+  const int page = c.table[(size_t)b * (Cap >> pshift) + l];
+  if (!paged_page(page, c.pages)) return;
+  const int t0 = max(l << pshift, span.x), t1 = min((l + 1) << pshift, span.x + span.y), P = 1 << pshift;
+  const int V = D / E;  // vectors of a token
+  const size_t at = (((size_t)page * Hkv + h) * P + (t0 & (P - 1))) * V;
+  uint4 *kd = static_cast<uint4*>(c.k) + at, *vd = static_cast<uint4*>(c.v) + at;
+  const T* ks = static_cast<const T*>(nw.k) + b * nw.kb + (int64_t)(t0 - span.x) * nw.kt + h * nw.kh;
+  const T* vs = static_cast<const T*>(nw.v) + b * nw.vb + (int64_t)(t0 - span.x) * nw.vt + h * nw.vh;
+  const int n = (t1 - t0) * V, ch = (threadIdx.x % V) * E, r0 = threadIdx.x / V, step = NT / V;
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  for (int i0 = threadIdx.x, r = r0; i0 < n; i0 += NT * U, r += step * U) {
+    uint4 k[U], v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * NT < n) {
+        k[u] = ldg_stream(ks + (int64_t)(r + u * step) * nw.kt + ch);
+        v[u] = ldg_stream(vs + (int64_t)(r + u * step) * nw.vt + ch);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * NT < n) {
+        kd[i0 + u * NT] = k[u];
+        vd[i0 + u * NT] = v[u];
+        if (c.kmin) {
+          if (i0 == (int)threadIdx.x && u == 0) lo = hi = k[u];
+          else PagedLimits<T>::fold(lo, hi, k[u], k[u]);
+        }
+      }
+  }
+  if (c.kmin) {
+    const size_t m = ((size_t)page * Hkv + h) * V;
+    write_limits<T, NT>(lo, hi, (int)threadIdx.x < n, (t0 & (P - 1)) != 0, static_cast<uint4*>(c.kmin) + m,
+                        static_cast<uint4*>(c.kmax) + m, V);
+  }
+}
+
+cudaError_t launch_paged_append(const Shape& s, const Paged& c, const PagedNew& n, int32_t* pos_out, cudaStream_t st) {
+  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, c, n.new_len, n.max_new, pos_out, s.B,
+                             s.Cap, s.pshift);
+  if (e == cudaSuccess && n.max_new > 0) {
+    const int most = std::min(n.max_new, s.Cap);  // more tokens fit no sequence
+    const dim3 grid((unsigned)(((most + s.P - 2) / s.P + 1) * s.Hkv), s.B);
+    e = s.dtype == 0 ? launch_pdl(paged_write_kernel<float>, grid, dim3(kPagedThreads), 0, st, c, n, s.Hkv, s.Cap, s.D, s.pshift)
+                     : launch_pdl(paged_write_kernel<bf16>, grid, dim3(kPagedThreads), 0, st, c, n, s.Hkv, s.Cap, s.D, s.pshift);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ------------------------------------------------------------------- fork
+
+// What becomes of sequence b: row `parent` (-1: nothing) cut to `len` tokens.
+struct ForkPlan {
+  int parent, len, was;
+  bool same, bad;
+};
+__device__ __forceinline__ ForkPlan fork_plan(const PagedFork& f, const int32_t* ctx, int b, int B, int Cap) {
+  ForkPlan p;
+  p.parent = f.parent[b];
+  p.was = clamp_len(ctx[b], Cap);
+  p.bad = p.parent < -1 || p.parent >= B;
+  if (p.bad) p.parent = b;
+  p.len = p.parent < 0 ? 0 : clamp_len(ctx[p.parent], Cap);
+  if (f.keep && !p.bad) p.len = min(p.len, max(f.keep[b], 0));
+  p.same = p.bad || (p.parent == b && p.len == p.was) || (p.len == 0 && p.was == 0);
+  return p;
+}
+
+// Entry l of a changed sequence before and after: pages it lets go (or -1) and pages it takes over whole.
+// Entries that stay are neither.
+__device__ __forceinline__ void fork_entry(const Paged& c, const ForkPlan& p, int b, int l, int MP, int pshift, int& old,
+                                           int& now) {
+  const int P = 1 << pshift;
+  old = l < (p.was + P - 1) >> pshift ? c.table[(size_t)b * MP + l] : -1;
+  now = l < p.len >> pshift ? (p.parent == b ? old : c.table[(size_t)p.parent * MP + l]) : -1;
+}
+
+// Counts of pages as after the fork, but for the partial pages of changed sequences.
+__global__ void __launch_bounds__(256)
+fork_count_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
+  pdl_wait_then_release();
+  const int b = blockIdx.y, MP = Cap >> pshift;
+  const ForkPlan p = fork_plan(f, c.ctx, b, B, Cap);
+  if (p.same) {
+    if (p.bad && blockIdx.x == 0 && threadIdx.x == 0) note_bad_pages(1);
+    return;
+  }
+  const int last = max((p.was + (1 << pshift) - 1) >> pshift, (p.len >> pshift) + 1);
+  for (int l = blockIdx.x * 256 + threadIdx.x; l < min(last, MP); l += gridDim.x * 256) {
+    int old, now;
+    fork_entry(c, p, b, l, MP, pshift, old, now);
+    if (old != now) {
+      if (paged_page(old, c.pages)) atomicAdd(c.refs + old, -1);
+      if (paged_page(now, c.pages)) atomicAdd(c.refs + now, 1);
+    }
+    // a partial last page: its source for now
+    if (l == p.len >> pshift && (p.len & ((1 << pshift) - 1))) now = c.table[(size_t)p.parent * MP + l];
+    f.rows[(size_t)b * MP + l] = now;
+  }
+}
+
+// Who keeps, and who copies, a partial page; the pages for the copies; the new lengths.
+__global__ void __launch_bounds__(kPlanThreads)
+fork_plan_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
+  __shared__ PlanShared sh;
+  __shared__ int s_src[kPagedMaxSeqs], s_copy[kPagedMaxSeqs];
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, MP = Cap >> pshift, free = c.state[0];
+  const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
+  constexpr int MOST = kPagedMaxSeqs / kPlanThreads;
+  ForkPlan p[MOST];
+  int src[MOST];
+  bool held[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int b = b0 + i;
+    src[i] = -1;
+    held[i] = false;
+    if (b >= b1) continue;
+    p[i] = fork_plan(f, c.ctx, b, B, Cap);
+    if (!p[i].same && (p[i].len & ((1 << pshift) - 1))) {
+      src[i] = f.rows[(size_t)b * MP + (p[i].len >> pshift)];
+      if (!paged_page(src[i], c.pages)) {
+        src[i] = -1;
+        note_bad_pages(1);
+      } else {
+        held[i] = c.refs[src[i]] > 0;
+      }
+    }
+    s_src[b] = held[i] ? -1 : src[i];
+  }
+  __syncthreads();
+  int copies = 0;
+  bool copy[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    copy[i] = src[i] >= 0 && held[i];
+    if (src[i] >= 0 && !held[i])  // nobody holds it whole: its lowest user keeps it
+      for (int k = 0; k < b0 + i && !copy[i]; ++k) copy[i] = s_src[k] == src[i];
+    copies += copy[i];
+  }
+  int total;
+  int rank = plan_scan(copies, sh.tmp, total);
+  const bool fail = total > free;
+  if (tid == 0) {
+    c.state[2] = fail;
+    if (f.done) *f.done = !fail;
+  }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int b = b0 + i;
+    if (b >= b1) continue;
+    const int part = src[i] < 0 ? 0 : p[i].len & ((1 << pshift) - 1);
+    f.copy[b] = make_int4(src[i], src[i], part, p[i].same ? -1 : p[i].was);
+    if (fail || p[i].same) continue;
+    c.ctx[b] = p[i].len;
+    if (copy[i]) s_copy[rank++] = b;
+    else if (src[i] >= 0) c.refs[src[i]] = 1;
+  }
+  __syncthreads();
+  if (fail || total == 0) return;
+  take_pages(c, total, sh, [&](int r, int page) {
+    const int b = s_copy[r];
+    f.copy[b].y = page;
+    f.rows[(size_t)b * MP + (c.ctx[b] >> pshift)] = page;
+    c.refs[page] = 1;
+  });
+}
+
+// New rows into the table, pages that nobody holds any more freed, partial pages copied (and
+// summarised anew).  Where the pool lacked pages: the counts as they were.
+template <typename T>
+__global__ void __launch_bounds__(256)
+fork_commit_kernel(const Paged c, const PagedFork f, int Hkv, int B, int Cap, int D, int pshift, int chunks) {
+  constexpr int E = Vec16<T>::N, NT = 256;
+  pdl_wait_then_release();
+  const int b = blockIdx.y, MP = Cap >> pshift, P = 1 << pshift;
+  const int4 cp = f.copy[b];
+  const bool fail = c.state[2] != 0;
+  if (cp.w < 0) return;
+  if ((int)blockIdx.x < chunks) {
+    if (fail) {
+      const ForkPlan p = fork_plan(f, c.ctx, b, B, Cap);
+      const int last = max((p.was + P - 1) >> pshift, (p.len >> pshift) + 1);
+      for (int l = blockIdx.x * NT + threadIdx.x; l < min(last, MP); l += chunks * NT) {
+        int old, now;
+        fork_entry(c, p, b, l, MP, pshift, old, now);
+        if (old != now) {
+          if (paged_page(old, c.pages)) atomicAdd(c.refs + old, 1);
+          if (paged_page(now, c.pages)) atomicAdd(c.refs + now, -1);
+        }
+      }
+      return;
+    }
+    const int had = (cp.w + P - 1) >> pshift, has = (c.ctx[b] + P - 1) >> pshift;
+    for (int l = blockIdx.x * NT + threadIdx.x; l < max(had, has); l += chunks * NT) {
+      const int old = l < had ? c.table[(size_t)b * MP + l] : -1, now = l < has ? f.rows[(size_t)b * MP + l] : -1;
+      if (old == now) continue;
+      c.table[(size_t)b * MP + l] = now;
+      if (paged_page(old, c.pages) && c.refs[old] == 0) {
+        const uint32_t bit = 1u << (old & 31);
+        if (!(atomicOr(paged_bits(c) + (old >> 5), bit) & bit)) {
+          atomicAdd(c.state, 1);
+          atomicMin(c.state + 1, old >> 5);
+        }
+      }
+    }
+    return;
+  }
+  if (fail || cp.z == 0) return;
+  const int h = blockIdx.x - chunks, V = D / E, n = cp.z * V;
+  const size_t from = ((size_t)cp.x * Hkv + h) * P * V, to = ((size_t)cp.y * Hkv + h) * P * V;
+  const uint4 *ks = static_cast<const uint4*>(c.k) + from, *vs = static_cast<const uint4*>(c.v) + from;
+  uint4 *kd = static_cast<uint4*>(c.k) + to, *vd = static_cast<uint4*>(c.v) + to;
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  const bool copy = cp.x != cp.y;
+  if (!copy && !c.kmin) return;
+  for (int i = threadIdx.x; i < n; i += NT) {
+    const uint4 k = ks[i];
+    if (copy) {
+      kd[i] = k;
+      vd[i] = vs[i];
+    }
+    if (i == (int)threadIdx.x) lo = hi = k;
+    else PagedLimits<T>::fold(lo, hi, k, k);
+  }
+  if (c.kmin) {
+    const size_t m = ((size_t)cp.y * Hkv + h) * V;
+    write_limits<T, NT>(lo, hi, (int)threadIdx.x < n, false, static_cast<uint4*>(c.kmin) + m,
+                        static_cast<uint4*>(c.kmax) + m, V);
+  }
+}
+
+size_t paged_fork_workspace(const Shape& s) {
+  return (size_t)s.B * sizeof(int4) + (size_t)s.B * (s.Cap >> s.pshift) * sizeof(int32_t);
+}
+
+cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* parent, const int32_t* keep, int32_t* done,
+                              void* ws, cudaStream_t st) {
+  PagedFork f = {parent, keep, done, static_cast<int4*>(ws), nullptr};
+  f.rows = reinterpret_cast<int32_t*>(f.copy + s.B);
+  const int MP = s.Cap >> s.pshift, chunks = std::min(64, (MP + 255) / 256);
+  cudaError_t e = launch_pdl(fork_count_kernel, dim3(chunks, s.B), dim3(256), 0, st, c, f, s.B, s.Cap, s.pshift);
+  if (e == cudaSuccess)
+    e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, c, f, s.B, s.Cap, s.pshift);
+  if (e == cudaSuccess) {
+    const dim3 grid(chunks + s.Hkv, s.B);
+    e = s.dtype == 0 ? launch_pdl(fork_commit_kernel<float>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks)
+                     : launch_pdl(fork_commit_kernel<bf16>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks);
+  }
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// ------------------------------------------------------------------- compaction
+
+// The i-th free page below U (the number of used pages) receives the i-th used one from U on:
+// holes[i], movers[i], and rank[p] = i of a mover p.  A CTA takes 1024 words of the bits and counts
+// what lies before them.
+__global__ void __launch_bounds__(kPlanThreads)
+compact_plan_kernel(const Paged c, const PagedCompact m) {
+  __shared__ PlanShared sh;
+  pdl_wait_then_release();
+  const uint32_t* bits = paged_bits(c);
+  const int words = paged_words(c.pages), tid = threadIdx.x, lane = tid & 31, U = c.pages - c.state[0];
+  const int w0 = blockIdx.x * kPlanThreads;
+  int before = 0, below = 0, all, holes;
+  // free pages before this CTA's words, and below page U
+  const int up = max(w0, (U >> 5) + 1);
+  for (int w = tid; w < min(up, words); w += kPlanThreads) {
+    const uint32_t x = bits[w];
+    if (w < w0) before += __popc(x);
+    if (w < U >> 5) below += __popc(x);
+    else if (w == U >> 5) below += __popc(x & ((1u << (U & 31)) - 1u));
+  }
+  plan_scan(before, sh.tmp, all);
+  before = all;
+  plan_scan(below, sh.tmp, holes);
+  if (blockIdx.x == 0 && tid == 0) *m.count = holes;
+  const uint32_t word = w0 + tid < words ? bits[w0 + tid] : 0u;
+  sh.word[tid] = word;
+  sh.base[tid] = before + plan_scan(__popc(word), sh.tmp, all);
+  __syncthreads();
+  for (int i = tid >> 5; i < kPlanThreads && w0 + i < words; i += kPlanThreads / 32) {
+    const int p = (w0 + i) * 32 + lane;
+    if (p >= c.pages) continue;
+    const int f = sh.base[i] + __popc(sh.word[i] & ((1u << lane) - 1u));  // free pages below p
+    const bool free = sh.word[i] >> lane & 1u;
+    if (free) {
+      if (p < U) m.holes[f] = p;
+    } else if (p >= U) {
+      const int r = p - U - (f - holes);
+      m.movers[r] = p;
+      m.rank[p] = r;
+    }
+    if (m.moved) m.moved[p] = free ? -1 : p;  // movers: below
+  }
+}
+
+constexpr int kMoveThreads = 256, kMoveUnroll = 8;
+
+// Copies the movers (units of a part of one page's K or V), then renames pages in the table and
+// writes the bits anew.
+__global__ void __launch_bounds__(kMoveThreads)
+compact_move_kernel(const Paged c, const PagedCompact m, int64_t page_vecs, int64_t meta_vecs, int B, int Cap, int pshift) {
+  constexpr int NT = kMoveThreads, U = kMoveUnroll;
+  pdl_wait_then_release();
+  const int count = *m.count, used = c.pages - c.state[0];
+  const int parts = (int)((page_vecs + NT * U - 1) / (NT * U));
+  const int64_t units = (int64_t)count * parts * 2;
+  for (int64_t x = blockIdx.x; x < units; x += gridDim.x) {
+    const int i = (int)(x / (2 * parts)), part = (int)(x % (2 * parts)) >> 1;
+    const int from = m.movers[i], to = m.holes[i];
+    uint4* pool = static_cast<uint4*>(x & 1 ? c.v : c.k);
+    const uint4* src = pool + from * page_vecs;
+    uint4* dst = pool + to * page_vecs;
+    const int64_t at = (int64_t)part * NT * U + threadIdx.x;
+    uint4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u * NT < page_vecs) v[u] = ldg_stream(src + at + u * NT);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (at + u * NT < page_vecs) dst[at + u * NT] = v[u];
+  }
+  const int64_t tid = (int64_t)blockIdx.x * NT + threadIdx.x, all = (int64_t)gridDim.x * NT;
+  if (meta_vecs)
+    for (int64_t x = tid; x < count * meta_vecs; x += all) {
+      const int i = (int)(x / meta_vecs);
+      const int64_t from = m.movers[i] * meta_vecs + x % meta_vecs, to = m.holes[i] * meta_vecs + x % meta_vecs;
+      static_cast<uint4*>(c.kmin)[to] = static_cast<const uint4*>(c.kmin)[from];
+      static_cast<uint4*>(c.kmax)[to] = static_cast<const uint4*>(c.kmax)[from];
+    }
+  for (int64_t x = tid; x < count; x += all) {
+    const int from = m.movers[x], to = m.holes[x];
+    c.refs[to] = c.refs[from];
+    c.refs[from] = 0;
+    if (m.moved) m.moved[from] = to;
+  }
+  const int MP = Cap >> pshift;
+  for (int64_t x = tid; x < (int64_t)B * MP; x += all) {
+    const int p = c.table[x];
+    if (p >= used && p < c.pages) {
+      const int r = m.rank[p];
+      if ((unsigned)r < (unsigned)count) c.table[x] = m.holes[r];
+    }
+  }
+  for (int64_t w = tid; w < paged_words(c.pages); w += all) {
+    uint32_t x = (w + 1) * 32 <= used ? 0u : w * 32 >= used ? 0xffffffffu : 0xffffffffu << (used & 31);
+    if (w == c.pages >> 5) x &= (1u << (c.pages & 31)) - 1u;
+    paged_bits(c)[w] = x;
+  }
+  if (tid == 0) c.state[1] = min(used >> 5, paged_words(c.pages) - 1);
+}
+
+size_t paged_compact_workspace(const Paged& c) { return 16 + 3 * (size_t)((c.pages + 3) & ~3) * sizeof(int32_t); }
+
+cudaError_t launch_paged_compact(const Shape& s, const Paged& c, int32_t* moved, void* ws, cudaStream_t st) {
+  const size_t n = (size_t)((c.pages + 3) & ~3);
+  PagedCompact m = {};
+  m.count = static_cast<int32_t*>(ws);
+  m.holes = m.count + 4;
+  m.movers = m.holes + n;
+  m.rank = m.movers + n;
+  m.moved = moved;
+  const int size = s.dtype == 0 ? 4 : 2;
+  const int64_t page_vecs = (int64_t)s.Hkv * s.P * s.D * size / 16, meta_vecs = c.kmin ? (int64_t)s.Hkv * s.D * size / 16 : 0;
+  const int ctas = (paged_words(c.pages) + kPlanThreads - 1) / kPlanThreads;
+  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, c, m);
+  if (e == cudaSuccess)
+    e = launch_pdl(compact_move_kernel, dim3(sm_count() * 4), dim3(kMoveThreads), 0, st, c, m, page_vecs, meta_vecs, s.B,
+                   s.Cap, s.pshift);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+DeviceStatus take_status_paged_cache() { return take_status_here(); }
+
+}  // namespace sls

@@ -21,6 +21,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mma.cuh"
+#include "status.cuh"
 
 
 namespace sls {
@@ -49,7 +50,18 @@ struct SelectArgs {
   int32_t* cand_count;  // [rows, ncmax]: candidates CTA c sent
   uint32_t* cand_tau;   // [rows, ncmax]: CTA c's threshold (0: it sent every key)
   int ncmax;            // scoring CTAs per row the arrays hold (npcap / 16)
+  // a paged cache (null otherwise): kmin and kmax are those of the pool's pages [pool, Hkv, D]
+  const int32_t* table;  // [B, npcap] page of the pool
+  int pool;
 };
+
+// Where the summary of logical page p of sequence b, head h lies in the pool; false for a table
+// entry that is no page of it (such pages score as zeros and are counted).
+__device__ __forceinline__ bool pool_summary(const SelectArgs& a, int b, int h, int p, size_t& at) {
+  const int page = __ldg(a.table + (size_t)b * a.npcap + p);
+  at = (size_t)page * a.Hkv + h;
+  return (unsigned)page < (unsigned)a.pool;
+}
 
 // Exclusive scan of one int per thread over the CTA; `total` gets the sum.
 template <int NT>
@@ -97,7 +109,7 @@ struct KeyRange {
 
 // Scores of pages [p0, p0 + nloc) of one row into keys[0 .. nloc).
 // A page's D channels are spread over L lanes as 16-byte vectors.
-template <typename T, int D, int GM, bool STAGE>
+template <typename T, int D, int GM, bool STAGE, bool PAGED>
 __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b, int h, int p0,
                                             int nloc, int first_local, uint32_t* keys, uint32_t* skeys,
                                             KeyRange& kr) {
@@ -128,7 +140,7 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
       }
     }
   }
-  const size_t base = ((size_t)row * (size_t)(a.Cap >> a.pshift) + p0) * D + sub * EPL;
+  const size_t base = PAGED ? sub * EPL : ((size_t)row * (size_t)(a.Cap >> a.pshift) + p0) * D + sub * EPL;
   const T* lo = static_cast<const T*>(a.kmin) + base;
   const T* hi = static_cast<const T*>(a.kmax) + base;
 
@@ -138,9 +150,16 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
       pi[u] = i0 + u * STRIDE + grp;
-      const bool ok = pi[u] < nloc;
-      vl[u] = ok ? ldg_stream(lo + (size_t)pi[u] * D) : make_uint4(0, 0, 0, 0);
-      if (!single) vh[u] = ok ? ldg_stream(hi + (size_t)pi[u] * D) : make_uint4(0, 0, 0, 0);
+      bool ok = pi[u] < nloc;
+      size_t off = (size_t)pi[u] * D;
+      if constexpr (PAGED) {
+        const bool in = ok;
+        if (in) ok = pool_summary(a, b, h, p0 + pi[u], off);
+        if (in && !ok && sub == 0) note_bad_pages(1);
+        off *= D;
+      }
+      vl[u] = ok ? ldg_stream(lo + off) : make_uint4(0, 0, 0, 0);
+      if (!single) vh[u] = ok ? ldg_stream(hi + off) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int u = 0; u < UNR; ++u) {
@@ -187,7 +206,7 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
 // Tensor-core scorer (bf16): 16 pages per warp step.  Lane (r, m) loads
 // rows r and r+8 of the 16-page tile, chunks 4s+m of kmax and kmin (or of the
 // key itself when a page is one token); the group's heads are the 8 columns.
-template <int D, bool SINGLE, int NT, bool STAGE>
+template <int D, bool SINGLE, int NT, bool STAGE, bool PAGED>
 __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, int b, int h, int p0,
                                                 int nloc, int first_local, uint32_t* keys,
                                                 uint32_t* skeys, KeyRange& kr) {
@@ -212,7 +231,7 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
       }
     }
   }
-  const size_t base = ((size_t)row * (size_t)(a.Cap >> a.pshift) + p0) * D;
+  const size_t base = PAGED ? 0 : ((size_t)row * (size_t)(a.Cap >> a.pshift) + p0) * D;
   const bf16* lo = static_cast<const bf16*>(a.kmin) + base;
   const bf16* hi = static_cast<const bf16*>(a.kmax) + base;
   const bool h0ok = 2 * m < G, h1ok = 2 * m + 1 < G;
@@ -226,10 +245,16 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const int p = pr + 8 * half;
-        const bool ok = p < nloc;
+        bool ok = p < nloc;
+        size_t at = (size_t)p;
+        if constexpr (PAGED) {
+          const bool in = ok;
+          if (in) ok = pool_summary(a, b, h, p0 + p, at);
+          if (in && !ok && m == 0) note_bad_pages(1);
+        }
 #pragma unroll
         for (int s = 0; s < NS; ++s) {
-          const size_t off = (size_t)p * D + (4 * s + m) * 8;
+          const size_t off = at * D + (4 * s + m) * 8;
           xh[u][half][s] = ok ? ldg_stream((SINGLE ? lo : hi) + off) : make_uint4(0, 0, 0, 0);
           if (!SINGLE) xl[u][half][s] = ok ? ldg_stream(lo + off) : make_uint4(0, 0, 0, 0);
         }
@@ -597,8 +622,9 @@ __device__ __forceinline__ void emit_candidates(const SelectArgs& a, int row, in
 // MODE 0: CUDA-core scorer (any dtype); 1: tensor-core scorer (bf16, P > 1);
 // 2: tensor-core scorer of one-token pages (bf16, P == 1).
 // Grid (CTAs per row, rows); CTA c scores pages [c*chunk, (c+1)*chunk).
-// CAND: the row is wide and the CTA also sends its candidates.
-template <typename T, int D, int GM, int MODE, bool CAND>
+// CAND: the row is wide and the CTA also sends its candidates.  PAGED: the pages'
+// summaries lie in a pool.
+template <typename T, int D, int GM, int MODE, bool CAND, bool PAGED>
 __global__ void __launch_bounds__(MODE == 0 ? kSelThreads : kSelThreadsMma)
 quest_score_kernel(const SelectArgs a) {
   pdl_wait_then_release();
@@ -619,9 +645,9 @@ quest_score_kernel(const SelectArgs a) {
   uint32_t* skeys = (CAND && a.chunk <= kCandStage) ? stage : nullptr;
   KeyRange kr;
   if constexpr (MODE == 0) {
-    score_chunk<T, D, GM, CAND>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
+    score_chunk<T, D, GM, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
   } else {
-    score_chunk_mma<D, MODE == 2, NT, CAND>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
+    score_chunk_mma<D, MODE == 2, NT, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
   }
   if constexpr (CAND) {
     __shared__ CandShared csh;
@@ -1043,9 +1069,9 @@ topk_reg_kernel(const SelectArgs a) {
 // ---------------------------------------------------------------- launches
 
 // Pages per scoring CTA: one wave of scoring CTAs over all rows.
-template <typename T, int D, int GM, int MODE, bool CAND>
+template <typename T, int D, int GM, int MODE, bool CAND, bool PAGED>
 static int score_chunk_for(int npcap, int rows) {
-  auto kern = quest_score_kernel<T, D, GM, MODE, CAND>;
+  auto kern = quest_score_kernel<T, D, GM, MODE, CAND, PAGED>;
   constexpr int NT = MODE == 0 ? kSelThreads : kSelThreadsMma;
   static int per_sm = 0;  // resident CTAs per SM of this kernel (same on every GB300)
   if (per_sm == 0) cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, NT, 0);
@@ -1054,11 +1080,11 @@ static int score_chunk_for(int npcap, int rows) {
   return max(16, ((npcap + cpr - 1) / cpr + 15) / 16 * 16);
 }
 
-template <typename T, int D, int GM, int MODE, bool CAND>
+template <typename T, int D, int GM, int MODE, bool CAND, bool PAGED>
 static cudaError_t score_launch_c(SelectArgs& a, int rows, cudaStream_t st) {
-  auto kern = quest_score_kernel<T, D, GM, MODE, CAND>;
+  auto kern = quest_score_kernel<T, D, GM, MODE, CAND, PAGED>;
   constexpr int NT = MODE == 0 ? kSelThreads : kSelThreadsMma;
-  a.chunk = score_chunk_for<T, D, GM, MODE, CAND>(a.npcap, rows);
+  a.chunk = score_chunk_for<T, D, GM, MODE, CAND, PAGED>(a.npcap, rows);
   dim3 grid((a.npcap + a.chunk - 1) / a.chunk, rows);
   const size_t smem = (a.cand_key && a.chunk <= kCandStage) ? (size_t)a.chunk * 4 : 0;  // staged keys
   cudaError_t e = launch_pdl(kern, grid, dim3(NT), smem, st, a);
@@ -1068,8 +1094,12 @@ static cudaError_t score_launch_c(SelectArgs& a, int rows, cudaStream_t st) {
 
 template <typename T, int D, int GM, int MODE>
 static cudaError_t score_launch(SelectArgs& a, int rows, cudaStream_t st) {
-  return a.cand_key ? score_launch_c<T, D, GM, MODE, true>(a, rows, st)
-                    : score_launch_c<T, D, GM, MODE, false>(a, rows, st);
+  if constexpr (MODE != 2)  // pages of a pool hold 16 tokens or more
+    if (a.table)
+      return a.cand_key ? score_launch_c<T, D, GM, MODE, true, true>(a, rows, st)
+                        : score_launch_c<T, D, GM, MODE, false, true>(a, rows, st);
+  return a.cand_key ? score_launch_c<T, D, GM, MODE, true, false>(a, rows, st)
+                    : score_launch_c<T, D, GM, MODE, false, false>(a, rows, st);
 }
 
 static cudaError_t topk_launch(const SelectArgs& a, int rows, cudaStream_t st) {
@@ -1123,11 +1153,13 @@ size_t select_pages_workspace(const Shape& s) {
   return bytes;
 }
 
-cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
-                                const void* kmax, const int32_t* ctx_len, int k,
-                                int n_sink_pages, int n_local_tokens, int32_t* page_idx,
-                                void* ws, cudaStream_t st) {
+static cudaError_t select_launch(const Shape& s, const void* q, const void* kmin,
+                                 const void* kmax, const int32_t* ctx_len, int k,
+                                 int n_sink_pages, int n_local_tokens, int32_t* page_idx,
+                                 void* ws, const int32_t* table, int pool, cudaStream_t st) {
   SelectArgs a;
+  a.table = table;
+  a.pool = pool;
   a.q = q; a.kmin = kmin; a.kmax = kmax; a.ctx_len = ctx_len; a.page_idx = page_idx;
   a.keys = static_cast<uint32_t*>(ws);
   a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
@@ -1160,6 +1192,20 @@ cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
   if (e != cudaSuccess) return e;
   return topk_launch(a, rows, st);
 }
+
+cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
+                                const void* kmax, const int32_t* ctx_len, int k,
+                                int n_sink_pages, int n_local_tokens, int32_t* page_idx,
+                                void* ws, cudaStream_t st) {
+  return select_launch(s, q, kmin, kmax, ctx_len, k, n_sink_pages, n_local_tokens, page_idx, ws, nullptr, 0, st);
+}
+
+cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, int k, int n_sink_pages, int n_local_tokens,
+                                int32_t* page_idx, void* ws, cudaStream_t st) {
+  return select_launch(s, q, c.kmin, c.kmax, c.ctx, k, n_sink_pages, n_local_tokens, page_idx, ws, c.table, c.pages, st);
+}
+
+DeviceStatus take_status_select_pages() { return take_status_here(); }
 
 unsigned long long take_select_rows_all_keys(bool reset) {
   unsigned long long v = 0;

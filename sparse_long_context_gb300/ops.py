@@ -369,7 +369,7 @@ def _binding():
         try:
             from . import _binding as fast
         except ImportError as e:
-            raise RuntimeError("the tensor binding of the norm/rotation and 8-bit cache calls is missing or does not load: "
+            raise RuntimeError("the tensor binding of the norm/rotation, 8-bit and paged cache calls is missing or does not load: "
                                f"build it first (python -m sparse_long_context_gb300.build): {e}") from e
         fast.bind(L.LIB_PATH)
         _fast = fast
@@ -535,6 +535,169 @@ def kv8_evict(desc: L.AttnDesc, cache: Kv8Cache, ctx_len, mass, keep: int, n_sin
     if status:
         L.check("sls_kv8_evict", status)
     return ctx_out, kept_idx
+
+
+# ------------------------------------------------------------- paged KV cache
+
+class PagedCache:
+    """A K/V cache whose pages lie in a pool and may be shared (sls_paged_cache): k_pages, v_pages [N, Hkv, P, D], and
+    optionally the pages' key summaries kmin, kmax [N, Hkv, D].  The lengths ctx_len [B], the table [B, Cap/P] and the
+    counts refs [N] are views of one int32 tensor, meta, which also holds the free pages: a copy of meta is a copy of
+    what the cache's sequences are.  A new cache holds no token."""
+
+    def __init__(self, desc: L.AttnDesc, k_pages, v_pages, kmin=None, kmax=None):
+        B, H, D, P = desc.batch, desc.num_kv_heads, desc.head_dim, desc.page_size
+        dt = torch.bfloat16 if desc.dtype == L.SLS_DTYPE_BF16 else torch.float32
+        N = int(k_pages.shape[0])
+        for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+            _need(t, name, dt, (N, H, P, D))
+        if (kmin is None) != (kmax is None):
+            raise ValueError("kmin and kmax: both or neither")
+        for t, name in ((kmin, "kmin"), (kmax, "kmax")):
+            if t is not None:
+                _need(t, name, dt, (N, H, D))
+        self.index = k_pages.get_device()
+        if any(t is not None and t.get_device() != self.index for t in (v_pages, kmin, kmax)):
+            raise ValueError("the cache's tensors must be on one device")
+        words = int(L.load().sls_paged_state_words(ctypes.byref(desc), N))
+        if not words:
+            raise ValueError(f"no paged cache of this descriptor and {N} pages: " + L.load().sls_last_error().decode())
+        mp, up = desc.capacity // P, lambda n: -(-n // 4) * 4  # the parts of meta start at 16 bytes
+        at = [0, up(B), up(B) + up(B * mp), up(B) + up(B * mp) + up(N)]
+        self.meta = torch.zeros(at[3] + words, dtype=torch.int32, device=k_pages.device)
+        self.ctx_len, self.table = self.meta[:B], self.meta[at[1]:at[1] + B * mp].view(B, mp)
+        self.refs, state = self.meta[at[2]:at[2] + N], self.meta[at[3]:]
+        self.shape = (B, H, desc.capacity, D, P, desc.dtype)
+        self.num_pages, self.k_pages, self.v_pages, self.kmin, self.kmax = N, k_pages, v_pages, kmin, kmax
+        self.c = L.PagedCacheDesc(N, *(None if t is None else t.data_ptr() for t in (
+            k_pages, v_pages, kmin, kmax, self.ctx_len, self.table, self.refs, state)))
+        paged_init(desc, self)
+
+    @classmethod
+    def empty(cls, desc: L.AttnDesc, num_pages: int, summaries: bool = False, device="cuda") -> "PagedCache":
+        """A new cache with a pool of num_pages pages (zero-filled); summaries: with kmin and kmax."""
+        H, D = desc.num_kv_heads, desc.head_dim
+        dt = torch.bfloat16 if desc.dtype == L.SLS_DTYPE_BF16 else torch.float32
+        new = lambda *shape: torch.zeros(shape, dtype=dt, device=device)  # noqa: E731
+        pool = (int(num_pages), H, desc.page_size, D)
+        return cls(desc, new(*pool), new(*pool), *((new(num_pages, H, D), new(num_pages, H, D)) if summaries else ()))
+
+    def load(self, table, ctx_len):
+        """Takes over a table [B, Cap/P] and lengths [B] made elsewhere (paged_init)."""
+        self.table.copy_(table)
+        self.ctx_len.copy_(ctx_len)
+        paged_init(self.desc(), self)
+
+    def desc(self) -> L.AttnDesc:
+        """A descriptor of the cache's shape, with as many query heads as KV heads."""
+        B, H, cap, D, P, dtype = self.shape
+        return make_desc(B, H, H, D, P, cap, dtype)
+
+    def _beside(self, index: int, desc: L.AttnDesc) -> L.PagedCacheDesc:
+        """The C structure, for a call with this descriptor on device `index`."""
+        if index != self.index:
+            raise ValueError("the cache must be on the device of the other tensors")
+        if (desc.batch, desc.num_kv_heads, desc.capacity, desc.head_dim, desc.page_size, desc.dtype) != self.shape:
+            raise ValueError(f"the descriptor's shape is not that of the cache, {self.shape}")
+        return self.c
+
+    def values(self, b: int):
+        """Sequence b's K and V [Hkv, n, D] in order (for inspection: reads its length)."""
+        n, P = int(self.ctx_len[b]), self.shape[4]
+        pages = self.table[b, :-(-n // P)].long()
+        return tuple(x[pages].transpose(0, 1).reshape(x.shape[1], -1, x.shape[3])[:, :n] for x in (self.k_pages, self.v_pages))
+
+
+def paged_init(desc: L.AttnDesc, cache: PagedCache):
+    """Derives the counts and the free pages from the cache's table and lengths (sls_paged_init)."""
+    L.call("sls_paged_init", ctypes.byref(desc), ctypes.byref(cache._beside(torch._C._cuda_getDevice(), desc)), _stream())
+
+
+def paged_append(desc: L.AttnDesc, cache: PagedCache, k_new, v_new, new_len=None, pos_out=None):
+    """Appends the first new_len[b] (None: all) tokens of k_new, v_new [B, T, Hkv, D] to every sequence, on pages taken
+    from the pool (sls_paged_append).  The new tensors may be strided views with contiguous channels.  Returns the
+    cache's ctx_len, advanced in place."""
+    status = (_fast or _binding()).paged_append(desc, cache._beside(k_new.get_device(), desc), k_new, v_new, new_len, pos_out)
+    if status:
+        L.check("sls_paged_append", status)
+    return cache.ctx_len
+
+
+def paged_select_workspace(desc: L.AttnDesc, cache: PagedCache):
+    """Scratch buffer of paged_select_pages (that of select_pages)."""
+    return select_pages_workspace(desc, cache.k_pages.device)
+
+
+def paged_select_pages(desc: L.AttnDesc, cache: PagedCache, q, k: int, n_sink_pages: int = 0, n_local_tokens: int = 0,
+                       out=None, workspace=None):
+    """Quest selection over a paged cache's summaries (sls_paged_select_pages).  Returns the logical pages
+    [B*Hkv, k] int32, ascending, -1 padded."""
+    if out is None:
+        out = torch.empty((desc.batch * desc.num_kv_heads, max(int(k), 0)), dtype=torch.int32, device=q.device)
+    if workspace is None:
+        workspace = paged_select_workspace(desc, cache)
+    status = (_fast or _binding()).paged_select_pages(desc, cache._beside(q.get_device(), desc), q, k, n_sink_pages,
+                                                      n_local_tokens, out, workspace)
+    if status:
+        L.check("sls_paged_select_pages", status)
+    return out
+
+
+def paged_attend_workspace(desc: L.AttnDesc, cache: PagedCache):
+    """Zero-filled workspace of paged_decode_attend (reusable, also by calls of other shapes that need no more bytes, one
+    after the other)."""
+    n = L.load().sls_paged_decode_attend_workspace_size(ctypes.byref(desc))
+    return torch.zeros(max(int(n), 1), dtype=torch.uint8, device=cache.k_pages.device)
+
+
+def paged_decode_attend(desc: L.AttnDesc, cache: PagedCache, q, page_idx=None, count=None, k_fixed: Optional[int] = None,
+                        sink=None, out=None, lse=None, workspace=None, want_lse: bool = True):
+    """Decode attention over a paged cache (sls_paged_decode_attend): dense, or over lists [rows, stride] of logical
+    pages.  Returns (out, lse)."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = paged_attend_workspace(desc, cache)
+    status = (_fast or _binding()).paged_decode_attend(desc, cache._beside(q.get_device(), desc), q, page_idx, count, k_fixed,
+                                                       sink, out, lse, workspace)
+    if status:
+        L.check("sls_paged_decode_attend", status)
+    return out, lse
+
+
+def paged_fork_workspace(desc: L.AttnDesc, cache: PagedCache):
+    """Workspace of paged_fork (reusable)."""
+    n = L.load().sls_paged_fork_workspace_size(ctypes.byref(desc))
+    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=cache.k_pages.device)
+
+
+def paged_fork(desc: L.AttnDesc, cache: PagedCache, parent, keep_len=None, done=None, workspace=None):
+    """Makes every sequence b the first keep_len[b] (None: all) tokens of what sequence parent[b] was (sls_paged_fork):
+    forks, reorders, cuts, and with parent[b] = -1 frees.  done [1] int32, if given, becomes 1, or 0 when the pool
+    lacked pages for the copies of partial pages (nothing has changed then)."""
+    if workspace is None:
+        workspace = paged_fork_workspace(desc, cache)
+    status = (_fast or _binding()).paged_fork(desc, cache._beside(parent.get_device(), desc), parent, keep_len, done, workspace)
+    if status:
+        L.check("sls_paged_fork", status)
+
+
+def paged_compact_workspace(desc: L.AttnDesc, cache: PagedCache):
+    """Workspace of paged_compact (reusable)."""
+    n = L.load().sls_paged_compact_workspace_size(cache.num_pages)
+    return torch.empty(max(int(n), 1), dtype=torch.uint8, device=cache.k_pages.device)
+
+
+def paged_compact(desc: L.AttnDesc, cache: PagedCache, moved=None, workspace=None):
+    """Moves the used pages to the front of the pool (sls_paged_compact).  moved [N] int32, if given, receives every
+    page's new number (-1: it was free)."""
+    if workspace is None:
+        workspace = paged_compact_workspace(desc, cache)
+    status = (_fast or _binding()).paged_compact(desc, cache._beside(workspace.get_device(), desc), moved, workspace)
+    if status:
+        L.check("sls_paged_compact", status)
 
 
 # ------------------------------------------------------------ decode step
