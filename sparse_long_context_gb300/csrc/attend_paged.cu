@@ -71,11 +71,10 @@ struct PgBf16 {
   using T = bf16;
   static constexpr int D = D_, W = 12, S = 2, SG = D == 128 ? 1 : 2, KS = D / 16;
   static constexpr int GROUP = 16 * D * 2, STAGE = 2 * SG * GROUP;
-  static constexpr int SQ = 0;  // floats of shared memory for the queries
   uint32_t qa[KS][2];
   float o[KS][4], m_run, l_run;  // head lane / 4; accumulator columns are heads 2m and 2m + 1
 
-  __device__ __forceinline__ void start(const T* q, int G, float*, int lane) {
+  __device__ __forceinline__ void start(const T* q, int G, int lane) {
     const int r = lane >> 2, m = lane & 3;
 #pragma unroll
     for (int c = 0; c < KS; ++c)
@@ -89,7 +88,7 @@ struct PgBf16 {
   }
 
   // A unit in `stage`: group s has lim[s] valid tokens.
-  __device__ __forceinline__ void unit(uint32_t stage, const int (&lim)[SG], float qscale, int, const float*, int lane) {
+  __device__ __forceinline__ void unit(uint32_t stage, const int (&lim)[SG], float qscale, int lane) {
     const int m = lane & 3, j = lane >> 3, row = 8 * (j >> 1) + (lane & 7);
     float x[SG][4], gm = kNegInf;
 #pragma unroll
@@ -215,105 +214,119 @@ __device__ __forceinline__ void pg_lds(uint32_t at, PgF2& a) {
   asm volatile("ld.shared.u64 %0, [%1];" : "=l"(a) : "r"(at));
 }
 
-// fp32 on the CUDA cores, no operand rounded: scores with a token and half of the channels a lane, then
-// values with D / 32 channels a lane and all heads' weights from shared memory.
-template <int D_>
+// fp32 on the CUDA cores, no operand rounded.  Scores: lane (tg, sl) takes channel chunks sl, sl + 8, ... of tokens
+// 4 j + tg, with the heads' queries in registers; the eight lanes of a token add up so that lane sl ends with head
+// sl.  The weights go to shared memory twice each (over the unit's keys, which are done with), as the pairs that the
+// value product multiplies a lane's D / 32 channels by.  GM: heads that are worked on (4 or 8; a check of each
+// against G would cost as many instructions as its products).
+template <int D_, int GM>
 struct PgF32 {
   using T = float;
   static constexpr int D = D_, W = D == 128 ? 6 : 12, S = 2, SG = 1;
-  static constexpr int GROUP = 16 * D * 4, STAGE = 2 * GROUP, NF = D / 64;
-  static constexpr int SQ = 8 * D + W * 16 * 8;  // queries, and each warp's weights [token][head]
-  PgF2 o[8][NF];
-  float m_run[8], l_run[8];  // the sums of the lane's token
+  static constexpr int GROUP = 16 * D * 4, STAGE = 2 * GROUP, NF = D / 64, NC = D / 32;
+  PgF2 q[GM][NC][2], o[GM][NF];
+  float m_run, l_run;  // of head sl % GM; the sum of this lane's tokens
 
-  __device__ __forceinline__ void start(const T* q, int G, float* sq, int) {
-    for (int i = threadIdx.x; i < G * D; i += W * 32) sq[i] = __ldg(q + i);
+  __device__ __forceinline__ void start(const T* qp, int G, int lane) {
+    const int sl = lane & 7;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
+    for (int g = 0; g < GM; ++g) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const float4 v = g < G ? __ldg(reinterpret_cast<const float4*>(qp + g * D + 32 * i + 4 * sl))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        q[g][i][0] = pg_f2(v.x, v.y);
+        q[g][i][1] = pg_f2(v.z, v.w);
+      }
 #pragma unroll
       for (int i = 0; i < NF; ++i) o[g][i] = 0ull;
-      m_run[g] = kNegInf;
-      l_run[g] = 0.f;
     }
-    __syncthreads();
+    m_run = kNegInf;
+    l_run = 0.f;
   }
 
-  __device__ __forceinline__ void unit(uint32_t stage, const int (&lims)[1], float qscale, int G, float* sq, int lane) {
-    const int t = lane & 15, half = lane >> 4, lim = lims[0];
-    const uint32_t q = smem_u32(sq) + half * (D / 2) * 4;
-    float* sp = sq + 8 * D + (threadIdx.x >> 5) * 128;
-    PgF2 s[8];
+  __device__ __forceinline__ void unit(uint32_t stage, const int (&lims)[1], float qscale, int lane) {
+    const int tg = lane >> 3, sl = lane & 7, lim = lims[0];
+    float x[4];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) s[g] = 0ull;
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      PgF2 k0, k1;
-      pg_lds(stage + pg_chunk(t, half * (D / 8) + c), k0, k1);
+    for (int j = 0; j < 4; ++j) {
+      PgF2 k[NC][2];
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
-        if (g < G) {
-          PgF2 a, b;
-          pg_lds(q + (g * D + 4 * c) * 4, a, b);
-          s[g] = pg_fma(b, k1, pg_fma(a, k0, s[g]));
+      for (int i = 0; i < NC; ++i) pg_lds(stage + pg_chunk(4 * j + tg, 8 * i + sl), k[i][0], k[i][1]);
+      float s[GM];
+#pragma unroll
+      for (int g = 0; g < GM; ++g) {
+        PgF2 a = pg_mul(q[g][0][0], k[0][0]);
+        a = pg_fma(q[g][0][1], k[0][1], a);
+#pragma unroll
+        for (int i = 1; i < NC; ++i) a = pg_fma(q[g][i][1], k[i][1], pg_fma(q[g][i][0], k[i][0], a));
+        const float2 d = pg_split(a);
+        s[g] = d.x + d.y;
+      }
+      // the heads over the eight lanes: half of what is left goes to the other half of the lanes
+      if constexpr (GM == 4)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], 4);
+#pragma unroll
+      for (int w = GM / 2; w > 0; w >>= 1)
+#pragma unroll
+        for (int g = 0; g < w; ++g) {
+          const float keep = sl & w ? s[g + w] : s[g], give = sl & w ? s[g] : s[g + w];
+          s[g] = keep + __shfl_xor_sync(0xffffffffu, give, w);
         }
+      x[j] = 4 * j + tg < lim ? s[0] * qscale : kNegInf;
     }
-    float p[8];
+    float gm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 8));
+    gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, 16));
+    const float mn = fmaxf(m_run, gm), mref = mn == kNegInf ? 0.f : mn;
+    const float alpha = pg_ex2(m_run - mref);
+    m_run = mn;
+    if (!__all_sync(0xffffffffu, alpha == 1.f)) {
+      l_run *= alpha;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      p[g] = 0.f;
-      if (g >= G) continue;
-      const float2 d = pg_split(s[g]);
-      float x = d.x + d.y;
-      x = (x + __shfl_xor_sync(0xffffffffu, x, 16)) * qscale;
-      x = t < lim ? x : kNegInf;
-      float gm = x;
+      for (int g = 0; g < GM; ++g) {
+        const float f = __shfl_sync(0xffffffffu, alpha, g);
 #pragma unroll
-      for (int w = 8; w > 0; w >>= 1) gm = fmaxf(gm, __shfl_xor_sync(0xffffffffu, gm, w));
-      const float mn = fmaxf(m_run[g], gm), mref = mn == kNegInf ? 0.f : mn;
-      const float alpha = pg_ex2(m_run[g] - mref);
-      m_run[g] = mn;
-      p[g] = pg_ex2(x - mref);
-      l_run[g] = fmaf(l_run[g], alpha, p[g]);
-      const PgF2 a2 = pg_f2(alpha, alpha);
-#pragma unroll
-      for (int i = 0; i < NF; ++i) o[g][i] = pg_mul(o[g][i], a2);
+        for (int i = 0; i < NF; ++i) o[g][i] = pg_mul(o[g][i], pg_f2(f, f));
+      }
     }
-    *reinterpret_cast<float4*>(sp + t * 8 + half * 4) =
-        half ? make_float4(p[4], p[5], p[6], p[7]) : make_float4(p[0], p[1], p[2], p[3]);
+    __syncwarp();  // every lane has read the keys
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = pg_ex2(x[j] - mref);
+      l_run += p;
+      asm volatile("st.shared.v2.f32 [%0], {%1, %1};" ::"r"(stage + (4 * j + tg) * 8 * GM + sl % GM * 8), "f"(p) : "memory");
+    }
     __syncwarp();
     const uint32_t v = stage + GROUP;
     const int n = min(lim, 16);  // rows behind the context are not read
 #pragma unroll 4
-    for (int k = 0; k < n; ++k) {
-      PgF2 x[NF];
-      if constexpr (NF == 2) pg_lds(v + pg_chunk(k, lane), x[0], x[1]);
-      else pg_lds(v + pg_chunk(k, lane >> 1) + 8 * (lane & 1), x[0]);
-      const float4 p0 = *reinterpret_cast<const float4*>(sp + k * 8), p1 = *reinterpret_cast<const float4*>(sp + k * 8 + 4);
-      const float pk[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
+    for (int t = 0; t < n; ++t) {
+      PgF2 y[NF], p[GM];
+      if constexpr (NF == 2) pg_lds(v + pg_chunk(t, lane), y[0], y[1]);
+      else pg_lds(v + pg_chunk(t, lane >> 1) + 8 * (lane & 1), y[0]);
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
-        if (g < G) {
+      for (int g = 0; g < GM; g += 2) pg_lds(stage + t * 8 * GM + g * 8, p[g], p[g + 1]);
 #pragma unroll
-          for (int i = 0; i < NF; ++i) o[g][i] = pg_fma(x[i], pg_f2(pk[g], pk[g]), o[g][i]);
-        }
+      for (int g = 0; g < GM; ++g)
+#pragma unroll
+        for (int i = 0; i < NF; ++i) o[g][i] = pg_fma(y[i], p[g], o[g][i]);
     }
-    __syncwarp();
   }
 
   __device__ __forceinline__ void finish(float* sO, float* sM, float* sL, bool ok, int lane) {
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 8);
+    l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);
+    if (lane < GM) {
+      sM[lane] = ok ? m_run : __int_as_float(0x7f800000);
+      sL[lane] = l_run;
+    }
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      float l = l_run[g];
-#pragma unroll
-      for (int w = 8; w > 0; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-      if (lane == 0) {
-        sM[g] = ok ? m_run[g] : __int_as_float(0x7f800000);
-        sL[g] = l;
-      }
+    for (int g = 0; g < GM; ++g)
 #pragma unroll
       for (int i = 0; i < NF; ++i)
         *reinterpret_cast<float2*>(sO + g * (D + 4) + lane * 2 * NF + 2 * i) = pg_split(o[g][i]);
-    }
   }
 };
 
@@ -358,7 +371,7 @@ struct PgLayout {
   static constexpr int MROW = Tile::D + 4;
   static constexpr size_t MERGE = (size_t)Tile::W * 8 * MROW * sizeof(float);
   static constexpr size_t REGION = RING > MERGE ? RING : MERGE;
-  static constexpr size_t smem(int rows) { return REGION + Tile::SQ * sizeof(float) + (size_t)(rows + 1) * sizeof(int) + 1024; }
+  static constexpr size_t smem(int rows) { return REGION + (size_t)(rows + 1) * sizeof(int) + 1024; }
 };
 
 // CL: the CTAs of a cluster take one row's units in equal shares and merge through
@@ -373,8 +386,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   extern __shared__ unsigned char smem_raw[];
   unsigned char* ring =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* s_q = reinterpret_cast<float*>(ring + L::REGION);
-  int* s_pref = reinterpret_cast<int*>(s_q + Tile::SQ);  // [rows + 1] first unit of each row
+  int* s_pref = reinterpret_cast<int*>(ring + L::REGION);  // [rows + 1] first unit of each row
   __shared__ PgSmem<CL> sh;
   __shared__ uint64_t full[W][S];
   __shared__ float sM[W][8], sL[W][8], sF[W][8], sHm[8], sHl[8];
@@ -564,7 +576,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       for (int j = 0; j < min(S - 1, nk); ++j) issue(j, 0);
     }
     Tile tile;
-    tile.start(static_cast<const T*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D, G, s_q, lane);
+    tile.start(static_cast<const T*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D, G, lane);
     for (int kb = 0; ok && kb < nk; kb += BATCH) {
       if (kb) load_batch(kb);
       const int kend = min(nk, kb + BATCH);
@@ -578,7 +590,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
         int n[SG], any = 0;
 #pragma unroll
         for (int s = 0; s < SG; ++s) any |= n[s] = __shfl_sync(0xffffffffu, lim[s], k - kb);
-        if (any) tile.unit(wring + st * Tile::STAGE, n, a.qscale, G, s_q, lane);
+        if (any) tile.unit(wring + st * Tile::STAGE, n, a.qscale, lane);
         // the stage is read before the copy engine may write it again
         __syncwarp();
         if (lane == 0) fence_proxy_async_smem();
@@ -926,7 +938,10 @@ static cudaError_t pg_launch(PagedAttend a, const Paged& c, cudaStream_t st) {
 
 template <bool LIST>
 static cudaError_t pg_dispatch(const Shape& s, const PagedAttend& a, const Paged& c, cudaStream_t st) {
-  if (s.dtype == 0) return s.D == 64 ? pg_launch<PgF32<64>, LIST>(a, c, st) : pg_launch<PgF32<128>, LIST>(a, c, st);
+  if (s.dtype == 0) {
+    if (s.G <= 4) return s.D == 64 ? pg_launch<PgF32<64, 4>, LIST>(a, c, st) : pg_launch<PgF32<128, 4>, LIST>(a, c, st);
+    return s.D == 64 ? pg_launch<PgF32<64, 8>, LIST>(a, c, st) : pg_launch<PgF32<128, 8>, LIST>(a, c, st);
+  }
   return s.D == 64 ? pg_launch<PgBf16<64>, LIST>(a, c, st) : pg_launch<PgBf16<128>, LIST>(a, c, st);
 }
 
