@@ -17,6 +17,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 
 #include "attend_common.cuh"
 #include "launch.h"
@@ -71,6 +72,7 @@ struct PgBf16 {
   using T = bf16;
   static constexpr int D = D_, W = 12, S = 2, SG = D == 128 ? 1 : 2, KS = D / 16;
   static constexpr int GROUP = 16 * D * 2, STAGE = 2 * SG * GROUP;
+  static constexpr double NS = D == 128 ? 4.6 : 3.0;  // a token of a CTA by itself
   uint32_t qa[KS][2];
   float o[KS][4], m_run, l_run;  // head lane / 4; accumulator columns are heads 2m and 2m + 1
 
@@ -224,6 +226,7 @@ struct PgF32 {
   using T = float;
   static constexpr int D = D_, W = D == 128 ? 6 : 12, S = 2, SG = 1;
   static constexpr int GROUP = 16 * D * 4, STAGE = 2 * GROUP, NF = D / 64, NC = D / 32;
+  static constexpr double NS = D == 128 ? 21.0 : 9.4;  // a token of a CTA by itself
   PgF2 q[GM][NC][2], o[GM][NF];
   float m_run, l_run;  // of head sl % GM; the sum of this lane's tokens
 
@@ -301,7 +304,7 @@ struct PgF32 {
     __syncwarp();
     const uint32_t v = stage + GROUP;
     const int n = min(lim, 16);  // rows behind the context are not read
-#pragma unroll 4
+#pragma unroll 8
     for (int t = 0; t < n; ++t) {
       PgF2 y[NF], p[GM];
       if constexpr (NF == 2) pg_lds(v + pg_chunk(t, lane), y[0], y[1]);
@@ -412,6 +415,33 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
   };
   auto units_of = [&](int row) { return (groups_of(row) + SG - 1) / SG; };
 
+  // the row holding unit x: the last row whose first unit (plus `beta` per
+  // earlier row) is <= x
+  auto row_at = [&](long long x, long long beta) {
+    int l = 0, u = rows - 1;
+    while (l < u) {
+      const int mid = (l + u + 1) >> 1;
+      if (s_pref[mid] + beta * mid <= x) l = mid;
+      else u = mid - 1;
+    }
+    return l;
+  };
+  // First unit of CTA k's range: equal shares of a list in which each row start after
+  // the first counts kPgSegCost tokens more.  Short jobs use fewer CTAs.
+  auto range_start = [&](int k, int n) {
+    const long long beta = kPgSegCost / UT, at = (s_pref[rows] + beta * (rows - 1)) * k / n;
+    const int l = row_at(at, beta);
+    return (int)min(at - beta * l, (long long)s_pref[l + 1]);
+  };
+  // rows without units: output 0, lse -inf (or the sink alone)
+  auto empty_rows = [&]() {
+    for (int er = cta; er < rows; er += gridDim.x) {
+      if (s_pref[er + 1] != s_pref[er]) continue;
+      for (int i = threadIdx.x; i < G * D; i += NT)
+        pg_finish<T, D>(a, (size_t)er * G + i / D, (er % a.Hkv) * G + i / D, kNegInf, 0.f, 0.f, i % D);
+    }
+  };
+
   int row = 0, lo = 0, hi = 0, grid = 1;
   if constexpr (CL) {
     row = cta / a.cluster;
@@ -449,41 +479,17 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       if (threadIdx.x == 0) s_pref[rows] = total;
       __syncthreads();
     }
-    const int T_ = s_pref[rows];
-    // the row holding unit x: the last row whose first unit (plus `beta` per
-    // earlier row) is <= x
-    auto row_at = [&](long long x, long long beta) {
-      int l = 0, u = rows - 1;
-      while (l < u) {
-        const int mid = (l + u + 1) >> 1;
-        if (s_pref[mid] + beta * mid <= x) l = mid;
-        else u = mid - 1;
-      }
-      return l;
-    };
-    // Every CTA's range: equal shares of a list in which each row start after
-    // the first counts kPgSegCost tokens more.  Short jobs use fewer CTAs.
-    grid = min((int)gridDim.x, max(1, T_ / kPgMinUnits));
-    {
-      const long long beta = kPgSegCost / UT, Tp = T_ + beta * (rows - 1);
-      for (int k = threadIdx.x; k <= grid; k += NT) {
-        const long long at = Tp * k / grid;
-        const int l = row_at(at, beta);
-        sh.s_lo[k] = (int)min(at - beta * l, (long long)s_pref[l + 1]);
-      }
+    const int total = s_pref[rows];
+    grid = min((int)gridDim.x, max(1, total / kPgMinUnits));
+    if (cta < grid) {
+      lo = range_start(cta, grid);
+      hi = range_start(cta + 1, grid);
+      row = row_at(lo, 0);
     }
-    __syncthreads();
-    // rows without units: output 0, lse -inf (or the sink alone)
-    for (int er = cta; er < rows; er += gridDim.x) {
-      if (s_pref[er + 1] != s_pref[er]) continue;
-      for (int i = threadIdx.x; i < G * D; i += NT)
-        pg_finish<T, D>(a, (size_t)er * G + i / D, (er % a.Hkv) * G + i / D, kNegInf, 0.f, 0.f, i % D);
+    if (lo >= hi) {
+      empty_rows();
+      return;
     }
-    if (cta >= grid) return;
-    lo = sh.s_lo[cta];
-    hi = sh.s_lo[cta + 1];
-    if (lo >= hi) return;
-    row = row_at(lo, 0);
   }
 
   // the wait-timeout test hook: the first CTA with a unit
@@ -577,6 +583,11 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
     Tile tile;
     tile.start(static_cast<const T*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D, G, lane);
+    if constexpr (!CL)
+      if (e == lo) {  // while the first copies are on their way
+        for (int c2 = threadIdx.x; c2 <= grid; c2 += NT) sh.s_lo[c2] = range_start(c2, grid);
+        empty_rows();
+      }
     for (int kb = 0; ok && kb < nk; kb += BATCH) {
       if (kb) load_batch(kb);
       const int kend = min(nk, kb + BATCH);
@@ -718,6 +729,16 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
       __syncthreads();
       if (sh.s_last) {
         const int n = sh.s_ncontrib;
+        // a thread's first output: the first contributors' values are in flight while the weights are formed
+        constexpr int U = 8;
+        auto part = [&](int it, int jj) {
+          return jj < n && it < G * (D / 4)
+                     ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[jj] * G + it / (D / 4)) * D) + it % (D / 4))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = part(threadIdx.x, u);
         for (int g = warp; g < G; g += W) {
           constexpr int H = kPgWeights / 32;
           // the contributors' max and sum in registers, loaded at once
@@ -757,16 +778,13 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
           }
         }
         __syncthreads();
-        constexpr int U = 8;
         for (int it = threadIdx.x; it < G * (D / 4); it += NT) {
           const int g4 = it / (D / 4), d4 = it % (D / 4);
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           for (int j0 = 0; j0 < n; j0 += U) {
-            float4 v[U];
+            if (j0 || it >= NT)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-              v[u] = j0 + u < n ? __ldcg(reinterpret_cast<const float4*>(a.po + ((size_t)sh.s_slot[j0 + u] * G + g4) * D) + d4)
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int u = 0; u < U; ++u) v[u] = part(it, j0 + u);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int jj = j0 + u;
@@ -897,17 +915,28 @@ static int pg_clusters(int c, PgDevice* d) {
   return n - 1;
 }
 
-// CTAs per row of the cluster kernel, or 0 for ranges over all rows, by their costs.
+// CTAs per row of the cluster kernel, or 0 for ranges over all rows, by their costs.  A
+// CTA takes Tile::NS ns a token and a cluster 5.3 us besides, in as many waves as the clusters need; the
+// ranges take 13 us and 23 / rows for rows that many CTAs share; both read at the memory's rate at
+// most (near it a cluster's two bounds add up as their cubes' root).
+// `most` bounds a row's tokens; where only the device knows them, rows are taken to hold four fifths
+// of it on average and a cluster to wait for one that is full.  Measured on 70 shapes of 1 to 256
+// rows, full and with lengths spread evenly from none: 16.9 us with two CTAs a row and 20 in ranges
+// for 64 lists of 2048 tokens, 25.7 and 32.1 for 64 full rows of 4k, 188 and 167 for 64 uneven ones of
+// up to 64k.  Where it takes the slower side it mostly loses less than 15%, 25% at most (64 full rows of 4k in fp32:
+// 36.5 us, 29.3 with two CTAs a row).
 template <typename Tile, bool LIST>
 static int pg_pick(int rows, double most, bool fixed, bool even, PgDevice* d) {
-  const double t = 2.0 * Tile::D * sizeof(typename Tile::T) * 2.0e-5, sms = sm_count();
-  const double mean = fixed ? most : 0.75 * most, longest = even ? mean : most;
-  double best = 13.0 + rows / sms * (mean * t + 6.0) + 0.1 * sms / rows;
+  const double t = Tile::NS * 1e-3, sms = sm_count();
+  const double mean = fixed ? most : 0.8 * most, longest = even ? mean : most;
+  const double memory = rows * 2.0 * Tile::D * sizeof(typename Tile::T) / 6.7e6;  // us a token of every row
+  double best = 13.0 + mean * std::max(memory, rows / sms * t) + 23.0 / rows;
   int pick = 0;
   for (int c = 1; c <= kPgMaxCluster; ++c) {
     const int n = c == 1 ? sm_count() : pg_clusters<Tile, LIST>(c, d);
     if (n < 1) continue;
-    const double us = ((rows + n - 1) / n) * (5.5 + longest / c * t);
+    const int waves = (rows + n - 1) / n;
+    const double us = waves * 5.3 + longest * std::cbrt(std::pow(waves * t / c, 3.0) + std::pow(memory, 3.0));
     if (us < best) {
       best = us;
       pick = c;
