@@ -3,7 +3,7 @@
 // state: kPagedHead words, then a bit per page (1: free), then two words per sequence
 // (the span of the append that is under way).  Head: word 0 the number of free
 // pages, word 1 a word of the bits below which no page is free, word 2 whether the
-// fork under way fails.
+// fork under way fails, word 3 the CTAs of the call under way that have arrived (0 between calls).
 #pragma once
 
 #include "common.cuh"

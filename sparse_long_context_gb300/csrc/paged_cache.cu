@@ -15,9 +15,13 @@
 
 namespace sls {
 
-constexpr int kPlanThreads = 1024;
+// Plans are made by one CTA, of 256 threads (1024 for more than 1024 sequences: a barrier of 32 warps
+// costs several of 8) with up to four sequences each.
+constexpr int kPlanThreads = 1024, kPlanFew = 256, kPlanMost = 4;
+static_assert(kPlanThreads * kPlanMost == kPagedMaxSeqs, "a plan holds every sequence");
 
 // Exclusive scan of one int per thread over the CTA; `total` gets the sum.
+template <int NT>
 __device__ __forceinline__ int plan_scan(int v, int* tmp, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
@@ -32,40 +36,39 @@ __device__ __forceinline__ int plan_scan(int v, int* tmp, int& total) {
   int before = 0;
   total = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
+  for (int w = 0; w < NT / 32; ++w) {
     before += w < warp ? tmp[w] : 0;
     total += tmp[w];
   }
   return before + x - v;
 }
 
+template <int NT>
 struct PlanShared {
-  uint32_t word[kPlanThreads];
-  int base[kPlanThreads], tmp[kPlanThreads / 32];
+  uint32_t word[NT];
+  int base[NT], tmp[NT / 32];
 };
 
-// Takes the `total` lowest-numbered free pages (there are as many): give(rank, page) for each, and
-// their bits cleared.  All threads of the one CTA call it.
-template <typename F>
-__device__ __forceinline__ void take_pages(const Paged& c, int total, PlanShared& sh, F give) {
+// The `total` lowest-numbered free pages (there are as many): give(rank, page) for each.  TAKE: their
+// bits are cleared.  All threads of the CTA call it.
+template <int NT, bool TAKE, typename F>
+__device__ __forceinline__ void find_pages(const Paged& c, int first, int total, PlanShared<NT>& sh, F give) {
   uint32_t* bits = paged_bits(c);
   const int words = paged_words(c.pages), tid = threadIdx.x, lane = tid & 31;
-  const int first = c.state[1];
   int got = 0;
-  __syncthreads();  // every thread has read the head
-  for (int w0 = max(first, 0); got < total && w0 < words; w0 += kPlanThreads) {
+  for (int w0 = max(first, 0); got < total && w0 < words; w0 += NT) {
     const uint32_t word = w0 + tid < words ? bits[w0 + tid] : 0u;
     int sum;
-    const int base = got + plan_scan(__popc(word), sh.tmp, sum);
+    const int base = got + plan_scan<NT>(__popc(word), sh.tmp, sum);
     sh.word[tid] = word;
     sh.base[tid] = base;
     __syncthreads();
-    for (int i = tid >> 5; i < kPlanThreads && sh.base[i] < total; i += kPlanThreads / 32) {
+    for (int i = tid >> 5; i < NT && sh.base[i] < total; i += NT / 32) {
       const uint32_t x = sh.word[i];
       const int r = sh.base[i] + __popc(x & ((1u << lane) - 1u));
       if ((x >> lane & 1u) && r < total) give(r, (w0 + i) * 32 + lane);
     }
-    if (word && base < total) {
+    if (TAKE && word && base < total) {
       uint32_t left = word;
       for (int k = base; k < total && left; ++k) left &= left - 1;
       bits[w0 + tid] = left;
@@ -74,7 +77,22 @@ __device__ __forceinline__ void take_pages(const Paged& c, int total, PlanShared
     got += sum;
     __syncthreads();
   }
-  if (tid == 0) c.state[0] -= total;
+  if (TAKE && tid == 0) c.state[0] -= total;
+}
+
+// Whether this CTA is the last of the grid's to get here: all others have read what they need of the
+// cache's integers, and their writes before this are seen.  The count is zero again afterwards.
+__device__ __forceinline__ bool last_to_arrive(const Paged& c, int ctas) {
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(c.state + 3, 1) == ctas - 1;
+    if (s_last) c.state[3] = 0;
+    __threadfence();
+  }
+  __syncthreads();
+  return s_last != 0;
 }
 
 // ------------------------------------------------------------------- the state from the table
@@ -128,68 +146,99 @@ cudaError_t launch_paged_init(const Shape& s, const Paged& c, cudaStream_t st) {
 
 // ------------------------------------------------------------------- append
 
-// Which sequences append, and the pages they take.  A sequence needs the pages between those it has
-// and those its new length takes; it appends if its tokens fit its capacity and its and the earlier
-// sequences' pages are there (or it needs none), and its partial page is its own.
-__global__ void __launch_bounds__(kPlanThreads)
-paged_plan_kernel(const Paged c, const int32_t* new_len, int max_new, int32_t* pos_out, int B, int Cap, int pshift) {
-  __shared__ PlanShared sh;
-  __shared__ int s_first[kPagedMaxSeqs], s_had[kPagedMaxSeqs];
-  __shared__ int s_total;
-  pdl_wait_then_release();
+// Which sequences append, and how many pages that takes in all.  A sequence needs the pages between
+// those it has and those its new length takes; it appends if its tokens fit its capacity and its and the
+// earlier sequences' pages are there (or it needs none), and its partial page is its own.  Thread i has
+// sequences [i per, (i + 1) per): start and n (0: it appends nothing), and the page of its partial one.
+struct AppendPlan {
+  int b0, b1, start[kPlanMost], n[kPlanMost], page[kPlanMost];
+};
+template <int NT>
+__device__ __forceinline__ int append_plan(const Paged& c, const int32_t* new_len, int max_new, int B, int Cap, int pshift,
+                                           bool count, AppendPlan& p, int* s_first, int* s_had, int* s_total, PlanShared<NT>& sh) {
   const int tid = threadIdx.x, P = 1 << pshift, MP = Cap >> pshift, free = c.state[0];
-  const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  constexpr int MOST = kPagedMaxSeqs / kPlanThreads;
-  int start[MOST], n[MOST], need[MOST], sum = 0;
+  const int per = (B + NT - 1) / NT;
+  p.b0 = min(tid * per, B);
+  p.b1 = min(p.b0 + per, B);
+  int need[kPlanMost], sum = 0;
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    const int b = b0 + i;
-    start[i] = n[i] = need[i] = 0;
-    if (b >= b1) continue;
-    start[i] = clamp_len(c.ctx[b], Cap);
-    n[i] = new_len ? min(max(new_len[b], 0), max_new) : max_new;
-    if (n[i] > Cap - start[i]) n[i] = 0;
-    if (n[i] && (start[i] & (P - 1))) {
-      const int p = c.table[(size_t)b * MP + (start[i] >> pshift)];
-      if (!paged_page(p, c.pages) || c.refs[p] != 1) {
-        note_bad_pages(1);
-        n[i] = 0;
+  for (int i = 0; i < kPlanMost; ++i) {
+    const int b = p.b0 + i;
+    p.start[i] = p.n[i] = need[i] = 0;
+    p.page[i] = -1;
+    if (b >= p.b1) continue;
+    p.start[i] = clamp_len(c.ctx[b], Cap);
+    p.n[i] = new_len ? min(max(new_len[b], 0), max_new) : max_new;
+    if (p.n[i] > Cap - p.start[i]) p.n[i] = 0;
+    if (p.n[i] && (p.start[i] & (P - 1))) {
+      p.page[i] = c.table[(size_t)b * MP + (p.start[i] >> pshift)];
+      if (!paged_page(p.page[i], c.pages) || c.refs[p.page[i]] != 1) {
+        if (count) note_bad_pages(1);
+        p.n[i] = 0;
       }
     }
-    const int had = (start[i] + P - 1) >> pshift;
-    if (n[i]) need[i] = (int)(((int64_t)start[i] + n[i] + P - 1) >> pshift) - had;
+    const int had = (p.start[i] + P - 1) >> pshift;
+    if (p.n[i]) need[i] = (int)(((int64_t)p.start[i] + p.n[i] + P - 1) >> pshift) - had;
     s_had[b] = had;
     sum += need[i];
   }
-  if (tid == 0) s_total = 0;
+  if (tid == 0) *s_total = 0;
   int all;
-  int first = plan_scan(sum, sh.tmp, all), most = 0;
+  int first = plan_scan<NT>(sum, sh.tmp, all), most = 0;
 #pragma unroll
-  for (int i = 0; i < MOST; ++i) {
-    const int b = b0 + i;
-    if (b >= b1) continue;
+  for (int i = 0; i < kPlanMost; ++i) {
+    const int b = p.b0 + i;
+    if (b >= p.b1) continue;
     s_first[b] = first;
     first += need[i];
     if (need[i] && first <= free) most = first;
-    else if (need[i]) n[i] = 0;
-    paged_spans(c)[b] = make_int2(start[i], n[i]);
-    if (n[i]) c.ctx[b] = start[i] + n[i];
-    if (pos_out) pos_out[b] = n[i] ? start[i] : -1;
+    else if (need[i]) p.n[i] = 0;
   }
   // the pages of the sequences that append are the first ones in order
   most = __reduce_max_sync(0xffffffffu, most);
-  if ((tid & 31) == 0) atomicMax(&s_total, most);
+  if ((tid & 31) == 0) atomicMax(s_total, most);
   __syncthreads();
-  const int total = s_total;
+  return *s_total;
+}
+// The sequence that takes the r-th page: the last one whose first page is r or before.
+__device__ __forceinline__ int append_taker(const int* s_first, int B, int r) {
+  int lo = 0, hi = B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (s_first[mid] <= r) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The new lengths and the positions reported.
+__device__ __forceinline__ void append_record(const Paged& c, const AppendPlan& p, int32_t* pos_out) {
+#pragma unroll
+  for (int i = 0; i < kPlanMost; ++i) {
+    const int b = p.b0 + i;
+    if (b >= p.b1) continue;
+    if (p.n[i]) c.ctx[b] = p.start[i] + p.n[i];
+    if (pos_out) pos_out[b] = p.n[i] ? p.start[i] : -1;
+  }
+}
+
+template <int NT>
+__global__ void __launch_bounds__(NT)
+paged_plan_kernel(const Paged c, const int32_t* new_len, int max_new, int32_t* pos_out, int B, int Cap, int pshift) {
+  __shared__ PlanShared<NT> sh;
+  __shared__ int s_first[NT * kPlanMost], s_had[NT * kPlanMost], s_total;
+  pdl_wait_then_release();
+  const int MP = Cap >> pshift, first = c.state[1];
+  AppendPlan p;
+  const int total = append_plan<NT>(c, new_len, max_new, B, Cap, pshift, true, p, s_first, s_had, &s_total, sh);
+#pragma unroll
+  for (int i = 0; i < kPlanMost; ++i)
+    if (p.b0 + i < p.b1) paged_spans(c)[p.b0 + i] = make_int2(p.start[i], p.n[i]);
+  append_record(c, p, pos_out);
   if (total == 0) return;
-  take_pages(c, total, sh, [&](int r, int page) {
-    int lo = 0, hi = B - 1;  // the last sequence whose first page is r or before
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (s_first[mid] <= r) lo = mid;
-      else hi = mid - 1;
-    }
-    c.table[(size_t)lo * MP + s_had[lo] + r - s_first[lo]] = page;
+  find_pages<NT, true>(c, first, total, sh, [&](int r, int page) {
+    const int b = append_taker(s_first, B, r);
+    c.table[(size_t)b * MP + s_had[b] + r - s_first[b]] = page;
     c.refs[page] = 1;
   });
 }
@@ -290,9 +339,82 @@ paged_write_kernel(const Paged c, const PagedNew nw, int Hkv, int Cap, int D, in
   }
 }
 
+// One token of every sequence in one launch: each CTA plans for itself and writes its share of the vectors, and the
+// last one to have read what was records what changes (32 sequences: 8.1 us in two launches, XX in one).
+constexpr int kOnePerSm = 2;  // CTAs that plan, at most
+
+template <typename T>
+__global__ void __launch_bounds__(kPlanFew)
+paged_append_one_kernel(const Paged c, const PagedNew nw, int32_t* pos_out, int Hkv, int B, int Cap, int D, int pshift) {
+  constexpr int E = Vec16<T>::N, NT = kPlanFew;
+  __shared__ PlanShared<NT> sh;
+  __shared__ int s_first[NT * kPlanMost], s_had[NT * kPlanMost], s_slot[NT * kPlanMost], s_page[NT * kPlanMost], s_total;
+  const int V = D / E, per = Hkv * V, all = B * per, tid = threadIdx.x, MP = Cap >> pshift, P = 1 << pshift;
+  pdl_wait_then_release();
+  const int first = c.state[1];
+  // the thread's first vectors, in flight with the plan
+  const int i0 = blockIdx.x * NT + tid;
+  auto load = [&](const void* src, int64_t sb, int64_t sh2, int i) {
+    return i < all ? ldg_stream(static_cast<const T*>(src) + i / per * sb + i % per / V * sh2 + i % V * E) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 k = load(nw.k, nw.kb, nw.kh, i0), x = load(nw.v, nw.vb, nw.vh, i0);
+  AppendPlan p;
+  const int total = append_plan<NT>(c, nw.new_len, 1, B, Cap, pshift, blockIdx.x == 0, p, s_first, s_had, &s_total, sh);
+#pragma unroll
+  for (int i = 0; i < kPlanMost; ++i)
+    if (p.b0 + i < p.b1) {
+      s_page[p.b0 + i] = p.n[i] ? p.page[i] : -1;
+      s_slot[p.b0 + i] = p.n[i] ? p.start[i] : -1;
+    }
+  __syncthreads();
+  if (total)
+    find_pages<NT, false>(c, first, total, sh, [&](int r, int page) { s_page[append_taker(s_first, B, r)] = page; });
+  const bool last = last_to_arrive(c, gridDim.x);
+  for (int i = i0; i < all; i += gridDim.x * NT) {
+    if (i != i0) {
+      k = load(nw.k, nw.kb, nw.kh, i);
+      x = load(nw.v, nw.vb, nw.vh, i);
+    }
+    const int b = i / per, h = i % per / V, v = i % V, at = s_slot[b];
+    if (at < 0) continue;
+    const size_t row = (size_t)s_page[b] * Hkv + h, to = (row * P + (at & (P - 1))) * V + v;
+    static_cast<uint4*>(c.k)[to] = k;
+    static_cast<uint4*>(c.v)[to] = x;
+    if (c.kmin) {
+      uint4 *kmin = static_cast<uint4*>(c.kmin) + row * V + v, *kmax = static_cast<uint4*>(c.kmax) + row * V + v, lo = k, hi = k;
+      if (at & (P - 1)) PagedLimits<T>::fold(lo, hi, *kmin, *kmax);
+      *kmin = lo;
+      *kmax = hi;
+    }
+  }
+  if (!last) return;
+  append_record(c, p, pos_out);
+#pragma unroll
+  for (int i = 0; i < kPlanMost; ++i) {
+    const int b = p.b0 + i;
+    if (b >= p.b1 || !p.n[i] || p.page[i] >= 0) continue;
+    c.table[(size_t)b * MP + s_had[b]] = s_page[b];
+    c.refs[s_page[b]] = 1;
+  }
+  if (total) find_pages<NT, true>(c, first, total, sh, [](int, int) {});
+}
+
 cudaError_t launch_paged_append(const Shape& s, const Paged& c, const PagedNew& n, int32_t* pos_out, cudaStream_t st) {
-  cudaError_t e = launch_pdl(paged_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, c, n.new_len, n.max_new, pos_out, s.B,
-                             s.Cap, s.pshift);
+  cudaError_t e;
+  const bool few = s.B <= kPlanFew * kPlanMost;
+  const int64_t vecs = (int64_t)s.B * s.Hkv * s.D * (s.dtype == 0 ? 4 : 2) / 16;
+  if (n.max_new == 1 && few && vecs <= (int64_t)kPlanFew * 4 * kOnePerSm * sm_count()) {
+    const dim3 grid((unsigned)std::min<int64_t>((vecs + kPlanFew - 1) / kPlanFew, kOnePerSm * sm_count()));
+    e = s.dtype == 0 ? launch_pdl(paged_append_one_kernel<float>, grid, dim3(kPlanFew), 0, st, c, n, pos_out, s.Hkv, s.B, s.Cap,
+                                  s.D, s.pshift)
+                     : launch_pdl(paged_append_one_kernel<bf16>, grid, dim3(kPlanFew), 0, st, c, n, pos_out, s.Hkv, s.B, s.Cap,
+                                  s.D, s.pshift);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  e = few ? launch_pdl(paged_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, c, n.new_len, n.max_new, pos_out, s.B, s.Cap,
+                       s.pshift)
+          : launch_pdl(paged_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, st, c, n.new_len, n.max_new, pos_out, s.B,
+                       s.Cap, s.pshift);
   if (e == cudaSuccess && n.max_new > 0) {
     const int most = std::min(n.max_new, s.Cap);  // more tokens fit no sequence
     const dim3 grid((unsigned)(((most + s.P - 2) / s.P + 1) * s.Hkv), s.B);
@@ -331,17 +453,17 @@ __device__ __forceinline__ void fork_entry(const Paged& c, const ForkPlan& p, in
 }
 
 // Counts of pages as after the fork, but for the partial pages of changed sequences.
-__global__ void __launch_bounds__(256)
-fork_count_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
-  pdl_wait_then_release();
-  const int b = blockIdx.y, MP = Cap >> pshift;
+// Threads first, first + step, ... of sequence b.
+__device__ __forceinline__ void fork_count(const Paged& c, const PagedFork& f, int b, int B, int Cap, int pshift, int first,
+                                           int step) {
+  const int MP = Cap >> pshift;
   const ForkPlan p = fork_plan(f, c.ctx, b, B, Cap);
   if (p.same) {
-    if (p.bad && blockIdx.x == 0 && threadIdx.x == 0) note_bad_pages(1);
+    if (p.bad && first == 0) note_bad_pages(1);
     return;
   }
   const int last = max((p.was + (1 << pshift) - 1) >> pshift, (p.len >> pshift) + 1);
-  for (int l = blockIdx.x * 256 + threadIdx.x; l < min(last, MP); l += gridDim.x * 256) {
+  for (int l = first; l < min(last, MP); l += step) {
     int old, now;
     fork_entry(c, p, b, l, MP, pshift, old, now);
     if (old != now) {
@@ -355,14 +477,13 @@ fork_count_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) 
 }
 
 // Who keeps, and who copies, a partial page; the pages for the copies; the new lengths.
-__global__ void __launch_bounds__(kPlanThreads)
-fork_plan_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
-  __shared__ PlanShared sh;
-  __shared__ int s_src[kPagedMaxSeqs], s_copy[kPagedMaxSeqs];
-  pdl_wait_then_release();
-  const int tid = threadIdx.x, MP = Cap >> pshift, free = c.state[0];
-  const int per = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(tid * per, B), b1 = min(b0 + per, B);
-  constexpr int MOST = kPagedMaxSeqs / kPlanThreads;
+template <int NT>
+__device__ __forceinline__ void fork_choose(const Paged& c, const PagedFork& f, int B, int Cap, int pshift) {
+  constexpr int MOST = kPlanMost;
+  __shared__ PlanShared<NT> sh;
+  __shared__ int s_src[NT * MOST], s_copy[NT * MOST];
+  const int tid = threadIdx.x, MP = Cap >> pshift, free = c.state[0], lowest = c.state[1];
+  const int per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
   ForkPlan p[MOST];
   int src[MOST];
   bool held[MOST];
@@ -395,7 +516,7 @@ fork_plan_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
     copies += copy[i];
   }
   int total;
-  int rank = plan_scan(copies, sh.tmp, total);
+  int rank = plan_scan<NT>(copies, sh.tmp, total);
   const bool fail = total > free;
   if (tid == 0) {
     c.state[2] = fail;
@@ -414,7 +535,7 @@ fork_plan_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
   }
   __syncthreads();
   if (fail || total == 0) return;
-  take_pages(c, total, sh, [&](int r, int page) {
+  find_pages<NT, true>(c, lowest, total, sh, [&](int r, int page) {
     const int b = s_copy[r];
     f.copy[b].y = page;
     f.rows[(size_t)b * MP + (c.ctx[b] >> pshift)] = page;
@@ -422,68 +543,99 @@ fork_plan_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
   });
 }
 
-// New rows into the table, pages that nobody holds any more freed, partial pages copied (and
-// summarised anew).  Where the pool lacked pages: the counts as they were.
-template <typename T>
-__global__ void __launch_bounds__(256)
-fork_commit_kernel(const Paged c, const PagedFork f, int Hkv, int B, int Cap, int D, int pshift, int chunks) {
-  constexpr int E = Vec16<T>::N, NT = 256;
-  pdl_wait_then_release();
-  const int b = blockIdx.y, MP = Cap >> pshift, P = 1 << pshift;
-  const int4 cp = f.copy[b];
-  const bool fail = c.state[2] != 0;
-  if (cp.w < 0) return;
-  if ((int)blockIdx.x < chunks) {
-    if (fail) {
-      const ForkPlan p = fork_plan(f, c.ctx, b, B, Cap);
-      const int last = max((p.was + P - 1) >> pshift, (p.len >> pshift) + 1);
-      for (int l = blockIdx.x * NT + threadIdx.x; l < min(last, MP); l += chunks * NT) {
-        int old, now;
-        fork_entry(c, p, b, l, MP, pshift, old, now);
-        if (old != now) {
-          if (paged_page(old, c.pages)) atomicAdd(c.refs + old, 1);
-          if (paged_page(now, c.pages)) atomicAdd(c.refs + now, -1);
-        }
-      }
-      return;
-    }
-    const int had = (cp.w + P - 1) >> pshift, has = (c.ctx[b] + P - 1) >> pshift;
-    for (int l = blockIdx.x * NT + threadIdx.x; l < max(had, has); l += chunks * NT) {
-      const int old = l < had ? c.table[(size_t)b * MP + l] : -1, now = l < has ? f.rows[(size_t)b * MP + l] : -1;
-      if (old == now) continue;
-      c.table[(size_t)b * MP + l] = now;
-      if (paged_page(old, c.pages) && c.refs[old] == 0) {
-        const uint32_t bit = 1u << (old & 31);
-        if (!(atomicOr(paged_bits(c) + (old >> 5), bit) & bit)) {
-          atomicAdd(c.state, 1);
-          atomicMin(c.state + 1, old >> 5);
-        }
+// New rows into the table, and pages that nobody holds any more freed.  Where the pool lacked pages:
+// the counts as they were.
+__device__ __forceinline__ void fork_commit(const Paged& c, const PagedFork& f, int b, int B, int Cap, int pshift, int first,
+                                            int step) {
+  const int MP = Cap >> pshift, P = 1 << pshift, was = f.copy[b].w;
+  if (was < 0) return;
+  if (c.state[2] != 0) {
+    const ForkPlan p = fork_plan(f, c.ctx, b, B, Cap);
+    const int last = max((p.was + P - 1) >> pshift, (p.len >> pshift) + 1);
+    for (int l = first; l < min(last, MP); l += step) {
+      int old, now;
+      fork_entry(c, p, b, l, MP, pshift, old, now);
+      if (old != now) {
+        if (paged_page(old, c.pages)) atomicAdd(c.refs + old, 1);
+        if (paged_page(now, c.pages)) atomicAdd(c.refs + now, -1);
       }
     }
     return;
   }
-  if (fail || cp.z == 0) return;
-  const int h = blockIdx.x - chunks, V = D / E, n = cp.z * V;
-  const size_t from = ((size_t)cp.x * Hkv + h) * P * V, to = ((size_t)cp.y * Hkv + h) * P * V;
-  const uint4 *ks = static_cast<const uint4*>(c.k) + from, *vs = static_cast<const uint4*>(c.v) + from;
-  uint4 *kd = static_cast<uint4*>(c.k) + to, *vd = static_cast<uint4*>(c.v) + to;
-  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  const int had = (was + P - 1) >> pshift, has = (c.ctx[b] + P - 1) >> pshift;
+  for (int l = first; l < max(had, has); l += step) {
+    const int old = l < had ? c.table[(size_t)b * MP + l] : -1, now = l < has ? f.rows[(size_t)b * MP + l] : -1;
+    if (old == now) continue;
+    c.table[(size_t)b * MP + l] = now;
+    if (paged_page(old, c.pages) && c.refs[old] == 0) {
+      const uint32_t bit = 1u << (old & 31);
+      if (!(atomicOr(paged_bits(c) + (old >> 5), bit) & bit)) {
+        atomicAdd(c.state, 1);
+        atomicMin(c.state + 1, old >> 5);
+      }
+    }
+  }
+}
+
+// Head h of the partial page of sequence b copied, and summarised anew, by the V = D * size / 16 threads that hold
+// vector `v` of its rows (one each, so a summary needs no more than its thread).
+template <typename T>
+__device__ __forceinline__ void fork_copy(const Paged& c, const PagedFork& f, int b, int h, int v, int Hkv, int D, int pshift) {
+  const int4 cp = f.copy[b];
+  if (cp.w < 0 || cp.z == 0 || c.state[2] != 0) return;
   const bool copy = cp.x != cp.y;
   if (!copy && !c.kmin) return;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    const uint4 k = ks[i];
-    if (copy) {
-      kd[i] = k;
-      vd[i] = vs[i];
-    }
-    if (i == (int)threadIdx.x) lo = hi = k;
-    else PagedLimits<T>::fold(lo, hi, k, k);
+  const int V = D / Vec16<T>::N;
+  const size_t from = ((((size_t)cp.x * Hkv + h) << pshift) * V) + v, to = ((((size_t)cp.y * Hkv + h) << pshift) * V) + v;
+  const uint4 *ks = static_cast<const uint4*>(c.k) + from, *vs = static_cast<const uint4*>(c.v) + from;
+  uint4 *kd = static_cast<uint4*>(c.k) + to, *vd = static_cast<uint4*>(c.v) + to;
+  uint4 lo = ks[0], hi = lo;
+  constexpr int U = 4;
+  for (int t = 0; t < cp.z; t += U) {
+    uint4 k[U], x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u < cp.z) {
+        k[u] = ks[(t + u) * V];
+        if (copy) x[u] = vs[(t + u) * V];
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (t + u < cp.z) {
+        if (copy) {
+          kd[(t + u) * V] = k[u];
+          vd[(t + u) * V] = x[u];
+        }
+        PagedLimits<T>::fold(lo, hi, k[u], k[u]);
+      }
   }
   if (c.kmin) {
-    const size_t m = ((size_t)cp.y * Hkv + h) * V;
-    write_limits<T, NT>(lo, hi, (int)threadIdx.x < n, false, static_cast<uint4*>(c.kmin) + m,
-                        static_cast<uint4*>(c.kmax) + m, V);
+    const size_t m = ((size_t)cp.y * Hkv + h) * V + v;
+    static_cast<uint4*>(c.kmin)[m] = lo;
+    static_cast<uint4*>(c.kmax)[m] = hi;
   }
+}
+
+// The counts, and, by the last CTA, the choice.
+template <int NT>
+__global__ void __launch_bounds__(NT)
+fork_count_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) {
+  pdl_wait_then_release();
+  fork_count(c, f, blockIdx.y, B, Cap, pshift, blockIdx.x * NT + threadIdx.x, gridDim.x * NT);
+  if (last_to_arrive(c, gridDim.x * gridDim.y)) fork_choose<NT>(c, f, B, Cap, pshift);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+fork_commit_kernel(const Paged c, const PagedFork f, int Hkv, int B, int Cap, int D, int pshift, int chunks) {
+  pdl_wait_then_release();
+  const int b = blockIdx.y, V = D / Vec16<T>::N;
+  if ((int)blockIdx.x < chunks) {
+    fork_commit(c, f, b, B, Cap, pshift, blockIdx.x * 256 + threadIdx.x, chunks * 256);
+    return;
+  }
+  const int i = (blockIdx.x - chunks) * 256 + threadIdx.x;
+  if (i < Hkv * V) fork_copy<T>(c, f, b, i / V, i % V, Hkv, D, pshift);
 }
 
 size_t paged_fork_workspace(const Shape& s) {
@@ -494,12 +646,14 @@ cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* par
                               void* ws, cudaStream_t st) {
   PagedFork f = {parent, keep, done, static_cast<int4*>(ws), nullptr};
   f.rows = reinterpret_cast<int32_t*>(f.copy + s.B);
-  const int MP = s.Cap >> s.pshift, chunks = std::min(64, (MP + 255) / 256);
-  cudaError_t e = launch_pdl(fork_count_kernel, dim3(chunks, s.B), dim3(256), 0, st, c, f, s.B, s.Cap, s.pshift);
-  if (e == cudaSuccess)
-    e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, c, f, s.B, s.Cap, s.pshift);
+  const int MP = s.Cap >> s.pshift, size = s.dtype == 0 ? 4 : 2;
+  cudaError_t e;
+  const int nt = s.B <= kPlanFew * kPlanMost ? kPlanFew : kPlanThreads, shares = std::min(64, (MP + nt - 1) / nt);
+  e = nt == kPlanFew ? launch_pdl(fork_count_kernel<kPlanFew>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift)
+                     : launch_pdl(fork_count_kernel<kPlanThreads>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift);
   if (e == cudaSuccess) {
-    const dim3 grid(chunks + s.Hkv, s.B);
+    const int chunks = std::min(64, (MP + 255) / 256);
+    const dim3 grid(chunks + (s.Hkv * s.D * size / 16 + 255) / 256, s.B);
     e = s.dtype == 0 ? launch_pdl(fork_commit_kernel<float>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks)
                      : launch_pdl(fork_commit_kernel<bf16>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks);
   }
@@ -509,15 +663,17 @@ cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* par
 // ------------------------------------------------------------------- compaction
 
 // The i-th free page below U (the number of used pages) receives the i-th used one from U on:
-// holes[i], movers[i], and rank[p] = i of a mover p.  A CTA takes 1024 words of the bits and counts
-// what lies before them.
+// holes[i], movers[i], and rank[p] = i of a mover p.  A CTA takes 64 words of the bits (one CTA for
+// 32768 pages takes 12 us) and counts what lies before them.
+constexpr int kCompactWords = 64;
+
 __global__ void __launch_bounds__(kPlanThreads)
 compact_plan_kernel(const Paged c, const PagedCompact m) {
-  __shared__ PlanShared sh;
+  __shared__ PlanShared<kPlanThreads> sh;
   pdl_wait_then_release();
   const uint32_t* bits = paged_bits(c);
   const int words = paged_words(c.pages), tid = threadIdx.x, lane = tid & 31, U = c.pages - c.state[0];
-  const int w0 = blockIdx.x * kPlanThreads;
+  const int w0 = blockIdx.x * kCompactWords, n = min(kCompactWords, words - w0);
   int before = 0, below = 0, all, holes;
   // free pages before this CTA's words, and below page U
   const int up = max(w0, (U >> 5) + 1);
@@ -527,15 +683,15 @@ compact_plan_kernel(const Paged c, const PagedCompact m) {
     if (w < U >> 5) below += __popc(x);
     else if (w == U >> 5) below += __popc(x & ((1u << (U & 31)) - 1u));
   }
-  plan_scan(before, sh.tmp, all);
+  plan_scan<kPlanThreads>(before, sh.tmp, all);
   before = all;
-  plan_scan(below, sh.tmp, holes);
+  plan_scan<kPlanThreads>(below, sh.tmp, holes);
   if (blockIdx.x == 0 && tid == 0) *m.count = holes;
-  const uint32_t word = w0 + tid < words ? bits[w0 + tid] : 0u;
+  const uint32_t word = tid < n ? bits[w0 + tid] : 0u;
   sh.word[tid] = word;
-  sh.base[tid] = before + plan_scan(__popc(word), sh.tmp, all);
+  sh.base[tid] = before + plan_scan<kPlanThreads>(__popc(word), sh.tmp, all);
   __syncthreads();
-  for (int i = tid >> 5; i < kPlanThreads && w0 + i < words; i += kPlanThreads / 32) {
+  for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
     const int p = (w0 + i) * 32 + lane;
     if (p >= c.pages) continue;
     const int f = sh.base[i] + __popc(sh.word[i] & ((1u << lane) - 1u));  // free pages below p
@@ -551,31 +707,31 @@ compact_plan_kernel(const Paged c, const PagedCompact m) {
   }
 }
 
-constexpr int kMoveThreads = 256, kMoveUnroll = 8;
+constexpr int kMoveThreads = 256, kMoveUnroll = 4;
 
-// Copies the movers (units of a part of one page's K or V), then renames pages in the table and
-// writes the bits anew.
+// Copies the movers (a warp: 2 KB of a page's K and of its V, all loads in flight), then renames pages
+// in the table and writes the bits anew.
 __global__ void __launch_bounds__(kMoveThreads)
 compact_move_kernel(const Paged c, const PagedCompact m, int64_t page_vecs, int64_t meta_vecs, int B, int Cap, int pshift) {
   constexpr int NT = kMoveThreads, U = kMoveUnroll;
   pdl_wait_then_release();
-  const int count = *m.count, used = c.pages - c.state[0];
-  const int parts = (int)((page_vecs + NT * U - 1) / (NT * U));
-  const int64_t units = (int64_t)count * parts * 2;
-  for (int64_t x = blockIdx.x; x < units; x += gridDim.x) {
-    const int i = (int)(x / (2 * parts)), part = (int)(x % (2 * parts)) >> 1;
-    const int from = m.movers[i], to = m.holes[i];
-    uint4* pool = static_cast<uint4*>(x & 1 ? c.v : c.k);
-    const uint4* src = pool + from * page_vecs;
-    uint4* dst = pool + to * page_vecs;
-    const int64_t at = (int64_t)part * NT * U + threadIdx.x;
-    uint4 v[U];
+  const int count = *m.count, used = c.pages - c.state[0], lane = threadIdx.x & 31;
+  const int parts = (int)(page_vecs / (32 * U));  // a page is whole units: 16 tokens of 64 channels in 2 bytes are one
+  const int64_t units = (int64_t)count * parts, warps = (int64_t)gridDim.x * (NT / 32);
+  for (int64_t x = (int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5); x < units; x += warps) {
+    const int i = (int)(x / parts), at = (int)(x % parts) * 32 * U + lane;
+    const int64_t from = m.movers[i] * page_vecs + at, to = m.holes[i] * page_vecs + at;
+    uint4 k[U], v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at + u * NT < page_vecs) v[u] = ldg_stream(src + at + u * NT);
+    for (int u = 0; u < U; ++u) {
+      k[u] = ldg_stream(static_cast<const uint4*>(c.k) + from + 32 * u);
+      v[u] = ldg_stream(static_cast<const uint4*>(c.v) + from + 32 * u);
+    }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (at + u * NT < page_vecs) dst[at + u * NT] = v[u];
+    for (int u = 0; u < U; ++u) {
+      static_cast<uint4*>(c.k)[to + 32 * u] = k[u];
+      static_cast<uint4*>(c.v)[to + 32 * u] = v[u];
+    }
   }
   const int64_t tid = (int64_t)blockIdx.x * NT + threadIdx.x, all = (int64_t)gridDim.x * NT;
   if (meta_vecs)
@@ -619,10 +775,10 @@ cudaError_t launch_paged_compact(const Shape& s, const Paged& c, int32_t* moved,
   m.moved = moved;
   const int size = s.dtype == 0 ? 4 : 2;
   const int64_t page_vecs = (int64_t)s.Hkv * s.P * s.D * size / 16, meta_vecs = c.kmin ? (int64_t)s.Hkv * s.D * size / 16 : 0;
-  const int ctas = (paged_words(c.pages) + kPlanThreads - 1) / kPlanThreads;
+  const int ctas = (paged_words(c.pages) + kCompactWords - 1) / kCompactWords;
   cudaError_t e = launch_pdl(compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, c, m);
   if (e == cudaSuccess)
-    e = launch_pdl(compact_move_kernel, dim3(sm_count() * 4), dim3(kMoveThreads), 0, st, c, m, page_vecs, meta_vecs, s.B,
+    e = launch_pdl(compact_move_kernel, dim3(sm_count() * 8), dim3(kMoveThreads), 0, st, c, m, page_vecs, meta_vecs, s.B,
                    s.Cap, s.pshift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

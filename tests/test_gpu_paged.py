@@ -233,6 +233,28 @@ def test_random_runs_of_all_calls(batch, hkv, d, page, dtype):
             pair.attend()
 
 
+@pytest.mark.parametrize("batch,cap", [(5, 16 * 60000), (300, 16 * 1000), (1100, 64)])
+def test_many_sequences_and_wide_tables(batch, cap):
+    """Single tokens and forks of more sequences, and of wider tables, than one launch takes."""
+    pair = Pair(batch, 1, 1, 64, 16, cap, 3 * batch + 40)
+    rng = pair.rng
+    for step in range(3):
+        pair.append([int(n) for n in rng.integers(0, 2, batch)])
+        pair.append([int(n) for n in rng.integers(0, 20, batch)])
+        kv = pair.new((batch, 1, 1, 64))
+        ops.paged_append(pair.desc, pair.cache, kv.cuda(), kv.cuda())
+        pair.plain.append(kv, kv, [1] * batch)
+        pair.check()
+        pair.fork([b if rng.random() < 0.5 else int(rng.integers(-1, batch)) for b in range(batch)],
+                  [int(n) for n in rng.integers(0, 40, batch)])
+        pair.check()
+    for _ in range(4):  # some of them for want of pages
+        pair.fork([int(rng.integers(0, batch)) for _ in range(batch)], [31] * batch)
+        pair.check()
+        pair.append([int(n) for n in rng.integers(0, 60, batch)])
+        pair.check()
+
+
 @pytest.mark.parametrize("pool,cap", [(31, 128), (32, 128), (33, 128), (1000, 2048), (40000, 65536)])
 def test_compact_pools_of_many_sizes(pool, cap):
     pair = Pair(12, 1, 1, 64, 16, cap, pool, summaries=pool < 2000)
