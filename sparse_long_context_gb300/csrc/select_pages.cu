@@ -18,6 +18,10 @@
 //         chosen pages are written in ascending order.  Ties on T go to the
 //         lowest page indices.
 
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 #include "mma.cuh"
@@ -206,13 +210,12 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
 // Tensor-core scorer (bf16): 16 pages per warp step.  Lane (r, m) loads
 // rows r and r+8 of the 16-page tile, chunks 4s+m of kmax and kmin (or of the
 // key itself when a page is one token); the group's heads are the 8 columns.
-template <int D, bool SINGLE, int NT, bool STAGE, bool PAGED>
+template <int D, bool SINGLE, int NT, bool STAGE, bool PAGED, int UT = SINGLE ? 4 : 2>
 __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, int b, int h, int p0,
                                                 int nloc, int first_local, uint32_t* keys,
                                                 uint32_t* skeys, KeyRange& kr) {
   constexpr int NS = D / 32;
   constexpr int NW = NT / 32;
-  constexpr int UT = SINGLE ? 4 : 2;  // tiles in flight per warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = lane >> 2, m = lane & 3;
   const int G = a.G;
@@ -1066,6 +1069,136 @@ topk_reg_kernel(const SelectArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- paged, one launch
+
+// Scores and top k of a row by one cluster: the CTAs score equal shares of its pages and leave the keys in
+// the first one's shared memory, which ranks them: histograms over the range of the keys that are not forced until the
+// k-th one's bin holds few, then exactly.  The same keys, order and ties as the two launches.
+constexpr int kFusedCluster = 8, kFusedKeep = 16;  // CTAs of a row, and keys a thread holds, at most
+constexpr int kFusedRank = 96;                     // keys ranked exactly
+template <int MODE> constexpr int kFusedThreads = MODE == 0 ? kSelThreads : 512;
+
+struct FusedShared {
+  uint32_t hist[2048];
+  uint32_t bin[kFusedRank];
+  RankShared rank;
+  uint32_t lo[32], hi[32], T;
+  int scan_tmp[32], nf[32], n, take;
+};
+
+template <typename T, int D, int GM, int MODE>
+__global__ void __launch_bounds__(kFusedThreads<MODE>)
+paged_select_kernel(const SelectArgs a, int cluster) {
+  namespace cg = cooperative_groups;
+  constexpr int NT = kFusedThreads<MODE>, NW = NT / 32;
+  extern __shared__ __align__(16) uint32_t skeys[];  // [npcap, a multiple of 4]
+  __shared__ FusedShared sh;
+  cg::cluster_group cl = cg::this_cluster();
+  pdl_wait_then_release();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.x / cluster, split = blockIdx.x % cluster;
+  const int b = row / a.Hkv, h = row % a.Hkv, k = a.k;
+  const int N = clamp_len(a.ctx_len[b], a.Cap), NP = (N + a.P - 1) >> a.pshift;
+  int32_t* out = a.page_idx + (size_t)row * k;
+  if (NP <= k) {  // every page
+    for (int i = split * NT + tid; i < k; i += cluster * NT) out[i] = i < NP ? i : -1;
+    return;
+  }
+  if (cluster > 1) cl.sync();  // the first CTA runs before the others write to it
+  const int chunk = ((NP + cluster - 1) / cluster + 15) & ~15;
+  const int p0 = split * chunk, nloc = max(0, min(chunk, NP - p0));
+  const int first_local = a.n_local > 0 ? (max(N - a.n_local, 0) >> a.pshift) : NP;
+  uint32_t* keys = (cluster > 1 ? cl.map_shared_rank(skeys, 0) : skeys) + p0;
+  KeyRange kr;
+  if (nloc > 0) {
+    if constexpr (MODE == 0) score_chunk<T, D, GM, false, true>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr);
+    else score_chunk_mma<D, false, NT, false, true, 1>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr);
+  }
+  if (cluster > 1) cl.sync();
+  else __syncthreads();
+  if (split) return;
+
+  // the thread's keys: pages [i0, i0 + per), per a multiple of 4 (0: none)
+  const int per = (((NP + NT - 1) / NT) + 3) & ~3, i0 = tid * per;
+  uint32_t kk[kFusedKeep];
+#pragma unroll
+  for (int j = 0; j < kFusedKeep; j += 4) {
+    const uint4 v = j < per && i0 + j < NP ? *reinterpret_cast<const uint4*>(skeys + i0 + j) : make_uint4(0u, 0u, 0u, 0u);
+    kk[j] = v.x; kk[j + 1] = v.y; kk[j + 2] = v.z; kk[j + 3] = v.w;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (j + u >= per || i0 + j + u >= NP) kk[j + u] = 0u;  // below every key
+      else kr.add(kk[j + u]);
+    }
+  }
+  uint32_t lo = __reduce_min_sync(0xffffffffu, kr.bot), hi = __reduce_max_sync(0xffffffffu, kr.top);
+  int nf = __reduce_add_sync(0xffffffffu, kr.nf);
+  if (lane == 0) {
+    sh.lo[warp] = lo;
+    sh.hi[warp] = hi;
+    sh.nf[warp] = nf;
+  }
+  if (tid == 0) sh.n = 0;
+  __syncthreads();
+  nf = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    lo = min(lo, sh.lo[w]);
+    hi = max(hi, sh.hi[w]);
+    nf += sh.nf[w];
+  }
+  // T, the k-th largest key, and how many of those equal to it are taken
+  uint32_t Tk = kForcedKey;
+  int take = k;
+  if (k > nf) {  // k - nf of the others, of which there are more
+    take = k - nf;
+    narrow_to_rank<NT, 2048>(skeys, NP, lo, hi, take, kFusedRank, sh.hist, sh.rank);
+    if (lo == hi) {
+      Tk = lo;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kFusedKeep; ++j)
+        if (kk[j] >= lo && kk[j] <= hi && kk[j] != kForcedKey) sh.bin[atomicAdd(&sh.n, 1)] = kk[j];
+      __syncthreads();
+      const int n = sh.n;  // at most kFusedRank
+      if (tid < n) {
+        const uint32_t v = sh.bin[tid];
+        int gt = 0, ge = 0;
+        for (int i = 0; i < n; ++i) {
+          gt += sh.bin[i] > v;
+          ge += sh.bin[i] >= v;
+        }
+        if (gt < take && ge >= take) {
+          sh.T = v;
+          sh.take = take - gt;
+        }
+      }
+      __syncthreads();
+      Tk = sh.T;
+      take = sh.take;
+    }
+  }
+  // positions: the keys above T, and the first `take` of those equal to it, in order
+  int gt = 0, eq = 0;
+#pragma unroll
+  for (int j = 0; j < kFusedKeep; ++j) {
+    gt += kk[j] > Tk;
+    eq += kk[j] == Tk;
+  }
+  int all;  // both counts stay below 2^15
+  const int e = block_excl_scan<NT>((gt << 16) | eq, sh.scan_tmp, all);
+  gt = e >> 16;
+  eq = e & 0xffff;
+#pragma unroll
+  for (int j = 0; j < kFusedKeep; ++j) {
+    if (kk[j] > Tk) {
+      out[gt++ + min(eq, take)] = i0 + j;
+    } else if (kk[j] == Tk) {
+      if (eq < take) out[gt + eq] = i0 + j;
+      ++eq;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- launches
 
 // Pages per scoring CTA: one wave of scoring CTAs over all rows.
@@ -1200,8 +1333,38 @@ cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
   return select_launch(s, q, kmin, kmax, ctx_len, k, n_sink_pages, n_local_tokens, page_idx, ws, nullptr, 0, st);
 }
 
+template <typename T, int D, int GM, int MODE>
+static cudaError_t fused_launch(const SelectArgs& a, int rows, int cluster, cudaStream_t st) {
+  const size_t smem = (size_t)((a.npcap + 15) & ~15) * sizeof(uint32_t);
+  return launch_pdl_cluster(paged_select_kernel<T, D, GM, MODE>, dim3(rows * cluster), dim3(kFusedThreads<MODE>), smem, cluster, st,
+                            a, cluster);
+}
+template <typename T, int D>
+static cudaError_t fused_g(const SelectArgs& a, int rows, int cluster, cudaStream_t st) {
+  if (a.G <= 1) return fused_launch<T, D, 1, 0>(a, rows, cluster, st);
+  if (a.G <= 2) return fused_launch<T, D, 2, 0>(a, rows, cluster, st);
+  if (a.G <= 4) return fused_launch<T, D, 4, 0>(a, rows, cluster, st);
+  return fused_launch<T, D, 8, 0>(a, rows, cluster, st);
+}
+
 cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, int k, int n_sink_pages, int n_local_tokens,
                                 int32_t* page_idx, void* ws, cudaStream_t st) {
+  const int rows = s.B * s.Hkv, npcap = s.Cap >> s.pshift;
+  const int cluster = std::min(std::max(sm_count() / rows, 1), kFusedCluster);
+  const int most = kFusedKeep * (s.dtype == 1 ? kFusedThreads<1> : kFusedThreads<0>);  // keys of a row
+  if (!(s.flags & 1) && rows <= sm_count() && npcap <= most) {
+    SelectArgs a = {};
+    a.q = q; a.kmin = c.kmin; a.kmax = c.kmax; a.ctx_len = c.ctx; a.page_idx = page_idx;
+    a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
+    a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift; a.npcap = npcap;
+    a.table = c.table; a.pool = c.pages;
+    cudaError_t e;
+    if (s.dtype == 1)
+      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1>(a, rows, cluster, st) : fused_launch<bf16, 128, 8, 1>(a, rows, cluster, st);
+    else
+      e = s.D == 64 ? fused_g<float, 64>(a, rows, cluster, st) : fused_g<float, 128>(a, rows, cluster, st);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
   return select_launch(s, q, c.kmin, c.kmax, c.ctx, k, n_sink_pages, n_local_tokens, page_idx, ws, c.table, c.pages, st);
 }
 

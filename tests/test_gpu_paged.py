@@ -396,6 +396,37 @@ def test_select_finds_what_the_row_selection_finds(dtype, d, page, k):
     pair.attend(q, got.tolist())
 
 
+@pytest.mark.parametrize("batch,hkv,cap,dtype", [(1, 1, 2048, BF16), (2, 3, 16 * 700, BF16), (40, 2, 16 * 130, BF16), (77, 1, 1024, F32),
+                                                 (90, 2, 1024, BF16), (3, 1, 16 * 2500, F32)])
+def test_select_clusters_ties_and_few_pages(batch, hkv, cap, dtype):
+    """One CTA or several a row, or two launches; scores that are equal; rows of no more pages than the budget."""
+    pair = Pair(batch, hkv * 2, hkv, 64, 16, cap, min(batch * cap // 16, 6000), dtype)
+    lens = [int(n) for n in pair.rng.integers(1, min(cap, 6000 // batch * 16), batch)]
+    lens[0], lens[-1] = 17, lens[-1]
+    pair.append(lens)
+    q = torch.round(pair.new((batch, hkv * 2, 64)) * 2) / 2
+    # summaries of few values: many equal scores
+    pair.cache.kmin.copy_(torch.round(pair.new(pair.cache.kmin.shape)).clamp(-1, 0))
+    pair.cache.kmax.copy_(torch.round(pair.new(pair.cache.kmin.shape)).clamp(0, 1))
+    at = pair.cache.table.clamp(min=0).long()
+    rows = lambda x: x[at].transpose(1, 2).contiguous()  # noqa: E731
+    lo, hi = rows(pair.cache.kmin), rows(pair.cache.kmax)
+    x = torch.einsum("bhgd,bhpd->bhgp", q.cuda().view(batch, hkv, 2, 64).double().clamp(min=0), hi.double()) + torch.einsum(
+        "bhgd,bhpd->bhgp", q.cuda().view(batch, hkv, 2, 64).double().clamp(max=0), lo.double())
+    x = x.amax(2).cpu()
+    for k, first, last in ((1, 0, 0), (5, 1, 16), (33, 0, 40), (64, 3, 100)):
+        got = ops.paged_select_pages(pair.desc, pair.cache, q.cuda(), k, first, last)
+        assert torch.equal(got, ops.select_pages(pair.desc, q.cuda(), lo, hi, pair.cache.ctx_len, k, first, last))
+        got = got.view(batch, hkv, k).tolist()
+        for b in range(batch):
+            n = -(-lens[b] // 16)
+            for j in range(hkv):
+                must = {p for p in range(n) if p < first or (last and p >= max(lens[b] - last, 0) // 16)}
+                others = sorted((p for p in range(n) if p not in must), key=lambda p: (-float(x[b, j, p]), p))
+                want = sorted([*must, *others[:max(k - len(must), 0)]])
+                assert got[b][j] == want + [-1] * (k - len(want)), (b, j)
+
+
 def test_select_of_rows_wider_than_one_cta():
     cap = 16 * 9000
     pair = Pair(1, 2, 1, 64, 16, cap, 9000, summaries=True)
