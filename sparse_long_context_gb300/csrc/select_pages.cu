@@ -59,10 +59,9 @@ struct SelectArgs {
   int pool;
 };
 
-// Where the summary of logical page p of sequence b, head h lies in the pool; false for a table
+// Where the summary of the page that a table entry gives lies in the pool, for head h; false for an
 // entry that is no page of it (such pages score as zeros and are counted).
-__device__ __forceinline__ bool pool_summary(const SelectArgs& a, int b, int h, int p, size_t& at) {
-  const int page = __ldg(a.table + (size_t)b * a.npcap + p);
+__device__ __forceinline__ bool pool_summary(const SelectArgs& a, int page, int h, size_t& at) {
   at = (size_t)page * a.Hkv + h;
   return (unsigned)page < (unsigned)a.pool;
 }
@@ -111,12 +110,13 @@ struct KeyRange {
   }
 };
 
-// Scores of pages [p0, p0 + nloc) of one row into keys[0 .. nloc).
+// Scores of pages [p0, p0 + nloc) of one row into keys[0 .. nloc).  PAGED: tab holds their table
+// entries (keys' own memory, where they are in shared memory: a page's key comes after its entry's last use).
 // A page's D channels are spread over L lanes as 16-byte vectors.
 template <typename T, int D, int GM, bool STAGE, bool PAGED>
 __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b, int h, int p0,
                                             int nloc, int first_local, uint32_t* keys, uint32_t* skeys,
-                                            KeyRange& kr) {
+                                            KeyRange& kr, const int32_t* tab = nullptr) {
   constexpr int EPL = Vec16<T>::N;
   constexpr int L = D / EPL;
   constexpr int TPW = 32 / L;
@@ -158,7 +158,7 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
       size_t off = (size_t)pi[u] * D;
       if constexpr (PAGED) {
         const bool in = ok;
-        if (in) ok = pool_summary(a, b, h, p0 + pi[u], off);
+        if (in) ok = pool_summary(a, tab[pi[u]], h, off);
         if (in && !ok && sub == 0) note_bad_pages(1);
         off *= D;
       }
@@ -213,7 +213,7 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
 template <int D, bool SINGLE, int NT, bool STAGE, bool PAGED, int UT = SINGLE ? 4 : 2>
 __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, int b, int h, int p0,
                                                 int nloc, int first_local, uint32_t* keys,
-                                                uint32_t* skeys, KeyRange& kr) {
+                                                uint32_t* skeys, KeyRange& kr, const int32_t* tab = nullptr) {
   constexpr int NS = D / 32;
   constexpr int NW = NT / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -252,7 +252,7 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
         size_t at = (size_t)p;
         if constexpr (PAGED) {
           const bool in = ok;
-          if (in) ok = pool_summary(a, b, h, p0 + p, at);
+          if (in) ok = pool_summary(a, tab[p], h, at);
           if (in && !ok && m == 0) note_bad_pages(1);
         }
 #pragma unroll
@@ -647,10 +647,11 @@ quest_score_kernel(const SelectArgs a) {
   extern __shared__ uint32_t stage[];
   uint32_t* skeys = (CAND && a.chunk <= kCandStage) ? stage : nullptr;
   KeyRange kr;
+  const int32_t* tab = PAGED ? a.table + (size_t)b * a.npcap + p0 : nullptr;
   if constexpr (MODE == 0) {
-    score_chunk<T, D, GM, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
+    score_chunk<T, D, GM, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr, tab);
   } else {
-    score_chunk_mma<D, MODE == 2, NT, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr);
+    score_chunk_mma<D, MODE == 2, NT, CAND, PAGED>(a, row, b, h, p0, nloc, first_local, keys, skeys, kr, tab);
   }
   if constexpr (CAND) {
     __shared__ CandShared csh;
@@ -1103,15 +1104,19 @@ paged_select_kernel(const SelectArgs a, int cluster) {
     for (int i = split * NT + tid; i < k; i += cluster * NT) out[i] = i < NP ? i : -1;
     return;
   }
-  if (cluster > 1) cl.sync();  // the first CTA runs before the others write to it
   const int chunk = ((NP + cluster - 1) / cluster + 15) & ~15;
   const int p0 = split * chunk, nloc = max(0, min(chunk, NP - p0));
   const int first_local = a.n_local > 0 ? (max(N - a.n_local, 0) >> a.pshift) : NP;
   uint32_t* keys = (cluster > 1 ? cl.map_shared_rank(skeys, 0) : skeys) + p0;
   KeyRange kr;
+  // the share's table entries, where the first CTA's keys will be
+  int32_t* tab = reinterpret_cast<int32_t*>(skeys) + p0;
+  for (int i = tid; i < nloc; i += NT) tab[i] = __ldg(a.table + (size_t)b * a.npcap + p0 + i);
+  if (cluster > 1) cl.sync();  // the first CTA runs before the others write to it
+  else __syncthreads();
   if (nloc > 0) {
-    if constexpr (MODE == 0) score_chunk<T, D, GM, false, true>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr);
-    else score_chunk_mma<D, false, NT, false, true, 1>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr);
+    if constexpr (MODE == 0) score_chunk<T, D, GM, false, true>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr, tab);
+    else score_chunk_mma<D, false, NT, false, true, 1>(a, row, b, h, p0, nloc, first_local, keys, nullptr, kr, tab);
   }
   if (cluster > 1) cl.sync();
   else __syncthreads();
