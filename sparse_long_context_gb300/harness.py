@@ -151,7 +151,7 @@ class Kv8DecodeLoop:
     def __init__(self, step: ops.Kv8Decode, sink=None):
         d = step.desc
         self.step, self.sink = step, sink
-        self.qkv = torch.zeros((d.batch, d.num_q_heads + 2 * d.num_kv_heads, d.head_dim), dtype=torch.bfloat16,
+        self.qkv = torch.zeros((d.batch, d.num_q_heads + 2 * d.num_kv_heads, d.head_dim), dtype=step.q.dtype,
                                device=step.q.device)
         self.graph = None
 
@@ -171,3 +171,11 @@ class Kv8DecodeLoop:
     def replay(self):
         self.graph.replay()
         return self.out, self.lse
+
+
+class PagedDecodeLoop(Kv8DecodeLoop):
+    """The same loop over a paged cache (ops.PagedDecode): a replay also takes the pages that its tokens need from the
+    pool, and forks and compactions between replays need no new capture."""
+
+    def __init__(self, step: ops.PagedDecode, sink=None):
+        super().__init__(step, sink)

@@ -911,3 +911,89 @@ class Kv8Decode:
         kept = kv8_evict(self.desc, self.cache, self.ctx_len, self.mass, keep, n_sink_blocks, n_recent_blocks)[1]
         self.evicted += held - self.ctx_len  # after the call: one that is refused moves no position
         return kept
+
+
+class PagedDecode:
+    """One decode step over a paged cache from the projected heads on: norm and rotation of q and k (qk_norm_rope),
+    append of the token on pages of the pool (paged_append), and the attention, dense or, with k_budget > 0, over the
+    k_budget pages per KV head that Quest selection picks (paged_select_pages).  The buffers are preallocated, so a step
+    can be captured in a CUDA graph.
+
+    A sequence at capacity, or for whose token the pool has no page left, is left unchanged: pos[b] is then -1, and its
+    query attends to what is held.  The same holds for a piece of a prompt."""
+
+    def __init__(self, desc: L.AttnDesc, rope: L.RopeDesc, num_pages: int, k_budget: int = 0, n_sink_pages: int = 0,
+                 n_local_tokens: int = 0, device="cuda", q_weight=None, k_weight=None):
+        if (rope.num_q_heads, rope.num_kv_heads, rope.head_dim, rope.dtype) != (
+                desc.num_q_heads, desc.num_kv_heads, desc.head_dim, desc.dtype):
+            raise ValueError("rope and desc must describe the same heads")
+        if desc.flags & ~L.SLS_FLAG_TEST_WAIT_TIMEOUT:
+            raise ValueError("the paged attend has one kernel: no path flags")
+        if k_budget:  # what the first step would refuse only after it has appended its token
+            forced = n_sink_pages + (-(-n_local_tokens // desc.page_size) + 1 if n_local_tokens > 0 else 0)
+            if min(n_sink_pages, n_local_tokens) < 0 or not max(1, forced) <= k_budget <= desc.capacity // desc.page_size:
+                raise ValueError(f"k_budget {k_budget} must hold the forced pages (up to {forced}) and be at most the "
+                                 f"{desc.capacity // desc.page_size} pages of a sequence")
+        if not L.load().sls_paged_decode_attend_workspace_size(ctypes.byref(desc)):
+            raise ValueError("the paged attend does not take this descriptor")
+        B, Hq, H, D = desc.batch, desc.num_q_heads, desc.num_kv_heads, desc.head_dim
+        dt = torch.bfloat16 if desc.dtype == L.SLS_DTYPE_BF16 else torch.float32
+        self.desc, self.rope = desc, rope
+        self.k, self.n_sink, self.n_local = int(k_budget), int(n_sink_pages), int(n_local_tokens)
+        self.q_weight, self.k_weight = q_weight, k_weight
+        self.cache = PagedCache.empty(desc, num_pages, summaries=self.k > 0, device=device)
+        new = lambda shape, dtype=dt: torch.zeros(shape, dtype=dtype, device=device)  # noqa: E731
+        self.q, self.k_new = new((B, Hq, D)), new((B, H, D))
+        self.out, self.lse = new((B, Hq, D)), new((B, Hq), torch.float32)
+        self.pos = new(B, torch.int32)  # positions written by the last step or piece of a prompt
+        self.done = new(1, torch.int32)
+        self.page_idx = self.select_workspace = None
+        if self.k:
+            self.page_idx = new((B * H, self.k), torch.int32)
+            self.select_workspace = paged_select_workspace(desc, self.cache)
+        self.workspace = paged_attend_workspace(desc, self.cache)
+        self.fork_workspace = paged_fork_workspace(desc, self.cache)
+        self.compact_workspace = paged_compact_workspace(desc, self.cache)
+
+    @property
+    def ctx_len(self):
+        """Tokens held by each sequence [B] int32 (the cache's own)."""
+        return self.cache.ctx_len
+
+    def prefill(self, qkv, new_len=None):
+        """Writes the keys and values of a prompt (or of its next piece): qkv [B, T, Hq + 2 Hkv, D], of which
+        sequence b has its first new_len[b] tokens.  Returns the rotated queries [B, T, Hq, D]."""
+        Hq, H, D = self.desc.num_q_heads, self.desc.num_kv_heads, self.desc.head_dim
+        B, T = qkv.shape[:2]
+        step = torch.arange(T, dtype=torch.int32, device=qkv.device)
+        pos = self.ctx_len[:, None] + step
+        if new_len is not None:
+            pos = torch.where(step < new_len[:, None], pos, -1)  # padding is skipped
+        flat = qkv[:, :, :Hq + H].reshape(B * T, Hq + H, D)  # a view, or a copy where qkv is a slice of a longer batch
+        q, k = qk_norm_rope(self.rope, flat[:, :Hq], flat[:, Hq:], pos.reshape(-1), self.q_weight, self.k_weight)
+        paged_append(self.desc, self.cache, k.view(B, T, H, D), qkv[:, :, Hq + H:], new_len=new_len, pos_out=self.pos)
+        return q.view(B, T, Hq, D)
+
+    def __call__(self, qkv, sink=None):
+        """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
+        d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
+        if sink is not None:
+            _need(sink, "sink", torch.float32, (Hq,))  # before the token is appended
+        qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.ctx_len, self.q_weight, self.k_weight, q_out=self.q,
+                     k_out=self.k_new)
+        paged_append(d, self.cache, self.k_new[:, None], qkv[:, None, Hq + H:], pos_out=self.pos)
+        if self.k:
+            paged_select_pages(d, self.cache, self.q, self.k, self.n_sink, self.n_local, out=self.page_idx,
+                               workspace=self.select_workspace)
+        return paged_decode_attend(d, self.cache, self.q, page_idx=self.page_idx, sink=sink, out=self.out, lse=self.lse,
+                                   workspace=self.workspace)
+
+    def fork(self, parent, keep_len=None):
+        """Forks, reorders, cuts and frees sequences (paged_fork).  Returns done [1]: 1, or 0 when the pool lacked pages
+        and nothing has changed."""
+        paged_fork(self.desc, self.cache, parent, keep_len=keep_len, done=self.done, workspace=self.fork_workspace)
+        return self.done
+
+    def compact(self):
+        """Moves the used pages to the front of the pool (paged_compact)."""
+        paged_compact(self.desc, self.cache, workspace=self.compact_workspace)
