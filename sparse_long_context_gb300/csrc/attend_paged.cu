@@ -11,6 +11,15 @@
 // A unit is streamed by one warp through its own ring of shared-memory stages (tensor-map boxes of
 // 16 rows, whose row numbers come from the table), so a late copy holds up one warp only.
 // Scores, statistics and sums are fp32.
+//
+// Bound by memory on long contexts, wherever their pages lie: 32 contexts of 49k to 64k tokens, 2 KV
+// heads of 6 query heads and 128 channels in bf16, 279 to 282 us for 1884 MB (6.7 TB/s, the measured copy rate).
+// Twelve warps of two stages fill the shared memory: 8 of three take 285 us, 6 of four 291, 6 of two
+// with 32 tokens each 282.  In fp32 instructions come next: seven contexts of 1 to 20000 tokens, 8 heads of 8 query heads and
+// 64 channels 52 us for 268 MB (floor 40).  Short rows are a chain of latencies (lengths, table, copies,
+// merge): 5.2 us for 1000 tokens of 4 heads, 16.8 for 64 lists of 128 pages (floor 10); in ranges the
+// prologue takes 3 us and the merge through global memory 3.7, so that 64 uneven rows of up to 4k tokens take 18 us with
+// two CTAs a row (floor 10) and 21.5 in ranges.  (Times of the device alone, calls replayed from a graph.)
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -34,7 +43,9 @@ constexpr int kPgMaxRows = 4096;   // rows whose first units are kept there
 // where another one's counters are.
 constexpr size_t kPgTicketBytes = kPgMaxRows * sizeof(int32_t);
 constexpr int kPgMinUnits = 4;     // least units of a CTA in ranges: a shorter job uses fewer CTAs
-constexpr int kPgSegCost = 1024;   // work of a row change (drain, merge, partial and refill) in tokens
+// Work of a row change (drain, merge, partial and refill) in tokens: 512, 1024 and 2048 took 53.3,
+// 53.0 and 56.6 us on the uneven fp32 rows above.
+constexpr int kPgSegCost = 1024;
 
 struct PagedAttend {
   const void* q;
@@ -219,7 +230,8 @@ __device__ __forceinline__ void pg_lds(uint32_t at, PgF2& a) {
 // fp32 on the CUDA cores, no operand rounded.  Scores: lane (tg, sl) takes channel chunks sl, sl + 8, ... of tokens
 // 4 j + tg, with the heads' queries in registers; the eight lanes of a token add up so that lane sl ends with head
 // sl.  The weights go to shared memory twice each (over the unit's keys, which are done with), as the pairs that the
-// value product multiplies a lane's D / 32 channels by.  GM: heads that are worked on (4 or 8; a check of each
+// value product multiplies a lane's D / 32 channels by.  12 warps at D = 64: 11, 10 and 8 (three stages) took 55, 60
+// and 56 us for 53.  GM: heads that are worked on (4 or 8; a check of each
 // against G would cost as many instructions as its products).
 template <int D_, int GM>
 struct PgF32 {

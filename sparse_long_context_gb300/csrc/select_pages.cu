@@ -1075,6 +1075,10 @@ topk_reg_kernel(const SelectArgs a) {
 // Scores and top k of a row by one cluster: the CTAs score equal shares of its pages and leave the keys in
 // the first one's shared memory, which ranks them: histograms over the range of the keys that are not forced until the
 // k-th one's bin holds few, then exactly.  The same keys, order and ties as the two launches.
+// 64 rows of 4096 pages: 27.4 us for 129 MB (the two launches 29.3; floor 19.3), of which the ranking takes 3.6;
+// three fp32 rows of 243 pages 7.7 (8.6).  Measured against: two tiles in flight a warp (31 us), 256 threads (32), two
+// CTAs an SM (30), the CTAs' histograms added up instead of the keys collected (30.5; 73 on the short
+// rows).  The pages' order in the pool makes no difference.
 constexpr int kFusedCluster = 8, kFusedKeep = 16;  // CTAs of a row, and keys a thread holds, at most
 constexpr int kFusedRank = 96;                     // keys ranked exactly
 template <int MODE> constexpr int kFusedThreads = MODE == 0 ? kSelThreads : 512;
