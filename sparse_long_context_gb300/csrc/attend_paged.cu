@@ -929,26 +929,26 @@ static int pg_clusters(int c, PgDevice* d) {
 
 // CTAs per row of the cluster kernel, or 0 for ranges over all rows, by their costs.  A
 // CTA takes Tile::NS ns a token and a cluster 5.3 us besides, in as many waves as the clusters need; the
-// ranges take 13 us and 23 / rows for rows that many CTAs share; both read at the memory's rate at
-// most (near it a cluster's two bounds add up as their cubes' root).
+// ranges take 12 us, 3 per row of a CTA, and 23 / rows for rows that many CTAs share; both read at the
+// memory's rate at most (near it a cluster's two bounds add up as their cubes' root).
 // `most` bounds a row's tokens; where only the device knows them, rows are taken to hold four fifths
-// of it on average and a cluster to wait for one that is full.  Measured on 70 shapes of 1 to 256
+// of it on average and a cluster to wait for one that is full.  Measured on 260 shapes of 1 to 256
 // rows, full and with lengths spread evenly from none: 16.9 us with two CTAs a row and 20 in ranges
 // for 64 lists of 2048 tokens, 25.7 and 32.1 for 64 full rows of 4k, 188 and 167 for 64 uneven ones of
-// up to 64k.  Where it takes the slower side it mostly loses less than 15%, 25% at most (64 full rows of 4k in fp32:
-// 36.5 us, 29.3 with two CTAs a row).
+// up to 64k.  Fifteen in sixteen shapes take within 8% of the faster side, the others lose up to a third (32 full fp32
+// rows of 4k at D = 128: 39 us, 30 with four CTAs a row).
 template <typename Tile, bool LIST>
 static int pg_pick(int rows, double most, bool fixed, bool even, PgDevice* d) {
   const double t = Tile::NS * 1e-3, sms = sm_count();
   const double mean = fixed ? most : 0.8 * most, longest = even ? mean : most;
   const double memory = rows * 2.0 * Tile::D * sizeof(typename Tile::T) / 6.7e6;  // us a token of every row
-  double best = 13.0 + mean * std::max(memory, rows / sms * t) + 23.0 / rows;
+  double best = 12.0 + 3.0 * rows / sms + mean * std::max(memory, rows / sms * t) + 23.0 / rows;
   int pick = 0;
   for (int c = 1; c <= kPgMaxCluster; ++c) {
     const int n = c == 1 ? sm_count() : pg_clusters<Tile, LIST>(c, d);
     if (n < 1) continue;
     const int waves = (rows + n - 1) / n;
-    const double us = waves * 5.3 + longest * std::cbrt(std::pow(waves * t / c, 3.0) + std::pow(memory, 3.0));
+    const double us = waves * 5.3 + std::cbrt(std::pow(waves * longest * t / c, 3.0) + std::pow(mean * memory, 3.0));
     if (us < best) {
       best = us;
       pick = c;

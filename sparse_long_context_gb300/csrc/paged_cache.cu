@@ -10,8 +10,8 @@
 // Appends and compactions move bytes, at the memory's rate on large ones: four prompts of up to 32k tokens of 8
 // heads of 128 channels 147 us for 973 MB (99% of the measured copy), 8100 of 16400 used pages of 32 KB moved 90 us
 // for 537 MB (89%; the copies alone 81). What is small is a chain of latencies: single tokens of 32
-// sequences 5.9 us, a reordering of 32 beams 10.2, of which the counts, the choice of the pages to copy and
-// the second launch are about a third each, and 250 pages of 8 KB moved 8.1. (Times of the device alone, calls
+// sequences 5.9 us, a reordering of 32 beams 9.6, of which the counts, the choice of the pages to copy and
+// the second launch are about a third each, and 250 pages of 8 KB moved 7.1. (Times of the device alone, calls
 // replayed from a graph.)
 #include <algorithm>
 
@@ -384,7 +384,7 @@ paged_append_one_kernel(const Paged c, const PagedNew nw, int32_t* pos_out, int 
       x = load(nw.v, nw.vb, nw.vh, i);
     }
     const int b = i / per, h = i % per / V, v = i % V, at = s_slot[b];
-    if (at < 0) continue;
+    if (at < 0 || !paged_page(s_page[b], c.pages)) continue;
     const size_t row = (size_t)s_page[b] * Hkv + h, to = (row * P + (at & (P - 1))) * V + v;
     static_cast<uint4*>(c.k)[to] = k;
     static_cast<uint4*>(c.v)[to] = x;
@@ -400,7 +400,7 @@ paged_append_one_kernel(const Paged c, const PagedNew nw, int32_t* pos_out, int 
 #pragma unroll
   for (int i = 0; i < kPlanMost; ++i) {
     const int b = p.b0 + i;
-    if (b >= p.b1 || !p.n[i] || p.page[i] >= 0) continue;
+    if (b >= p.b1 || !p.n[i] || p.page[i] >= 0 || !paged_page(s_page[b], c.pages)) continue;
     c.table[(size_t)b * MP + s_had[b]] = s_page[b];
     c.refs[s_page[b]] = 1;
   }
@@ -489,7 +489,7 @@ template <int NT>
 __device__ __forceinline__ void fork_choose(const Paged& c, const PagedFork& f, int B, int Cap, int pshift) {
   constexpr int MOST = kPlanMost;
   __shared__ PlanShared<NT> sh;
-  __shared__ int s_src[NT * MOST], s_copy[NT * MOST];
+  __shared__ int s_copy[NT * MOST];
   const int tid = threadIdx.x, MP = Cap >> pshift, free = c.state[0], lowest = c.state[1];
   const int per = (B + NT - 1) / NT, b0 = min(tid * per, B), b1 = min(b0 + per, B);
   ForkPlan p[MOST];
@@ -511,16 +511,19 @@ __device__ __forceinline__ void fork_choose(const Paged& c, const PagedFork& f, 
         held[i] = c.refs[src[i]] > 0;
       }
     }
-    s_src[b] = held[i] ? -1 : src[i];
   }
+  __syncthreads();
+  // a page that nobody holds whole: its lowest user keeps it, found by its number (below zero) in the page's count
+  constexpr int kBelow = 1 << 30;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    if (src[i] >= 0 && !held[i]) atomicMin(c.refs + src[i], b0 + i - kBelow);
   __syncthreads();
   int copies = 0;
   bool copy[MOST];
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
-    copy[i] = src[i] >= 0 && held[i];
-    if (src[i] >= 0 && !held[i])  // nobody holds it whole: its lowest user keeps it
-      for (int k = 0; k < b0 + i && !copy[i]; ++k) copy[i] = s_src[k] == src[i];
+    copy[i] = src[i] >= 0 && (held[i] || __ldcg(c.refs + src[i]) != b0 + i - kBelow);
     copies += copy[i];
   }
   int total;
@@ -536,10 +539,11 @@ __device__ __forceinline__ void fork_choose(const Paged& c, const PagedFork& f, 
     if (b >= b1) continue;
     const int part = src[i] < 0 ? 0 : p[i].len & ((1 << pshift) - 1);
     f.copy[b] = make_int4(src[i], src[i], part, p[i].same ? -1 : p[i].was);
-    if (fail || p[i].same) continue;
+    if (p[i].same) continue;
+    if (src[i] >= 0 && !copy[i]) c.refs[src[i]] = !fail;
+    if (fail) continue;
     c.ctx[b] = p[i].len;
     if (copy[i]) s_copy[rank++] = b;
-    else if (src[i] >= 0) c.refs[src[i]] = 1;
   }
   __syncthreads();
   if (fail || total == 0) return;
@@ -624,6 +628,12 @@ __device__ __forceinline__ void fork_copy(const Paged& c, const PagedFork& f, in
   }
 }
 
+// CTAs of a sequence in the steps over table rows: enough for a thread an entry, up to eight CTAs an SM in all
+// (their arrivals are counted one by one).
+static int fork_shares(int B, int pages, int nt) {
+  return std::max(1, std::min((pages + nt - 1) / nt, 8 * sm_count() / B));
+}
+
 // The counts, and, by the last CTA, the choice (as a launch of its own: 0.6 us more).  All three steps in one
 // launch of a cluster were slower: its eight CTAs took 14 us for 32 beams and 24 for 48 prompts' prefixes.
 template <int NT>
@@ -657,11 +667,11 @@ cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* par
   f.rows = reinterpret_cast<int32_t*>(f.copy + s.B);
   const int MP = s.Cap >> s.pshift, size = s.dtype == 0 ? 4 : 2;
   cudaError_t e;
-  const int nt = s.B <= kPlanFew * kPlanMost ? kPlanFew : kPlanThreads, shares = std::min(64, (MP + nt - 1) / nt);
+  const int nt = s.B <= kPlanFew * kPlanMost ? kPlanFew : kPlanThreads, shares = fork_shares(s.B, MP, nt);
   e = nt == kPlanFew ? launch_pdl(fork_count_kernel<kPlanFew>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift)
                      : launch_pdl(fork_count_kernel<kPlanThreads>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift);
   if (e == cudaSuccess) {
-    const int chunks = std::min(64, (MP + 255) / 256);
+    const int chunks = fork_shares(s.B, MP, 256);
     const dim3 grid(chunks + (s.Hkv * s.D * size / 16 + 255) / 256, s.B);
     e = s.dtype == 0 ? launch_pdl(fork_commit_kernel<float>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks)
                      : launch_pdl(fork_commit_kernel<bf16>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks);
@@ -672,104 +682,113 @@ cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* par
 // ------------------------------------------------------------------- compaction
 
 // The i-th free page below U (the number of used pages) receives the i-th used one from U on:
-// holes[i], movers[i], and rank[p] = i of a mover p.  A CTA takes 64 words of the bits (one CTA for
-// 32768 pages takes 12 us) and counts what lies before them.
-constexpr int kCompactWords = 64;
+// holes[i], movers[i], and rank[p] = i of a mover p.  A CTA takes `per` words of the bits and counts what lies
+// before them: 64 words, or a 128th of the map where that is more (one CTA for 32768 pages takes 12 us).
+constexpr int kCompactWords = 64, kCompactCtas = 128;
 
-__global__ void __launch_bounds__(kPlanThreads)
-compact_plan_kernel(const Paged c, const PagedCompact m) {
-  __shared__ PlanShared<kPlanThreads> sh;
+__global__ void __launch_bounds__(kPlanFew)
+compact_plan_kernel(const Paged c, const PagedCompact m, int per) {
+  constexpr int NT = kPlanFew;
+  __shared__ PlanShared<NT> sh;
   pdl_wait_then_release();
   const uint32_t* bits = paged_bits(c);
   const int words = paged_words(c.pages), tid = threadIdx.x, lane = tid & 31, U = c.pages - c.state[0];
-  const int w0 = blockIdx.x * kCompactWords, n = min(kCompactWords, words - w0);
+  const int w0 = blockIdx.x * per, w1 = min(w0 + per, words);
   int before = 0, below = 0, all, holes;
   // free pages before this CTA's words, and below page U
-  const int up = max(w0, (U >> 5) + 1);
-  for (int w = tid; w < min(up, words); w += kPlanThreads) {
+#pragma unroll 4
+  for (int w = tid; w < min(max(w0, (U >> 5) + 1), words); w += NT) {
     const uint32_t x = bits[w];
     if (w < w0) before += __popc(x);
     if (w < U >> 5) below += __popc(x);
     else if (w == U >> 5) below += __popc(x & ((1u << (U & 31)) - 1u));
   }
-  plan_scan<kPlanThreads>(before, sh.tmp, all);
+  plan_scan<NT>(before, sh.tmp, all);
   before = all;
-  plan_scan<kPlanThreads>(below, sh.tmp, holes);
+  plan_scan<NT>(below, sh.tmp, holes);
   if (blockIdx.x == 0 && tid == 0) *m.count = holes;
-  const uint32_t word = tid < n ? bits[w0 + tid] : 0u;
-  sh.word[tid] = word;
-  sh.base[tid] = before + plan_scan<kPlanThreads>(__popc(word), sh.tmp, all);
-  __syncthreads();
-  for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
-    const int p = (w0 + i) * 32 + lane;
-    if (p >= c.pages) continue;
-    const int f = sh.base[i] + __popc(sh.word[i] & ((1u << lane) - 1u));  // free pages below p
-    const bool free = sh.word[i] >> lane & 1u;
-    if (free) {
-      if (p < U) m.holes[f] = p;
-    } else if (p >= U) {
-      const int r = p - U - (f - holes);
-      m.movers[r] = p;
-      m.rank[p] = r;
+  for (int w = w0; w < w1; w += NT) {
+    const uint32_t word = w + tid < w1 ? bits[w + tid] : 0u;
+    const int base = before + plan_scan<NT>(__popc(word), sh.tmp, all);
+    sh.word[tid] = word;
+    sh.base[tid] = base;
+    before += all;
+    __syncthreads();
+    for (int i = tid >> 5; i < min(NT, w1 - w); i += NT / 32) {
+      const int p = (w + i) * 32 + lane;
+      if (p >= c.pages) continue;
+      const int f = sh.base[i] + __popc(sh.word[i] & ((1u << lane) - 1u));  // free pages below p
+      const bool free = sh.word[i] >> lane & 1u;
+      if (free) {
+        if (p < U) m.holes[f] = p;
+      } else if (p >= U) {
+        const int r = p - U - (f - holes);
+        m.movers[r] = p;
+        m.rank[p] = r;
+      }
+      if (m.moved) m.moved[p] = free ? -1 : p;  // movers: below
     }
-    if (m.moved) m.moved[p] = free ? -1 : p;  // movers: below
   }
 }
 
-constexpr int kMoveThreads = 256, kMoveUnroll = 4;
+constexpr int kMoveThreads = 256, kMoveUnroll = 4, kMovePerSm = 8;
 
-// Copies the movers (a warp: 2 KB of a page's K and of its V, all loads in flight), then renames pages
-// in the table and writes the bits anew.  Eight CTAs an SM: 91.5 us for the pool above, 92.7 with two, 96 with four.
+// Copies the movers (a warp: 2 KB of a page's K and of its V, all loads in flight); the first eighth of the
+// CTAs renames pages in the table and writes the bits anew before that, while the others copy.  Eight CTAs an SM: 90.4
+// us for the pool above, 92 with two, 95 with four; 250 small pages 7.1 us, 8.1 with the renaming at the end.
 __global__ void __launch_bounds__(kMoveThreads)
 compact_move_kernel(const Paged c, const PagedCompact m, int64_t page_vecs, int64_t meta_vecs, int B, int Cap, int pshift) {
-  constexpr int NT = kMoveThreads, U = kMoveUnroll;
+  constexpr uint32_t NT = kMoveThreads, U = kMoveUnroll;
   pdl_wait_then_release();
   const int count = *m.count, used = c.pages - c.state[0], lane = threadIdx.x & 31;
-  const int parts = (int)(page_vecs / (32 * U));  // a page is whole units: 16 tokens of 64 channels in 2 bytes are one
-  const int64_t units = (int64_t)count * parts, warps = (int64_t)gridDim.x * (NT / 32);
-  for (int64_t x = (int64_t)blockIdx.x * (NT / 32) + (threadIdx.x >> 5); x < units; x += warps) {
-    const int i = (int)(x / parts), at = (int)(x % parts) * 32 * U + lane;
-    const int64_t from = m.movers[i] * page_vecs + at, to = m.holes[i] * page_vecs + at;
+  const uint32_t renamers = (gridDim.x + 7) / 8;
+  if (blockIdx.x < renamers) {
+    const int64_t tid = (int64_t)blockIdx.x * NT + threadIdx.x, all = (int64_t)renamers * NT;
+    if (meta_vecs)
+      for (int64_t x = tid; x < count * meta_vecs; x += all) {
+        const int64_t i = x / meta_vecs, at = x % meta_vecs, from = m.movers[i] * meta_vecs + at, to = m.holes[i] * meta_vecs + at;
+        static_cast<uint4*>(c.kmin)[to] = static_cast<const uint4*>(c.kmin)[from];
+        static_cast<uint4*>(c.kmax)[to] = static_cast<const uint4*>(c.kmax)[from];
+      }
+    for (int64_t x = tid; x < count; x += all) {
+      const int from = m.movers[x], to = m.holes[x];
+      c.refs[to] = c.refs[from];
+      c.refs[from] = 0;
+      if (m.moved) m.moved[from] = to;
+    }
+    const int MP = Cap >> pshift;
+    for (int64_t x = tid; x < (int64_t)B * MP; x += all) {
+      const int p = c.table[x];
+      if (p >= used && p < c.pages) {
+        const int r = m.rank[p];
+        if ((unsigned)r < (unsigned)count) c.table[x] = m.holes[r];
+      }
+    }
+    for (int64_t w = tid; w < paged_words(c.pages); w += all) {
+      uint32_t x = (w + 1) * 32 <= used ? 0u : w * 32 >= used ? 0xffffffffu : 0xffffffffu << (used & 31);
+      if (w == c.pages >> 5) x &= (1u << (c.pages & 31)) - 1u;
+      paged_bits(c)[w] = x;
+    }
+    if (tid == 0) c.state[1] = min(used >> 5, paged_words(c.pages) - 1);
+  }
+  // a page is whole units: 16 tokens of 64 channels in 2 bytes are one; the pool has less than 2^31 rows, so
+  // fewer units
+  const uint32_t parts = (uint32_t)(page_vecs / (32 * U)), units = (uint32_t)count * parts, warps = gridDim.x * (NT / 32);
+  for (uint32_t x = blockIdx.x * (NT / 32) + (threadIdx.x >> 5); x < units; x += warps) {
+    const uint32_t i = x / parts;
+    const int64_t at = (int64_t)(x % parts) * 32 * U + lane, from = m.movers[i] * page_vecs + at, to = m.holes[i] * page_vecs + at;
     uint4 k[U], v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (uint32_t u = 0; u < U; ++u) {
       k[u] = ldg_stream(static_cast<const uint4*>(c.k) + from + 32 * u);
       v[u] = ldg_stream(static_cast<const uint4*>(c.v) + from + 32 * u);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (uint32_t u = 0; u < U; ++u) {
       static_cast<uint4*>(c.k)[to + 32 * u] = k[u];
       static_cast<uint4*>(c.v)[to + 32 * u] = v[u];
     }
   }
-  const int64_t tid = (int64_t)blockIdx.x * NT + threadIdx.x, all = (int64_t)gridDim.x * NT;
-  if (meta_vecs)
-    for (int64_t x = tid; x < count * meta_vecs; x += all) {
-      const int i = (int)(x / meta_vecs);
-      const int64_t from = m.movers[i] * meta_vecs + x % meta_vecs, to = m.holes[i] * meta_vecs + x % meta_vecs;
-      static_cast<uint4*>(c.kmin)[to] = static_cast<const uint4*>(c.kmin)[from];
-      static_cast<uint4*>(c.kmax)[to] = static_cast<const uint4*>(c.kmax)[from];
-    }
-  for (int64_t x = tid; x < count; x += all) {
-    const int from = m.movers[x], to = m.holes[x];
-    c.refs[to] = c.refs[from];
-    c.refs[from] = 0;
-    if (m.moved) m.moved[from] = to;
-  }
-  const int MP = Cap >> pshift;
-  for (int64_t x = tid; x < (int64_t)B * MP; x += all) {
-    const int p = c.table[x];
-    if (p >= used && p < c.pages) {
-      const int r = m.rank[p];
-      if ((unsigned)r < (unsigned)count) c.table[x] = m.holes[r];
-    }
-  }
-  for (int64_t w = tid; w < paged_words(c.pages); w += all) {
-    uint32_t x = (w + 1) * 32 <= used ? 0u : w * 32 >= used ? 0xffffffffu : 0xffffffffu << (used & 31);
-    if (w == c.pages >> 5) x &= (1u << (c.pages & 31)) - 1u;
-    paged_bits(c)[w] = x;
-  }
-  if (tid == 0) c.state[1] = min(used >> 5, paged_words(c.pages) - 1);
 }
 
 size_t paged_compact_workspace(const Paged& c) { return 16 + 3 * (size_t)((c.pages + 3) & ~3) * sizeof(int32_t); }
@@ -783,12 +802,12 @@ cudaError_t launch_paged_compact(const Shape& s, const Paged& c, int32_t* moved,
   m.rank = m.movers + n;
   m.moved = moved;
   const int size = s.dtype == 0 ? 4 : 2;
-  const int64_t page_vecs = (int64_t)s.Hkv * s.P * s.D * size / 16, meta_vecs = c.kmin ? (int64_t)s.Hkv * s.D * size / 16 : 0;
-  const int ctas = (paged_words(c.pages) + kCompactWords - 1) / kCompactWords;
-  cudaError_t e = launch_pdl(compact_plan_kernel, dim3(ctas), dim3(kPlanThreads), 0, st, c, m);
+  const int64_t meta_vecs = (int64_t)s.Hkv * s.D * size / 16, page_vecs = meta_vecs * s.P;
+  const int words = paged_words(c.pages), per = std::max(kCompactWords, (words + kCompactCtas - 1) / kCompactCtas);
+  cudaError_t e = launch_pdl(compact_plan_kernel, dim3((words + per - 1) / per), dim3(kPlanFew), 0, st, c, m, per);
   if (e == cudaSuccess)
-    e = launch_pdl(compact_move_kernel, dim3(sm_count() * 8), dim3(kMoveThreads), 0, st, c, m, page_vecs, meta_vecs, s.B,
-                   s.Cap, s.pshift);
+    e = launch_pdl(compact_move_kernel, dim3(sm_count() * kMovePerSm), dim3(kMoveThreads), 0, st, c, m, page_vecs,
+                   c.kmin ? meta_vecs : 0, s.B, s.Cap, s.pshift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -396,6 +396,57 @@ def test_select_finds_what_the_row_selection_finds(dtype, d, page, k):
     pair.attend(q, got.tolist())
 
 
+@pytest.mark.parametrize("batch", [3, 100])
+@pytest.mark.parametrize("dtype,flags", [(F32, {}), (BF16, dict(cuda_cores=True)), (BF16, {})])
+@pytest.mark.parametrize("g", [1, 2, 4, 7])
+def test_select_group_sizes_and_kernels(g, dtype, flags, batch):
+    """Every scorer, in one launch (few rows) and in two (many rows, or the CUDA-core flag)."""
+    for d in (64, 128):
+        pair = Pair(batch, 2 * g, 2, d, 16, 1024, 1500, dtype)
+        pair.append([int(n) for n in pair.rng.integers(1, 240 if batch > 9 else 1024, batch)])
+        desc = ops.make_desc(batch, 2 * g, 2, d, 16, 1024, dtype, **flags)
+        q = pair.new((batch, 2 * g, d)).cuda()
+        at = pair.cache.table.clamp(min=0).long()
+        lo, hi = (x[at].transpose(1, 2).contiguous() for x in (pair.cache.kmin, pair.cache.kmax))
+        for k, first, last in ((6, 1, 17), (11, 0, 0)):
+            assert torch.equal(ops.paged_select_pages(desc, pair.cache, q, k, first, last),
+                               ops.select_pages(desc, q, lo, hi, pair.cache.ctx_len, k, first, last))
+    ops.pipeline_check()
+
+
+def test_select_counts_bad_entries_and_scores_them_as_zeros():
+    pair = Pair(2, 4, 2, 64, 16, 1024, 130)
+    pair.append([1000, 640])
+    q = pair.new((2, 4, 64)).cuda()
+    at = pair.cache.table.clamp(min=0).long()
+    lo, hi = (x[at].transpose(1, 2).contiguous() for x in (pair.cache.kmin, pair.cache.kmax))
+    pair.cache.table[0, 7], pair.cache.table[0, 9], pair.cache.table[1, 30] = -1, 130, 1 << 30
+    for b, p in ((0, 7), (0, 9), (1, 30)):
+        lo[b, :, p] = hi[b, :, p] = 0
+    got = ops.paged_select_pages(pair.desc, pair.cache, q, 12, 1, 20)
+    with pytest.raises(L.SlsError, match="6 page-list entries"):  # for each of the two KV heads
+        ops.pipeline_check()
+    assert torch.equal(got, ops.select_pages(pair.desc, q, lo, hi, pair.cache.ctx_len, 12, 1, 20))
+
+
+@pytest.mark.parametrize("pool", [1, 2, 3])
+def test_pools_of_a_few_pages(pool):
+    pair = Pair(3, 2, 1, 64, 16, 64, pool)
+    pair.append([5, 16, 1])
+    pair.check()
+    pair.attend()
+    pair.fork([1, 0, 2])
+    pair.check()
+    pair.fork([0, 0, 0], [3, 5, 1])
+    pair.check()
+    pair.fork([-1, 1, 2])
+    pair.compact()
+    pair.check()
+    pair.append([1, 1, 1])
+    pair.check()
+    pair.attend()
+
+
 @pytest.mark.parametrize("batch,hkv,cap,dtype", [(1, 1, 2048, BF16), (2, 3, 16 * 700, BF16), (40, 2, 16 * 130, BF16), (77, 1, 1024, F32),
                                                  (90, 2, 1024, BF16), (3, 1, 16 * 2500, F32)])
 def test_select_clusters_ties_and_few_pages(batch, hkv, cap, dtype):
