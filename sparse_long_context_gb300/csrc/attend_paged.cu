@@ -46,6 +46,11 @@ constexpr int kPgMinUnits = 4;     // least units of a CTA in ranges: a shorter 
 // Work of a row change (drain, merge, partial and refill) in tokens: 512, 1024 and 2048 took 53.3,
 // 53.0 and 56.6 us on the uneven fp32 rows above.
 constexpr int kPgSegCost = 1024;
+// Rows are not cut (and not merged) where that costs the longest range less than this many ns of work: 64 rows of 1000
+// tokens 15.7 -> 13.3 us, 128 of 2000 32.0 -> 27.8, 256 of up to 500 21.6 -> 17.0, 64 of 100 11.2 -> 8.4 (5000 ns: 128
+// rows of up to 2000 tokens 24.0 for 21.2; moving every border that is within 4 us of a row's start: 64 of up to 4096
+// tokens 23.2 for 21.5).
+constexpr double kPgWhole = 7000;
 
 struct PagedAttend {
   const void* q;
@@ -438,12 +443,13 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
     return l;
   };
-  // First unit of CTA k's range: equal shares of a list in which each row start after
-  // the first counts kPgSegCost tokens more.  Short jobs use fewer CTAs.
+  // First unit of CTA k's range: equal shares of a list in which each row start after the first counts
+  // kPgSegCost tokens more, moved to the nearest start of a row if rows are not to be cut.  Short jobs use fewer CTAs.
+  bool snap = false;
   auto range_start = [&](int k, int n) {
     const long long beta = kPgSegCost / UT, at = (s_pref[rows] + beta * (rows - 1)) * k / n;
-    const int l = row_at(at, beta);
-    return (int)min(at - beta * l, (long long)s_pref[l + 1]);
+    const int l = row_at(at, beta), first = s_pref[l], end = s_pref[l + 1], x = (int)min(at - beta * l, (long long)end);
+    return !snap ? x : x - first <= end - x ? first : end;
   };
   // rows without units: output 0, lse -inf (or the sink alone)
   auto empty_rows = [&]() {
@@ -465,23 +471,33 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     // s_pref: exclusive prefix sum of the rows' units
     {
       const int rpt = (rows + NT - 1) / NT, r0 = threadIdx.x * rpt;
-      int sum = 0, one = 0;  // one: the units of a thread's only row, read once
+      int sum = 0, one = 0, longest = 0;  // one: the units of a thread's only row, read once
       for (int i = 0; i < rpt; ++i)
-        if (r0 + i < rows) sum += one = units_of(r0 + i);
+        if (r0 + i < rows) {
+          sum += one = units_of(r0 + i);
+          longest = max(longest, one);
+        }
+      longest = __reduce_max_sync(0xffffffffu, longest);
       int x = sum;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 31) sh.s_tmp[warp] = x;
+      if (lane == 31) {
+        sh.s_tmp[warp] = x;
+        sh.s_tmp[16 + warp] = longest;
+      }
       __syncthreads();
       int before = 0, total = 0;
 #pragma unroll
       for (int w = 0; w < W; ++w) {
         before += w < warp ? sh.s_tmp[w] : 0;
         total += sh.s_tmp[w];
+        longest = max(longest, sh.s_tmp[16 + w]);
       }
+      constexpr int WHOLE = (int)(kPgWhole / (Tile::NS * UT));  // in units
+      snap = longest <= 2 * WHOLE && longest - total / (int)gridDim.x <= WHOLE;
       int acc = before + x - sum;
       for (int i = 0; i < rpt; ++i)
         if (r0 + i < rows) {
