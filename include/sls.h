@@ -94,9 +94,9 @@ typedef int sls_status;
 #define SLS_FLAG_NO_TMA 2
 /* Test hook of the bounded waits, not for production: in the tensor-map fed
  * kernels (sls_sparse_decode_attend[_combine] on bf16 pages of >= 16 tokens,
- * the one-launch sls_quest_decode_step, and sls_kv8_decode_attend), the first
- * CTA of the launch
- * announces 16 bytes on its first attend stage that it never requests, and
+ * the one-launch sls_quest_decode_step, sls_kv8_decode_attend and
+ * sls_paged_decode_attend), the first CTA of the launch (of the paged attend, the
+ * first one that has tokens) announces 16 bytes on its first attend stage that it never requests, and
  * that CTA's waits poll a short while only.  The waits on that stage
  * give up, the first row's outputs become NaN, and the next
  * sls_pipeline_check() returns SLS_ETIMEOUT.  No copy is issued for the
@@ -888,7 +888,9 @@ const char* sls_last_error(void);
  *     through shared memory poll their copies a bounded number of times; the
  *     affected outputs become NaN);
  *   - a page-list entry that is neither a page of the pool [0, Cap/P) nor the
- *     -1 padding (the attend and recall kernels skip it: it gives no token).
+ *     -1 padding (the attend and recall kernels skip it: it gives no token);
+ *     and what the calls of a paged cache count as bad: table entries, partial
+ *     pages that are shared, parents that do not exist.
  * This call synchronises the device, reads and clears the counts (one atomic
  * exchange per word, so no count is lost), and returns SLS_ETIMEOUT if any
  * wait gave up, else SLS_EDEVICE if any bad entry was met, else SLS_OK
