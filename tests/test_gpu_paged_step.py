@@ -254,3 +254,75 @@ print("fine")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("cap", [512, 8192])
+def test_values_that_are_not_finite_stay_in_their_channel_or_head(dtype, cap):
+    """(In a cluster and in ranges.)  A key of -inf or of the type's lowest value takes its token out; NaN and infinite values show
+    in their channel, a NaN query in its head."""
+    pair = Pair(3, 8, 2, 64, 16, cap, 3 * cap // 16, dtype, summaries=False)
+    pair.append([cap - 3, 200, 33])
+    q = pair.new((3, 8, 64))
+    q[:, :, 5] = q[:, :, 5].abs() + 0.5   # channel 5 of every query is positive
+    page = lambda b, t: (pair.plain.rows[b][t // 16], t % 16)  # noqa: E731
+    for b, t, x in ((0, 7, -math.inf), (0, 100, torch.finfo(dtype).min), (1, 199, -math.inf), (2, 0, torch.finfo(dtype).min)):
+        p, r = page(b, t)
+        for side in (pair.plain.k, pair.cache.k_pages):
+            side[p, :, r, 5] = x
+    want, lse, size, dots, count = pair.plain.attend(q, 0.125)
+    pair.plain.k[pair.plain.k.isinf()] = 0     # for the tolerances: the tokens' own scores are exact
+    pair.plain.k[pair.plain.k == torch.finfo(dtype).min] = 0
+    dots = pair.plain.attend(q, 0.125)[3]
+    tol, tol_lse = plain.bounds(dtype, 64, want, size, dots, count)
+    out, got = ops.paged_decode_attend(pair.desc, pair.cache, q.cuda())
+    assert bool(((out.cpu().double() - want).abs() <= tol).all()) and bool(((got.cpu().double() - lse).abs() <= tol_lse + 1e-5).all())
+    # NaN and infinities among the values of the newest token but one (whose weights are above zero), a NaN query
+    for b, x, ch in ((0, math.nan, 3), (1, math.inf, 40), (2, -math.inf, 63)):
+        p, r = page(b, pair.plain.ctx[b] - 2)
+        pair.cache.v_pages[p, 1, r, ch] = x
+    q[2, 1, 0] = math.nan
+    odd, odd_lse = ops.paged_decode_attend(pair.desc, pair.cache, q.cuda())
+    hit = torch.zeros_like(odd, dtype=torch.bool)
+    hit[0, 4:, 3] = hit[1, 4:, 40] = hit[2, 4:, 63] = hit[2, 1] = True
+    assert torch.equal(odd.isfinite(), ~hit) and torch.equal(odd[~hit], out[~hit])
+    assert odd[0, 4:, 3].isnan().all() and bool((odd[1, 4:, 40] == math.inf).all()) and bool((odd[2, 4:, 63] == -math.inf).all())
+    assert odd_lse[2, 1].isnan() and odd_lse.isnan().sum() == 1
+
+
+def test_sinks_of_every_size():
+    pair = Pair(2, 4, 2, 64, 16, 256, 40, summaries=False)
+    pair.append([100, 0])
+    q = pair.new((2, 4, 64))
+    none = ops.paged_decode_attend(pair.desc, pair.cache, q.cuda())
+    out, lse = ops.paged_decode_attend(pair.desc, pair.cache, q.cuda(), sink=torch.full((4,), -math.inf, device="cuda"))
+    assert same(out, none[0]) and same(lse, none[1])
+    pair.attend(q, sink=torch.tensor([-1e30, 0.0, 20.0, 1e4]))
+
+
+def test_two_caches_on_two_streams():
+    pairs = [Pair(4, 8, 2, 128, 16, 2048, 400, seed=s) for s in range(2)]
+    streams = [torch.cuda.Stream() for _ in pairs]
+    outs = []
+    for _ in range(4):
+        for pair in pairs:
+            pair.kv = pair.new((4, 60, 4, 128))
+            pair.dev, pair.q = pair.kv.cuda(), pair.new((4, 8, 128)).cuda()
+        torch.cuda.synchronize()
+        outs = []
+        for pair, stream in zip(pairs, streams):
+            with torch.cuda.stream(stream):
+                ops.paged_append(pair.desc, pair.cache, pair.dev[:, :, :2], pair.dev[:, :, 2:])
+                ops.paged_fork(pair.desc, pair.cache, torch.tensor([1, 0, 2, 2], dtype=torch.int32, device="cuda"))
+                idx = ops.paged_select_pages(pair.desc, pair.cache, pair.q, 3, 1)
+                outs.append((ops.paged_decode_attend(pair.desc, pair.cache, pair.q, page_idx=idx), idx))
+                ops.paged_compact(pair.desc, pair.cache)
+        torch.cuda.synchronize()
+        for pair, ((out, _), idx) in zip(pairs, outs):
+            pair.plain.append(pair.kv[:, :, :2], pair.kv[:, :, 2:], [60] * 4)
+            assert pair.plain.fork([1, 0, 2, 2], None)
+            pair.plain.compact()
+            pair.check()
+            want = pair.plain.attend(pair.q, 1 / math.sqrt(128), idx.tolist())
+            tol, _ = plain.bounds(BF16, 128, want[0], *want[2:])
+            assert bool(((out.cpu().double() - want[0]).abs() <= tol).all())
