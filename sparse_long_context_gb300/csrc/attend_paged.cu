@@ -16,7 +16,7 @@
 // heads of 6 query heads and 128 channels in bf16, 279 to 282 us for 1884 MB (6.7 TB/s, the measured copy rate).
 // Twelve warps of two stages fill the shared memory: 8 of three take 285 us, 6 of four 291, 6 of two
 // with 32 tokens each 282.  In fp32 instructions come next: seven contexts of 1 to 20000 tokens, 8 heads of 8 query heads and
-// 64 channels 52 us for 268 MB (floor 40).  Short rows are a chain of latencies (lengths, table, copies,
+// 64 channels 51 us for 268 MB (floor 40).  Short rows are a chain of latencies (lengths, table, copies,
 // merge): 5.2 us for 1000 tokens of 4 heads, 16.8 for 64 lists of 128 pages (floor 10); in ranges the
 // prologue takes 3 us and the merge through global memory 3.7, so that 64 uneven rows of up to 4k tokens take 18 us with
 // two CTAs a row (floor 10) and 21.5 in ranges.  (Times of the device alone, calls replayed from a graph.)
@@ -243,7 +243,7 @@ struct PgF32 {
   using T = float;
   static constexpr int D = D_, W = D == 128 ? 6 : 12, S = 2, SG = 1;
   static constexpr int GROUP = 16 * D * 4, STAGE = 2 * GROUP, NF = D / 64, NC = D / 32;
-  static constexpr double NS = D == 128 ? 21.0 : 9.4;  // a token of a CTA by itself
+  static constexpr double NS = D == 128 ? 19.0 : 8.3;  // a token of a CTA by itself
   PgF2 q[GM][NC][2], o[GM][NF];
   float m_run, l_run;  // of head sl % GM; the sum of this lane's tokens
 
@@ -253,7 +253,8 @@ struct PgF32 {
     for (int g = 0; g < GM; ++g) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const float4 v = g < G ? __ldg(reinterpret_cast<const float4*>(qp + g * D + 32 * i + 4 * sl))
+        const int h = g ^ (sl & (GM - 1));  // so that what a lane keeps when the lanes add up has fixed places
+        const float4 v = h < G ? __ldg(reinterpret_cast<const float4*>(qp + h * D + 32 * i + 4 * sl))
                                : make_float4(0.f, 0.f, 0.f, 0.f);
         q[g][i][0] = pg_f2(v.x, v.y);
         q[g][i][1] = pg_f2(v.z, v.w);
@@ -283,17 +284,15 @@ struct PgF32 {
         const float2 d = pg_split(a);
         s[g] = d.x + d.y;
       }
-      // the heads over the eight lanes: half of what is left goes to the other half of the lanes
+      // the heads over the eight lanes (place g of lane sl is head g ^ sl): half of what is left goes to the other
+      // half of the lanes
       if constexpr (GM == 4)
 #pragma unroll
         for (int g = 0; g < 4; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g], 4);
 #pragma unroll
       for (int w = GM / 2; w > 0; w >>= 1)
 #pragma unroll
-        for (int g = 0; g < w; ++g) {
-          const float keep = sl & w ? s[g + w] : s[g], give = sl & w ? s[g] : s[g + w];
-          s[g] = keep + __shfl_xor_sync(0xffffffffu, give, w);
-        }
+        for (int g = 0; g < w; ++g) s[g] += __shfl_xor_sync(0xffffffffu, s[g + w], w);
       x[j] = 4 * j + tg < lim ? s[0] * qscale : kNegInf;
     }
     float gm = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
@@ -320,9 +319,7 @@ struct PgF32 {
     }
     __syncwarp();
     const uint32_t v = stage + GROUP;
-    const int n = min(lim, 16);  // rows behind the context are not read
-#pragma unroll 8
-    for (int t = 0; t < n; ++t) {
+    auto token = [&](int t) {
       PgF2 y[NF], p[GM];
       if constexpr (NF == 2) pg_lds(v + pg_chunk(t, lane), y[0], y[1]);
       else pg_lds(v + pg_chunk(t, lane >> 1) + 8 * (lane & 1), y[0]);
@@ -332,6 +329,13 @@ struct PgF32 {
       for (int g = 0; g < GM; ++g)
 #pragma unroll
         for (int i = 0; i < NF; ++i) o[g][i] = pg_fma(y[i], p[g], o[g][i]);
+    };
+    if (lim >= 16) {
+#pragma unroll
+      for (int t = 0; t < 16; ++t) token(t);
+    } else {  // rows behind the context are not read
+#pragma unroll 1
+      for (int t = 0; t < lim; ++t) token(t);
     }
   }
 
@@ -951,8 +955,8 @@ static int pg_clusters(int c, PgDevice* d) {
 // of it on average and a cluster to wait for one that is full.  Measured on 260 shapes of 1 to 256
 // rows, full and with lengths spread evenly from none: 16.9 us with two CTAs a row and 20 in ranges
 // for 64 lists of 2048 tokens, 25.7 and 32.1 for 64 full rows of 4k, 188 and 167 for 64 uneven ones of
-// up to 64k.  Fifteen in sixteen shapes take within 8% of the faster side, the others lose up to a third (32 full fp32
-// rows of 4k at D = 128: 39 us, 30 with four CTAs a row).
+// up to 64k.  Nine in ten shapes take within 8% of the faster side, the others lose up to a quarter (64 full fp32
+// rows of 4k at D = 128: 61 us, 50 with two CTAs a row).
 template <typename Tile, bool LIST>
 static int pg_pick(int rows, double most, bool fixed, bool even, PgDevice* d) {
   const double t = Tile::NS * 1e-3, sms = sm_count();
