@@ -24,7 +24,7 @@ namespace sls {
 
 // Plans are made by one CTA, of 256 threads (1024 for more than 1024 sequences: a barrier of 32 warps
 // costs several of 8) with up to four sequences each.
-constexpr int kPlanThreads = 1024, kPlanFew = 256, kPlanMost = 4;
+constexpr int kPlanThreads = 1024, kPlanFew = 256, kPlanMost = 4, kPlanPages = 1024;
 static_assert(kPlanThreads * kPlanMost == kPagedMaxSeqs, "a plan holds every sequence");
 
 // Exclusive scan of one int per thread over the CTA; `total` gets the sum.
@@ -277,73 +277,96 @@ struct PagedLimits<float> {
   }
 };
 
-// Folds the threads' limits of one head's keys (thread i: vector i % V of a row) and writes
-// the page's; `merge`: with what is stored.
-template <typename T, int NT>
-__device__ __forceinline__ void write_limits(uint4 lo, uint4 hi, bool any, bool merge, uint4* kmin, uint4* kmax, int V) {
-  __shared__ uint4 s_lo[NT], s_hi[NT];
-  __shared__ bool s_any[NT];
-  s_lo[threadIdx.x] = lo;
-  s_hi[threadIdx.x] = hi;
-  s_any[threadIdx.x] = any;
-  __syncthreads();
-  if (threadIdx.x < V) {
-    const int v = threadIdx.x;  // every page written has a row, whose vectors the first V threads hold
-    lo = s_lo[v];
-    hi = s_hi[v];
-    for (int i = v + V; i < NT && s_any[i]; i += V) PagedLimits<T>::fold(lo, hi, s_lo[i], s_hi[i]);
-    if (merge) PagedLimits<T>::fold(lo, hi, kmin[v], kmax[v]);
-    kmin[v] = lo;
-    kmax[v] = hi;
-  }
+__device__ __forceinline__ uint4 shfl_vec(uint4 v, int lane) {
+  return make_uint4(__shfl_sync(0xffffffffu, v.x, lane), __shfl_sync(0xffffffffu, v.y, lane),
+                    __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
 }
 
-constexpr int kPagedThreads = 128, kPagedUnroll = 4;
+constexpr int kWriteThreads = 128, kWriteUnroll = 4;
+constexpr int kWriteWide = 512;  // vectors of a page's head from which a CTA writes it
 
-// A CTA writes the new tokens of one page and KV head, four 16-byte vectors of K and of V a thread in flight.
-template <typename T>
-__global__ void __launch_bounds__(kPagedThreads)
+// WPP warps (one, or the CTA's four) write the new tokens of one page and KV head: four 16-byte vectors of K and of V
+// a lane in flight, the page's min/max by shuffles (and through shared memory).  Four prompts of 32k tokens of 8 heads,
+// with min/max, a warp or a CTA each: 154 and 331 us on pages of 16 tokens at D = 128, 83 and 297 at D = 64; 152.6 and 149.8 on
+// pages of 32 at D = 128, 155 and 151 on pages of 64 (floors 146 to 150, 75 at D = 64).  CTAs of eight warps: 153.5
+// on pages of 64, 150 for 155 on pages of 256.
+template <typename T, int WPP>
+__global__ void __launch_bounds__(kWriteThreads)
 paged_write_kernel(const Paged c, const PagedNew nw, int Hkv, int Cap, int D, int pshift) {
-  constexpr int NT = kPagedThreads, U = kPagedUnroll, E = Vec16<T>::N;
+  constexpr int U = kWriteUnroll, E = Vec16<T>::N, NW = kWriteThreads / 32;
+  static_assert(WPP == 1 || WPP == NW, "a page is a warp's or the CTA's, so that returns are uniform");
   pdl_wait_then_release();
-  const int b = blockIdx.y, h = blockIdx.x % Hkv, unit = blockIdx.x / Hkv;
+  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t unit = WPP == 1 ? blockIdx.x * NW + warp : blockIdx.x;
+  const int h = unit % (uint32_t)Hkv;
   const int2 span = paged_spans(c)[b];
-  const int l = (span.x >> pshift) + unit;
+  const int64_t l = (span.x >> pshift) + (int64_t)(unit / (uint32_t)Hkv);
   if (span.y == 0 || l > (span.x + span.y - 1) >> pshift) return;
   const int page = c.table[(size_t)b * (Cap >> pshift) + l];
   if (!paged_page(page, c.pages)) return;
-  const int t0 = max(l << pshift, span.x), t1 = min((l + 1) << pshift, span.x + span.y), P = 1 << pshift;
-  const int V = D / E;  // vectors of a token
-  const size_t at = (((size_t)page * Hkv + h) * P + (t0 & (P - 1))) * V;
+  const int P = 1 << pshift, t0 = max((int)l << pshift, span.x), rows = min(((int)l + 1) << pshift, span.x + span.y) - t0;
+  // vectors of a token; the lane's, and its first row
+  const int V = D / E, v = lane % V, r0 = ((WPP == 1 ? 0 : warp * 32) + lane) / V, step = 32 * WPP / V;
+  const size_t at = (((size_t)page * Hkv + h) * P + (t0 & (P - 1))) * V + v;
   uint4 *kd = static_cast<uint4*>(c.k) + at, *vd = static_cast<uint4*>(c.v) + at;
-  const T* ks = static_cast<const T*>(nw.k) + b * nw.kb + (int64_t)(t0 - span.x) * nw.kt + h * nw.kh;
-  const T* vs = static_cast<const T*>(nw.v) + b * nw.vb + (int64_t)(t0 - span.x) * nw.vt + h * nw.vh;
-  const int n = (t1 - t0) * V, ch = (threadIdx.x % V) * E, r0 = threadIdx.x / V, step = NT / V;
+  const T* ks = static_cast<const T*>(nw.k) + b * nw.kb + (int64_t)(t0 - span.x) * nw.kt + h * nw.kh + v * E;
+  const T* vs = static_cast<const T*>(nw.v) + b * nw.vb + (int64_t)(t0 - span.x) * nw.vt + h * nw.vh + v * E;
   uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-  for (int i0 = threadIdx.x, r = r0; i0 < n; i0 += NT * U, r += step * U) {
-    uint4 k[U], v[U];
+  for (int r = r0; r < rows; r += step * U) {
+    uint4 k[U], x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u * NT < n) {
-        k[u] = ldg_stream(ks + (int64_t)(r + u * step) * nw.kt + ch);
-        v[u] = ldg_stream(vs + (int64_t)(r + u * step) * nw.vt + ch);
+      if (r + u * step < rows) {
+        k[u] = ldg_stream(ks + (r + u * step) * nw.kt);
+        x[u] = ldg_stream(vs + (r + u * step) * nw.vt);
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (i0 + u * NT < n) {
-        kd[i0 + u * NT] = k[u];
-        vd[i0 + u * NT] = v[u];
+      if (r + u * step < rows) {
+        kd[(r + u * step) * V] = k[u];
+        vd[(r + u * step) * V] = x[u];
         if (c.kmin) {
-          if (i0 == (int)threadIdx.x && u == 0) lo = hi = k[u];
+          if (r == r0 && u == 0) lo = hi = k[u];
           else PagedLimits<T>::fold(lo, hi, k[u], k[u]);
         }
       }
   }
-  if (c.kmin) {
-    const size_t m = ((size_t)page * Hkv + h) * V;
-    write_limits<T, NT>(lo, hi, (int)threadIdx.x < n, (t0 & (P - 1)) != 0, static_cast<uint4*>(c.kmin) + m,
-                        static_cast<uint4*>(c.kmax) + m, V);
+  if (!c.kmin) return;
+  __syncwarp();
+  // lanes without a row take those of the warp's first row (warps without one are left out)
+  const int from = r0 < rows ? lane : v;
+  lo = shfl_vec(lo, from);
+  hi = shfl_vec(hi, from);
+  for (int w = V; w < 32; w <<= 1) PagedLimits<T>::fold(lo, hi, shfl_vec(lo, lane ^ w), shfl_vec(hi, lane ^ w));
+  if constexpr (WPP > 1) {
+    __shared__ uint4 s_lo[NW][32], s_hi[NW][32];
+    if (lane < V) {
+      s_lo[warp][lane] = lo;
+      s_hi[warp][lane] = hi;
+    }
+    __syncthreads();
+    if (warp == 0 && lane < V)
+      for (int w = 1; w < NW && w * 32 / V < rows; ++w) PagedLimits<T>::fold(lo, hi, s_lo[w][lane], s_hi[w][lane]);
   }
+  if (r0 == 0) {
+    const size_t m = ((size_t)page * Hkv + h) * V + v;
+    uint4 *kmin = static_cast<uint4*>(c.kmin) + m, *kmax = static_cast<uint4*>(c.kmax) + m;
+    if (t0 & (P - 1)) PagedLimits<T>::fold(lo, hi, *kmin, *kmax);
+    *kmin = lo;
+    *kmax = hi;
+  }
+}
+
+template <typename T>
+static cudaError_t write_launch(const Shape& s, const Paged& c, const PagedNew& n, cudaStream_t st) {
+  constexpr int NW = kWriteThreads / 32;
+  const int most = std::min(n.max_new, s.Cap);  // more tokens fit no sequence
+  const int64_t units = ((int64_t)(most - 1 + s.P - 1) / s.P + 1) * s.Hkv;  // pages and heads of a sequence
+  if (s.P * (s.D / Vec16<T>::N) >= kWriteWide)
+    return launch_pdl(paged_write_kernel<T, NW>, dim3((unsigned)units, s.B), dim3(kWriteThreads), 0, st, c, n, s.Hkv, s.Cap, s.D,
+                      s.pshift);
+  return launch_pdl(paged_write_kernel<T, 1>, dim3((unsigned)((units + NW - 1) / NW), s.B), dim3(kWriteThreads), 0, st, c, n,
+                    s.Hkv, s.Cap, s.D, s.pshift);
 }
 
 // One token of every sequence in one launch: each CTA plans for itself and writes its share of the vectors, and the
@@ -419,16 +442,13 @@ cudaError_t launch_paged_append(const Shape& s, const Paged& c, const PagedNew& 
                                   s.D, s.pshift);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
-  e = few ? launch_pdl(paged_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, c, n.new_len, n.max_new, pos_out, s.B, s.Cap,
-                       s.pshift)
-          : launch_pdl(paged_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, st, c, n.new_len, n.max_new, pos_out, s.B,
-                       s.Cap, s.pshift);
-  if (e == cudaSuccess && n.max_new > 0) {
-    const int most = std::min(n.max_new, s.Cap);  // more tokens fit no sequence
-    const dim3 grid((unsigned)(((most + s.P - 2) / s.P + 1) * s.Hkv), s.B);
-    e = s.dtype == 0 ? launch_pdl(paged_write_kernel<float>, grid, dim3(kPagedThreads), 0, st, c, n, s.Hkv, s.Cap, s.D, s.pshift)
-                     : launch_pdl(paged_write_kernel<bf16>, grid, dim3(kPagedThreads), 0, st, c, n, s.Hkv, s.Cap, s.D, s.pshift);
-  }
+  // 1024 threads where there are many pages to give as well (32768: 27 us with 256, 8 with 1024)
+  const bool quick = few && (int64_t)s.B * (std::min(n.max_new, s.Cap) / s.P + 1) <= kPlanPages;
+  e = quick ? launch_pdl(paged_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, c, n.new_len, n.max_new, pos_out, s.B, s.Cap,
+                         s.pshift)
+            : launch_pdl(paged_plan_kernel<kPlanThreads>, dim3(1), dim3(kPlanThreads), 0, st, c, n.new_len, n.max_new, pos_out,
+                         s.B, s.Cap, s.pshift);
+  if (e == cudaSuccess && n.max_new > 0) e = s.dtype == 0 ? write_launch<float>(s, c, n, st) : write_launch<bf16>(s, c, n, st);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
