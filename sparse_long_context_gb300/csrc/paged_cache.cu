@@ -10,7 +10,7 @@
 // Appends and compactions move bytes, at the memory's rate on large ones: four prompts of up to 32k tokens of 8
 // heads of 128 channels 147 us for 973 MB (99% of the measured copy), 8100 of 16400 used pages of 32 KB moved 90 us
 // for 537 MB (89%; the copies alone 81). What is small is a chain of latencies: single tokens of 32
-// sequences 5.9 us, a reordering of 32 beams 9.6, of which the counts, the choice of the pages to copy and
+// sequences 5.9 us, a reordering of 32 beams 9.0, of which the counts, the choice of the pages to copy and
 // the second launch are about a third each, and 250 pages of 8 KB moved 7.1. (Times of the device alone, calls
 // replayed from a graph.)
 #include <algorithm>
@@ -282,6 +282,35 @@ __device__ __forceinline__ uint4 shfl_vec(uint4 v, int lane) {
                     __shfl_sync(0xffffffffu, v.z, lane), __shfl_sync(0xffffffffu, v.w, lane));
 }
 
+// The limits of one head's keys, rows [0, rows) of which NW warps have: a lane vector v of rows r0, r0 + 32 NW / V, ...
+// (at least the first row is there).  Writes the page's; `merge`: with what is stored.
+template <typename T, int NW>
+__device__ __forceinline__ void write_limits(uint4 lo, uint4 hi, int rows, int r0, int v, int V, bool merge, uint4* kmin,
+                                             uint4* kmax) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncwarp();
+  // lanes without a row take those of the warp's first row (warps without one are left out)
+  const int from = r0 < rows ? lane : v;
+  lo = shfl_vec(lo, from);
+  hi = shfl_vec(hi, from);
+  for (int w = V; w < 32; w <<= 1) PagedLimits<T>::fold(lo, hi, shfl_vec(lo, lane ^ w), shfl_vec(hi, lane ^ w));
+  if constexpr (NW > 1) {
+    __shared__ uint4 s_lo[NW][32], s_hi[NW][32];
+    if (lane < V) {
+      s_lo[warp][lane] = lo;
+      s_hi[warp][lane] = hi;
+    }
+    __syncthreads();
+    if (warp == 0 && lane < V)
+      for (int w = 1; w < NW && w * 32 / V < rows; ++w) PagedLimits<T>::fold(lo, hi, s_lo[w][lane], s_hi[w][lane]);
+  }
+  if (r0 == 0) {
+    if (merge) PagedLimits<T>::fold(lo, hi, kmin[v], kmax[v]);
+    kmin[v] = lo;
+    kmax[v] = hi;
+  }
+}
+
 constexpr int kWriteThreads = 128, kWriteUnroll = 4;
 constexpr int kWriteWide = 512;  // vectors of a page's head from which a CTA writes it
 
@@ -332,29 +361,9 @@ paged_write_kernel(const Paged c, const PagedNew nw, int Hkv, int Cap, int D, in
       }
   }
   if (!c.kmin) return;
-  __syncwarp();
-  // lanes without a row take those of the warp's first row (warps without one are left out)
-  const int from = r0 < rows ? lane : v;
-  lo = shfl_vec(lo, from);
-  hi = shfl_vec(hi, from);
-  for (int w = V; w < 32; w <<= 1) PagedLimits<T>::fold(lo, hi, shfl_vec(lo, lane ^ w), shfl_vec(hi, lane ^ w));
-  if constexpr (WPP > 1) {
-    __shared__ uint4 s_lo[NW][32], s_hi[NW][32];
-    if (lane < V) {
-      s_lo[warp][lane] = lo;
-      s_hi[warp][lane] = hi;
-    }
-    __syncthreads();
-    if (warp == 0 && lane < V)
-      for (int w = 1; w < NW && w * 32 / V < rows; ++w) PagedLimits<T>::fold(lo, hi, s_lo[w][lane], s_hi[w][lane]);
-  }
-  if (r0 == 0) {
-    const size_t m = ((size_t)page * Hkv + h) * V + v;
-    uint4 *kmin = static_cast<uint4*>(c.kmin) + m, *kmax = static_cast<uint4*>(c.kmax) + m;
-    if (t0 & (P - 1)) PagedLimits<T>::fold(lo, hi, *kmin, *kmax);
-    *kmin = lo;
-    *kmax = hi;
-  }
+  const size_t m = ((size_t)page * Hkv + h) * V;
+  write_limits<T, WPP>(lo, hi, rows, r0, v, V, (t0 & (P - 1)) != 0, static_cast<uint4*>(c.kmin) + m,
+                       static_cast<uint4*>(c.kmax) + m);
 }
 
 template <typename T>
@@ -442,7 +451,8 @@ cudaError_t launch_paged_append(const Shape& s, const Paged& c, const PagedNew& 
                                   s.D, s.pshift);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
-  // 1024 threads where there are many pages to give as well (32768: 27 us with 256, 8 with 1024)
+  // 1024 threads where there are many pages to give as well (16 prompts of one head of 64 channels that take 32768 pages:
+  // 78 us with 256, 56 with 1024)
   const bool quick = few && (int64_t)s.B * (std::min(n.max_new, s.Cap) / s.P + 1) <= kPlanPages;
   e = quick ? launch_pdl(paged_plan_kernel<kPlanFew>, dim3(1), dim3(kPlanFew), 0, st, c, n.new_len, n.max_new, pos_out, s.B, s.Cap,
                          s.pshift)
@@ -609,43 +619,43 @@ __device__ __forceinline__ void fork_commit(const Paged& c, const PagedFork& f, 
   }
 }
 
-// Head h of the partial page of sequence b copied, and summarised anew, by the V = D * size / 16 threads that hold
-// vector `v` of its rows (one each, so a summary needs no more than its thread).
+// Head h of the partial page of sequence b copied, and summarised anew, by the CTA (a thread for all rows of a vector:
+// 33 us for 32 beams on pages of 256 tokens, this 12).
+constexpr int kForkThreads = 256;
 template <typename T>
-__device__ __forceinline__ void fork_copy(const Paged& c, const PagedFork& f, int b, int h, int v, int Hkv, int D, int pshift) {
+__device__ __forceinline__ void fork_copy(const Paged& c, const PagedFork& f, int b, int h, int Hkv, int D, int pshift) {
+  constexpr int NW = kForkThreads / 32, U = 4;
   const int4 cp = f.copy[b];
   if (cp.w < 0 || cp.z == 0 || c.state[2] != 0) return;
   const bool copy = cp.x != cp.y;
   if (!copy && !c.kmin) return;
-  const int V = D / Vec16<T>::N;
+  const int V = D / Vec16<T>::N, v = threadIdx.x % V, r0 = threadIdx.x / V, step = kForkThreads / V;
   const size_t from = ((((size_t)cp.x * Hkv + h) << pshift) * V) + v, to = ((((size_t)cp.y * Hkv + h) << pshift) * V) + v;
   const uint4 *ks = static_cast<const uint4*>(c.k) + from, *vs = static_cast<const uint4*>(c.v) + from;
   uint4 *kd = static_cast<uint4*>(c.k) + to, *vd = static_cast<uint4*>(c.v) + to;
-  uint4 lo = ks[0], hi = lo;
-  constexpr int U = 4;
-  for (int t = 0; t < cp.z; t += U) {
+  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+  for (int r = r0; r < cp.z; r += step * U) {
     uint4 k[U], x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t + u < cp.z) {
-        k[u] = ks[(t + u) * V];
-        if (copy) x[u] = vs[(t + u) * V];
+      if (r + u * step < cp.z) {
+        k[u] = ks[(r + u * step) * V];
+        if (copy) x[u] = vs[(r + u * step) * V];
       }
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (t + u < cp.z) {
+      if (r + u * step < cp.z) {
         if (copy) {
-          kd[(t + u) * V] = k[u];
-          vd[(t + u) * V] = x[u];
+          kd[(r + u * step) * V] = k[u];
+          vd[(r + u * step) * V] = x[u];
         }
-        PagedLimits<T>::fold(lo, hi, k[u], k[u]);
+        if (r == r0 && u == 0) lo = hi = k[u];
+        else PagedLimits<T>::fold(lo, hi, k[u], k[u]);
       }
   }
-  if (c.kmin) {
-    const size_t m = ((size_t)cp.y * Hkv + h) * V + v;
-    static_cast<uint4*>(c.kmin)[m] = lo;
-    static_cast<uint4*>(c.kmax)[m] = hi;
-  }
+  if (!c.kmin) return;
+  const size_t m = ((size_t)cp.y * Hkv + h) * V;
+  write_limits<T, NW>(lo, hi, cp.z, r0, v, V, false, static_cast<uint4*>(c.kmin) + m, static_cast<uint4*>(c.kmax) + m);
 }
 
 // CTAs of a sequence in the steps over table rows: enough for a thread an entry, up to eight CTAs an SM in all
@@ -665,16 +675,12 @@ fork_count_kernel(const Paged c, const PagedFork f, int B, int Cap, int pshift) 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kForkThreads)
 fork_commit_kernel(const Paged c, const PagedFork f, int Hkv, int B, int Cap, int D, int pshift, int chunks) {
   pdl_wait_then_release();
-  const int b = blockIdx.y, V = D / Vec16<T>::N;
-  if ((int)blockIdx.x < chunks) {
-    fork_commit(c, f, b, B, Cap, pshift, blockIdx.x * 256 + threadIdx.x, chunks * 256);
-    return;
-  }
-  const int i = (blockIdx.x - chunks) * 256 + threadIdx.x;
-  if (i < Hkv * V) fork_copy<T>(c, f, b, i / V, i % V, Hkv, D, pshift);
+  const int b = blockIdx.y;
+  if ((int)blockIdx.x < chunks) fork_commit(c, f, b, B, Cap, pshift, blockIdx.x * kForkThreads + threadIdx.x, chunks * kForkThreads);
+  else fork_copy<T>(c, f, b, blockIdx.x - chunks, Hkv, D, pshift);
 }
 
 size_t paged_fork_workspace(const Shape& s) {
@@ -685,16 +691,16 @@ cudaError_t launch_paged_fork(const Shape& s, const Paged& c, const int32_t* par
                               void* ws, cudaStream_t st) {
   PagedFork f = {parent, keep, done, static_cast<int4*>(ws), nullptr};
   f.rows = reinterpret_cast<int32_t*>(f.copy + s.B);
-  const int MP = s.Cap >> s.pshift, size = s.dtype == 0 ? 4 : 2;
+  const int MP = s.Cap >> s.pshift;
   cudaError_t e;
   const int nt = s.B <= kPlanFew * kPlanMost ? kPlanFew : kPlanThreads, shares = fork_shares(s.B, MP, nt);
   e = nt == kPlanFew ? launch_pdl(fork_count_kernel<kPlanFew>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift)
                      : launch_pdl(fork_count_kernel<kPlanThreads>, dim3(shares, s.B), dim3(nt), 0, st, c, f, s.B, s.Cap, s.pshift);
   if (e == cudaSuccess) {
-    const int chunks = fork_shares(s.B, MP, 256);
-    const dim3 grid(chunks + (s.Hkv * s.D * size / 16 + 255) / 256, s.B);
-    e = s.dtype == 0 ? launch_pdl(fork_commit_kernel<float>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks)
-                     : launch_pdl(fork_commit_kernel<bf16>, grid, dim3(256), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks);
+    const int chunks = fork_shares(s.B, MP, kForkThreads);
+    const dim3 grid(chunks + s.Hkv, s.B);
+    e = s.dtype == 0 ? launch_pdl(fork_commit_kernel<float>, grid, dim3(kForkThreads), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks)
+                     : launch_pdl(fork_commit_kernel<bf16>, grid, dim3(kForkThreads), 0, st, c, f, s.Hkv, s.B, s.Cap, s.D, s.pshift, chunks);
   }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
