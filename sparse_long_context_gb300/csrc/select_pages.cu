@@ -21,6 +21,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
@@ -1342,24 +1343,56 @@ cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
   return select_launch(s, q, kmin, kmax, ctx_len, k, n_sink_pages, n_local_tokens, page_idx, ws, nullptr, 0, st);
 }
 
+// Clusters of c CTAs of the kernel that run at once (asked once per device).
 template <typename T, int D, int GM, int MODE>
-static cudaError_t fused_launch(const SelectArgs& a, int rows, int cluster, cudaStream_t st) {
+static int fused_clusters(int c) {
+  static std::atomic<int> known[64][kFusedCluster + 1];  // 0: not asked yet, else 1 + the number
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][c].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = dim3(kFusedThreads<MODE>);
+    cfg.dynamicSmemBytes = kFusedKeep * kFusedThreads<MODE> * sizeof(uint32_t);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = c;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int got = 0;
+    if (cudaOccupancyMaxActiveClusters(&got, paged_select_kernel<T, D, GM, MODE>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      got = 0;
+    }
+    n = 1 + got;
+    known[dev][c].store(n, std::memory_order_relaxed);
+  }
+  return n - 1;
+}
+
+// The most CTAs a row with which all rows' clusters run at once: 48 rows of 960 pages of D = 64 take 12.3 us with as
+// many as the SMs would hold (3) and 8.7 so, 16 rows of 464 pages of D = 128 10.7 (8) and 7.5.
+template <typename T, int D, int GM, int MODE>
+static cudaError_t fused_launch(const SelectArgs& a, int rows, cudaStream_t st) {
+  int cluster = std::min(std::max(sm_count() / rows, 1), kFusedCluster);
+  while (cluster > 1 && fused_clusters<T, D, GM, MODE>(cluster) < rows) --cluster;
   const size_t smem = (size_t)((a.npcap + 15) & ~15) * sizeof(uint32_t);
   return launch_pdl_cluster(paged_select_kernel<T, D, GM, MODE>, dim3(rows * cluster), dim3(kFusedThreads<MODE>), smem, cluster, st,
                             a, cluster);
 }
 template <typename T, int D>
-static cudaError_t fused_g(const SelectArgs& a, int rows, int cluster, cudaStream_t st) {
-  if (a.G <= 1) return fused_launch<T, D, 1, 0>(a, rows, cluster, st);
-  if (a.G <= 2) return fused_launch<T, D, 2, 0>(a, rows, cluster, st);
-  if (a.G <= 4) return fused_launch<T, D, 4, 0>(a, rows, cluster, st);
-  return fused_launch<T, D, 8, 0>(a, rows, cluster, st);
+static cudaError_t fused_g(const SelectArgs& a, int rows, cudaStream_t st) {
+  if (a.G <= 1) return fused_launch<T, D, 1, 0>(a, rows, st);
+  if (a.G <= 2) return fused_launch<T, D, 2, 0>(a, rows, st);
+  if (a.G <= 4) return fused_launch<T, D, 4, 0>(a, rows, st);
+  return fused_launch<T, D, 8, 0>(a, rows, st);
 }
 
 cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, int k, int n_sink_pages, int n_local_tokens,
                                 int32_t* page_idx, void* ws, cudaStream_t st) {
   const int rows = s.B * s.Hkv, npcap = s.Cap >> s.pshift;
-  const int cluster = std::min(std::max(sm_count() / rows, 1), kFusedCluster);
   const int most = kFusedKeep * (s.dtype == 1 ? kFusedThreads<1> : kFusedThreads<0>);  // keys of a row
   if (!(s.flags & 1) && rows <= sm_count() && npcap <= most) {
     SelectArgs a = {};
@@ -1369,9 +1402,9 @@ cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, i
     a.table = c.table; a.pool = c.pages;
     cudaError_t e;
     if (s.dtype == 1)
-      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1>(a, rows, cluster, st) : fused_launch<bf16, 128, 8, 1>(a, rows, cluster, st);
+      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1>(a, rows, st) : fused_launch<bf16, 128, 8, 1>(a, rows, st);
     else
-      e = s.D == 64 ? fused_g<float, 64>(a, rows, cluster, st) : fused_g<float, 128>(a, rows, cluster, st);
+      e = s.D == 64 ? fused_g<float, 64>(a, rows, st) : fused_g<float, 128>(a, rows, st);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
   return select_launch(s, q, c.kmin, c.kmax, c.ctx, k, n_sink_pages, n_local_tokens, page_idx, ws, c.table, c.pages, st);
