@@ -1082,7 +1082,11 @@ topk_reg_kernel(const SelectArgs a) {
 // rows).  The pages' order in the pool makes no difference.
 constexpr int kFusedCluster = 8, kFusedKeep = 16;  // CTAs of a row, and keys a thread holds, at most
 constexpr int kFusedRank = 96;                     // keys ranked exactly
-template <int MODE> constexpr int kFusedThreads = MODE == 0 ? kSelThreads : 512;
+// Threads: 512 on the tensor cores where each SM has one row or part of it at most, else 256, so that a CTA ranks
+// while another one scores (384 rows of 256 pages 18.8 us, 26.2 with 512 and 25.1 in two launches; 40 rows of 2048 pages 16.0
+// and 13.9).
+constexpr int kFusedWide = 512, kFusedMany = 256;
+static_assert(kFusedMany == kSelThreads, "the CUDA-core scorer's threads");
 
 struct FusedShared {
   uint32_t hist[2048];
@@ -1092,11 +1096,11 @@ struct FusedShared {
   int scan_tmp[32], nf[32], n, take;
 };
 
-template <typename T, int D, int GM, int MODE>
-__global__ void __launch_bounds__(kFusedThreads<MODE>)
+template <typename T, int D, int GM, int MODE, int NT>
+__global__ void __launch_bounds__(NT)
 paged_select_kernel(const SelectArgs a, int cluster) {
   namespace cg = cooperative_groups;
-  constexpr int NT = kFusedThreads<MODE>, NW = NT / 32;
+  constexpr int NW = NT / 32;
   extern __shared__ __align__(16) uint32_t skeys[];  // [npcap, a multiple of 4]
   __shared__ FusedShared sh;
   cg::cluster_group cl = cg::this_cluster();
@@ -1344,7 +1348,7 @@ cudaError_t launch_select_pages(const Shape& s, const void* q, const void* kmin,
 }
 
 // Clusters of c CTAs of the kernel that run at once (asked once per device).
-template <typename T, int D, int GM, int MODE>
+template <typename T, int D, int GM, int MODE, int NT>
 static int fused_clusters(int c) {
   static std::atomic<int> known[64][kFusedCluster + 1];  // 0: not asked yet, else 1 + the number
   int dev = 0;
@@ -1353,8 +1357,8 @@ static int fused_clusters(int c) {
   if (n == 0) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(c);
-    cfg.blockDim = dim3(kFusedThreads<MODE>);
-    cfg.dynamicSmemBytes = kFusedKeep * kFusedThreads<MODE> * sizeof(uint32_t);
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = kFusedKeep * NT * sizeof(uint32_t);
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = c;
@@ -1362,7 +1366,7 @@ static int fused_clusters(int c) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int got = 0;
-    if (cudaOccupancyMaxActiveClusters(&got, paged_select_kernel<T, D, GM, MODE>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&got, paged_select_kernel<T, D, GM, MODE, NT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       got = 0;
     }
@@ -1374,35 +1378,37 @@ static int fused_clusters(int c) {
 
 // The most CTAs a row with which all rows' clusters run at once: 48 rows of 960 pages of D = 64 take 12.3 us with as
 // many as the SMs would hold (3) and 8.7 so, 16 rows of 464 pages of D = 128 10.7 (8) and 7.5.
-template <typename T, int D, int GM, int MODE>
+template <typename T, int D, int GM, int MODE, int NT>
 static cudaError_t fused_launch(const SelectArgs& a, int rows, cudaStream_t st) {
   int cluster = std::min(std::max(sm_count() / rows, 1), kFusedCluster);
-  while (cluster > 1 && fused_clusters<T, D, GM, MODE>(cluster) < rows) --cluster;
+  while (cluster > 1 && fused_clusters<T, D, GM, MODE, NT>(cluster) < rows) --cluster;
   const size_t smem = (size_t)((a.npcap + 15) & ~15) * sizeof(uint32_t);
-  return launch_pdl_cluster(paged_select_kernel<T, D, GM, MODE>, dim3(rows * cluster), dim3(kFusedThreads<MODE>), smem, cluster, st,
+  return launch_pdl_cluster(paged_select_kernel<T, D, GM, MODE, NT>, dim3(rows * cluster), dim3(NT), smem, cluster, st,
                             a, cluster);
 }
 template <typename T, int D>
 static cudaError_t fused_g(const SelectArgs& a, int rows, cudaStream_t st) {
-  if (a.G <= 1) return fused_launch<T, D, 1, 0>(a, rows, st);
-  if (a.G <= 2) return fused_launch<T, D, 2, 0>(a, rows, st);
-  if (a.G <= 4) return fused_launch<T, D, 4, 0>(a, rows, st);
-  return fused_launch<T, D, 8, 0>(a, rows, st);
+  if (a.G <= 1) return fused_launch<T, D, 1, 0, kFusedMany>(a, rows, st);
+  if (a.G <= 2) return fused_launch<T, D, 2, 0, kFusedMany>(a, rows, st);
+  if (a.G <= 4) return fused_launch<T, D, 4, 0, kFusedMany>(a, rows, st);
+  return fused_launch<T, D, 8, 0, kFusedMany>(a, rows, st);
 }
 
 cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, int k, int n_sink_pages, int n_local_tokens,
                                 int32_t* page_idx, void* ws, cudaStream_t st) {
   const int rows = s.B * s.Hkv, npcap = s.Cap >> s.pshift;
-  const int most = kFusedKeep * (s.dtype == 1 ? kFusedThreads<1> : kFusedThreads<0>);  // keys of a row
-  if (!(s.flags & 1) && rows <= sm_count() && npcap <= most) {
+  const bool wide = s.dtype == 1 && rows <= sm_count();
+  if (!(s.flags & 1) && npcap <= kFusedKeep * (wide ? kFusedWide : kFusedMany)) {  // a row's keys in one CTA's threads
     SelectArgs a = {};
     a.q = q; a.kmin = c.kmin; a.kmax = c.kmax; a.ctx_len = c.ctx; a.page_idx = page_idx;
     a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
     a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift; a.npcap = npcap;
     a.table = c.table; a.pool = c.pages;
     cudaError_t e;
-    if (s.dtype == 1)
-      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1>(a, rows, st) : fused_launch<bf16, 128, 8, 1>(a, rows, st);
+    if (wide)
+      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1, kFusedWide>(a, rows, st) : fused_launch<bf16, 128, 8, 1, kFusedWide>(a, rows, st);
+    else if (s.dtype == 1)
+      e = s.D == 64 ? fused_launch<bf16, 64, 8, 1, kFusedMany>(a, rows, st) : fused_launch<bf16, 128, 8, 1, kFusedMany>(a, rows, st);
     else
       e = s.D == 64 ? fused_g<float, 64>(a, rows, st) : fused_g<float, 128>(a, rows, st);
     return e != cudaSuccess ? e : cudaGetLastError();

@@ -396,6 +396,21 @@ def test_select_finds_what_the_row_selection_finds(dtype, d, page, k):
     pair.attend(q, got.tolist())
 
 
+@pytest.mark.parametrize("dtype,hkv,batch,cap", [(BF16, 3, 60, 2048), (F32, 4, 90, 1024), (BF16, 8, 25, 16 * 4096), (BF16, 2, 80, 16 * 4200),
+                                                 (F32, 1, 2, 16 * 4097)])
+def test_select_of_more_rows_than_sms_and_of_the_widest_rows(dtype, hkv, batch, cap):
+    pair = Pair(batch, 4 * hkv, hkv, 64, 16, cap, 9000, dtype)
+    lens = [int(n) for n in pair.rng.integers(1, min(cap, 9000 // batch * 16 - 16), batch)]
+    pair.append(lens[:-1] + [min(cap, 8000)])
+    q = pair.new((batch, 4 * hkv, 64)).cuda()
+    at = pair.cache.table.clamp(min=0).long()
+    lo, hi = (x[at].transpose(1, 2).contiguous() for x in (pair.cache.kmin, pair.cache.kmax))
+    for k, first, last in ((20, 1, 64), (63, 0, 0)):
+        assert torch.equal(ops.paged_select_pages(pair.desc, pair.cache, q, k, first, last),
+                           ops.select_pages(pair.desc, q, lo, hi, pair.cache.ctx_len, k, first, last))
+    ops.pipeline_check()
+
+
 @pytest.mark.parametrize("batch", [3, 100])
 @pytest.mark.parametrize("dtype,flags", [(F32, {}), (BF16, dict(cuda_cores=True)), (BF16, {})])
 @pytest.mark.parametrize("g", [1, 2, 4, 7])
