@@ -515,3 +515,12 @@ def test_attend_wait_that_gives_up_is_reported():
     assert e.value.code == L.SLS_ETIMEOUT
     assert out[0, :2].isnan().all() and not out[1].isnan().any()
     pair.attend(q.cpu())
+
+
+def test_attend_refuses_lists_without_entries():
+    pair = Pair(2, 4, 2, 128, 16, 256, 40, summaries=False)
+    pair.append([200, 130])
+    q = pair.new((2, 4, 128)).cuda()
+    with pytest.raises(ValueError, match="page_idx"):
+        ops.paged_decode_attend(pair.desc, pair.cache, q, page_idx=torch.empty((4, 0), dtype=torch.int32, device="cuda"))
+    pair.attend(q.cpu(), pages=[[-1]] * 4)  # a list that holds nothing
