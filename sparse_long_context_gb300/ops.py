@@ -584,6 +584,10 @@ class PagedCache:
 
     def load(self, table, ctx_len):
         """Takes over a table [B, Cap/P] and lengths [B] made elsewhere (paged_init)."""
+        self._beside(torch._C._cuda_getDevice(), self.desc())  # before anything changes
+        for t, mine, name in ((table, self.table, "table"), (ctx_len, self.ctx_len, "ctx_len")):
+            if t.shape != mine.shape or t.is_floating_point():
+                raise ValueError(f"{name} must be integers of shape {tuple(mine.shape)}, got {t.dtype} {tuple(t.shape)}")
         self.table.copy_(table)
         self.ctx_len.copy_(ctx_len)
         paged_init(self.desc(), self)

@@ -524,3 +524,15 @@ def test_attend_refuses_lists_without_entries():
     with pytest.raises(ValueError, match="page_idx"):
         ops.paged_decode_attend(pair.desc, pair.cache, q, page_idx=torch.empty((4, 0), dtype=torch.int32, device="cuda"))
     pair.attend(q.cpu(), pages=[[-1]] * 4)  # a list that holds nothing
+
+
+def test_load_refuses_before_it_changes_anything():
+    pair = Pair(2, 4, 2, 128, 16, 256, 40, summaries=False)
+    pair.append([200, 130])
+    table, lens = pair.cache.table.clone(), pair.cache.ctx_len.clone()
+    for t, n in ((table[0], lens), (table[:1], lens), (table, lens[:1]), (table, lens[0]), (table.float(), lens)):
+        with pytest.raises(ValueError):
+            pair.cache.load(t, n)
+        pair.check()
+    pair.cache.load(table.cpu().long(), lens.cpu().long())
+    pair.check()
