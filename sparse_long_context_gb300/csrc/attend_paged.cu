@@ -524,8 +524,10 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
     }
   }
 
-  // the wait-timeout test hook: the first CTA with a unit
-  const bool plant = a.test_wait && (CL ? row == 0 && lo == 0 && hi > 0 : cta == 0) && warp == 0;
+  // the wait-timeout test hook: the first CTA with a unit (ranges of CTAs before it may be empty, and so may rows)
+  bool plant = a.test_wait && lo == 0 && hi > 0 && warp == 0;
+  if constexpr (CL)
+    for (int r = 0; plant && r < row; ++r) plant = units_of(r) == 0;
   const uint32_t tries = plant ? kTestWaitTries : kWaitTries;
   const uint32_t wring = smem_u32(ring) + (uint32_t)warp * S * Tile::STAGE;
   uint32_t wseq = 0;  // this warp's ring position

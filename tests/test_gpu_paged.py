@@ -536,3 +536,19 @@ def test_load_refuses_before_it_changes_anything():
         pair.check()
     pair.cache.load(table.cpu().long(), lens.cpu().long())
     pair.check()
+
+
+# the first sequence empty (a row's cluster); a first range that is moved to the start of the second one
+@pytest.mark.parametrize("cap,lens", [(256, [0, 200, 130]), (65536, [1504] + [88] * 99)])
+def test_attend_wait_that_gives_up_is_that_of_the_first_tokens(cap, lens):
+    desc = ops.make_desc(len(lens), 2, 1, 128, 16, cap, BF16, test_wait_timeout=True)
+    pair = Pair(len(lens), 2, 1, 128, 16, cap, 1000, summaries=False)
+    pair.append(lens)
+    q = pair.new((len(lens), 2, 128)).cuda()
+    out, _ = ops.paged_decode_attend(desc, pair.cache, q)
+    with pytest.raises(L.SlsError) as e:
+        ops.pipeline_check()
+    assert e.value.code == L.SLS_ETIMEOUT
+    first = next(i for i, n in enumerate(lens) if n)
+    assert out[first].isnan().all() and not out[:first].isnan().any() and not out[first + 1:].isnan().any()
+    pair.attend(q.cpu())
