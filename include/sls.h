@@ -242,6 +242,10 @@ sls_status sls_thumb_residual_update(const sls_attn_desc* desc, const void* k_ca
  * the top (k - #forced) other pages by score, ties to the lower page
  * index, sorted ascending.  When the row has <= k pages all of them are
  * listed and the rest of the list is -1.
+ * The summaries may hold infinities: a channel adds q kmax where q > 0, q kmin
+ * where q < 0 and nothing where q is 0 or NaN.  A page one of whose heads has a
+ * U that is no number (infinities of both signs, a NaN summary) ranks above every
+ * score and below the forced pages, ties to the lower page index.
  *   q        [B, Hq, D] dtype (read)
  *   kmin     [B, Hkv, Cap/P, D] dtype (read); kmax likewise.  With P == 1
  *            a page is one token, its min and max are the key itself:

@@ -27,6 +27,7 @@
 // Nothing of the step goes through global memory but its inputs and outputs.
 #include "attend_tma.cuh"
 #include "launch.h"
+#include "page_bound.cuh"
 
 #include <algorithm>
 
@@ -99,18 +100,13 @@ __device__ __forceinline__ void score_stage(uint32_t stage, const uint32_t (&bp)
     v1 = ch[2] + cl[2];
   }
   if (h1) {
-    v0 = fmaxf(v0, ch[1] + cl[1]);
-    v1 = fmaxf(v1, ch[3] + cl[3]);
+    v0 = max_nan(v0, ch[1] + cl[1]);
+    v1 = max_nan(v1, ch[3] + cl[3]);
   }
-  v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
-  v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
-  v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, 1));
-  v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, 2));
-}
-
-__device__ __forceinline__ uint32_t order_key(float f) {
-  const uint32_t u = __float_as_uint(f);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
+  v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
+  v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, v1, 1));
+  v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, v1, 2));
 }
 
 // Exclusive scan of one int per thread over the CTA; `total` gets the sum.
@@ -732,6 +728,7 @@ quest_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         }
       }
       const uint32_t ring_u32 = smem_u32(ring);
+      bool none = false;
       for (int i = (W + warp - (int)(seq % W)) % W; i < n1; i += W) {
         const uint32_t q = seq + i;
         const int st = q % NST;
@@ -745,11 +742,26 @@ quest_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         if (lane == 0) mbar_arrive(&empty[st]);
         if (m == 0) {
           const int i0 = 16 * i + r, i1 = i0 + 8;
-          const int pg0 = p0 + i0, pg1 = p0 + i1;
-          if (i0 < nloc) keys[i0] = (pg0 < sa.n_sink || pg0 >= first_local) ? kForcedKey32 : order_key(v0);
-          if (i1 < nloc) keys[i1] = (pg1 < sa.n_sink || pg1 >= first_local) ? kForcedKey32 : order_key(v1);
+          auto put = [&](int at, float v) {
+            if (at >= nloc) return;
+            const int pg = p0 + at;
+            const uint32_t key = (pg < sa.n_sink || pg >= first_local) ? kForcedKey32 : score_key(v);
+            none |= key == kNoScoreKey;
+            keys[at] = key;
+          };
+          put(i0, v0);
+          put(i1, v1);
         }
       }
+      if (none)  // the lane's pages without a score
+        for (int i = (W + warp - (int)(seq % W)) % W; i < n1; i += W)
+          for (int at = 16 * i + r; at < min(16 * i + 16, nloc); at += 8)
+            if (keys[at] == kNoScoreKey) {
+              const size_t page = ((size_t)row * sa.npcap + p0 + at) * D;
+              keys[at] = defined_page_key<bf16>(static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D,
+                                                static_cast<const bf16*>(sa.kmin) + page,
+                                                static_cast<const bf16*>(sa.kmax) + page, G, D);
+            }
     }
     seq += n1;
     __syncthreads();  // keys complete; the ring is free

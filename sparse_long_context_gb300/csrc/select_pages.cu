@@ -26,6 +26,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "mma.cuh"
+#include "page_bound.cuh"
 #include "status.cuh"
 
 
@@ -58,6 +59,8 @@ struct SelectArgs {
   // a paged cache (null otherwise): kmin and kmax are those of the pool's pages [pool, Hkv, D]
   const int32_t* table;  // [B, npcap] page of the pool
   int pool;
+  int D;
+  bool f32;  // of q, kmin and kmax
 };
 
 // Where the summary of the page that a table entry gives lies in the pool, for head h; false for an
@@ -65,6 +68,21 @@ struct SelectArgs {
 __device__ __forceinline__ bool pool_summary(const SelectArgs& a, int page, int h, size_t& at) {
   at = (size_t)page * a.Hkv + h;
   return (unsigned)page < (unsigned)a.pool;
+}
+
+// The key of page p of a row by its definition, where the scorer's sum was no number (kNoScoreKey).  Left to what ranks the
+// keys and sees them all: in a scorer it costs registers, whether in its loop or after it.
+__device__ __forceinline__ uint32_t page_key_again(const SelectArgs& a, int row, int p) {
+  const int b = row / a.Hkv, h = row % a.Hkv;
+  const size_t q = ((size_t)b * a.Hq + (size_t)h * a.G) * a.D;
+  size_t at = (size_t)row * a.npcap + p;
+  const bool there = !a.table || pool_summary(a, a.table[(size_t)b * a.npcap + p], h, at);
+  auto key = [&](auto type) {
+    using T = decltype(type);
+    const T *lo = static_cast<const T*>(a.kmin) + at * a.D, *hi = static_cast<const T*>(a.kmax) + at * a.D;
+    return defined_page_key<T>(static_cast<const T*>(a.q) + q, there ? lo : nullptr, hi, a.G, a.D);
+  };
+  return a.f32 ? key(0.f) : key(bf16());
 }
 
 // Exclusive scan of one int per thread over the CTA; `total` gets the sum.
@@ -193,11 +211,11 @@ __device__ __forceinline__ void score_chunk(const SelectArgs& a, int row, int b,
       float best = s[0];
 #pragma unroll
       for (int g = 1; g < GM; ++g)
-        if (g < G) best = fmaxf(best, s[g]);
+        if (g < G) best = max_nan(best, s[g]);
       if (sub == 0 && pi[u] < nloc) {
         const int p = p0 + pi[u];
         const bool forced = p < a.n_sink || p >= first_local;
-        const uint32_t key = forced ? kForcedKey : float_key(best);
+        const uint32_t key = forced ? kForcedKey : score_key(best);
         keys[pi[u]] = key;
         if constexpr (STAGE) {
           if (skeys) skeys[pi[u]] = key;
@@ -279,11 +297,11 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
       // page score = max over the group's heads (columns 2m, 2m+1 here)
       float v0 = kNegInf, v1 = kNegInf;
       if (h0ok) { v0 = c[0]; v1 = c[2]; }
-      if (h1ok) { v0 = fmaxf(v0, c[1]); v1 = fmaxf(v1, c[3]); }
-      v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
-      v0 = fmaxf(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
-      v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, 1));
-      v1 = fmaxf(v1, __shfl_xor_sync(0xffffffffu, v1, 2));
+      if (h1ok) { v0 = max_nan(v0, c[1]); v1 = max_nan(v1, c[3]); }
+      v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, v0, 1));
+      v0 = max_nan(v0, __shfl_xor_sync(0xffffffffu, v0, 2));
+      v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, v1, 1));
+      v1 = max_nan(v1, __shfl_xor_sync(0xffffffffu, v1, 2));
       if (m == 0) {
         const int pr = ((t0 + u * NW) << 4) + r;
 #pragma unroll
@@ -292,8 +310,8 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
           if (i < nloc) {
             const int p = p0 + i;
             const bool forced = p < a.n_sink || p >= first_local;
-            const uint32_t key = forced ? kForcedKey : float_key(half ? v1 : v0);
-            keys[i] = key;
+            const uint32_t key = forced ? kForcedKey : score_key(half ? v1 : v0);
+                keys[i] = key;
             if constexpr (STAGE) {
               if (skeys) skeys[i] = key;
               kr.add(key);
@@ -500,7 +518,8 @@ __device__ __forceinline__ bool narrow_to_rank(const uint32_t* keys, int n, uint
 // the top reaches want.  The bin of a score is monotone in the score, so the
 // keys sent are exactly those >= tau, the smallest key sent; no exact local
 // rank is needed.  The candidates are written in page order; tau = 0 means
-// the CTA sent every key.  The top-k CTA later proves that its result is
+// the CTA sent every key, as one with a page without a score does (its
+// range is no number).  The top-k CTA later proves that its result is
 // exact: its k-th key T must be >= every CTA's tau, so that no unsent key can
 // reach T.  The scorer also writes the CTA's keys to shared memory when its
 // chunk holds at most kCandStage pages; otherwise they are read back from
@@ -758,34 +777,43 @@ topk_wide_kernel(const SelectArgs a) {
     }
     __syncthreads();
     // 3. forced keys and the largest other candidate
-    uint32_t top = 0;
-    int nf = 0;
-    for (int i = tid; i < n; i += NT) {
-      const uint32_t kk = skey[i];
-      if (kk == kForcedKey) ++nf;
-      else top = max(top, kk);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      nf += __shfl_xor_sync(0xffffffffu, nf, o);
-    }
-    if (lane == 0) {
-      sh.w.red[warp] = top;
-      sh.w.red_n[warp] = nf;
-    }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t t = 0;
-      int f = 0;
-      for (int w = 0; w < NWp; ++w) {
-        t = max(t, sh.w.red[w]);
-        f += sh.w.red_n[w];
+    auto range = [&] {
+      uint32_t top = 0;
+      int nf = 0;
+      for (int i = tid; i < n; i += NT) {
+        const uint32_t kk = skey[i];
+        if (kk == kForcedKey) ++nf;
+        else top = max(top, kk);
       }
-      sh.w.top = t;
-      sh.w.nforced = f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        nf += __shfl_xor_sync(0xffffffffu, nf, o);
+      }
+      if (lane == 0) {
+        sh.w.red[warp] = top;
+        sh.w.red_n[warp] = nf;
+      }
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t t = 0;
+        int f = 0;
+        for (int w = 0; w < NWp; ++w) {
+          t = max(t, sh.w.red[w]);
+          f += sh.w.red_n[w];
+        }
+        sh.w.top = t;
+        sh.w.nforced = f;
+      }
+      __syncthreads();
+    };
+    range();
+    if (sh.w.top == kNoScoreKey) {  // uniform: pages without a score (all of their CTA's keys were sent)
+      for (int i = tid; i < n; i += NT)
+        if (skey[i] == kNoScoreKey) skey[i] = page_key_again(a, row, spage[i]);
+      __syncthreads();
+      range();
     }
-    __syncthreads();
     const int need = a.k - sh.w.nforced;
     if (need <= 0) {
       if (tid == 0) {
@@ -867,6 +895,11 @@ topk_wide_kernel(const SelectArgs a) {
   // fallback: every key of the row, from global memory
   __syncthreads();
   if (tid == 0) atomicAdd(&g_select_rows_all_keys, 1ull);
+  for (int i = tid; i < NP; i += NT) {
+    uint32_t* key = a.keys + (size_t)row * a.npcap + i;
+    if (__ldcg(key) == kNoScoreKey) *key = page_key_again(a, row, i);
+  }
+  __syncthreads();
   row_topk<NT>(a.keys + (size_t)row * a.npcap, NP, a.k, 0, out, sh.radix);
 }
 
@@ -941,25 +974,37 @@ topk_reg_kernel(const SelectArgs a) {
     kk[j] = i < n ? __ldcg(src + i) : 0u;
   }
   // 1. largest non-forced top-16 value, forced count; clear the window
-  uint32_t mx = 0;
-  int nf = 0;
+  uint32_t top;
+  int nforced;
+  auto range = [&] {
+    uint32_t mx = 0;
+    int nf = 0;
 #pragma unroll
-  for (int j = 0; j < KPT; ++j) {
-    if (kk[j] == kForcedKey) ++nf;
-    else mx = max(mx, kk[j] >> 16);
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  nf = __reduce_add_sync(0xffffffffu, nf);
-  if (lane == 0) {
-    red_max[warp] = mx;
-    red_nf[warp] = nf;
-  }
+    for (int j = 0; j < KPT; ++j) {
+      if (kk[j] == kForcedKey) ++nf;
+      else mx = max(mx, kk[j] >> 16);
+    }
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    nf = __reduce_add_sync(0xffffffffu, nf);
+    if (lane == 0) {
+      red_max[warp] = mx;
+      red_nf[warp] = nf;
+    }
+    __syncthreads();
+    top = __reduce_max_sync(0xffffffffu, lane < NWp ? red_max[lane] : 0u);
+    nforced = __reduce_add_sync(0xffffffffu, lane < NWp ? red_nf[lane] : 0);
+  };
 #pragma unroll
   for (int i = 0; i < BPT; ++i) hist[tid * BPT + i] = 0;
   if (tid == 0) s_ncand = 0;
-  __syncthreads();
-  const uint32_t top = __reduce_max_sync(0xffffffffu, lane < NWp ? red_max[lane] : 0u);
-  const int nforced = __reduce_add_sync(0xffffffffu, lane < NWp ? red_nf[lane] : 0);
+  range();
+  if (top == kNoScoreKey >> 16) {  // pages without a score
+#pragma unroll
+    for (int j = 0; j < KPT; ++j)
+      if (kk[j] == kNoScoreKey) kk[j] = page_key_again(a, row, tid * KPT + j);
+    __syncthreads();  // every thread has read the first range
+    range();
+  }
   const int need = k - nforced;
   bool fast = true;
   uint32_t T = kForcedKey;
@@ -1087,6 +1132,12 @@ constexpr int kFusedRank = 96;                     // keys ranked exactly
 // and 13.9).
 constexpr int kFusedWide = 512, kFusedMany = 256;
 static_assert(kFusedMany == kSelThreads, "the CUDA-core scorer's threads");
+// Registers as for one CTA an SM where that is how they run, and for up to four fp32 heads (64 rows of 4096 pages of bf16 and D = 64:
+// 23.0 us as the compiler chooses, 19.7 so; 32 fp32 rows of 2048 pages of 4 heads and D = 128: 40.0 and 37.0; but 200 rows of
+// 512 pages of 8 fp32 heads 54 and 89, of bf16 15.0 and 23.4).
+constexpr int fused_min_ctas(int mode, int heads, int threads) {
+  return threads == kFusedWide || (mode == 0 && heads <= 4) ? 1 : 0;
+}
 
 struct FusedShared {
   uint32_t hist[2048];
@@ -1097,7 +1148,7 @@ struct FusedShared {
 };
 
 template <typename T, int D, int GM, int MODE, int NT>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, fused_min_ctas(MODE, GM, NT))
 paged_select_kernel(const SelectArgs a, int cluster) {
   namespace cg = cooperative_groups;
   constexpr int NW = NT / 32;
@@ -1159,6 +1210,16 @@ paged_select_kernel(const SelectArgs a, int cluster) {
     lo = min(lo, sh.lo[w]);
     hi = max(hi, sh.hi[w]);
     nf += sh.nf[w];
+  }
+  if (hi == kNoScoreKey) {  // pages without a score get one; the range is that of every key then
+#pragma unroll 1
+    for (int i = i0; i < min(i0 + per, NP); ++i)
+      if (skeys[i] == kNoScoreKey) skeys[i] = page_key_again(a, row, i);
+#pragma unroll
+    for (int j = 0; j < kFusedKeep; ++j)
+      if (kk[j] == kNoScoreKey) kk[j] = skeys[i0 + j];
+    lo = 1;  // above the empty places' 0
+    __syncthreads();
   }
   // T, the k-th largest key, and how many of those equal to it are taken
   uint32_t Tk = kForcedKey;
@@ -1310,6 +1371,7 @@ static cudaError_t select_launch(const Shape& s, const void* q, const void* kmin
   a.q = q; a.kmin = kmin; a.kmax = kmax; a.ctx_len = ctx_len; a.page_idx = page_idx;
   a.keys = static_cast<uint32_t*>(ws);
   a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
+  a.D = s.D; a.f32 = s.dtype == 0;
   a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift;
   a.npcap = s.Cap >> s.pshift;
   a.chunk = 0;
@@ -1402,7 +1464,8 @@ cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, i
     SelectArgs a = {};
     a.q = q; a.kmin = c.kmin; a.kmax = c.kmax; a.ctx_len = c.ctx; a.page_idx = page_idx;
     a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
-    a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift; a.npcap = npcap;
+    a.D = s.D; a.f32 = s.dtype == 0;
+  a.Hq = s.Hq; a.Hkv = s.Hkv; a.G = s.G; a.Cap = s.Cap; a.P = s.P; a.pshift = s.pshift; a.npcap = npcap;
     a.table = c.table; a.pool = c.pages;
     cudaError_t e;
     if (wide)
