@@ -95,7 +95,7 @@ typedef int sls_status;
 /* Test hook of the bounded waits, not for production: in the tensor-map fed
  * kernels (sls_sparse_decode_attend[_combine] on bf16 pages of >= 16 tokens,
  * the one-launch sls_quest_decode_step, sls_kv8_decode_attend and
- * sls_paged_decode_attend), the first CTA of the launch (of the paged attend, the
+ * sls_paged_decode_attend), the first CTA of the launch (of the last two, the
  * first one that has tokens) announces 16 bytes on its first attend stage that it never requests, and
  * that CTA's waits poll a short while only.  The waits on that stage
  * give up, the first row's outputs become NaN, and the next

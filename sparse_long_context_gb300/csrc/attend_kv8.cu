@@ -449,7 +449,10 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
   row = row_at(lo, 0);
   }
 
-  const bool plant = a.test_wait && cta == 0 && warp == 0;  // the wait-timeout test hook
+  // the wait-timeout test hook: the first CTA with a unit (ranges of CTAs before it may be empty, and so may rows)
+  bool plant = a.test_wait && lo == 0 && hi > 0 && warp == 0;
+  if constexpr (CL)
+    for (int r0 = 0; plant && r0 < row; ++r0) plant = units_of(r0) == 0;
   const uint32_t tries = plant ? kTestWaitTries : kWaitTries;
   const uint32_t wring = smem_u32(ring) + (uint32_t)warp * S * L::STAGE;
   uint32_t wseq = 0;  // this warp's ring position
