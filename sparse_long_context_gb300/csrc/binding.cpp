@@ -209,6 +209,8 @@ PyObject* kv8_decode_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (!a.none(4)) {
       const at::Tensor& p = a.any(4, "page_idx");
       if (p.dim() != 2 || p.size(1) > INT32_MAX) bad("page_idx must be [B * Hkv, entries], got " + text(p.sizes()));
+      // a list without columns has no memory, and no pointer to it means every page
+      if (p.size(1) < 1) bad("page_idx must have at least one entry a row (count says how many hold)");
       stride = p.size(1);
       pages = a.data<int32_t>(4, "page_idx", I32, {B * H, stride});
       count = a.data<int32_t>(5, "count", I32, {B * H});

@@ -36,6 +36,16 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _list_width(page_idx) -> int:
+    """Entries a row of optional page lists.  Lists without columns have no memory, and no pointer to one means every page."""
+    if page_idx is None:
+        return 0
+    if page_idx.dim() != 2 or page_idx.shape[1] < 1:
+        raise ValueError("page_idx must be [rows, entries] with at least one entry a row (count says how many hold), got "
+                         f"{tuple(page_idx.shape)}")
+    return int(page_idx.shape[1])
+
+
 def make_desc(batch, num_q_heads, num_kv_heads, head_dim, page_size, capacity, dtype,
               scale: float = 0.0, cuda_cores: bool = False, no_tma: bool = False,
               test_wait_timeout: bool = False) -> L.AttnDesc:
@@ -213,7 +223,7 @@ def sparse_decode_attend(desc: L.AttnDesc, q, k_cache, v_cache, page_idx, ctx_le
     _need(k_cache, "k_cache")
     _need(v_cache, "v_cache")
     o, m, l = partials(desc, num_splits, q.device) if parts is None else parts
-    stride = int(page_idx.shape[1]) if page_idx is not None else 0
+    stride = _list_width(page_idx)
     kf = stride if k_fixed is None else int(k_fixed)
     L.call("sls_sparse_decode_attend", ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
            _ptr(page_idx), stride, _ptr(count), kf, _ptr(ctx_len), int(num_splits), _ptr(o),
@@ -242,7 +252,7 @@ def sparse_decode_attend_combine(desc: L.AttnDesc, q, k_cache, v_cache, page_idx
     if sink is not None:
         _need(sink, "sink", torch.float32, (Hq,))
     workspace = attend_combine_workspace(desc, num_splits, q.device) if workspace is None else workspace
-    stride = int(page_idx.shape[1]) if page_idx is not None else 0
+    stride = _list_width(page_idx)
     kf = stride if k_fixed is None else int(k_fixed)
     L.call("sls_sparse_decode_attend_combine", ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(v_cache),
            _ptr(page_idx), stride, _ptr(count), kf, _ptr(ctx_len), int(num_splits), _ptr(sink),
@@ -349,7 +359,7 @@ def selection_recall(desc: L.AttnDesc, q, k_cache, page_idx, ctx_len, count=None
         if recall is None else recall
     n = L.load().sls_selection_recall_workspace_size(ctypes.byref(desc))
     workspace = torch.empty(max(int(n), 1), dtype=torch.uint8, device=q.device) if workspace is None else workspace
-    stride = int(page_idx.shape[1]) if page_idx is not None else 0
+    stride = _list_width(page_idx)
     kf = stride if k_fixed is None else int(k_fixed)
     L.call("sls_selection_recall", ctypes.byref(desc), _ptr(q), _ptr(k_cache), _ptr(page_idx), stride, _ptr(count),
            kf, _ptr(ctx_len), _ptr(recall), _ptr(workspace), workspace.numel(), _stream())
