@@ -98,7 +98,8 @@ typedef int sls_status;
  * sls_paged_decode_attend), the first CTA of the launch (of the last two, the
  * first one that has tokens) announces 16 bytes on its first attend stage that it never requests, and
  * that CTA's waits poll a short while only.  The waits on that stage
- * give up, the first row's outputs become NaN, and the next
+ * give up, the first row's outputs become NaN (and those of the rows that the
+ * same CTA works on after it), and the next
  * sls_pipeline_check() returns SLS_ETIMEOUT.  No copy is issued for the
  * announced bytes, so nothing faults and nothing waits forever. */
 #define SLS_FLAG_TEST_WAIT_TIMEOUT 4

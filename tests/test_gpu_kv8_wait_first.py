@@ -30,9 +30,12 @@ def test_wait_that_gives_up_is_that_of_the_first_tokens(cap, lens):
     with pytest.raises(L.SlsError) as err:
         ops.pipeline_check()
     assert err.value.code == L.SLS_ETIMEOUT
+    # that CTA issues no copies any more, so its later rows (of a range; a cluster has one row) have no answer either
     first = next(i for i, n in enumerate(lens) if n)
-    keep = torch.arange(batch) != first
-    assert out[first].isnan().all() and lse[first].isnan().all()
+    keep = ~lse.isnan().any(1).cpu()
+    lost = (~keep).nonzero().flatten().tolist()
+    assert lost == list(range(first, first + len(lost))) and len(lost) >= 1 and (cap > 4096 or len(lost) == 1)
+    assert out[~keep].isnan().all() and lse[~keep].isnan().all()
     assert torch.equal(out[keep], ref[keep]) and torch.equal(lse[keep], ref_lse[keep])
     again, _ = ops.kv8_decode_attend(desc, cache, q, ctx, workspace=ws)
     ops.pipeline_check()
