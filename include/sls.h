@@ -821,7 +821,8 @@ size_t sls_paged_decode_attend_workspace_size(const sls_attn_desc* desc);
  *   desc      G <= 8, D 64 or 128, B*Hkv <= 4096; of the flags only
  *             SLS_FLAG_TEST_WAIT_TIMEOUT
  *   page_idx, idx_stride, count, k_fixed   as in sls_sparse_decode_attend
- *             (-1 entries are skipped, bad ones counted and skipped)
+ *             (-1 entries are skipped, bad ones counted and skipped); count
+ *             only with page_idx
  *   q [B, Hq, D] dtype; sink [Hq] float or NULL; out [B, Hq, D] dtype; lse
  *             [B, Hq] float or NULL
  *   workspace >= sls_paged_decode_attend_workspace_size() bytes, 16-byte

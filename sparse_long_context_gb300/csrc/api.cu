@@ -1049,6 +1049,8 @@ sls_status sls_paged_decode_attend(const sls_attn_desc* desc, const sls_paged_ca
       return fail(SLS_EOVERFLOW, "idx_stride %d pages of %d tokens", idx_stride, s.P);
     if (!count && (k_fixed < 0 || k_fixed > idx_stride))
       return fail(SLS_EINVAL, "k_fixed %d not in [0, idx_stride=%d]", k_fixed, idx_stride);
+  } else if (count) {
+    return fail(SLS_EINVAL, "count without page_idx");
   }
   const size_t need = sls::paged_attend_workspace(s);
   if (!workspace || workspace_bytes < need)
@@ -1057,7 +1059,7 @@ sls_status sls_paged_decode_attend(const sls_attn_desc* desc, const sls_paged_ca
   const int64_t rows = (int64_t)s.B * s.Hkv, heads = (int64_t)s.B * s.Hq, e = s.dtype == SLS_DTYPE_F32 ? 4 : 2;
   if ((r = check_paged_apart(sp, {at(out, heads * s.D * e), at(lse, heads * 4), at(workspace, (int64_t)need),
                                   at(q, heads * s.D * e), at(page_idx, rows * idx_stride * 4),
-                                  at(page_idx ? count : nullptr, rows * 4), at(sink, (int64_t)s.Hq * 4)}, 3)))
+                                  at(count, rows * 4), at(sink, (int64_t)s.Hq * 4)}, 3)))
     return r;
   return cuda_status(sls::launch_paged_attend(s, c, q, page_idx, idx_stride, count, k_fixed, sink, out, lse, workspace,
                                               (cudaStream_t)stream),

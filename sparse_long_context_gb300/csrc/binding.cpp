@@ -331,6 +331,8 @@ PyObject* paged_decode_attend(PyObject*, PyObject* const* args, Py_ssize_t n) {
       pages = a.data<int32_t>(3, "page_idx", I32, {B * H, stride});
       count = a.data<int32_t>(4, "count", I32, {B * H});
       fixed = a.none(5) ? (int32_t)stride : word(a, 5, "k_fixed");
+    } else if (!a.none(4) || !a.none(5)) {
+      bad("count and k_fixed say how much of page_idx holds, and there is no page_idx");
     }
     const float* sink = a.data<float>(6, "sink", F32, {Hq});
     void* out = a.tensor(7, "out", dt, {B, Hq, D}).data_ptr();

@@ -45,3 +45,20 @@ def test_eight_bit_cache():
         ops.kv8_decode_attend(desc, cache, q, lens, page_idx=NONE.cuda())
     out, lse = ops.kv8_decode_attend(desc, cache, q, lens, page_idx=torch.full((4, 1), -1, dtype=torch.int32, device="cuda"))
     assert not out.any() and bool((lse == -torch.inf).all())
+
+
+def test_counts_without_lists_of_a_paged_cache():
+    desc, q, k, v, ctx = setup()
+    cache = ops.PagedCache.empty(desc, 40)
+    ops.paged_append(desc, cache, k.transpose(1, 2).contiguous(), v.transpose(1, 2).contiguous(), new_len=ctx)
+    count = torch.ones(4, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError, match="count"):
+        ops.paged_decode_attend(desc, cache, q, count=count)
+    with pytest.raises(ValueError, match="k_fixed"):
+        ops.paged_decode_attend(desc, cache, q, k_fixed=3)
+    ops.paged_decode_attend(desc, cache, q)
+    lists = torch.arange(3, dtype=torch.int32, device="cuda").repeat(4, 1)
+    one = ops.paged_decode_attend(desc, cache, q, page_idx=lists, count=count)
+    fixed = ops.paged_decode_attend(desc, cache, q, page_idx=lists, k_fixed=1)
+    assert torch.equal(one[0], fixed[0]) and torch.equal(one[1], fixed[1])
+    ops.pipeline_check()
