@@ -920,7 +920,7 @@ typedef struct sls_stats {
   uint64_t step_rows_dense;           /* rows the sparsity gate sent to dense attention */
   uint64_t step_rows_all_keys;        /* rows whose cluster selected from all of the row's keys
                                          (long rows, or the candidate check failed) */
-  uint64_t select_pages;              /* sls_select_pages(_static) launches */
+  uint64_t select_pages;              /* sls_select_pages(_static) and sls_paged_select_pages calls */
   uint64_t select_delta_tensor_cores; /* top-delta scans on the tensor cores */
   uint64_t select_delta_cuda_cores;   /* ... on the CUDA cores (fp32, or the CUDA-core flag) */
   uint64_t attend_tma;                /* split-K attends by kernel: tensor-map fed, */
@@ -937,9 +937,13 @@ typedef struct sls_stats {
                                          ranked all of the row's keys (the candidate check failed) */
   uint64_t attend_stream_k_tma;       /* of attend_stream_k: the tensor-map fed kernel */
   uint64_t attend_refined_tma;        /* of attend_refined: the tensor-map fed kernel */
+  uint64_t attend_kv8;                /* attends over an 8-bit cache */
+  uint64_t attend_paged;              /* attends over a paged cache */
+  uint64_t select_paged_one_launch;   /* of select_pages: selections over a paged cache run as one kernel */
 } sls_stats;
 
-/* Fills *out with the counters (synchronising the device to read the row
+/* Fills *out (the sls_stats of this header: counters are added at its end)
+ * with the counters (synchronising the device to read the row
  * counters); reset != 0 zeroes them.  SLS_EINVAL for a NULL out. */
 sls_status sls_get_stats(sls_stats* out, int32_t reset);
 

@@ -141,6 +141,9 @@ sls_status sls_get_stats(sls_stats* out, int32_t reset) {
   out->recall = take(sls::kStatRecall);
   out->attend_stream_k_tma = take(sls::kStatAttendStreamKTma);
   out->attend_refined_tma = take(sls::kStatAttendRefinedTma);
+  out->attend_kv8 = take(sls::kStatAttendKv8);
+  out->attend_paged = take(sls::kStatAttendPaged);
+  out->select_paged_one_launch = take(sls::kStatSelectPagedOneLaunch);
   if (cudaDeviceSynchronize() != cudaSuccess) return fail(SLS_ECUDA, "device synchronisation failed");
   unsigned long long dense = 0, all_keys = 0;
   sls::take_step_row_stats(&dense, &all_keys, reset != 0);
@@ -802,6 +805,7 @@ sls_status sls_kv8_decode_attend(const sls_attn_desc* desc, const sls_kv8_cache*
     for (int j = 0; j < i; ++j)
       if (overlap(to[i].p, to[i].n, to[j].p, to[j].n)) return fail(SLS_EINVAL, "two outputs (or one and the workspace) share memory");
   }
+  sls::stat_add(sls::kStatAttendKv8);
   return cuda_status(sls::launch_kv8_attend(s, c, q, page_idx, idx_stride, count, k_fixed, ctx_len, sink, out, lse,
                                             mass_in, mass_out, workspace, (cudaStream_t)stream),
                      "sls_kv8_decode_attend");
@@ -1061,6 +1065,7 @@ sls_status sls_paged_decode_attend(const sls_attn_desc* desc, const sls_paged_ca
                                   at(q, heads * s.D * e), at(page_idx, rows * idx_stride * 4),
                                   at(count, rows * 4), at(sink, (int64_t)s.Hq * 4)}, 3)))
     return r;
+  sls::stat_add(sls::kStatAttendPaged);
   return cuda_status(sls::launch_paged_attend(s, c, q, page_idx, idx_stride, count, k_fixed, sink, out, lse, workspace,
                                               (cudaStream_t)stream),
                      "sls_paged_decode_attend");

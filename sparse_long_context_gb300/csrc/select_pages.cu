@@ -1461,6 +1461,7 @@ cudaError_t launch_paged_select(const Shape& s, const Paged& c, const void* q, i
   const int rows = s.B * s.Hkv, npcap = s.Cap >> s.pshift;
   const bool wide = s.dtype == 1 && rows <= sm_count();
   if (!(s.flags & 1) && npcap <= kFusedKeep * (wide ? kFusedWide : kFusedMany)) {  // a row's keys in one CTA's threads
+    stat_add(kStatSelectPagedOneLaunch);
     SelectArgs a = {};
     a.q = q; a.kmin = c.kmin; a.kmax = c.kmax; a.ctx_len = c.ctx; a.page_idx = page_idx;
     a.k = k; a.n_sink = n_sink_pages; a.n_local = n_local_tokens;
