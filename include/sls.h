@@ -272,7 +272,7 @@ sls_status sls_select_pages(const sls_attn_desc* desc, const void* q,
                             size_t workspace_bytes, void* stream);
 
 /* Bytes of workspace sls_select_pages needs for this descriptor (0 if the
- * descriptor is invalid). */
+ * descriptor is invalid or its rows hold too many pages). */
 size_t sls_select_pages_workspace_size(const sls_attn_desc* desc);
 
 /*

@@ -268,7 +268,7 @@ sls_status sls_thumb_residual_update(const sls_attn_desc* desc, const void* k_ca
 
 size_t sls_select_pages_workspace_size(const sls_attn_desc* desc) {
   sls::Shape s;
-  if (check_desc(desc, &s)) return 0;
+  if (check_desc(desc, &s) || (s.Cap >> s.pshift) > sls::select_pages_max_pages()) return 0;
   return sls::select_pages_workspace(s);
 }
 

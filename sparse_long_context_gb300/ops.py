@@ -948,6 +948,9 @@ class PagedDecode:
             if min(n_sink_pages, n_local_tokens) < 0 or not max(1, forced) <= k_budget <= desc.capacity // desc.page_size:
                 raise ValueError(f"k_budget {k_budget} must hold the forced pages (up to {forced}) and be at most the "
                                  f"{desc.capacity // desc.page_size} pages of a sequence")
+            if not L.load().sls_select_pages_workspace_size(ctypes.byref(desc)):
+                raise ValueError("the selection does not take this descriptor (262144 pages a sequence at most, got "
+                                 f"{desc.capacity // desc.page_size})")
         if not L.load().sls_paged_decode_attend_workspace_size(ctypes.byref(desc)):
             raise ValueError("the paged attend does not take this descriptor")
         B, Hq, H, D = desc.batch, desc.num_q_heads, desc.num_kv_heads, desc.head_dim
