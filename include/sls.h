@@ -818,11 +818,12 @@ size_t sls_paged_decode_attend_workspace_size(const sls_attn_desc* desc);
  * < ctx_len[b] (page_idx NULL) or over the valid tokens of the listed LOGICAL
  * pages, with the sink as in sls_combine_splits.  Rows of uneven length are cut
  * into equal ranges over the GPU.
- *   desc      G <= 8, D 64 or 128, B*Hkv <= 4096; of the flags only
- *             SLS_FLAG_TEST_WAIT_TIMEOUT
+ *   desc      G <= 8, D 64 or 128, B*Hkv <= 4096, B*Hkv*(Cap/16 + 1) < 2^30;
+ *             of the flags only SLS_FLAG_TEST_WAIT_TIMEOUT
  *   page_idx, idx_stride, count, k_fixed   as in sls_sparse_decode_attend
  *             (-1 entries are skipped, bad ones counted and skipped); count
- *             only with page_idx
+ *             only with page_idx; idx_stride*P < 2^31 and
+ *             B*Hkv*idx_stride*(P/16) <= 2^30, else SLS_EOVERFLOW
  *   q [B, Hq, D] dtype; sink [Hq] float or NULL; out [B, Hq, D] dtype; lse
  *             [B, Hq] float or NULL
  *   workspace >= sls_paged_decode_attend_workspace_size() bytes, 16-byte
