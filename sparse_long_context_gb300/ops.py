@@ -595,11 +595,12 @@ class PagedCache:
     def load(self, table, ctx_len):
         """Takes over a table [B, Cap/P] and lengths [B] made elsewhere (paged_init)."""
         self._beside(torch._C._cuda_getDevice(), self.desc())  # before anything changes
-        for t, mine, name in ((table, self.table, "table"), (ctx_len, self.ctx_len, "ctx_len")):
-            if t.shape != mine.shape or t.is_floating_point():
+        both = ((table, self.table, "table"), (ctx_len, self.ctx_len, "ctx_len"))
+        for t, mine, name in both:
+            if t.shape != mine.shape or t.dtype not in (torch.int64, torch.int32, torch.int16, torch.int8, torch.uint8):
                 raise ValueError(f"{name} must be integers of shape {tuple(mine.shape)}, got {t.dtype} {tuple(t.shape)}")
-        self.table.copy_(table)
-        self.ctx_len.copy_(ctx_len)
+        for t, mine, _ in both:  # numbers that 32 bits cannot hold stay out of range
+            mine.copy_(t.clamp(-1 << 31, (1 << 31) - 1) if t.dtype == torch.int64 else t)
         paged_init(self.desc(), self)
 
     def desc(self) -> L.AttnDesc:

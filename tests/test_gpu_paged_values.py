@@ -1,5 +1,5 @@
 """The paged cache where its other tests compare calls with each other: lists cut by count and k_fixed, steps captured in a graph and
-the positions of a step, against the plain form; repeated calls."""
+the positions of a step, against the plain form; tables and lengths of 64 bits; repeated calls."""
 import math
 
 import numpy as np
@@ -102,6 +102,32 @@ def test_a_captured_run_gives_what_the_same_run_gives_without_a_graph():
             assert same(getattr(one.cache, name), getattr(two.cache, name)), name
         assert two.ctx_len.tolist() == p.ctx and torch.equal(two.cache.table.cpu(), p.table()) and two.done.item() == 1
     ops.pipeline_check()
+
+
+def test_tables_and_lengths_of_64_bits_keep_their_values():
+    """A number that 32 bits cannot hold stays what it is: a page that does not exist, a length above the capacity."""
+    pair = Pair(2, 2, 1, 64, 16, 64, 8, summaries=False)
+    pair.append([64, 20])
+    table, lens = pair.cache.table.long().cpu(), pair.cache.ctx_len.long().cpu()
+    for dev in ("cpu", "cuda"):
+        odd, long = table.clone(), lens.clone()
+        odd[0, 1] += 1 << 32
+        odd[0, 2] = -(1 << 32) + 3
+        long[1] = (1 << 32) + 20
+        odd[1] = torch.tensor([4, 5, 6, 7])
+        pair.cache.load(odd.to(dev), long.to(dev))
+        with pytest.raises(L.SlsError, match="2 page-list entries"):
+            ops.pipeline_check()
+        held = pair.cache.table.cpu()
+        assert not 0 <= held[0, 1] < 8 and not 0 <= held[0, 2] < 8 and held[0, [0, 3]].tolist() == table[0, [0, 3]].tolist()
+        refs = [0] * 8
+        for p in (int(table[0, 0]), int(table[0, 3]), 4, 5, 6, 7):  # all four pages: the length counts as the capacity
+            refs[p] += 1
+        assert pair.cache.refs.tolist() == refs
+        with pytest.raises(ValueError, match="integers"):
+            pair.cache.load(odd.bool().to(dev), lens.to(dev))
+    pair.cache.load(table, lens)
+    pair.check()
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
