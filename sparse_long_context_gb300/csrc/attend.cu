@@ -206,8 +206,8 @@ attend_cc_kernel(const AttendArgs a) {
 // normaliser; the accumulators of up to 8 splits are loaded together.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-combine_kernel(const float* __restrict__ o_part, const float* __restrict__ m_part,
-               const float* __restrict__ l_part, int S, const float* __restrict__ sink,
+combine_kernel(const float* o_part, const float* m_part,
+               const float* l_part, int S, const float* sink,
                T* __restrict__ out, float* __restrict__ lse, int Hq, int total) {
   pdl_wait_then_release();
   constexpr int CPL = D / 32;

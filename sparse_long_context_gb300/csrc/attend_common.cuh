@@ -59,7 +59,7 @@ __device__ __forceinline__ void stage_page_list(int* s_pg, int cap, const int32_
                                                 int npages, int tid, int nthreads) {
   unsigned int bad = 0;
   for (int e = tid; e < nent; e += nthreads) {
-    const int pg = plist ? __ldg(plist + e) : e0 + e;
+    const int pg = plist ? ld_global(plist + e) : e0 + e;
     if (e < cap) s_pg[e] = pg;
     bad += bad_page_id(pg, npages) ? 1u : 0u;
   }

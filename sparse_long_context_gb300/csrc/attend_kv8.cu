@@ -473,7 +473,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     auto load_q = [&](uint2 (&raw)[KS]) {
 #pragma unroll
       for (int c = 0; c < KS; ++c)
-        raw[c] = r < G ? __ldg(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
+        raw[c] = r < G ? ld_global(reinterpret_cast<const uint2*>(qh + 16 * c + 4 * m)) : make_uint2(0u, 0u);
     };
     uint32_t qa[KS][2];
     float qmul;
@@ -530,7 +530,7 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         if (k < nk && g < ng) {
           int at = g << 4;
           if constexpr (LIST) {
-            const int pg = __ldg(list + (at >> a.pshift)), in = at & (a.P - 1);
+            const int pg = ld_global(list + (at >> a.pshift)), in = at & (a.P - 1);
             // counted once: by the unit holding the page's first group, when first loaded
             bad += in == 0 && (kb == 0 || lane >= S - 1) && bad_page_id(pg, a.Cap >> a.pshift);
             at = (unsigned)pg < (unsigned)(a.Cap >> a.pshift) ? (pg << a.pshift) + in : a.Cap;
@@ -538,8 +538,8 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           if (at < N) {
             base[s] = at;
             if (at >> a.c.bshift < newest) {
-              ksc[s] = __ldg(a.c.ks + row_blk + (at >> a.c.bshift));
-              vsc[s] = __ldg(a.c.vs + row_blk + (at >> a.c.bshift));
+              ksc[s] = ld_global(a.c.ks + row_blk + (at >> a.c.bshift));
+              vsc[s] = ld_global(a.c.vs + row_blk + (at >> a.c.bshift));
             }
           }
         }

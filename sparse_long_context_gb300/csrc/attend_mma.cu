@@ -70,7 +70,7 @@ __device__ __forceinline__ void group_positions(const AttendArgs& a, const Seg& 
     if (j0 < ntok) {
       const int J = sl.joff + j0;
       const int e = J >> a.pshift;
-      const int pg = e < kStagedEntries ? s_pg[e] : (plist ? __ldg(plist + e) : sl.e0 + e);
+      const int pg = e < kStagedEntries ? s_pg[e] : (plist ? ld_global(plist + e) : sl.e0 + e);
       if ((unsigned)pg < (unsigned)(a.Cap >> a.pshift)) {
         base = (pg << a.pshift) + (J & (a.P - 1));
         lim = min(sl.N - base, ntok - j0);  // inside the context and inside the run
@@ -89,7 +89,7 @@ __device__ __forceinline__ void group_positions(const AttendArgs& a, const Seg& 
     if (j < ntok) {
       const int J = sl.joff + j;
       const int e = J >> a.pshift;
-      const int pg = e < kStagedEntries ? s_pg[e] : (plist ? __ldg(plist + e) : sl.e0 + e);
+      const int pg = e < kStagedEntries ? s_pg[e] : (plist ? ld_global(plist + e) : sl.e0 + e);
       mypos = token_position(a, pg, J, sl.N);
     }
     pk0 = __shfl_sync(0xffffffffu, mypos, r);

@@ -98,7 +98,7 @@ struct PgBf16 {
     for (int c = 0; c < KS; ++c)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        qa[c][i] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(q + r * D + 16 * c + 8 * i + 2 * m)) : 0u;
+        qa[c][i] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(q + r * D + 16 * c + 8 * i + 2 * m)) : 0u;
 #pragma unroll
     for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
     m_run = kNegInf;
@@ -254,7 +254,7 @@ struct PgF32 {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         const int h = g ^ (sl & (GM - 1));  // so that what a lane keeps when the lanes add up has fixed places
-        const float4 v = h < G ? __ldg(reinterpret_cast<const float4*>(qp + h * D + 32 * i + 4 * sl))
+        const float4 v = h < G ? ld_global(reinterpret_cast<const float4*>(qp + h * D + 32 * i + 4 * sl))
                                : make_float4(0.f, 0.f, 0.f, 0.f);
         q[g][i][0] = pg_f2(v.x, v.y);
         q[g][i][1] = pg_f2(v.z, v.w);
@@ -557,7 +557,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
           // entries are counted once: by the unit holding the page's first group, when first loaded
           const bool once = in == 0 && (kb == 0 || lane >= S - 1);
           if constexpr (LIST) {
-            lp = __ldg(list + lp);
+            lp = ld_global(list + lp);
             if ((unsigned)lp >= (unsigned)MP) {
               bad += once && lp != -1;
               continue;
@@ -565,7 +565,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constan
             pos = (lp << a.pshift) + in;
           }
           if (pos < N) {
-            const int page = __ldg(table + lp);
+            const int page = ld_global(table + lp);
             if (paged_page(page, a.pool)) {
               at[s] = ((page * a.Hkv + h) << a.pshift) + in;
               lim[s] = min(16, N - pos);

@@ -85,12 +85,12 @@ __device__ __forceinline__ void refined_fold(float (&sc)[2][2][4]) {
 
 __device__ __forceinline__ uint2 ldg_stream2(const void* p) {
   uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
   return r;
 }
 __device__ __forceinline__ uint32_t ldg_stream1(const void* p) {
   uint32_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.u32 %0, [%1];" : "=r"(r) : "l"(p));
   return r;
 }
 
@@ -145,7 +145,7 @@ __device__ __forceinline__ void load_rgroup(RGroup<D>& g, const RefinedArgs& ra,
   int base = -1, lim = 0, pg = -1;
   if (j0 < sl.ntok) {
     const int e = j0 >> a.pshift;
-    pg = e < kRefStaged ? s_pg[e] : __ldg(plist + e);
+    pg = e < kRefStaged ? s_pg[e] : ld_global(plist + e);
     if ((unsigned)pg < (unsigned)(a.Cap >> a.pshift)) {
       base = (pg << a.pshift) + (j0 & (a.P - 1));
       lim = min(sl.N - base, 16);
@@ -216,7 +216,7 @@ __device__ __forceinline__ void compute_rgroup(const RGroup<D>& g, const Refined
     for (int s = 0; s < NS; ++s) {
       uint32_t hi[4], lo[4];
       if (fresh) {
-        const uint4 s8 = __ldg(reinterpret_cast<const uint4*>(sp + 8 * s));
+        const uint4 s8 = ld_global(reinterpret_cast<const uint4*>(sp + 8 * s));
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           const uint32_t sw = (&s8.x)[p];
@@ -724,7 +724,7 @@ __device__ __forceinline__ int stream_group_base(const AttendArgs& a, int N, con
                                                  int gi, int& lim) {
   const int j0 = gi << 4;
   const int e = j0 >> a.pshift;
-  const int pg = s_pg && e < kRefStaged ? s_pg[e] : __ldg(plist + e);
+  const int pg = s_pg && e < kRefStaged ? s_pg[e] : ld_global(plist + e);
   lim = 0;
   if ((unsigned)pg >= (unsigned)(a.Cap >> a.pshift)) return 0;
   const int base = (pg << a.pshift) + (j0 & (a.P - 1));
@@ -824,8 +824,8 @@ attend_stream_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
     const bf16* qp = static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      qa[ks][0] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
-      qa[ks][1] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
+      qa[ks][0] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
+      qa[ks][1] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
     }
     bool ok = !failed;
     int k = 0;
@@ -993,7 +993,7 @@ attend_refined_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_c
     const int nblk = nent > warp ? (nent - warp + W - 1) / W : 0;  // this warp's blocks: warp + W j
     const int nk = nblk * gpb;
     const int* pg_src = nullptr;  // page ids from global memory until the list is staged
-    auto page_of = [&](int eb) { return eb < kRefStaged ? sh.s_pg[eb] : __ldg(plist + eb); };
+    auto page_of = [&](int eb) { return eb < kRefStaged ? sh.s_pg[eb] : ld_global(plist + eb); };
     // group k of this warp: group k % gpb of its block k / gpb
     auto group_of = [&](int k) { return (warp + W * (k / gpb)) * gpb + (k % gpb); };
     auto refined_at = [&](int base, int lim) { return lim > 0 && (((base >> a.pshift) + 1) << a.pshift) <= N; };
@@ -1031,7 +1031,7 @@ attend_refined_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_c
     {
       const uint4* qg = reinterpret_cast<const uint4*>(static_cast<const bf16*>(a.q) +
                                                        ((size_t)b * a.Hq + (size_t)h * G) * D);
-      for (int i = threadIdx.x; i < G * D / 8; i += NT) reinterpret_cast<uint4*>(s_q)[i] = __ldg(qg + i);
+      for (int i = threadIdx.x; i < G * D / 8; i += NT) reinterpret_cast<uint4*>(s_q)[i] = ld_global(qg + i);
     }
     __syncthreads();
     pg_src = sh.s_pg;
@@ -1051,7 +1051,7 @@ attend_refined_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_c
       const bool okp = (unsigned)pg < (unsigned)(a.Cap >> a.pshift);
 #pragma unroll
       for (int s = 0; s < NS; ++s)
-        sv[s] = okp ? __ldg(reinterpret_cast<const uint4*>(srow + (size_t)pg * D + 8 * s)) : make_uint4(0, 0, 0, 0);
+        sv[s] = okp ? ld_global(reinterpret_cast<const uint4*>(srow + (size_t)pg * D + 8 * s)) : make_uint4(0, 0, 0, 0);
     };
     if (nk > 0) load_scales(warp);
     uint32_t whi[NS][4], wlo[NS][4];

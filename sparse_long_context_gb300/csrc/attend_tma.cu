@@ -37,7 +37,7 @@ __device__ __forceinline__ int group_base(const AttendArgs& a, const Slice& sl, 
                                           const int32_t* plist, int gi, int& lim) {
   const int j0 = gi << 4;
   const int e = j0 >> a.pshift;
-  const int pg = e < kTmaStaged ? s_pg[e] : (plist ? __ldg(plist + e) : sl.e0 + e);
+  const int pg = e < kTmaStaged ? s_pg[e] : (plist ? ld_global(plist + e) : sl.e0 + e);
   lim = 0;
   if ((unsigned)pg >= (unsigned)(a.Cap >> a.pshift)) return 0;
   const int base = (pg << a.pshift) + (j0 & (a.P - 1));
@@ -134,8 +134,8 @@ attend_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const bf16* qp = static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      qa[ks][0] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
-      qa[ks][1] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
+      qa[ks][0] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
+      qa[ks][1] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
     }
     const float sl2 = a.qscale;
     const uint32_t ring_u32 = smem_u32(ring);

@@ -16,10 +16,31 @@ using bf16 = __nv_bfloat16;
 // Elements of T in one 16-byte vector.
 template <typename T> struct Vec16 { static constexpr int N = 16 / sizeof(T); };
 
-// Streaming 16-byte load through the read-only path, not kept in L1.
+// Loads.  None of a kernel's takes the read-only path: what it reads the kernel before may have written while this one already
+// waited for it, and that path is for data that nobody writes in a kernel's lifetime.
+
+// 4, 8 or 16 bytes.
+template <typename T>
+__device__ __forceinline__ T ld_global(const T* p) {
+  static_assert(sizeof(T) == 4 || sizeof(T) == 8 || sizeof(T) == 16, "a register, two or four");
+  union {
+    uint32_t w[sizeof(T) / 4];
+    T v;
+  } r;
+  if constexpr (sizeof(T) == 4)
+    asm volatile("ld.global.b32 %0, [%1];" : "=r"(r.w[0]) : "l"(p));
+  else if constexpr (sizeof(T) == 8)
+    asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "l"(p));
+  else
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "l"(p));
+  return r.v;
+}
+
+// Streaming 16-byte load, not kept in L1.
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }

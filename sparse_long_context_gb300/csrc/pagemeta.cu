@@ -51,7 +51,7 @@ pagemeta_build_kernel(const T* __restrict__ k, const int32_t* __restrict__ ctx_l
 // One warp per (b, kv head) row.
 template <typename T, int D>
 __global__ void __launch_bounds__(128)
-pagemeta_update_kernel(const T* __restrict__ k, const int32_t* __restrict__ pos, T* kmin,
+pagemeta_update_kernel(const T* k, const int32_t* pos, T* kmin,
                        T* kmax, int rows, int Hkv, int Cap, int P, int pshift) {
   constexpr int EPL = Vec16<T>::N;
   constexpr int L = D / EPL;
@@ -86,7 +86,7 @@ pagemeta_update_kernel(const T* __restrict__ k, const int32_t* __restrict__ pos,
 // the barrier; only then does thread 0 advance it.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-decode_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new, T* k, T* v, T* kmin, T* kmax,
+decode_append_kernel(const T* k_new, const T* v_new, T* k, T* v, T* kmin, T* kmax,
                      int32_t* ctx_len, int32_t* pos_out, int Hkv, int Cap, int P, int pshift) {
   // after the previous step (which reads ctx_len and the cache); the next
   // kernel of the loop may then start its launch, and waits for this one
@@ -96,21 +96,35 @@ decode_append_kernel(const T* __restrict__ k_new, const T* __restrict__ v_new, T
   __syncthreads();
   const bool ok = t >= 0 && t < Cap;
   if (ok) {
-    for (int i = threadIdx.x; i < Hkv * D; i += blockDim.x) {
-      const size_t row = (size_t)b * Hkv + i / D;
-      const int c = i % D;
-      const T kx = k_new[row * D + c];
-      k[(row * Cap + t) * D + c] = kx;
-      v[(row * Cap + t) * D + c] = v_new[row * D + c];
-      if (kmin) {
-        const size_t o = (row * (Cap >> pshift) + (t >> pshift)) * D + c;
-        if ((t & (P - 1)) == 0) {
-          kmin[o] = kx;
-          kmax[o] = kx;
-        } else {
-          const float x = to_f32<T>(kx);
-          kmin[o] = from_f32<T>(fminf(to_f32<T>(kmin[o]), x));
-          kmax[o] = from_f32<T>(fmaxf(to_f32<T>(kmax[o]), x));
+    constexpr int U = 4;  // elements of a thread whose loads are in flight together
+    const bool first = (t & (P - 1)) == 0;
+    for (int i0 = threadIdx.x; i0 < Hkv * D; i0 += U * blockDim.x) {
+      T kx[U], vx[U], lo[U], hi[U];
+      size_t at[U], meta[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * blockDim.x;
+        if (i >= Hkv * D) break;
+        const size_t row = (size_t)b * Hkv + i / D;
+        const int c = i % D;
+        at[u] = (row * Cap + t) * D + c;
+        meta[u] = (row * (Cap >> pshift) + (t >> pshift)) * D + c;
+        kx[u] = k_new[row * D + c];
+        vx[u] = v_new[row * D + c];
+        if (kmin && !first) {
+          lo[u] = kmin[meta[u]];
+          hi[u] = kmax[meta[u]];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (i0 + u * (int)blockDim.x >= Hkv * D) break;
+        k[at[u]] = kx[u];
+        v[at[u]] = vx[u];
+        if (kmin) {
+          const float x = to_f32<T>(kx[u]);
+          kmin[meta[u]] = first ? kx[u] : from_f32<T>(fminf(to_f32<T>(lo[u]), x));
+          kmax[meta[u]] = first ? kx[u] : from_f32<T>(fmaxf(to_f32<T>(hi[u]), x));
         }
       }
     }
@@ -145,7 +159,7 @@ __device__ __forceinline__ int8_t residual_code(float x, float s, uint32_t code)
 // Quantise block j of `row` (block tokens, all valid), and its residuals
 // when `res` is given.  blockDim.x == D.
 template <typename T, int D>
-__device__ __forceinline__ void quantise_block(const T* __restrict__ k, uint8_t* codes, T* scales,
+__device__ __forceinline__ void quantise_block(const T* k, uint8_t* codes, T* scales,
                                                int8_t* res, int row, int j, int Cap, int block, int nblk_cap) {
   __shared__ float s_half[D];
   const int c = threadIdx.x;
@@ -187,7 +201,7 @@ thumb_build_kernel(const T* __restrict__ k, const int32_t* __restrict__ ctx_len,
 
 template <typename T, int D>
 __global__ void __launch_bounds__(D)
-thumb_update_kernel(const T* __restrict__ k, const int32_t* __restrict__ pos, uint8_t* codes,
+thumb_update_kernel(const T* k, const int32_t* pos, uint8_t* codes,
                     T* scales, int8_t* res, int Hkv, int Cap, int block, int nblk_cap) {
   pdl_wait_then_release();
   const int row = blockIdx.x;

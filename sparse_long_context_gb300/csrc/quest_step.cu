@@ -721,7 +721,7 @@ quest_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
         for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t w = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 * u + 2 * m)) : 0u;
+            const uint32_t w = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 * u + 2 * m)) : 0u;
             bp[ks][u] = bf16x2_relu(w);
             bn[ks][u] = bf16x2_negpart(w);
           }
@@ -966,8 +966,8 @@ quest_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const bf16* qp = static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G + r) * D;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      qa[ks][0] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
-      qa[ks][1] = r < G ? __ldg(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
+      qa[ks][0] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * m)) : 0u;
+      qa[ks][1] = r < G ? ld_global(reinterpret_cast<const uint32_t*>(qp + 16 * ks + 8 + 2 * m)) : 0u;
     }
     const uint32_t ring_u32 = smem_u32(ring);
     for (int gi = (W + warp - (int)(seq % W)) % W; gi < ngroups; gi += W) {

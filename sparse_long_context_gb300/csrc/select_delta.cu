@@ -195,7 +195,7 @@ delta_scan_kernel(const DeltaArgs a) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int t = t0 + u * TPS + grp;
-        cw[u] = t < a.block ? __ldg(cb + (size_t)t * WPT) : 0u;
+        cw[u] = t < a.block ? ld_global(cb + (size_t)t * WPT) : 0u;
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
@@ -298,7 +298,7 @@ __device__ __forceinline__ void load_scan_scales(uint4 (&sv)[D / 32], const bf16
   const int m = lane & 3;
 #pragma unroll
   for (int v = 0; v < D / 32; ++v)
-    sv[v] = valid ? __ldg(reinterpret_cast<const uint4*>(sblk + m * (D / 4) + 8 * v)) : make_uint4(0u, 0u, 0u, 0u);
+    sv[v] = valid ? ld_global(reinterpret_cast<const uint4*>(sblk + m * (D / 4) + 8 * v)) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Best margin over the block's tokens for this lane's output columns 2m,

@@ -1171,7 +1171,7 @@ paged_select_kernel(const SelectArgs a, int cluster) {
   KeyRange kr;
   // the share's table entries, where the first CTA's keys will be
   int32_t* tab = reinterpret_cast<int32_t*>(skeys) + p0;
-  for (int i = tid; i < nloc; i += NT) tab[i] = __ldg(a.table + (size_t)b * a.npcap + p0 + i);
+  for (int i = tid; i < nloc; i += NT) tab[i] = ld_global(a.table + (size_t)b * a.npcap + p0 + i);
   if (cluster > 1) cl.sync();  // the first CTA runs before the others write to it
   else __syncthreads();
   if (nloc > 0) {
