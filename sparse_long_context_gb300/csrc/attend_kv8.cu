@@ -464,7 +464,8 @@ kv8_attend_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
     const int N = clamp_len(a.ctx_len[b], a.Cap), ng = groups_of(row), newest = N >> a.c.bshift;
     const int nseg = seg_end - e;
     const int nk = nseg > warp ? (nseg - warp + W - 1) / W : 0;  // this warp's units: u0 + warp + W k
-    const bool failed = sh.s_fail != 0;                          // an earlier segment gave up: no more copies
+    // a wait gave up: no more copies.  (One value for the warp: another warp may set it at any time.)
+    const bool failed = __any_sync(0xffffffffu, sh.s_fail != 0);
     const int32_t* list = LIST ? a.page_idx + (size_t)row * a.idx_stride : nullptr;
     const size_t row_blk = (size_t)row * (a.Cap >> a.c.bshift);
 

@@ -778,8 +778,8 @@ attend_stream_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_co
     const int N = clamp_len(a.ctx_len[b], a.Cap);
     const int nent = (int)(seg_end - e);
     const int32_t* plist = a.page_idx + (size_t)row * a.idx_stride + (int)(e - s_pref[row]);
-    // an earlier segment gave up: no more copies (set before that segment's closing barrier)
-    const bool failed = sh.s_fail != 0;
+    // a wait gave up: no more copies.  (One value for the warp: another warp may set it at any time.)
+    const bool failed = __any_sync(0xffffffffu, sh.s_fail != 0);
     const int ngroups = (nent << a.pshift) >> 4;
     const int nk = ngroups > warp ? (ngroups - warp + W - 1) / W : 0;  // this warp's groups: warp + W k
     const int* pg_src = nullptr;  // page ids from global memory until the list is staged
@@ -988,8 +988,8 @@ attend_refined_tma_kernel(const __grid_constant__ CUtensorMap tk, const __grid_c
     const int N = clamp_len(a.ctx_len[b], a.Cap);
     const int nent = (int)(seg_end - e);
     const int32_t* plist = a.page_idx + (size_t)row * a.idx_stride + (int)(e - s_pref[row]);
-    // an earlier segment gave up: no more copies (set before that segment's closing barrier)
-    const bool failed = sh.s_fail != 0;
+    // a wait gave up: no more copies.  (One value for the warp: another warp may set it at any time.)
+    const bool failed = __any_sync(0xffffffffu, sh.s_fail != 0);
     const int nblk = nent > warp ? (nent - warp + W - 1) / W : 0;  // this warp's blocks: warp + W j
     const int nk = nblk * gpb;
     const int* pg_src = nullptr;  // page ids from global memory until the list is staged
