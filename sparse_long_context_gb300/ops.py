@@ -36,6 +36,13 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+def _need_sink(sink, heads: int, index: int):
+    """A sink for a step on device `index`."""
+    _need(sink, "sink", torch.float32, (heads,))
+    if sink.get_device() != index:
+        raise ValueError("sink must be on the step's device")
+
+
 def _list_width(page_idx) -> int:
     """Entries a row of optional page lists.  Lists without columns have no memory, and no pointer to one means every page."""
     if page_idx is None:
@@ -905,7 +912,7 @@ class Kv8Decode:
         """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
         d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
         if sink is not None:
-            _need(sink, "sink", torch.float32, (Hq,))  # before the token is appended
+            _need_sink(sink, Hq, self.cache.index)  # before the token is appended
         torch.add(self.ctx_len, self.evicted, out=self.positions)
         qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.positions, self.q_weight, self.k_weight,
                      q_out=self.q, k_out=self.k_new)
@@ -996,7 +1003,7 @@ class PagedDecode:
         """qkv [B, Hq + 2 Hkv, D]: the projected heads of one token per sequence.  Returns (out, lse)."""
         d, Hq, H = self.desc, self.desc.num_q_heads, self.desc.num_kv_heads
         if sink is not None:
-            _need(sink, "sink", torch.float32, (Hq,))  # before the token is appended
+            _need_sink(sink, Hq, self.cache.index)  # before the token is appended
         qk_norm_rope(self.rope, qkv[:, :Hq], qkv[:, Hq:Hq + H], self.ctx_len, self.q_weight, self.k_weight, q_out=self.q,
                      k_out=self.k_new)
         paged_append(d, self.cache, self.k_new[:, None], qkv[:, None, Hq + H:], pos_out=self.pos)
