@@ -1132,11 +1132,12 @@ constexpr int kFusedRank = 96;                     // keys ranked exactly
 // and 13.9).
 constexpr int kFusedWide = 512, kFusedMany = 256;
 static_assert(kFusedMany == kSelThreads, "the CUDA-core scorer's threads");
-// Registers as for one CTA an SM where that is how they run, and for up to four fp32 heads (64 rows of 4096 pages of bf16 and D = 64:
-// 23.0 us as the compiler chooses, 19.7 so; 32 fp32 rows of 2048 pages of 4 heads and D = 128: 40.0 and 37.0; but 200 rows of
-// 512 pages of 8 fp32 heads 54 and 89, of bf16 15.0 and 23.4).
-constexpr int fused_min_ctas(int mode, int heads, int threads) {
-  return threads == kFusedWide || (mode == 0 && heads <= 4) ? 1 : 0;
+// CTAs an SM whose registers the kernels are built for (0: the compiler chooses).  One where that is how they run and for up to four
+// fp32 heads (64 rows of 4096 pages of bf16 and D = 64: 23.0 us as the compiler chooses, 19.7 so; 32 fp32 rows of 2048 pages of
+// 4 heads and D = 128: 40.0 and 37.0; but 200 rows of 512 pages of 8 fp32 heads 54 and 89, of bf16 15.0 and 23.4); three for
+// many bf16 rows of D = 64 (384 of 256 pages 11.7 and 11.1; of D = 128 with two 20.0 and 20.6).
+constexpr int fused_min_ctas(int mode, int heads, int threads, int D) {
+  return threads == kFusedWide || (mode == 0 && heads <= 4) ? 1 : mode == 1 && D == 64 ? 3 : 0;
 }
 
 struct FusedShared {
@@ -1148,7 +1149,7 @@ struct FusedShared {
 };
 
 template <typename T, int D, int GM, int MODE, int NT>
-__global__ void __launch_bounds__(NT, fused_min_ctas(MODE, GM, NT))
+__global__ void __launch_bounds__(NT, fused_min_ctas(MODE, GM, NT, D))
 paged_select_kernel(const SelectArgs a, int cluster) {
   namespace cg = cooperative_groups;
   constexpr int NW = NT / 32;
