@@ -8,10 +8,10 @@
 // shared page.
 //
 // Appends and compactions move bytes, at the memory's rate on large ones: four prompts of up to 32k tokens of 8
-// heads of 128 channels 147 us for 973 MB (99% of the measured copy), 8100 of 16400 used pages of 32 KB moved 90 us
-// for 537 MB (89%; the copies alone 81). What is small is a chain of latencies: single tokens of 32
+// heads of 128 channels 147 us for 973 MB (99% of the measured copy), 8100 of 16400 used pages of 32 KB moved 87 us
+// for 537 MB (92%). What is small is a chain of latencies: single tokens of 32
 // sequences 5.9 us, a reordering of 32 beams 9.0, of which the counts, the choice of the pages to copy and
-// the second launch are about a third each, and 250 pages of 8 KB moved 7.1. (Times of the device alone, calls
+// the second launch are about a third each, and 250 pages of 8 KB moved 6.7. (Times of the device alone, calls
 // replayed from a graph.)
 #include <algorithm>
 
@@ -761,7 +761,8 @@ constexpr int kMoveThreads = 256, kMoveUnroll = 4, kMovePerSm = 8;
 
 // Copies the movers (a warp: 2 KB of a page's K and of its V, all loads in flight); the first eighth of the
 // CTAs renames pages in the table and writes the bits anew before that, while the others copy.  Eight CTAs an SM: 90.4
-// us for the pool above, 92 with two, 95 with four; 250 small pages 7.1 us, 8.1 with the renaming at the end.
+// us for the pool above, 92 with two, 95 with four (through the read-only path; 87 with plain loads); 250 small pages 6.7 us, 8.1
+// with the renaming at the end.
 __global__ void __launch_bounds__(kMoveThreads)
 compact_move_kernel(const Paged c, const PagedCompact m, int64_t page_vecs, int64_t meta_vecs, int B, int Cap, int pshift) {
   constexpr uint32_t NT = kMoveThreads, U = kMoveUnroll;
