@@ -311,7 +311,7 @@ __device__ __forceinline__ void score_chunk_mma(const SelectArgs& a, int row, in
             const int p = p0 + i;
             const bool forced = p < a.n_sink || p >= first_local;
             const uint32_t key = forced ? kForcedKey : score_key(half ? v1 : v0);
-                keys[i] = key;
+            keys[i] = key;
             if constexpr (STAGE) {
               if (skeys) skeys[i] = key;
               kr.add(key);
