@@ -45,17 +45,17 @@ METRIC = "decode-step µs and achieved HBM GB/s (% of GB300 peak) for select+att
 # written; traffic grows with the rows, so x4 for batch 32).  Reported only
 # for that workload and only while the kernel's sources hash to the ones
 # captured; otherwise null.
-STEP_TRAFFIC_B32 = 4 * (50.470656e6 + 0.0896e6)
+STEP_TRAFFIC_B32 = 4 * (50.470144e6 + 0.109312e6)
 STEP_SOURCES = ("quest_step.cu", "page_bound.cuh", "attend_tma.cuh", "tma.cuh", "mma.cuh", "attend_common.cuh",
                 "common.cuh", "status.cuh")
-STEP_SOURCES_SHA256 = "6c142f0c02d89e989b38c5301a9662819dd78d17eec6ca7c590b9f63d49cde58"
+STEP_SOURCES_SHA256 = "89b2d1dae943f36d83a24d022ab8137f3818e2cf63a71bf46e15dadf1bab42c1"
 
 
 # DRAM bytes per launch of the top-delta step's bf16-key attend
 # (attend_stream_tma_kernel) on the ffd workload, from the committed capture
 # (profiles/topdelta_ffd_256k.md, read + written; the kept set is the seeded
 # workload's), under the same source-hash rule.
-FFD_ATTEND_TRAFFIC = 490.947328e6 + 2.676736e6
+FFD_ATTEND_TRAFFIC = 490.944e6 + 3.047424e6
 FFD_ATTEND_SOURCES = ('attend_refined.cu', 'attend_tma.cuh', 'tma.cuh', 'mma.cuh', 'attend_common.cuh', 'common.cuh', 'status.cuh')
 FFD_ATTEND_SOURCES_SHA256 = "f6cb7c3fe29f1ad01fc651500751a125df759eb6a82532fa1788319fd94eb521"
 

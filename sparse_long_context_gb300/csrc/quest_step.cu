@@ -753,15 +753,21 @@ quest_step_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant_
           put(i1, v1);
         }
       }
-      if (none)  // the lane's pages without a score
-        for (int i = (W + warp - (int)(seq % W)) % W; i < n1; i += W)
-          for (int at = 16 * i + r; at < min(16 * i + 16, nloc); at += 8)
-            if (keys[at] == kNoScoreKey) {
-              const size_t page = ((size_t)row * sa.npcap + p0 + at) * D;
-              keys[at] = defined_page_key<bf16>(static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D,
-                                                static_cast<const bf16*>(sa.kmin) + page,
-                                                static_cast<const bf16*>(sa.kmax) + page, G, D);
-            }
+      if (__any_sync(0xffffffffu, none)) {  // the warp's pages without a score, one after the other
+        __syncwarp();
+        for (int i = (W + warp - (int)(seq % W)) % W; i < n1; i += W) {
+          const int at0 = 16 * i;
+          unsigned todo = __ballot_sync(0xffffffffu, lane < min(16, nloc - at0) && keys[min(at0 + lane, nloc - 1)] == kNoScoreKey);
+          for (; todo; todo &= todo - 1) {
+            const int at = at0 + __ffs(todo) - 1;
+            const size_t page = ((size_t)row * sa.npcap + p0 + at) * D;
+            const uint32_t key = defined_page_key<bf16>(
+                static_cast<const bf16*>(a.q) + ((size_t)b * a.Hq + (size_t)h * G) * D,
+                static_cast<const bf16*>(sa.kmin) + page, static_cast<const bf16*>(sa.kmax) + page, G, D);
+            if (lane == 0) keys[at] = key;
+          }
+        }
+      }
     }
     seq += n1;
     __syncthreads();  // keys complete; the ring is free
